@@ -353,6 +353,118 @@ blink_status blink_label_readout_noalloc(const blink_bf16 *hidden, int64_t hidde
                                          const int32_t *d_label_ids, int32_t B, int32_t sum_k, float temperature,
                                          float *d_probs, float *h_probs, float *d_logits, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Attention weight received by each prefix key -- the quantity a cache is evicted by.  The pages
+ * evict whole cached prefixes; this call and the next are additions of this library for callers
+ * that shorten a cached prefix instead (long documents held for many questions).
+ *
+ * For kv head h and prefix position p:
+ *   w[h][p] = decay * prev[h][p] + sum over rows i and the g = Hq / Hkv query heads j of the group
+ *             of exp(scale * q[i][h g + j] . k_pre[p][h] - lse[h g + j][i])
+ * i.e. the softmax weights blink_prefix_tail_attention gave that key, summed over the rows and the
+ * query heads that share it, when lse is that call's output.  A row whose lse is -inf (a row owned
+ * by no question) adds nothing, whatever its q holds; a NaN in any other row or its lse makes the
+ * weights of that kv head NaN.  lse must not be smaller than the scores it normalises by more than
+ * 80 (an attention's own lse never is).
+ *
+ * q       [rows, Hq, d] bf16, rows >= 1 (one row: a single decoded token)
+ * k_pre   [P, Hkv, d]   bf16 rows pre_row_stride elements apart, as for the attention; P in 1..131072
+ * lse     fp32 natural-log log-sum-exp, head h at lse + h * lse_stride (lse_stride >= rows), so the
+ *         rows of one request can be passed as a slice of a larger launch
+ * scale   softmax scale; <= 0 selects 1/sqrt(d).  d in {64, 128}, Hq/Hkv <= 128
+ * decay   finite, >= 0; 0: d_prev is not read and may be NULL
+ * d_prev  fp32, head h at d_prev + h * prev_stride (stride >= P); may be d_weights itself with the
+ *         same stride (accumulation in place), otherwise the two must not overlap
+ * d_weights  fp32 output, head h at d_weights + h * w_stride (stride >= P)
+ * d_ws    workspace of blink_prefix_key_weights_workspace(...) bytes, its first 256 zero-filled
+ *         before its first use; not shared by calls that may run at the same time
+ * The sum's order is fixed by the shapes and the GPU: repeated calls give the same bits.
+ * Errors: BLINK_INVALID_ARG, BLINK_OUT_OF_RANGE, BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR;
+ * device-side: BLINK_DEVICE_TIMEOUT.
+ * ------------------------------------------------------------------------------------------ */
+size_t blink_prefix_key_weights_workspace(int32_t rows, int32_t P, int32_t Hq, int32_t Hkv, int32_t d);
+
+blink_status blink_prefix_key_weights(const blink_bf16 *q, const blink_bf16 *k_pre, int64_t pre_row_stride,
+                                      const float *lse, int64_t lse_stride, int32_t rows, int32_t P, int32_t Hq,
+                                      int32_t Hkv, int32_t d, float scale, float decay, const float *d_prev,
+                                      int64_t prev_stride, float *d_weights, int64_t w_stride, void *d_ws,
+                                      size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Eviction of a cached prefix's lightest keys -- every kv head keeps `keep` of its P keys and its
+ * arena region is compacted to slots [0, keep).  Keys carry their positions (they are stored after
+ * the rotation), so the attention reads the kept ones in any order: pass P = keep to it.
+ *
+ * Order of a head's keys: protected keys first (position < sink or >= recent_from), then larger
+ * weight first (a NaN weight counts as the smallest), then lower slot first; the first `keep` are
+ * kept.  A kept key in a slot below `keep` stays there; the other slots below `keep` receive the kept
+ * keys of the slots at `keep` and above, both in ascending slot order.  So at most min(keep, P - keep)
+ * keys per head move when the region is compacted in place.
+ *
+ * d_weights   fp32, head h's P weights at d_weights + h * w_stride
+ * d_pos       int32, original position of the key in each slot, head h at d_pos + h * pos_stride;
+ *             NULL: slot s holds position s (a region that was never evicted)
+ * P, keep     1 <= keep <= P <= 131072
+ * sink        >= 0; recent_from >= 0 (INT32_MAX protects no recent position)
+ * k, v        [P, Hkv, d] bf16 rows row_stride elements apart (d a multiple of 8, at most 1024;
+ *             16-byte aligned; strides multiples of 8)
+ * k_dst, v_dst  where the kept keys go, rows dst_row_stride elements apart: k and v themselves with
+ *             the same stride (in place), or memory that overlaps neither k nor v
+ * d_slots     [Hkv][keep] int32 output: the slot each kept key came from
+ * d_weights_dst, d_pos_dst  optional outputs [Hkv][keep] (row strides wd_stride, pd_stride): weights
+ *             and positions of the kept keys; each may be its input itself with the same stride, or
+ *             memory that overlaps neither input
+ * d_ws        workspace of blink_kv_evict_workspace(...) bytes; not shared by calls that may run at
+ *             the same time
+ * Errors: BLINK_INVALID_ARG (null, alignment, strides, overlap), BLINK_OUT_OF_RANGE (P, keep, Hkv, d),
+ * BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR.
+ * ------------------------------------------------------------------------------------------ */
+size_t blink_kv_evict_workspace(int32_t P, int32_t keep, int32_t Hkv);
+
+blink_status blink_kv_evict(const float *d_weights, int64_t w_stride, const int32_t *d_pos, int64_t pos_stride,
+                            int32_t P, int32_t keep, int32_t sink, int32_t recent_from, int32_t Hkv, int32_t d,
+                            const blink_bf16 *k, const blink_bf16 *v, int64_t row_stride, blink_bf16 *k_dst,
+                            blink_bf16 *v_dst, int64_t dst_row_stride, int32_t *d_slots, float *d_weights_dst,
+                            int64_t wd_stride, int32_t *d_pos_dst, int64_t pd_stride, void *d_ws, size_t ws_bytes,
+                            cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Log probabilities over the whole vocabulary -- the label readout's next-token distribution
+ * without the restriction to the offered labels: how likely a given token is, how uncertain the
+ * model is, and which tokens it prefers (so also how much of the distribution the labels hold).
+ *
+ * For row r: z = hidden[idx[r]] . unembed^T / temperature (FP32 accumulation; the logits are never
+ * written to memory), lse = logsumexp(z), and
+ *   d_logprob[r] = z[d_targets[r]] - lse      d_entropy[r] = lse - sum softmax(z) z  (nats)
+ *   d_lse[r] = lse      d_top_ids[r][j], d_top_logprobs[r][j]: the j-th largest z - lse, equal
+ *   logits by ascending token id
+ *
+ * hidden [hidden_rows, H] bf16, row r at hidden + r * hidden_row_stride (multiple of 8 elements)
+ * d_row_idx  int32 [n] hidden rows (in any order, repeats allowed); NULL: row r of hidden (n <= hidden_rows)
+ * unembed [V, H] bf16 row-major; H a multiple of 8, 16-byte aligned; H in 8..32768, V in 1..2^24
+ * n          1..131072 rows (one row: a single decoded token)
+ * d_targets  int32 [n]; -1: the row has no target (its log probability is NaN).  NULL without d_logprob
+ * temperature  > 0 and finite
+ * top        0..BLINK_MAX_TOP_TOKENS alternatives per row, at most V
+ * Outputs: each may be NULL, not all; d_top_ids and d_top_logprobs [n][top] together, when top > 0
+ * d_ws       workspace of blink_token_logprobs_workspace(...) bytes (of the current device), its first
+ *            256 zero-filled before its first use; not shared by calls that may run at the same time
+ * A row index outside [0, hidden_rows) latches BLINK_DEVICE_FLAG and makes the row's outputs NaN and
+ * -1; a target outside [-1, V) latches it and makes that log probability NaN.  A row with a NaN logit
+ * gets NaN (ids: those of its other logits, then -1); logits must not be infinite.
+ * Errors: BLINK_INVALID_ARG, BLINK_OUT_OF_RANGE, BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR;
+ * device-side: BLINK_DEVICE_FLAG, BLINK_DEVICE_TIMEOUT.
+ * ------------------------------------------------------------------------------------------ */
+#define BLINK_MAX_TOP_TOKENS 32
+
+size_t blink_token_logprobs_workspace(int32_t n, int32_t H, int32_t V, int32_t top);
+
+blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t hidden_row_stride, int32_t hidden_rows,
+                                  const int32_t *d_row_idx, const blink_bf16 *unembed, int32_t V, int32_t H,
+                                  const int32_t *d_targets, int32_t n, float temperature, int32_t top,
+                                  float *d_logprob, float *d_entropy, float *d_lse, int32_t *d_top_ids,
+                                  float *d_top_logprobs, void *d_ws, size_t ws_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,6 +27,7 @@ MAX_OPTIONS = 255
 MAX_QUESTIONS = 512
 MAX_INPUT_TOKENS = 131072
 MAX_PLAN_SEQUENCES = 32768
+MAX_TOP_TOKENS = 32
 
 
 class BlinkError(RuntimeError):
@@ -66,6 +67,15 @@ _SIGNATURES = {
                                    _vp, _vp, _vp, _vp, _sz, _vp]),
     "blink_label_readout_noalloc": (_i32, [_vp, _i64, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _i32, _f32, _vp,
                                            _vp, _vp, _vp]),
+    "blink_prefix_key_weights_workspace": (_sz, [_i32] * 5),
+    "blink_prefix_key_weights": (_i32, [_vp, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _f32, _f32, _vp, _i64,
+                                        _vp, _i64, _vp, _sz, _vp]),
+    "blink_kv_evict_workspace": (_sz, [_i32] * 3),
+    "blink_kv_evict": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _i64,
+                              _vp, _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
+    "blink_token_logprobs_workspace": (_sz, [_i32] * 4),
+    "blink_token_logprobs": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _f32, _i32] + [_vp] * 6 +
+                             [_sz, _vp]),
 }
 
 
@@ -350,3 +360,196 @@ def blink_rotation_debias(logits, pass_off, key_of_pos, question_pass, raw_off, 
                                      _ptr(ws), ws.numel(), _stream(stream))
     _check(st, "blink_rotation_debias")
     return probs, raw, answers
+
+
+# ------------------------------------------------------------------------------------------------ cache eviction
+INT32_MAX = 2**31 - 1
+
+
+def _need(name, t, dtype, shape=None, inner: int = 1):
+    """`t` is a CUDA tensor of `dtype` (and `shape`, where given: None leaves a size free) whose last
+    `inner` dimensions are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    want = 1
+    for s, st in list(zip(t.shape, t.stride()))[::-1][:inner]:
+        if s != 1 and st != want:
+            raise ValueError(f"{name}: the last {inner} dimension(s) must be contiguous")
+        want *= s
+
+
+def _row_stride(t) -> int:
+    """Elements between the rows (first dimension) of `t`; a single row has any stride."""
+    return int(t.stride(0)) if t.shape[0] > 1 else int(t[0].numel())
+
+
+class _Launch:
+    """The device of the call's tensors made current and its stream: `stream`, or that device's
+    current one.  What the call allocates belongs to that stream, and its inputs are marked as used on
+    it, so a caller that passes another stream than its tensors' own may drop them after the call."""
+
+    def __init__(self, stream, *tensors):
+        ts = [t for t in tensors if t is not None]
+        self.device = ts[0].device
+        if any(t.device != self.device for t in ts):
+            raise ValueError("tensors passed to one call must be on one device")
+        self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if self.stream.device != self.device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self.tensors = ts
+        self.explicit = stream is not None
+
+    def __enter__(self):
+        self._dev = torch.cuda.device(self.device)
+        self._str = torch.cuda.stream(self.stream)
+        self._dev.__enter__()
+        self._str.__enter__()
+        if self.explicit and not torch.cuda.is_current_stream_capturing():
+            for t in self.tensors:
+                t.record_stream(self.stream)
+        return self
+
+    def __exit__(self, *exc):
+        self._str.__exit__(*exc)
+        self._dev.__exit__(*exc)
+
+    def workspace(self, ws, nbytes: int):
+        """`ws`, or a new workspace whose header (all that has to start at zero) is cleared."""
+        if ws is None:
+            ws = torch.empty(max(256, (nbytes + 255) // 256 * 256), dtype=torch.uint8, device=self.device)
+            ws[:256].zero_()
+        return ws
+
+
+def _need_ws(ws):
+    if ws is not None:
+        _need("ws", ws, torch.uint8, (None,))
+
+
+def key_weights_workspace_bytes(rows, P, Hq, Hkv, d) -> int:
+    return int(lib().blink_prefix_key_weights_workspace(int(rows), int(P), int(Hq), int(Hkv), int(d)))
+
+
+def blink_prefix_key_weights(q, k_pre, lse, prev=None, decay: float = 0.0, scale: float = 0.0, out=None, ws=None,
+                             stream=None):
+    """Attention weight each prefix key received: q [rows, Hq, d] and k_pre [P, Hkv, d] bf16 (the rows
+    of k_pre may be strided: an arena region), lse [Hq, rows] fp32 from blink_prefix_tail_attention
+    (a slice of a wider one is fine).  Returns (weights [Hkv, P] fp32, ws); with `prev` and `decay` > 0
+    decay * prev is added (`out=prev` accumulates in place)."""
+    _need("q", q, torch.bfloat16, (None, None, None), inner=3)
+    rows, Hq, d = q.shape
+    _need("k_pre", k_pre, torch.bfloat16, (None, None, d), inner=2)
+    P, Hkv = k_pre.shape[:2]
+    _need("lse", lse, torch.float32, (Hq, rows))
+    if prev is not None:
+        _need("prev", prev, torch.float32, (Hkv, P))
+    if out is not None:
+        _need("out", out, torch.float32, (Hkv, P))
+    _need_ws(ws)
+    with _Launch(stream, q, k_pre, lse, prev, out, ws) as call:
+        if out is None:
+            out = torch.empty(Hkv, P, dtype=torch.float32, device=q.device)
+        ws = call.workspace(ws, key_weights_workspace_bytes(rows, P, Hq, Hkv, d))
+        st = lib().blink_prefix_key_weights(
+            _ptr(q), _ptr(k_pre), _row_stride(k_pre), _ptr(lse), _row_stride(lse), int(rows), int(P), int(Hq), int(Hkv),
+            int(d), float(scale), float(decay), _ptr(prev), _row_stride(prev) if prev is not None else 0, _ptr(out),
+            _row_stride(out), _ptr(ws), ws.numel(), _stream(call.stream))
+    _check(st, "blink_prefix_key_weights")
+    return out, ws
+
+
+def kv_evict_workspace_bytes(P, keep, Hkv) -> int:
+    return int(lib().blink_kv_evict_workspace(int(P), int(keep), int(Hkv)))
+
+
+def blink_kv_evict(weights, k, v, keep: int, pos=None, sink: int = 0, recent_from: int | None = None, k_dst=None,
+                   v_dst=None, weights_dst=None, pos_dst=None, slots=None, ws=None, stream=None) -> dict:
+    """Keep the `keep` heaviest of the P keys of every kv head: weights [Hkv, P] fp32, k and v
+    [P, Hkv, d] bf16 arena regions (strided rows are fine), pos [Hkv, P] int32 positions (None: the slots).
+    Without k_dst / v_dst the regions are compacted in place into their first `keep` rows; with them the
+    kept rows are written there.  weights_dst / pos_dst may be views of weights / pos (in place).
+    Returns {"slots", "k", "v", "weights", "pos", "ws"}, all of `keep` keys per head."""
+    _need("weights", weights, torch.float32, (None, None))
+    Hkv, P = weights.shape
+    _need("k", k, torch.bfloat16, (P, Hkv, None), inner=2)
+    d = k.shape[2]
+    _need("v", v, torch.bfloat16, (P, Hkv, d), inner=2)
+    keep = int(keep)
+    if not 1 <= keep <= P:
+        raise ValueError(f"keep must be in 1..{P}, not {keep}")
+    if pos is not None:
+        _need("pos", pos, torch.int32, (Hkv, P))
+    if (k_dst is None) != (v_dst is None):
+        raise ValueError("k_dst and v_dst go together")
+    if _row_stride(k) != _row_stride(v) and P > 1:
+        raise ValueError("k and v must have the same row stride")
+    k_out = k[:keep] if k_dst is None else k_dst
+    v_out = v[:keep] if v_dst is None else v_dst
+    _need("k_dst", k_out, torch.bfloat16, (keep, Hkv, d), inner=2)
+    _need("v_dst", v_out, torch.bfloat16, (keep, Hkv, d), inner=2)
+    dst_stride = _row_stride(k) if k_dst is None else _row_stride(k_out)
+    if k_dst is not None and keep > 1 and _row_stride(v_out) != dst_stride:
+        raise ValueError("k_dst and v_dst must have the same row stride")
+    for name, t, dt in (("weights_dst", weights_dst, torch.float32), ("pos_dst", pos_dst, torch.int32),
+                        ("slots", slots, torch.int32)):
+        if t is not None:
+            _need(name, t, dt, (Hkv, keep), inner=2 if name == "slots" else 1)
+    _need_ws(ws)
+    with _Launch(stream, weights, k, v, pos, k_dst, v_dst, weights_dst, pos_dst, slots, ws) as call:
+        dev = weights.device
+        if slots is None:
+            slots = torch.empty(Hkv, keep, dtype=torch.int32, device=dev)
+        if weights_dst is None:
+            weights_dst = torch.empty(Hkv, keep, dtype=torch.float32, device=dev)
+        if pos_dst is None:
+            pos_dst = torch.empty(Hkv, keep, dtype=torch.int32, device=dev)
+        ws = call.workspace(ws, kv_evict_workspace_bytes(P, keep, Hkv))
+        st = lib().blink_kv_evict(
+            _ptr(weights), _row_stride(weights), _ptr(pos), _row_stride(pos) if pos is not None else 0, int(P), keep,
+            int(sink), INT32_MAX if recent_from is None else int(recent_from), int(Hkv), int(d), _ptr(k), _ptr(v),
+            _row_stride(k), _ptr(k_out), _ptr(v_out), dst_stride, _ptr(slots), _ptr(weights_dst),
+            _row_stride(weights_dst), _ptr(pos_dst), _row_stride(pos_dst), _ptr(ws), ws.numel(), _stream(call.stream))
+    _check(st, "blink_kv_evict")
+    return {"slots": slots, "k": k_out, "v": v_out, "weights": weights_dst, "pos": pos_dst, "ws": ws}
+
+
+# ------------------------------------------------------------------------------------------------ whole vocabulary
+def token_logprobs_workspace_bytes(n, H, V, top) -> int:
+    return int(lib().blink_token_logprobs_workspace(int(n), int(H), int(V), int(top)))
+
+
+def blink_token_logprobs(hidden, unembed, targets=None, row_idx=None, temperature: float = 1.0, top: int = 0, ws=None,
+                         stream=None) -> dict:
+    """Whole-vocabulary readout of hidden rows [rows, H] bf16 (all of them, or those of int32 `row_idx`)
+    against unembed [V, H] bf16.  Returns {"logprob" (of int32 `targets`, else None), "entropy", "lse",
+    "top_ids", "top_logprobs" ([n, top], None for top = 0), "ws"}; nothing is copied to the host.
+    Device-side problems (a bad row index or target) are read with blink_read_device_status(ws)."""
+    _need("hidden", hidden, torch.bfloat16, (None, None))
+    rows, H = hidden.shape
+    _need("unembed", unembed, torch.bfloat16, (None, H), inner=2)
+    V = unembed.shape[0]
+    if row_idx is not None:
+        _need("row_idx", row_idx, torch.int32, (None,))
+    n = rows if row_idx is None else row_idx.numel()
+    if targets is not None:
+        _need("targets", targets, torch.int32, (n,))
+    _need_ws(ws)
+    top = int(top)
+    with _Launch(stream, hidden, unembed, targets, row_idx, ws) as call:
+        def new(dtype, *shape):
+            return torch.empty(*shape, dtype=dtype, device=hidden.device)
+        r = {"logprob": new(torch.float32, n) if targets is not None else None, "entropy": new(torch.float32, n),
+             "lse": new(torch.float32, n), "top_ids": new(torch.int32, n, top) if top > 0 else None,
+             "top_logprobs": new(torch.float32, n, top) if top > 0 else None}
+        ws = call.workspace(ws, token_logprobs_workspace_bytes(n, H, V, top))
+        st = lib().blink_token_logprobs(
+            _ptr(hidden), _row_stride(hidden) if rows else int(H), int(rows), _ptr(row_idx), _ptr(unembed), int(V), int(H), _ptr(targets),
+            int(n), float(temperature), top, _ptr(r["logprob"]), _ptr(r["entropy"]), _ptr(r["lse"]), _ptr(r["top_ids"]),
+            _ptr(r["top_logprobs"]), _ptr(ws), ws.numel(), _stream(call.stream))
+    _check(st, "blink_token_logprobs")
+    r["ws"] = ws
+    return r

@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libblink.so")
-SOURCES = ["common.cu", "plan.cu", "readout.cu", "attention.cu", "prefix.cu", "debias.cu"]
+SOURCES = ["common.cu", "plan.cu", "readout.cu", "attention.cu", "prefix.cu", "debias.cu",
+           "keyweights.cu", "evict.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
