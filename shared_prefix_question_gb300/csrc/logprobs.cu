@@ -1,208 +1,701 @@
 // logprobs.cu -- log probabilities of given tokens, entropy and top alternatives over the whole
-// vocabulary, without writing the logits.
+// vocabulary (blink_token_logprobs), without writing the logits.
 //
 // Mathematics.  With y = z log2(e) / T for the raw product z = h . w, a part of the vocabulary is
 // summarised by m = max y, s = sum 2^(y - m) and u = sum 2^(y - m) (y - m); two parts merge by
 // rescaling to the larger m:  s = a s1 + b s2,  u = a (u1 + s1 (m1 - m)) + b (u2 + s2 (m2 - m)) with
-// a = 2^(m1 - m), b = 2^(m2 - m).  Then lse = ln2 (m + log2 s) and entropy = ln2 (log2 s - u / s).
+// a = 2^(m1 - m), b = 2^(m2 - m).  Then lse = ln2 (m + log2 s) and entropy = ln2 (log2 s - u / s),
+// whose two terms are both small when the distribution is peaked.  Alternatives and the target keep
+// the raw z, which the temperature does not reorder.
 //
-// One block per (8 hidden rows, part of the vocabulary): a warp takes a vocabulary row, its lanes
-// split H, and after the reduction lane r folds the product of hidden row r into its state.
+// Work.  Hidden rows are the M rows of the product (a tensor-memory lane, so a thread, holds one row
+// and folds the logits into its state without any exchange), vocabulary rows the N columns, 256 per
+// tile.  Up to 128 rows one block works alone (M = 128: the call is bound by reading the unembedding
+// once, and the tensor time of 128 rows stays below that); above, a pair of blocks works on 256
+// rows (cta_group::2, M = 256, N = 256: each block loads half of the vocabulary tile, so a byte
+// staged in shared memory feeds twice the products).
+// Rows beyond one tile run in passes of up to a few row tiles; within a pass every row tile is cut
+// into the same vocabulary chunks, and the workers on one chunk run side by side so that the
+// unembedding comes from HBM once per pass.  A worker carries its rows' state in registers through its
+// chunk and writes it once; the merge launch joins the chunks of a row.
+//
+// Precision.  The tensor core's fp32 accumulator truncates: over a sum of H / 16 steps the loss grows
+// with H (measured against 64 bits, logits of 12: 2.7e-6 of the logit at H = 2560, 5.4e-6 at 5120, and
+// four times that where all products have one sign).  So a product runs over kPartBlocks * 64 of H
+// only, and the row's thread adds the parts in registers, rounded to nearest: the loss stays that of
+// one part whatever H is.
+//
+// Roles (384 threads a block): warps 0-7 the states (thread t and t + 128 share row t, 128 of a tile's
+// columns each), warp 8 TMA producer, warp 9 MMA issuer (of the even block).  Tensor memory: two
+// accumulators of 256 columns, so one part is read out and folded while the next is multiplied.  The
+// states take 232 registers a thread (128 of them the tile's logits), the other warps 40.
 #include <cstdint>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace blink {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kRows = 8;
-constexpr int kWarps = 8;
 constexpr int kMaxTop = BLINK_MAX_TOP_TOKENS;
-constexpr int kParts = 64;
+constexpr int kVocabTile = 256;
+constexpr int kBlockRows = 128;
+constexpr int kThreadsLP = 384;
+constexpr int kStateWarps = 8;
+constexpr int kProducerLP = 8, kIssuerLP = 9;
+constexpr int kRegsNeeded = 256 * 232 + 128 * 40;
+constexpr int kHalves = 2;      // threads that share a row
+constexpr int kHalfCols = kVocabTile / kHalves;
+constexpr int kPartBlocks = 8;  // 64-wide blocks of H per product
+constexpr int kNoToken = 0x7FFFFFFF;
+constexpr int kMaxWorkers = 160;
+constexpr int kMaxStages = 8;
 
-__device__ __forceinline__ float lo16(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi16(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+// How the rows and the vocabulary are shared out (computed on the host, walked by every role).
+struct LogprobPlan {
+    int blocks_per_worker;  // 1, or 2 (a pair)
+    int workers;
+    int row_tiles, tile_rows;  // rows per tile: 128 per block
+    int vocab_tiles;
+    int group;                // row tiles of a full pass
+    int full_passes, chunks;  // vocabulary chunks of a full pass
+    int rest, rest_chunks;    // row tiles and chunks of the last, smaller pass (rest = 0: none)
+    __host__ __device__ int passes() const { return full_passes + (rest > 0 ? 1 : 0); }
+    __host__ __device__ int tiles_of(int pass) const { return pass < full_passes ? group : rest; }
+    __host__ __device__ int chunks_of(int pass) const { return pass < full_passes ? chunks : rest_chunks; }
+    __host__ __device__ int64_t first_cell(int pass) const
+    {
+        return static_cast<int64_t>(pass) * group * chunks * kHalves * tile_rows;
+    }
+    __host__ __device__ int64_t cells() const
+    {
+        return first_cell(full_passes) + static_cast<int64_t>(rest) * rest_chunks * kHalves * tile_rows;
+    }
+};
+
+// A worker's part of one pass: vocabulary tiles [v0, v1) of one row tile, and the cell its states go to.
+struct Share {
+    int row_tile, v0, v1;
+    int64_t cell, half_step;  // of the first half's states; from there to the second half's
+    bool any;
+};
+
+__host__ __device__ inline Share share_of(const LogprobPlan &p, int pass, int worker)
+{
+    Share s;
+    const int g = p.tiles_of(pass), nc = p.chunks_of(pass);
+    s.any = worker < g * nc;
+    const int t = worker % g;
+    // chunks differ by one tile; each pass deals them to the workers from another place
+    const int chunk = (worker / g + pass * 7) % nc;
+    s.row_tile = pass * p.group + t;
+    s.v0 = static_cast<int>(static_cast<int64_t>(p.vocab_tiles) * chunk / nc);
+    s.v1 = static_cast<int>(static_cast<int64_t>(p.vocab_tiles) * (chunk + 1) / nc);
+    s.cell = p.first_cell(pass) + (static_cast<int64_t>(chunk) * kHalves * g + t) * p.tile_rows;
+    s.half_step = static_cast<int64_t>(g) * p.tile_rows;
+    return s;
+}
+
+LogprobPlan make_plan(int n, int V, int sms)
+{
+    LogprobPlan p{};
+    p.blocks_per_worker = n > kBlockRows ? 2 : 1;
+    p.tile_rows = kBlockRows * p.blocks_per_worker;
+    p.workers = sms / p.blocks_per_worker;
+    if (p.workers < 1) p.workers = 1;
+    if (p.workers > kMaxWorkers) p.workers = kMaxWorkers;
+    p.row_tiles = (n + p.tile_rows - 1) / p.tile_rows;
+    p.vocab_tiles = (V + kVocabTile - 1) / kVocabTile;
+    auto chunks_for = [&](int tiles) {
+        const int c = p.workers / tiles;
+        return c < p.vocab_tiles ? c : p.vocab_tiles;
+    };
+    // Row tiles per full pass: the count of 2..6 that leaves the fewest workers idle, the larger of
+    // equals (fewer passes over the unembedding); all of them when there are no more than that.
+    int best = 1, best_used = 0;
+    for (int g = 2; g <= 6 && g <= p.workers; ++g) {
+        const int used = p.workers / g * g;
+        if (used >= best_used) best = g, best_used = used;
+    }
+    p.group = best < p.row_tiles ? best : p.row_tiles;
+    p.full_passes = p.row_tiles / p.group;
+    p.chunks = chunks_for(p.group);
+    p.rest = p.row_tiles - p.full_passes * p.group;
+    p.rest_chunks = p.rest > 0 ? chunks_for(p.rest) : 0;
+    return p;
+}
 
 struct LogprobArgs {
-    const uint16_t *hidden;
-    int64_t hidden_stride;
-    int hidden_rows;
-    const int32_t *row_idx;
-    const uint16_t *W;
+    LogprobPlan plan;
     int V, H, n, top;
+    int a_rows;  // rows of one copy of hidden states (a multiple of 8, at most 128)
+    const int32_t *row_idx;
+    int hidden_rows;
     const int32_t *targets;
-    float c;  // log2(e) / T
-    float4 *stat;  // [parts][n]: m, s, u, target's raw product (NaN: not in this part)
-    float *top_z;  // [parts][n][top] raw products, descending
-    int32_t *top_id;
+    float c;       // log2(e) / T
+    float4 *stat;  // [cells]: m, s, u, target's raw product (NaN: not in this part)
+    int2 *best;    // [cells][top]: raw product (as bits) and token, descending
     float *logprob, *entropy, *lse, *top_lp;
     int32_t *top_ids;
     int *err;
+    int gathered;  // the hidden rows were gathered by the launch before
 };
 
-__device__ __forceinline__ void merge_stat(float &m, float &s, float &u, float m2, float s2, float u2)
-{
-    if (m2 == -INFINITY) {
-        s += s2;  // an empty part, or one of NaN alone
-        return;
+template <int kCtas>
+struct LpLayout {
+    static constexpr int kABytes = kBlockRows * 128;               // 64 of H per stage
+    static constexpr int kBRows = kVocabTile / kCtas;
+    static constexpr int kBBytes = kBRows * 128;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = kCtas == 1 ? 4 : 6;
+    static constexpr int kScoreOff = kStages * kStageBytes;        // [32][threads of the states] floats
+    static constexpr int kBarOff = kScoreOff + 32 * kStateWarps * 32 * 4;
+    static constexpr int kBytes = kBarOff + 256;
+};
+
+// State of one row: running (m, s, u), the target's product and the best kTop products so far.
+// The list holds `top` entries in its last places; the places before them are +inf and never move.
+template <int kTop>
+struct RowState {
+    float m, s, u, tz;
+    float v[kTop > 0 ? kTop : 1];
+    int32_t id[kTop > 0 ? kTop : 1];
+    __device__ __forceinline__ void clear(int top)
+    {
+        m = -INFINITY;
+        s = u = 0.f;
+        tz = __int_as_float(0x7FC00000);
+#pragma unroll
+        for (int j = 0; j < kTop; ++j) {
+            v[j] = j < kTop - top ? INFINITY : -INFINITY;
+            id[j] = kNoToken;
+        }
     }
-    const float M = fmaxf(m, m2);
-    const float d1 = m == -INFINITY ? 0.f : m - M, d2 = m2 - M;
-    const float a = exp2f(d1), b = exp2f(d2);
-    u = a * (u + s * d1) + b * (u2 + s2 * d2);
-    s = a * s + b * s2;
-    m = M;
+    // Tokens come in ascending id, so an equal product goes behind those already listed.
+    __device__ __forceinline__ void insert(float z, int32_t i)
+    {
+        bool moved = false;
+#pragma unroll
+        for (int j = 0; j < kTop; ++j) {
+            moved = moved || z > v[j];
+            const float ov = v[j];
+            const int32_t oi = id[j];
+            v[j] = moved ? z : ov;
+            id[j] = moved ? i : oi;
+            z = moved ? ov : z;
+            i = moved ? oi : i;
+        }
+    }
+};
+
+// Folds 32 logits of a row, tokens id0 .. id0 + 31, into its state.
+template <int kTop>
+__device__ __forceinline__ void fold_columns(RowState<kTop> &r, float *z, int id0, int V, float c, int target, float *zs,
+                                             int zs_step)
+{
+    if (id0 >= V) return;
+    const bool whole = id0 + 32 <= V;
+    if (!whole) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (id0 + j >= V) z[j] = -INFINITY;
+    }
+    float m0 = fmaxf(z[0], z[1]), m1 = fmaxf(z[2], z[3]);
+#pragma unroll
+    for (int j = 4; j < 32; j += 4) {
+        m0 = ptx::max3(m0, z[j], z[j + 1]);
+        m1 = ptx::max3(m1, z[j + 2], z[j + 3]);
+    }
+    const float zmax = fmaxf(m0, m1);
+    const float ym = zmax * c;
+    if (ym > r.m) {
+        const float d = r.m == -INFINITY ? 0.f : r.m - ym, f = ptx::ex2(d);
+        r.u = f * fmaf(r.s, d, r.u);
+        r.s *= f;
+        r.m = ym;
+    }
+    const float nm = r.m == -INFINITY ? 0.f : -r.m;  // all NaN so far
+    float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
+    if (whole) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const float x0 = fmaf(z[j], c, nm), x1 = fmaf(z[j + 1], c, nm);
+            const float e0 = ptx::ex2(x0), e1 = ptx::ex2(x1);
+            s0 += e0;
+            s1 += e1;
+            u0 = fmaf(e0, x0, u0);
+            u1 = fmaf(e1, x1, u1);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (id0 + j < V) {
+                const float x0 = fmaf(z[j], c, nm), e0 = ptx::ex2(x0);
+                s0 += e0;
+                u0 = fmaf(e0, x0, u0);
+            }
+        }
+    }
+    r.s += s0 + s1;
+    r.u += u0 + u1;
+    if (__any_sync(0xFFFFFFFFu, static_cast<uint32_t>(target - id0) < 32u)) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (target == id0 + j) r.tz = z[j];
+    }
+    if constexpr (kTop > 0) {
+        // Candidates: products above the list's last.  Each round every row takes its next one (through
+        // shared memory: the place varies by row), so the rounds are the largest count in the warp.
+        if (__any_sync(0xFFFFFFFFu, zmax > r.v[kTop - 1])) {
+            uint32_t cand = 0u;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                zs[j * zs_step] = z[j];
+                cand |= z[j] > r.v[kTop - 1] ? 1u << j : 0u;
+            }
+            while (__any_sync(0xFFFFFFFFu, cand != 0u)) {
+                float zc = -INFINITY;
+                int j = 0;
+                if (cand) {
+                    j = __ffs(cand) - 1;
+                    cand &= cand - 1;
+                    zc = zs[j * zs_step];
+                }
+                r.insert(zc, id0 + j);  // no change unless above the last
+            }
+        }
+    }
 }
 
-// Inserts (z, id) into a descending list of n entries, equal values staying in front; NaN never enters.
-__device__ __forceinline__ void insert_top(float *v, int32_t *id, int n, float z, int32_t i)
+template <int kCtas, int kTop>
+__global__ void __launch_bounds__(kThreadsLP, 1)
+    logprob_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_w, const LogprobArgs a)
 {
-    if (!(z > v[n - 1]) && !(z == v[n - 1] && i < id[n - 1])) return;
-    int j = n - 1;
-    while (j > 0 && (v[j - 1] < z || (v[j - 1] == z && id[j - 1] > i))) {
-        v[j] = v[j - 1];
-        id[j] = id[j - 1];
-        --j;
-    }
-    v[j] = z;
-    id[j] = i;
-}
-
-__global__ void __launch_bounds__(kWarps * 32) logprob_part_kernel(const LogprobArgs a)
-{
-    extern __shared__ uint4 hs[];  // [kRows][H / 8]
-    __shared__ float tv[kWarps][kRows][kMaxTop];
-    __shared__ int32_t ti[kWarps][kRows][kMaxTop];
-    __shared__ float4 st[kWarps][kRows];
-    const int r0 = blockIdx.x * kRows, part = blockIdx.y;
+    using L = LpLayout<kCtas>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
+    uint64_t *full = bars, *empty = bars + kMaxStages;
+    uint64_t *acc_full = bars + 2 * kMaxStages, *acc_empty = acc_full + 2;
+    uint64_t *mma_done = acc_empty + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
+    int *abort_word = reinterpret_cast<int *>(tmem_holder + 1);
+    volatile int *abort_flag = abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nch = a.H / 8;
-    for (int i = threadIdx.x; i < kRows * nch; i += kWarps * 32) {
-        const int r = r0 + i / nch;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < a.n) {
-            const int hr = a.row_idx ? a.row_idx[r] : r;
-            if (hr >= 0 && hr < a.hidden_rows)
-                x = reinterpret_cast<const uint4 *>(a.hidden + hr * a.hidden_stride)[i % nch];
+    const uint32_t rank = kCtas == 2 ? ptx::cluster_rank() : 0u;
+    const int worker = blockIdx.x / kCtas;
+    const int passes = a.plan.passes();
+    const int k_blocks = (a.H + 63) / 64;
+    const bool aligned = (ptx::smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need it
+    if (!aligned && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+
+    if (warp == kProducerLP && lane == 0) {
+        for (int i = 0; i < L::kStages; ++i) {
+            ptx::mbar_init(full + i, 1);
+            ptx::mbar_init(empty + i, 1);
         }
-        hs[i] = x;
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(acc_full + i, 1);
+            ptx::mbar_init(acc_empty + i, kStateWarps * kCtas);
+        }
+        ptx::mbar_init(mma_done, 1);
+        ptx::fence_mbar_init();
+        *abort_word = aligned ? 0 : 1;
+        ptx::tma_prefetch_desc(&tm_h);
+        ptx::tma_prefetch_desc(&tm_w);
     }
-    for (int i = threadIdx.x; i < kWarps * kRows * kMaxTop; i += kWarps * 32) {
-        (&tv[0][0][0])[i] = -INFINITY;
-        (&ti[0][0][0])[i] = 0x7FFFFFFF;
+    if (warp == 0) {
+        if constexpr (kCtas == 2) {
+            ptx::tmem_alloc_pair(tmem_holder, 512);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(tmem_holder, 512);
+            ptx::tmem_relinquish();
+        }
     }
-    __syncthreads();
-    float m = -INFINITY, s = 0.f, u = 0.f, tz = __int_as_float(0x7FC00000);
-    const int target = (a.targets && lane < kRows && r0 + lane < a.n) ? a.targets[r0 + lane] : -1;
-    const int64_t v0 = static_cast<int64_t>(a.V) * part / gridDim.y, v1 = static_cast<int64_t>(a.V) * (part + 1) / gridDim.y;
-    for (int64_t v = v0 + warp; v < v1; v += kWarps) {
-        float acc[kRows] = {};
-        const uint4 *wr = reinterpret_cast<const uint4 *>(a.W + v * a.H);
-        for (int c = lane; c < nch; c += 32) {
-            const uint4 x = __ldg(wr + c);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const uint4 h = hs[r * nch + c];
-                acc[r] = fmaf(lo16(x.x), lo16(h.x), acc[r]);
-                acc[r] = fmaf(hi16(x.x), hi16(h.x), acc[r]);
-                acc[r] = fmaf(lo16(x.y), lo16(h.y), acc[r]);
-                acc[r] = fmaf(hi16(x.y), hi16(h.y), acc[r]);
-                acc[r] = fmaf(lo16(x.z), lo16(h.z), acc[r]);
-                acc[r] = fmaf(hi16(x.z), hi16(h.z), acc[r]);
-                acc[r] = fmaf(lo16(x.w), lo16(h.w), acc[r]);
-                acc[r] = fmaf(hi16(x.w), hi16(h.w), acc[r]);
+    __syncwarp();
+    ptx::tc_fence_before();
+    if constexpr (kCtas == 2)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+
+    // Registers by role: 128 threads at 40 and 256 at 232 are the 384 at 168 of the launch.
+    if (warp >= kStateWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (!aligned) {
+        // nothing was started: straight to the end
+    } else if (warp == kProducerLP) {
+        if (lane == 0) {
+            const uint32_t a_bytes = static_cast<uint32_t>(a.a_rows) * 128u;
+            const uint32_t bytes = (a_bytes + L::kBBytes) * kCtas;  // of both blocks, counted on the even one
+            int it = 0;
+            bool ok = true, waited = a.gathered == 0;
+            for (int ps = 0; ok && ps < passes; ++ps) {
+                const Share sh = share_of(a.plan, ps, worker);
+                if (!sh.any) continue;
+                const int row0 = sh.row_tile * a.plan.tile_rows + static_cast<int>(rank) * kBlockRows;
+                for (int vt = sh.v0; ok && vt < sh.v1; ++vt) {
+                    const int col0 = vt * kVocabTile + static_cast<int>(rank) * L::kBRows;
+                    for (int kb = 0; kb < k_blocks; ++kb, ++it) {
+                        const int st = it % L::kStages;
+                        if (!(ok = ptx::mbar_wait(empty + st, ((it / L::kStages) & 1) ^ 1, abort_flag, a.err,
+                                                  BLINK_DEVICE_TIMEOUT)))
+                            break;
+                        uint8_t *dst = smem + st * L::kStageBytes;
+                        if constexpr (kCtas == 2) {
+                            const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(full + st), 0);
+                            if (rank == 0) ptx::mbar_arrive_expect_tx(full + st, bytes);
+                            ptx::tma_load_3d_pair(dst + L::kABytes, &tm_w, kb * 64, col0, 0, bar);
+                            if (!waited) ptx::grid_dep_wait(), waited = true;
+                            ptx::tma_load_3d_pair(dst, &tm_h, kb * 64, row0, 0, bar);
+                        } else {
+                            ptx::mbar_arrive_expect_tx(full + st, bytes);
+                            ptx::tma_load_3d(dst + L::kABytes, &tm_w, kb * 64, col0, 0, full + st);
+                            if (!waited) ptx::grid_dep_wait(), waited = true;
+                            ptx::tma_load_3d(dst, &tm_h, kb * 64, row0, 0, full + st);
+                        }
+                    }
+                }
+            }
+            ptx::grid_launch_dependents();
+            // Every copy issued must have landed before a block of the pair may exit; they are counted
+            // on the even block, which the other waits for at the cluster barrier below.
+            if (rank == 0) {
+                volatile int no_abort = 0;
+                for (int n = it > L::kStages ? it - L::kStages : 0; n < it; ++n, no_abort = 0)
+                    ptx::mbar_wait(full + n % L::kStages, (n / L::kStages) & 1, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
             }
         }
-        float z = 0.f;
+    } else if (warp == kIssuerLP) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = ptx::idesc_bf16_f32(kBlockRows * kCtas, kVocabTile, false);
+            const uint32_t base = ptx::smem_u32(smem);
+            int it = 0, part = 0;
+            bool ok = true;
+            for (int ps = 0; ok && ps < passes; ++ps) {
+                const Share sh = share_of(a.plan, ps, worker);
+                if (!sh.any) continue;
+                for (int vt = sh.v0; ok && vt < sh.v1; ++vt) {
+                    for (int k0 = 0; ok && k0 < k_blocks; k0 += kPartBlocks, ++part) {
+                        const int buf = part & 1;
+                        if (!(ok = ptx::mbar_wait(acc_empty + buf, ((part >> 1) & 1) ^ 1, abort_flag, a.err,
+                                                  BLINK_DEVICE_TIMEOUT)))
+                            break;
+                        if constexpr (kCtas == 2) ptx::fence_acquire_cluster();
+                        ptx::tc_fence_after();
+                        const uint32_t d = tmem + buf * kVocabTile;
+                        const int kn = min(kPartBlocks, k_blocks - k0);
+                        for (int kb = 0; kb < kn; ++kb, ++it) {
+                            const int st = it % L::kStages;
+                            if (!(ok = ptx::mbar_wait(full + st, (it / L::kStages) & 1, abort_flag, a.err,
+                                                      BLINK_DEVICE_TIMEOUT)))
+                                break;
+                            ptx::tc_fence_after();
+                            const uint64_t ad = ptx::smem_desc_sw128(base + st * L::kStageBytes, 16, 1024);
+                            const uint64_t bd = ptx::smem_desc_sw128(base + st * L::kStageBytes + L::kABytes, 16, 1024);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            float t = acc[r];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-            if (lane == r) z = t;
-        }
-        if (lane < kRows) {
-            const float y = z * a.c;
-            if (y > m) {
-                const float d = m == -INFINITY ? 0.f : m - y, f = exp2f(d);
-                u = f * (u + s * d);
-                s *= f;
-                m = y;
+                            for (int kk = 0; kk < 4; ++kk) {  // 16 of H: 32 bytes, 2 in the descriptor's units
+                                const uint32_t acc = kb > 0 || kk > 0;
+                                if constexpr (kCtas == 2)
+                                    ptx::mma_ss_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, acc);
+                                else
+                                    ptx::mma_ss(d, ad + 2 * kk, bd + 2 * kk, idesc, acc);
+                            }
+                            if constexpr (kCtas == 2)
+                                ptx::mma_commit_pair(empty + st);
+                            else
+                                ptx::mma_commit(empty + st);
+                        }
+                        if (!ok) break;
+                        if constexpr (kCtas == 2)
+                            ptx::mma_commit_pair(acc_full + buf);
+                        else
+                            ptx::mma_commit(acc_full + buf);
+                    }
+                }
             }
-            const float x = y - m, e = exp2f(x);
-            s += e;
-            u = fmaf(e, x, u);
-            if (v == target) tz = z;
-            if (a.top) insert_top(tv[warp][lane], ti[warp][lane], a.top, z, static_cast<int32_t>(v));
+            // every product issued must be complete before tensor memory is released
+            if constexpr (kCtas == 2)
+                ptx::mma_commit_pair(mma_done);
+            else
+                ptx::mma_commit(mma_done);
+            volatile int no_abort = 0;
+            ptx::mbar_wait(mma_done, 0, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
         }
-        __syncwarp();
+    } else if (warp < kStateWarps) {
+        // ------------------------------------------------------------ states: a row per two threads
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int half = warp >> 2, lane_row = (warp & 3) * 32 + lane;
+        const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * kHalfCols;
+        float *zs = reinterpret_cast<float *>(smem + L::kScoreOff) + threadIdx.x;  // this thread's column
+        constexpr int kZsStep = kStateWarps * 32;
+        const float c = a.c;
+        int part = 0;
+        bool ok = true;
+        for (int ps = 0; ok && ps < passes; ++ps) {
+            const Share sh = share_of(a.plan, ps, worker);
+            if (!sh.any) continue;
+            const int row_w = sh.row_tile * a.plan.tile_rows + static_cast<int>(rank) * kBlockRows + (warp & 3) * 32;
+            const int row = row_w + lane;
+            const bool live = row_w < a.n;  // of the warp: it has rows at all
+            const int target = a.targets && row < a.n ? __ldg(a.targets + row) : -1;
+            RowState<kTop> r;
+            r.clear(a.top);
+            for (int vt = sh.v0; vt < sh.v1; ++vt) {
+                float z[kHalfCols];
+                for (int k0 = 0; k0 < k_blocks; k0 += kPartBlocks, ++part) {
+                    const int buf = part & 1;
+                    if (!(ok = ptx::mbar_wait(acc_full + buf, (part >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT)))
+                        break;
+                    ptx::tc_fence_after();
+                    if (live) {
+                        const bool add = k0 > 0;
+#pragma unroll
+                        for (int q = 0; q < kHalfCols / 32; ++q) {
+                            uint32_t raw[32];
+                            ptx::tmem_ld32(trow + buf * kVocabTile + q * 32, raw);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float x = __uint_as_float(raw[j]);
+                                z[q * 32 + j] = add ? z[q * 32 + j] + x : x;
+                            }
+                        }
+                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (kCtas == 2)
+                            ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(acc_empty + buf), 0));
+                        else
+                            ptx::mbar_arrive(acc_empty + buf);
+                    }
+                }
+                if (!ok) break;
+                const int first_id = vt * kVocabTile + half * kHalfCols;
+                if (live && first_id < a.V) {
+#pragma unroll
+                    for (int q = 0; q < kHalfCols / 32; ++q)
+                        fold_columns<kTop>(r, z + q * 32, first_id + q * 32, a.V, c, target, zs, kZsStep);
+                }
+            }
+            if (!ok) break;
+            if (row < a.n) {
+                const int64_t cell = sh.cell + half * sh.half_step + static_cast<int>(rank) * kBlockRows + lane_row;
+                a.stat[cell] = make_float4(r.m, r.s, r.u, r.tz);
+                if constexpr (kTop > 0) {
+#pragma unroll
+                    for (int j = 0; j < kTop; ++j) {
+                        const int o = j - (kTop - a.top);
+                        if (o >= 0) a.best[cell * a.top + o] = make_int2(__float_as_int(r.v[j]), r.id[j]);
+                    }
+                }
+            }
+        }
+    } else {
+        // the two warps that fill the last warpgroup
     }
-    if (lane < kRows) st[warp][lane] = make_float4(m, s, u, tz);
-    __syncthreads();
-    if (threadIdx.x < kRows && r0 + threadIdx.x < a.n) {
-        const int r = threadIdx.x;
-        float4 x = st[0][r];
-        for (int w = 1; w < kWarps; ++w) {
-            const float4 y = st[w][r];
-            merge_stat(x.x, x.y, x.z, y.x, y.y, y.z);
-            if (y.w == y.w) x.w = y.w;
-            for (int j = 0; j < a.top; ++j) insert_top(tv[0][r], ti[0][r], a.top, tv[w][r][j], ti[w][r][j]);
-        }
-        const int64_t row = static_cast<int64_t>(part) * a.n + r0 + r;
-        a.stat[row] = x;
-        for (int j = 0; j < a.top; ++j) {
-            a.top_z[row * a.top + j] = tv[0][r][j];
-            a.top_id[row * a.top + j] = ti[0][r][j];
-        }
+    __syncwarp();
+    if (aligned && rank == 1 && warp == 0 && lane == 0) {
+        // the last commit arrives on this block's barrier too: not to leave before it has
+        volatile int no_abort = 0;
+        ptx::mbar_wait(mma_done, 0, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    if constexpr (kCtas == 2)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 0) {
+        if constexpr (kCtas == 2)
+            ptx::tmem_dealloc_pair(tmem, 512);
+        else
+            ptx::tmem_dealloc(tmem, 512);
     }
 }
 
-__global__ void logprob_merge_kernel(const LogprobArgs a, int parts)
+// Hidden rows of an index list, gathered into consecutive rows (a row outside the tensor: zeros).
+__global__ void __launch_bounds__(256) logprob_gather_kernel(const uint4 *__restrict__ hidden, int64_t stride, int hidden_rows,
+                                                             const int32_t *__restrict__ idx, int n, int pieces,
+                                                             uint4 *__restrict__ dst)
 {
-    const int r = blockIdx.x * blockDim.x + threadIdx.x;
-    if (r >= a.n) return;
-    float m = -INFINITY, s = 0.f, u = 0.f, tz = __int_as_float(0x7FC00000);
-    float tv[kMaxTop];
-    int32_t ti[kMaxTop];
-    for (int j = 0; j < a.top; ++j) tv[j] = -INFINITY, ti[j] = 0x7FFFFFFF;
-    for (int p = 0; p < parts; ++p) {
-        const int64_t row = static_cast<int64_t>(p) * a.n + r;
-        const float4 x = a.stat[row];
-        merge_stat(m, s, u, x.x, x.y, x.z);
-        if (x.w == x.w) tz = x.w;
-        for (int j = 0; j < a.top; ++j) insert_top(tv, ti, a.top, a.top_z[row * a.top + j], a.top_id[row * a.top + j]);
-    }
-    const float nan = __int_as_float(0x7FC00000);
-    const int hr = a.row_idx ? a.row_idx[r] : r;
-    const bool bad = hr < 0 || hr >= a.hidden_rows;
-    const int t = a.targets ? a.targets[r] : -1;
-    if (bad || t < -1 || t >= a.V) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
-    const float l2 = bad ? nan : m + log2f(s);
-    if (a.lse) a.lse[r] = l2 * kLn2;
-    if (a.entropy) a.entropy[r] = bad ? nan : (log2f(s) - u / s) * kLn2;
-    if (a.logprob) a.logprob[r] = (tz * a.c - l2) * kLn2;
-    for (int j = 0; j < a.top; ++j) {
-        const bool none = bad || ti[j] == 0x7FFFFFFF;
-        a.top_ids[static_cast<int64_t>(r) * a.top + j] = none ? -1 : ti[j];
-        a.top_lp[static_cast<int64_t>(r) * a.top + j] = none ? nan : (tv[j] * a.c - l2) * kLn2;
+    ptx::grid_launch_dependents();
+    const int64_t total = static_cast<int64_t>(n) * pieces;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; t < total;
+         t += static_cast<int64_t>(gridDim.x) * 256) {
+        const int r = static_cast<int>(t / pieces), p = static_cast<int>(t - static_cast<int64_t>(r) * pieces);
+        const int hr = __ldg(idx + r);
+        dst[t] = hr >= 0 && hr < hidden_rows ? __ldg(hidden + hr * stride + p) : make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
-struct Layout {
-    size_t stat, top_z, top_id, total;
+constexpr int kMergeWarps = 8;
+constexpr int kMergeLists = kMaxWorkers * kHalves / 32;  // lists per lane
+constexpr int kMergeDepth = 4;                           // entries of a list kept in shared memory
+
+// One warp per row: joins the parts' statistics and takes the best of their lists.
+__global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const LogprobArgs a, int max_lists)
+{
+    extern __shared__ int2 heads[];  // per warp [max_lists][kMergeDepth]: the first entries of each list
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.x * (blockDim.x >> 5) + warp;
+    ptx::grid_dep_wait();
+    if (r >= a.n) return;
+    const int rt = r / a.plan.tile_rows;
+    const int pass = min(rt / a.plan.group, a.plan.passes() - 1);
+    const int g = a.plan.tiles_of(pass), lists = a.plan.chunks_of(pass) * kHalves;
+    const int64_t cell0 = a.plan.first_cell(pass) + static_cast<int64_t>(rt - pass * a.plan.group) * a.plan.tile_rows +
+                          r % a.plan.tile_rows;
+    const int64_t step = static_cast<int64_t>(g) * a.plan.tile_rows;
+    const int top = a.top, depth = min(top, kMergeDepth);
+    int2 *hd = heads + static_cast<int64_t>(warp) * max_lists * kMergeDepth;
+    for (int q = lane; q < lists; q += 32) {
+#pragma unroll
+        for (int j = 0; j < kMergeDepth; ++j)
+            if (j < depth) hd[q * kMergeDepth + j] = __ldcg(a.best + (cell0 + q * step) * top + j);
+    }
+    float m = -INFINITY, tz = __int_as_float(0x7FC00000);
+    float4 st[kMergeLists];
+#pragma unroll
+    for (int q = 0; q < kMergeLists; ++q) {
+        const int ch = lane + 32 * q;
+        st[q] = ch < lists ? __ldcg(a.stat + cell0 + ch * step) : make_float4(-INFINITY, 0.f, 0.f, tz);
+        m = fmaxf(m, st[q].x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float s = 0.f, u = 0.f;
+    bool has = false;
+#pragma unroll
+    for (int q = 0; q < kMergeLists; ++q) {
+        const float d = st[q].x == -INFINITY ? 0.f : st[q].x - m;  // an empty part, or one of NaN alone
+        const float f = exp2f(d);
+        s = fmaf(f, st[q].y, s);
+        u = fmaf(f, fmaf(st[q].y, d, st[q].z), u);
+        if (st[q].w == st[q].w) tz = st[q].w, has = true;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+    }
+    const uint32_t who = __ballot_sync(0xFFFFFFFFu, has);
+    tz = __shfl_sync(0xFFFFFFFFu, tz, who ? __ffs(who) - 1 : 0);
+    const float nan = __int_as_float(0x7FC00000);
+    const int hr = a.row_idx ? __ldg(a.row_idx + r) : r;
+    const bool bad = hr < 0 || hr >= a.hidden_rows;
+    const float l2s = log2f(s);
+    const float l2 = bad ? nan : m + l2s;
+    if (lane == 0) {
+        const int t = a.targets ? __ldg(a.targets + r) : -1;
+        if (bad || t < -1 || t >= a.V) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+        if (a.lse) a.lse[r] = l2 * kLn2;
+        if (a.entropy) a.entropy[r] = bad ? nan : (l2s - u / s) * kLn2;
+        if (a.logprob) a.logprob[r] = t >= 0 && t < a.V ? fmaf(tz, a.c, -l2) * kLn2 : nan;
+    }
+    if (top == 0) return;
+    __syncwarp();
+    int at[kMergeLists];     // next entry of each of the lane's lists
+    int2 head[kMergeLists];  // and that entry
+    const int2 none = make_int2(__float_as_int(-INFINITY), kNoToken);
+#pragma unroll
+    for (int q = 0; q < kMergeLists; ++q) {
+        at[q] = 0;
+        head[q] = lane + 32 * q < lists ? hd[(lane + 32 * q) * kMergeDepth] : none;
+    }
+    for (int k = 0; k < top; ++k) {
+        float bv = -INFINITY;
+        int bi = kNoToken;
+#pragma unroll
+        for (int q = 0; q < kMergeLists; ++q) {
+            const float v = __int_as_float(head[q].x);
+            if (v > bv || (v == bv && head[q].y < bi)) bv = v, bi = head[q].y;
+        }
+        const int mine = bi;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float ov = __shfl_xor_sync(0xFFFFFFFFu, bv, o);
+            const int oi = __shfl_xor_sync(0xFFFFFFFFu, bi, o);
+            if (ov > bv || (ov == bv && oi < bi)) bv = ov, bi = oi;
+        }
+        if (mine == bi && bi != kNoToken) {  // tokens are in one list each: one lane, one list
+#pragma unroll
+            for (int q = 0; q < kMergeLists; ++q) {
+                if (head[q].y == bi) {
+                    const int j = ++at[q], l = lane + 32 * q;
+                    head[q] = j >= top ? none
+                                       : j < depth ? hd[l * kMergeDepth + j] : __ldcg(a.best + (cell0 + l * step) * top + j);
+                }
+            }
+        }
+        if (lane == 0) {
+            const bool no = bad || bi == kNoToken;
+            a.top_ids[static_cast<int64_t>(r) * top + k] = no ? -1 : bi;
+            a.top_lp[static_cast<int64_t>(r) * top + k] = no ? nan : fmaf(bv, a.c, -l2) * kLn2;
+        }
+    }
+}
+
+struct WsLayout {
+    size_t stat, best, rows, total;
 };
 
-Layout layout_of(int n, int top)
+WsLayout ws_layout(const LogprobPlan &p, int n, int H, int top)
 {
-    Layout l{};
-    const size_t cells = static_cast<size_t>(kParts) * n;
+    WsLayout l{};
+    const size_t cells = static_cast<size_t>(p.cells());
     l.stat = kHeaderBytes;
-    l.top_z = l.stat + align_up(cells * sizeof(float4), 256);
-    l.top_id = l.top_z + align_up(cells * top * sizeof(float), 256);
-    l.total = l.top_id + align_up(cells * top * sizeof(int32_t), 256);
+    l.best = l.stat + align_up(cells * sizeof(float4), 256);
+    l.rows = l.best + align_up(cells * top * sizeof(int2), 256);
+    l.total = l.rows + align_up(static_cast<size_t>(n) * H * sizeof(uint16_t), 256);
     return l;
+}
+
+int sm_count()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
+template <int kCtas, int kTop>
+cudaError_t launch_logprob(const CUtensorMap &tm_h, const CUtensorMap &tm_w, const LogprobArgs &a, cudaStream_t stream)
+{
+    auto kern = logprob_kernel<kCtas, kTop>;
+    // The split of registers by role has to fit the registers of the launch: checked once.
+    static const bool fits = [kern] {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, kern) == cudaSuccess && fa.numRegs * kThreadsLP >= kRegsNeeded;
+    }();
+    if (!fits) return cudaErrorLaunchOutOfResources;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LpLayout<kCtas>::kBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (kCtas > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = kCtas;
+        attr[na].val.clusterDim.y = 1;
+        attr[na++].val.clusterDim.z = 1;
+    }
+    if (a.gathered) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(a.plan.workers * kCtas));
+    cfg.blockDim = dim3(kThreadsLP);
+    cfg.dynamicSmemBytes = LpLayout<kCtas>::kBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = static_cast<unsigned>(na);
+    return cudaLaunchKernelEx(&cfg, kern, tm_h, tm_w, a);
 }
 
 }  // namespace
@@ -211,8 +704,10 @@ Layout layout_of(int n, int top)
 extern "C" size_t blink_token_logprobs_workspace(int32_t n, int32_t H, int32_t V, int32_t top)
 {
     using namespace blink;
-    if (n < 1 || n > BLINK_MAX_INPUT_TOKENS || H < 1 || V < 1 || top < 0 || top > kMaxTop) return kHeaderBytes;
-    return layout_of(n, top).total;
+    if (n < 1 || n > BLINK_MAX_INPUT_TOKENS || H < 1 || H > 32768 || V < 1 || V > (1 << 24) || top < 0 || top > kMaxTop)
+        return kHeaderBytes;
+    const int sms = sm_count();
+    return ws_layout(make_plan(n, V, sms > 0 ? sms : 1), n, H, top).total;
 }
 
 extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t hidden_row_stride, int32_t hidden_rows,
@@ -234,36 +729,77 @@ extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t h
     if (n < 1 || n > BLINK_MAX_INPUT_TOKENS) return BLINK_OUT_OF_RANGE;
     if (!d_row_idx && n > hidden_rows) return BLINK_INVALID_ARG;
     if (ws_bytes < blink_token_logprobs_workspace(n, H, V, top)) return BLINK_WORKSPACE_TOO_SMALL;
-    const Layout l = layout_of(n, top);
-    auto *wsb = static_cast<uint8_t *>(d_ws);
+
+    const int sms = sm_count();
+    if (sms < 2) return BLINK_CUDA_ERROR;
     LogprobArgs a{};
-    a.hidden = hidden;
-    a.hidden_stride = hidden_row_stride;
-    a.hidden_rows = hidden_rows;
-    a.row_idx = d_row_idx;
-    a.W = unembed;
+    a.plan = make_plan(n, V, sms);
+    const WsLayout l = ws_layout(a.plan, n, H, top);
+    auto *wsb = static_cast<uint8_t *>(d_ws);
     a.V = V;
     a.H = H;
     a.n = n;
     a.top = top;
+    a.a_rows = n < kBlockRows ? (n + 7) / 8 * 8 : kBlockRows;
+    a.row_idx = d_row_idx;
+    a.hidden_rows = hidden_rows;
     a.targets = d_targets;
     a.c = kLog2e / temperature;
     a.stat = reinterpret_cast<float4 *>(wsb + l.stat);
-    a.top_z = reinterpret_cast<float *>(wsb + l.top_z);
-    a.top_id = reinterpret_cast<int32_t *>(wsb + l.top_id);
+    a.best = reinterpret_cast<int2 *>(wsb + l.best);
     a.logprob = d_logprob;
     a.entropy = d_entropy;
     a.lse = d_lse;
     a.top_lp = d_top_logprobs;
     a.top_ids = d_top_ids;
     a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
-    const int smem = kRows * H * 2;
-    if (cudaFuncSetAttribute(logprob_part_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    a.gathered = d_row_idx != nullptr;
+
+    const blink_bf16 *rows = hidden;
+    int64_t row_stride = hidden_row_stride;
+    if (d_row_idx) {
+        auto *dst = reinterpret_cast<blink_bf16 *>(wsb + l.rows);
+        const int64_t pieces = static_cast<int64_t>(n) * (H / 8), want = (pieces + 255) / 256;
+        logprob_gather_kernel<<<static_cast<unsigned>(want < 4096 ? want : 4096), 256, 0, stream>>>(
+            reinterpret_cast<const uint4 *>(hidden), hidden_row_stride / 8, hidden_rows, d_row_idx, n, H / 8,
+            reinterpret_cast<uint4 *>(dst));
+        if (cudaGetLastError() != cudaSuccess) return BLINK_CUDA_ERROR;
+        rows = dst;
+        row_stride = H;
+    }
+    CUtensorMap tm_h, tm_w;
+    const uint64_t e = 2;
+    const uint64_t hs = static_cast<uint64_t>(row_stride) * e, wst = static_cast<uint64_t>(H) * e;
+    if (!encode_tmap_3d_bf16(&tm_h, rows, H, n, 1, hs, hs * n, 64, a.a_rows, 1) ||
+        !encode_tmap_3d_bf16(&tm_w, unembed, H, V, 1, wst, wst * V, 64, kVocabTile / a.plan.blocks_per_worker, 1))
         return BLINK_CUDA_ERROR;
-    const dim3 grid(static_cast<unsigned>((n + kRows - 1) / kRows), kParts);
-    logprob_part_kernel<<<grid, kWarps * 32, smem, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return BLINK_CUDA_ERROR;
-    logprob_merge_kernel<<<(n + 127) / 128, 128, 0, stream>>>(a, kParts);
-    if (cudaGetLastError() != cudaSuccess) return BLINK_CUDA_ERROR;
+    const bool pair = a.plan.blocks_per_worker == 2;
+    cudaError_t err;
+    if (top == 0)
+        err = pair ? launch_logprob<2, 0>(tm_h, tm_w, a, stream) : launch_logprob<1, 0>(tm_h, tm_w, a, stream);
+    else if (top <= 8)
+        err = pair ? launch_logprob<2, 8>(tm_h, tm_w, a, stream) : launch_logprob<1, 8>(tm_h, tm_w, a, stream);
+    else
+        err = pair ? launch_logprob<2, 32>(tm_h, tm_w, a, stream) : launch_logprob<1, 32>(tm_h, tm_w, a, stream);
+    if (err != cudaSuccess) return BLINK_CUDA_ERROR;
+
+    const int lists = (a.plan.chunks > a.plan.rest_chunks ? a.plan.chunks : a.plan.rest_chunks) * kHalves;
+    const int warp_bytes = top > 0 ? lists * kMergeDepth * static_cast<int>(sizeof(int2)) : 0;  // at most 10 KB
+    const int warps = n >= 4 * kMergeWarps * sms ? kMergeWarps : 4;
+    const int smem = warps * warp_bytes;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(logprob_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return BLINK_CUDA_ERROR;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>((n + warps - 1) / warps));
+    cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, logprob_merge_kernel, a, lists) != cudaSuccess) return BLINK_CUDA_ERROR;
     return BLINK_OK;
 }
