@@ -48,7 +48,10 @@ constexpr int kProducerLP = 8, kIssuerLP = 9;
 constexpr int kRegsNeeded = 256 * 232 + 128 * 40;
 constexpr int kHalves = 2;      // threads that share a row
 constexpr int kHalfCols = kVocabTile / kHalves;
-constexpr int kPartBlocks = 8;  // 64-wide blocks of H per product
+#ifndef KPB
+#define KPB 8
+#endif
+constexpr int kPartBlocks = KPB;  // 64-wide blocks of H per product
 constexpr int kNoToken = 0x7FFFFFFF;
 constexpr int kMaxWorkers = 160;
 constexpr int kMaxStages = 8;
@@ -77,7 +80,7 @@ struct LogprobPlan {
 
 // A worker's part of one pass: vocabulary tiles [v0, v1) of one row tile, and the cell its states go to.
 struct Share {
-    int row_tile, v0, v1;
+    int row_tile, chunk, v0, v1;
     int64_t cell, half_step;  // of the first half's states; from there to the second half's
     bool any;
 };
@@ -91,6 +94,7 @@ __host__ __device__ inline Share share_of(const LogprobPlan &p, int pass, int wo
     // chunks differ by one tile; each pass deals them to the workers from another place
     const int chunk = (worker / g + pass * 7) % nc;
     s.row_tile = pass * p.group + t;
+    s.chunk = chunk;
     s.v0 = static_cast<int>(static_cast<int64_t>(p.vocab_tiles) * chunk / nc);
     s.v1 = static_cast<int>(static_cast<int64_t>(p.vocab_tiles) * (chunk + 1) / nc);
     s.cell = p.first_cell(pass) + (static_cast<int64_t>(chunk) * kHalves * g + t) * p.tile_rows;
@@ -136,11 +140,13 @@ struct LogprobArgs {
     const int32_t *targets;
     float c;       // log2(e) / T
     float4 *stat;  // [cells]: m, s, u, target's raw product (NaN: not in this part)
-    int2 *best;    // [cells][top]: raw product (as bits) and token, descending
+    int2 *best;    // [cells][best_stride]: raw product (as bits) and token, descending
+    int best_stride;
     float *logprob, *entropy, *lse, *top_lp;
     int32_t *top_ids;
     int *err;
-    int gathered;  // the hidden rows were gathered by the launch before
+    uint32_t *bounds;  // [n][kMaxTop]: see RowBound
+    int prepared;      // a launch before gathered the hidden rows and cleared the bounds
 };
 
 template <int kCtas>
@@ -173,42 +179,83 @@ struct RowState {
             id[j] = kNoToken;
         }
     }
-    // Tokens come in ascending id, so an equal product goes behind those already listed.
+    // Tokens come in ascending id, so an equal product goes behind those already listed.  No entry
+    // waits for another: the list is descending, so entry j moves one place down exactly when the one
+    // before it is below z (a chain of swaps took 500 cycles for 32 entries).
     __device__ __forceinline__ void insert(float z, int32_t i)
     {
-        bool moved = false;
 #pragma unroll
-        for (int j = 0; j < kTop; ++j) {
-            moved = moved || z > v[j];
-            const float ov = v[j];
-            const int32_t oi = id[j];
-            v[j] = moved ? z : ov;
-            id[j] = moved ? i : oi;
-            z = moved ? ov : z;
-            i = moved ? oi : i;
+        for (int j = kTop - 1; j > 0; --j) {
+            const bool here = z > v[j], shift = z > v[j - 1];
+            v[j] = shift ? v[j - 1] : here ? z : v[j];
+            id[j] = shift ? id[j - 1] : here ? i : id[j];
         }
+        if (z > v[0]) v[0] = z, id[0] = i;
     }
 };
 
-// Folds 32 logits of a row, tokens id0 .. id0 + 31, into its state.
-template <int kTop>
-__device__ __forceinline__ void fold_columns(RowState<kTop> &r, float *z, int id0, int V, float c, int target, float *zs,
-                                             int zs_step)
+__device__ __forceinline__ uint32_t order_of(float z)  // larger unsigned = larger z; 0 below every number
 {
-    if (id0 >= V) return;
-    const bool whole = id0 + 32 <= V;
+    const uint32_t b = __float_as_uint(z + 0.f);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_order(uint32_t o) { return __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o); }
+
+// A row's bound: `top` words, each the largest product seen so far in its own share of the vocabulary
+// (a thread's groups of 32 columns are dealt to the words), kept by every worker with atomic maxima.
+// `top` products are at least the smallest of them, so a product below it is no alternative
+// of the row and need not enter a list.  How far the others have come varies from run to run, and with
+// it what the lists hold, but not their best `top`: the result does not vary.
+template <int kTop>
+__device__ __forceinline__ float row_bound(const uint32_t *words, int top)
+{
+    uint32_t lo = 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < kTop; j += 4) {
+        if (j < top) {
+            const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(words + j));
+            lo = min(lo, w.x);
+            if (j + 1 < top) lo = min(lo, w.y);
+            if (j + 2 < top) lo = min(lo, w.z);
+            if (j + 3 < top) lo = min(lo, w.w);
+        }
+    }
+    return lo == 0u ? -INFINITY : of_order(lo);
+}
+
+// Folds a row's logits of a tile, tokens id0 .. id0 + kHalfCols - 1, into its state.
+template <int kTop>
+__device__ __forceinline__ void fold_tile(RowState<kTop> &r, float (&z)[kHalfCols], int id0, int V, float c, int target,
+                                          float *zs, uint32_t *words, int top, int slot0, float &bound)
+{
+    constexpr int kGroups = kHalfCols / 32, kZsStep = kStateWarps * 32;
+    const bool whole = id0 + kHalfCols <= V;
     if (!whole) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < kHalfCols; ++j)
             if (id0 + j >= V) z[j] = -INFINITY;
     }
-    float m0 = fmaxf(z[0], z[1]), m1 = fmaxf(z[2], z[3]);
+    float gmax[kGroups];
 #pragma unroll
-    for (int j = 4; j < 32; j += 4) {
-        m0 = ptx::max3(m0, z[j], z[j + 1]);
-        m1 = ptx::max3(m1, z[j + 2], z[j + 3]);
+    for (int q = 0; q < kGroups; ++q) {
+        const float *y = z + 32 * q;
+        float m0 = fmaxf(y[0], y[1]), m1 = fmaxf(y[2], y[3]);
+#pragma unroll
+        for (int j = 4; j < 32; j += 4) {
+            m0 = ptx::max3(m0, y[j], y[j + 1]);
+            m1 = ptx::max3(m1, y[j + 2], y[j + 3]);
+        }
+        gmax[q] = fmaxf(m0, m1);
+        if constexpr (kTop > 0) {
+            if (gmax[q] > bound && gmax[q] > -INFINITY) {
+                int w = slot0 + q;
+                w = w >= top ? w % top : w;
+                atomicMax(words + w, order_of(gmax[q]));
+            }
+        }
     }
-    const float zmax = fmaxf(m0, m1);
+    const float zmax = fmaxf(fmaxf(gmax[0], gmax[1]), fmaxf(gmax[2], gmax[3]));
+    static_assert(kGroups == 4, "four groups of 32 columns");
     const float ym = zmax * c;
     if (ym > r.m) {
         const float d = r.m == -INFINITY ? 0.f : r.m - ym, f = ptx::ex2(d);
@@ -217,20 +264,25 @@ __device__ __forceinline__ void fold_columns(RowState<kTop> &r, float *z, int id
         r.m = ym;
     }
     const float nm = r.m == -INFINITY ? 0.f : -r.m;  // all NaN so far
-    float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, u0 = 0.f, u1 = 0.f, u2 = 0.f, u3 = 0.f;
     if (whole) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            const float x0 = fmaf(z[j], c, nm), x1 = fmaf(z[j + 1], c, nm);
-            const float e0 = ptx::ex2(x0), e1 = ptx::ex2(x1);
+        for (int j = 0; j < kHalfCols; j += 4) {
+            const float x0 = fmaf(z[j], c, nm), x1 = fmaf(z[j + 1], c, nm), x2 = fmaf(z[j + 2], c, nm),
+                        x3 = fmaf(z[j + 3], c, nm);
+            const float e0 = ptx::ex2(x0), e1 = ptx::ex2(x1), e2 = ptx::ex2(x2), e3 = ptx::ex2(x3);
             s0 += e0;
             s1 += e1;
+            s2 += e2;
+            s3 += e3;
             u0 = fmaf(e0, x0, u0);
             u1 = fmaf(e1, x1, u1);
+            u2 = fmaf(e2, x2, u2);
+            u3 = fmaf(e3, x3, u3);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < kHalfCols; ++j) {
             if (id0 + j < V) {
                 const float x0 = fmaf(z[j], c, nm), e0 = ptx::ex2(x0);
                 s0 += e0;
@@ -238,32 +290,40 @@ __device__ __forceinline__ void fold_columns(RowState<kTop> &r, float *z, int id
             }
         }
     }
-    r.s += s0 + s1;
-    r.u += u0 + u1;
-    if (__any_sync(0xFFFFFFFFu, static_cast<uint32_t>(target - id0) < 32u)) {
+    r.s += (s0 + s1) + (s2 + s3);
+    r.u += (u0 + u1) + (u2 + u3);
+    if (__any_sync(0xFFFFFFFFu, static_cast<uint32_t>(target - id0) < static_cast<uint32_t>(kHalfCols))) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < kHalfCols; ++j)
             if (target == id0 + j) r.tz = z[j];
     }
     if constexpr (kTop > 0) {
-        // Candidates: products above the list's last.  Each round every row takes its next one (through
-        // shared memory: the place varies by row), so the rounds are the largest count in the warp.
-        if (__any_sync(0xFFFFFFFFu, zmax > r.v[kTop - 1])) {
-            uint32_t cand = 0u;
+        if (__any_sync(0xFFFFFFFFu, zmax > r.v[kTop - 1] && zmax >= bound)) {
+            if (bound < INFINITY) bound = row_bound<kTop>(words, top);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                zs[j * zs_step] = z[j];
-                cand |= z[j] > r.v[kTop - 1] ? 1u << j : 0u;
-            }
-            while (__any_sync(0xFFFFFFFFu, cand != 0u)) {
-                float zc = -INFINITY;
-                int j = 0;
-                if (cand) {
-                    j = __ffs(cand) - 1;
-                    cand &= cand - 1;
-                    zc = zs[j * zs_step];
+            for (int q = 0; q < kGroups; ++q) {
+                // Candidates: products above the list's last.  Each round every row takes its next one
+                // (through shared memory: the place varies by row), so the rounds are the largest count
+                // in the warp.
+                if (__any_sync(0xFFFFFFFFu, gmax[q] > r.v[kTop - 1] && gmax[q] >= bound)) {
+                    uint32_t cand = 0u;
+                    const float last = r.v[kTop - 1];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        zs[j * kZsStep] = z[32 * q + j];
+                        cand |= z[32 * q + j] > last && z[32 * q + j] >= bound ? 1u << j : 0u;
+                    }
+                    while (__any_sync(0xFFFFFFFFu, cand != 0u)) {
+                        float zc = -INFINITY;
+                        int j = 0;
+                        if (cand) {
+                            j = __ffs(cand) - 1;
+                            cand &= cand - 1;
+                            zc = zs[j * kZsStep];
+                        }
+                        r.insert(zc, id0 + 32 * q + j);  // no change unless above the last
+                    }
                 }
-                r.insert(zc, id0 + j);  // no change unless above the last
             }
         }
     }
@@ -332,7 +392,7 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
             const uint32_t a_bytes = static_cast<uint32_t>(a.a_rows) * 128u;
             const uint32_t bytes = (a_bytes + L::kBBytes) * kCtas;  // of both blocks, counted on the even one
             int it = 0;
-            bool ok = true, waited = a.gathered == 0;
+            bool ok = true, waited = a.prepared == 0;
             for (int ps = 0; ok && ps < passes; ++ps) {
                 const Share sh = share_of(a.plan, ps, worker);
                 if (!sh.any) continue;
@@ -384,7 +444,6 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
                         if (!(ok = ptx::mbar_wait(acc_empty + buf, ((part >> 1) & 1) ^ 1, abort_flag, a.err,
                                                   BLINK_DEVICE_TIMEOUT)))
                             break;
-                        if constexpr (kCtas == 2) ptx::fence_acquire_cluster();
                         ptx::tc_fence_after();
                         const uint32_t d = tmem + buf * kVocabTile;
                         const int kn = min(kPartBlocks, k_blocks - k0);
@@ -431,8 +490,8 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
         const int half = warp >> 2, lane_row = (warp & 3) * 32 + lane;
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * kHalfCols;
         float *zs = reinterpret_cast<float *>(smem + L::kScoreOff) + threadIdx.x;  // this thread's column
-        constexpr int kZsStep = kStateWarps * 32;
         const float c = a.c;
+        if (kTop > 0) ptx::grid_dep_wait();  // the bounds have been cleared
         int part = 0;
         bool ok = true;
         for (int ps = 0; ok && ps < passes; ++ps) {
@@ -442,6 +501,9 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
             const int row = row_w + lane;
             const bool live = row_w < a.n;  // of the warp: it has rows at all
             const int target = a.targets && row < a.n ? __ldg(a.targets + row) : -1;
+            uint32_t *words = a.bounds + static_cast<int64_t>(min(row, a.n - 1)) * kMaxTop;
+            const int slot0 = kTop > 0 ? ((sh.chunk * kHalves + half) * (kHalfCols / 32)) % a.top : 0;
+            float bound = row < a.n ? -INFINITY : INFINITY;  // no row: nothing to publish or list
             RowState<kTop> r;
             r.clear(a.top);
             for (int vt = sh.v0; vt < sh.v1; ++vt) {
@@ -476,11 +538,8 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
                 }
                 if (!ok) break;
                 const int first_id = vt * kVocabTile + half * kHalfCols;
-                if (live && first_id < a.V) {
-#pragma unroll
-                    for (int q = 0; q < kHalfCols / 32; ++q)
-                        fold_columns<kTop>(r, z + q * 32, first_id + q * 32, a.V, c, target, zs, kZsStep);
-                }
+                if (live && first_id < a.V)
+                    fold_tile<kTop>(r, z, first_id, a.V, c, target, zs, words, a.top, slot0, bound);
             }
             if (!ok) break;
             if (row < a.n) {
@@ -490,7 +549,7 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
 #pragma unroll
                     for (int j = 0; j < kTop; ++j) {
                         const int o = j - (kTop - a.top);
-                        if (o >= 0) a.best[cell * a.top + o] = make_int2(__float_as_int(r.v[j]), r.id[j]);
+                        if (o >= 0) a.best[cell * a.best_stride + o] = make_int2(__float_as_int(r.v[j]), r.id[j]);
                     }
                 }
             }
@@ -519,31 +578,35 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
     }
 }
 
-// Hidden rows of an index list, gathered into consecutive rows (a row outside the tensor: zeros).
-__global__ void __launch_bounds__(256) logprob_gather_kernel(const uint4 *__restrict__ hidden, int64_t stride, int hidden_rows,
-                                                             const int32_t *__restrict__ idx, int n, int pieces,
-                                                             uint4 *__restrict__ dst)
+// What the products need first: hidden rows of an index list gathered into consecutive rows (a row
+// outside the tensor: zeros), and the rows' bounds cleared.
+__global__ void __launch_bounds__(256) logprob_prepare_kernel(const uint4 *__restrict__ hidden, int64_t stride, int hidden_rows,
+                                                              const int32_t *__restrict__ idx, int64_t pieces,
+                                                              int row_pieces, uint4 *__restrict__ dst,
+                                                              uint4 *__restrict__ bounds, int64_t bound_pieces)
 {
     ptx::grid_launch_dependents();
-    const int64_t total = static_cast<int64_t>(n) * pieces;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; t < total;
-         t += static_cast<int64_t>(gridDim.x) * 256) {
-        const int r = static_cast<int>(t / pieces), p = static_cast<int>(t - static_cast<int64_t>(r) * pieces);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 256, t0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    for (int64_t t = t0; t < bound_pieces; t += step) bounds[t] = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t t = t0; t < pieces; t += step) {
+        const int r = static_cast<int>(t / row_pieces), p = static_cast<int>(t - static_cast<int64_t>(r) * row_pieces);
         const int hr = __ldg(idx + r);
         dst[t] = hr >= 0 && hr < hidden_rows ? __ldg(hidden + hr * stride + p) : make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
-constexpr int kMergeWarps = 8;
-constexpr int kMergeLists = kMaxWorkers * kHalves / 32;  // lists per lane
-constexpr int kMergeDepth = 4;                           // entries of a list kept in shared memory
+constexpr int kMergeWarps = 4;
+constexpr int kMaxLists = kMaxWorkers * kHalves;
+constexpr int kMergeDepth = 4;  // entries of a list kept in shared memory
 
-// One warp per row: joins the parts' statistics and takes the best of their lists.
-__global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const LogprobArgs a, int max_lists)
+// One warp per row: joins the parts of a row, kMine of them a lane.  The best `top` of their sorted
+// lists by taking the best first entry `top` times: two warp reductions a round.
+template <int kMine>
+__global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const LogprobArgs a)
 {
-    extern __shared__ int2 heads[];  // per warp [max_lists][kMergeDepth]: the first entries of each list
+    __shared__ int2 first[kMergeWarps][kMergeDepth][kMine * 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.x * (blockDim.x >> 5) + warp;
+    const int r = blockIdx.x * kMergeWarps + warp;
     ptx::grid_dep_wait();
     if (r >= a.n) return;
     const int rt = r / a.plan.tile_rows;
@@ -552,98 +615,111 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const L
     const int64_t cell0 = a.plan.first_cell(pass) + static_cast<int64_t>(rt - pass * a.plan.group) * a.plan.tile_rows +
                           r % a.plan.tile_rows;
     const int64_t step = static_cast<int64_t>(g) * a.plan.tile_rows;
-    const int top = a.top, depth = min(top, kMergeDepth);
-    int2 *hd = heads + static_cast<int64_t>(warp) * max_lists * kMergeDepth;
-    for (int q = lane; q < lists; q += 32) {
+    const int top = a.top, stride = a.best_stride, depth = min(top, kMergeDepth);
+    const float nan = __int_as_float(0x7FC00000);
+    const int target = a.targets ? __ldg(a.targets + r) : -1;
+    const int hr = a.row_idx ? __ldg(a.row_idx + r) : r;
+    const int2 none = make_int2(__float_as_int(-INFINITY), kNoToken);
+    float4 st[kMine];
+    int4 e01[kMine], e23[kMine];  // lists are 16-byte aligned and padded to kMergeDepth entries
 #pragma unroll
-        for (int j = 0; j < kMergeDepth; ++j)
-            if (j < depth) hd[q * kMergeDepth + j] = __ldcg(a.best + (cell0 + q * step) * top + j);
+    for (int q = 0; q < kMine; ++q) {
+        const int l = lane + 32 * q;
+        const int64_t cell = cell0 + l * step;
+        st[q] = l < lists ? __ldcg(a.stat + cell) : make_float4(-INFINITY, 0.f, 0.f, nan);
+        if (top > 0 && l < lists) {
+            const int4 *p = reinterpret_cast<const int4 *>(a.best + cell * stride);
+            e01[q] = __ldcg(p);
+            e23[q] = __ldcg(p + 1);
+        }
     }
-    float m = -INFINITY, tz = __int_as_float(0x7FC00000);
-    float4 st[kMergeLists];
+    float m = -INFINITY, tz = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < kMergeLists; ++q) {
-        const int ch = lane + 32 * q;
-        st[q] = ch < lists ? __ldcg(a.stat + cell0 + ch * step) : make_float4(-INFINITY, 0.f, 0.f, tz);
+    for (int q = 0; q < kMine; ++q) {
         m = fmaxf(m, st[q].x);
+        tz = fmaxf(tz, st[q].w);  // NaN in every part but the target's
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        tz = fmaxf(tz, __shfl_xor_sync(0xFFFFFFFFu, tz, o));
+    }
     float s = 0.f, u = 0.f;
-    bool has = false;
 #pragma unroll
-    for (int q = 0; q < kMergeLists; ++q) {
+    for (int q = 0; q < kMine; ++q) {
         const float d = st[q].x == -INFINITY ? 0.f : st[q].x - m;  // an empty part, or one of NaN alone
         const float f = exp2f(d);
         s = fmaf(f, st[q].y, s);
         u = fmaf(f, fmaf(st[q].y, d, st[q].z), u);
-        if (st[q].w == st[q].w) tz = st[q].w, has = true;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
     }
-    const uint32_t who = __ballot_sync(0xFFFFFFFFu, has);
-    tz = __shfl_sync(0xFFFFFFFFu, tz, who ? __ffs(who) - 1 : 0);
-    const float nan = __int_as_float(0x7FC00000);
-    const int hr = a.row_idx ? __ldg(a.row_idx + r) : r;
     const bool bad = hr < 0 || hr >= a.hidden_rows;
     const float l2s = log2f(s);
     const float l2 = bad ? nan : m + l2s;
     if (lane == 0) {
-        const int t = a.targets ? __ldg(a.targets + r) : -1;
-        if (bad || t < -1 || t >= a.V) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+        if (bad || target < -1 || target >= a.V) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
         if (a.lse) a.lse[r] = l2 * kLn2;
         if (a.entropy) a.entropy[r] = bad ? nan : (l2s - u / s) * kLn2;
-        if (a.logprob) a.logprob[r] = t >= 0 && t < a.V ? fmaf(tz, a.c, -l2) * kLn2 : nan;
+        if (a.logprob) a.logprob[r] = target >= 0 && target < a.V ? fmaf(tz, a.c, -l2) * kLn2 : nan;
     }
     if (top == 0) return;
-    __syncwarp();
-    int at[kMergeLists];     // next entry of each of the lane's lists
-    int2 head[kMergeLists];  // and that entry
-    const int2 none = make_int2(__float_as_int(-INFINITY), kNoToken);
+    uint32_t key[kMine];  // order of the first entry left of each list, its token, its place
+    int token[kMine], at[kMine];
 #pragma unroll
-    for (int q = 0; q < kMergeLists; ++q) {
+    for (int q = 0; q < kMine; ++q) {
+        const int l = lane + 32 * q;
         at[q] = 0;
-        head[q] = lane + 32 * q < lists ? hd[(lane + 32 * q) * kMergeDepth] : none;
+        key[q] = 0u;
+        token[q] = kNoToken;
+        if (l < lists) {
+            first[warp][1][l] = make_int2(e01[q].z, e01[q].w);
+            first[warp][2][l] = make_int2(e23[q].x, e23[q].y);
+            first[warp][3][l] = make_int2(e23[q].z, e23[q].w);
+            token[q] = e01[q].y;
+            key[q] = token[q] == kNoToken ? 0u : order_of(__int_as_float(e01[q].x));
+        }
     }
     for (int k = 0; k < top; ++k) {
-        float bv = -INFINITY;
-        int bi = kNoToken;
+        uint32_t bk = 0u;
 #pragma unroll
-        for (int q = 0; q < kMergeLists; ++q) {
-            const float v = __int_as_float(head[q].x);
-            if (v > bv || (v == bv && head[q].y < bi)) bv = v, bi = head[q].y;
+        for (int q = 0; q < kMine; ++q) bk = max(bk, key[q]);
+        const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, bk);
+        int bt = kNoToken;
+#pragma unroll
+        for (int q = 0; q < kMine; ++q)
+            if (key[q] == best) bt = min(bt, token[q]);
+        const int tok = __reduce_min_sync(0xFFFFFFFFu, bt);
+        if (lane == 0) {
+            const bool no = bad || tok == kNoToken;
+            a.top_ids[static_cast<int64_t>(r) * top + k] = no ? -1 : tok;
+            a.top_lp[static_cast<int64_t>(r) * top + k] = no ? nan : fmaf(of_order(best), a.c, -l2) * kLn2;
         }
-        const int mine = bi;
+        if (bt == tok && tok != kNoToken) {  // a token is in one list: one lane goes on in one list
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float ov = __shfl_xor_sync(0xFFFFFFFFu, bv, o);
-            const int oi = __shfl_xor_sync(0xFFFFFFFFu, bi, o);
-            if (ov > bv || (ov == bv && oi < bi)) bv = ov, bi = oi;
-        }
-        if (mine == bi && bi != kNoToken) {  // tokens are in one list each: one lane, one list
-#pragma unroll
-            for (int q = 0; q < kMergeLists; ++q) {
-                if (head[q].y == bi) {
+            for (int q = 0; q < kMine; ++q) {
+                if (token[q] == tok && key[q] == best) {
                     const int j = ++at[q], l = lane + 32 * q;
-                    head[q] = j >= top ? none
-                                       : j < depth ? hd[l * kMergeDepth + j] : __ldcg(a.best + (cell0 + l * step) * top + j);
+                    int2 e = none;
+                    if (j < top) e = j < depth ? first[warp][j][l] : __ldcg(a.best + (cell0 + l * step) * stride + j);
+                    token[q] = e.y;
+                    key[q] = e.y == kNoToken ? 0u : order_of(__int_as_float(e.x));
                 }
             }
-        }
-        if (lane == 0) {
-            const bool no = bad || bi == kNoToken;
-            a.top_ids[static_cast<int64_t>(r) * top + k] = no ? -1 : bi;
-            a.top_lp[static_cast<int64_t>(r) * top + k] = no ? nan : fmaf(bv, a.c, -l2) * kLn2;
         }
     }
 }
 
 struct WsLayout {
-    size_t stat, best, rows, total;
+    size_t stat, best, bounds, rows, total;
 };
+
+// Entries of a list in memory: even, so that lists start at 16 bytes, and enough for the merge's
+// first loads.
+int best_stride(int top) { return top == 0 ? 0 : top <= 4 ? 4 : (top + 1) / 2 * 2; }
 
 WsLayout ws_layout(const LogprobPlan &p, int n, int H, int top)
 {
@@ -651,7 +727,8 @@ WsLayout ws_layout(const LogprobPlan &p, int n, int H, int top)
     const size_t cells = static_cast<size_t>(p.cells());
     l.stat = kHeaderBytes;
     l.best = l.stat + align_up(cells * sizeof(float4), 256);
-    l.rows = l.best + align_up(cells * top * sizeof(int2), 256);
+    l.bounds = l.best + align_up(cells * best_stride(top) * sizeof(int2), 256);
+    l.rows = l.bounds + (top > 0 ? static_cast<size_t>(n) * kMaxTop * sizeof(uint32_t) : 0);
     l.total = l.rows + align_up(static_cast<size_t>(n) * H * sizeof(uint16_t), 256);
     return l;
 }
@@ -685,7 +762,7 @@ cudaError_t launch_logprob(const CUtensorMap &tm_h, const CUtensorMap &tm_w, con
         attr[na].val.clusterDim.y = 1;
         attr[na++].val.clusterDim.z = 1;
     }
-    if (a.gathered) {
+    if (a.prepared) {
         attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[na++].val.programmaticStreamSerializationAllowed = 1;
     }
@@ -747,25 +824,31 @@ extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t h
     a.c = kLog2e / temperature;
     a.stat = reinterpret_cast<float4 *>(wsb + l.stat);
     a.best = reinterpret_cast<int2 *>(wsb + l.best);
+    a.best_stride = best_stride(top);
     a.logprob = d_logprob;
     a.entropy = d_entropy;
     a.lse = d_lse;
     a.top_lp = d_top_logprobs;
     a.top_ids = d_top_ids;
     a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
-    a.gathered = d_row_idx != nullptr;
+    a.prepared = d_row_idx != nullptr || top > 0;
+    a.bounds = reinterpret_cast<uint32_t *>(wsb + l.bounds);
 
     const blink_bf16 *rows = hidden;
     int64_t row_stride = hidden_row_stride;
-    if (d_row_idx) {
+    if (a.prepared) {
         auto *dst = reinterpret_cast<blink_bf16 *>(wsb + l.rows);
-        const int64_t pieces = static_cast<int64_t>(n) * (H / 8), want = (pieces + 255) / 256;
-        logprob_gather_kernel<<<static_cast<unsigned>(want < 4096 ? want : 4096), 256, 0, stream>>>(
-            reinterpret_cast<const uint4 *>(hidden), hidden_row_stride / 8, hidden_rows, d_row_idx, n, H / 8,
-            reinterpret_cast<uint4 *>(dst));
+        const int64_t pieces = d_row_idx ? static_cast<int64_t>(n) * (H / 8) : 0;
+        const int64_t bound_pieces = top > 0 ? static_cast<int64_t>(n) * kMaxTop / 4 : 0;
+        const int64_t want = ((pieces > bound_pieces ? pieces : bound_pieces) + 255) / 256;
+        logprob_prepare_kernel<<<static_cast<unsigned>(want < 4096 ? want : 4096), 256, 0, stream>>>(
+            reinterpret_cast<const uint4 *>(hidden), hidden_row_stride / 8, hidden_rows, d_row_idx, pieces, H / 8,
+            reinterpret_cast<uint4 *>(dst), reinterpret_cast<uint4 *>(a.bounds), bound_pieces);
         if (cudaGetLastError() != cudaSuccess) return BLINK_CUDA_ERROR;
-        rows = dst;
-        row_stride = H;
+        if (d_row_idx) {
+            rows = dst;
+            row_stride = H;
+        }
     }
     CUtensorMap tm_h, tm_w;
     const uint64_t e = 2;
@@ -779,27 +862,23 @@ extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t h
         err = pair ? launch_logprob<2, 0>(tm_h, tm_w, a, stream) : launch_logprob<1, 0>(tm_h, tm_w, a, stream);
     else if (top <= 8)
         err = pair ? launch_logprob<2, 8>(tm_h, tm_w, a, stream) : launch_logprob<1, 8>(tm_h, tm_w, a, stream);
+    else if (top <= 20)
+        err = pair ? launch_logprob<2, 20>(tm_h, tm_w, a, stream) : launch_logprob<1, 20>(tm_h, tm_w, a, stream);
     else
         err = pair ? launch_logprob<2, 32>(tm_h, tm_w, a, stream) : launch_logprob<1, 32>(tm_h, tm_w, a, stream);
     if (err != cudaSuccess) return BLINK_CUDA_ERROR;
 
     const int lists = (a.plan.chunks > a.plan.rest_chunks ? a.plan.chunks : a.plan.rest_chunks) * kHalves;
-    const int warp_bytes = top > 0 ? lists * kMergeDepth * static_cast<int>(sizeof(int2)) : 0;  // at most 10 KB
-    const int warps = n >= 4 * kMergeWarps * sms ? kMergeWarps : 4;
-    const int smem = warps * warp_bytes;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(logprob_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return BLINK_CUDA_ERROR;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>((n + warps - 1) / warps));
-    cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.gridDim = dim3(static_cast<unsigned>((n + kMergeWarps - 1) / kMergeWarps));
+    cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, logprob_merge_kernel, a, lists) != cudaSuccess) return BLINK_CUDA_ERROR;
+    auto merge = lists <= 64 ? logprob_merge_kernel<2> : logprob_merge_kernel<(kMaxLists + 31) / 32>;
+    if (cudaLaunchKernelEx(&cfg, merge, a) != cudaSuccess) return BLINK_CUDA_ERROR;
     return BLINK_OK;
 }

@@ -296,14 +296,13 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank)
     return r;
 }
 
-// Arrive on a barrier of another block of the cluster (address from map_to_rank).
+// Arrive on a barrier of another block of the cluster (address from map_to_rank).  Relaxed: it hands
+// over tensor memory, ordered by the tcgen05 fences around it, and no data in other memory (a release
+// at cluster scope, with the matching acquire, cost several hundred cycles per hand-over).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-
-// Acquire, at cluster scope, of a phase already seen complete (arrivals came from another block).
-__device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // The copy into this block's shared memory completes on `bar`, a barrier of either block of the pair.
 __device__ __forceinline__ void tma_load_3d_pair(void *smem_dst, const void *tmap, int32_t x, int32_t y, int32_t z,
