@@ -140,8 +140,7 @@ struct LogprobArgs {
     const int32_t *targets;
     float c;       // log2(e) / T
     float4 *stat;  // [cells]: m, s, u, target's raw product (NaN: not in this part)
-    int2 *best;    // [cells][best_stride]: raw product (as bits) and token, descending
-    int best_stride;
+    int2 *best;    // [cells][top]: raw product (as bits) and token, descending
     float *logprob, *entropy, *lse, *top_lp;
     int32_t *top_ids;
     int *err;
@@ -549,7 +548,7 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
 #pragma unroll
                     for (int j = 0; j < kTop; ++j) {
                         const int o = j - (kTop - a.top);
-                        if (o >= 0) a.best[cell * a.best_stride + o] = make_int2(__float_as_int(r.v[j]), r.id[j]);
+                        if (o >= 0) a.best[cell * a.top + o] = make_int2(__float_as_int(r.v[j]), r.id[j]);
                     }
                 }
             }
@@ -595,44 +594,67 @@ __global__ void __launch_bounds__(256) logprob_prepare_kernel(const uint4 *__res
     }
 }
 
-constexpr int kMergeWarps = 4;
 constexpr int kMaxLists = kMaxWorkers * kHalves;
-constexpr int kMergeDepth = 4;  // entries of a list kept in shared memory
+constexpr int kWideRow = kMaxLists;  // threads of a row with many parts: one per part
+constexpr int kMaxCand = 256;
 
-// One warp per row: joins the parts of a row, kMine of them a lane.  The best `top` of their sorted
-// lists by taking the best first entry `top` times: two warp reductions a round.
-template <int kMine>
-__global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const LogprobArgs a)
+// A listed product as one number: larger is better (larger product, then lower token); 0: none.
+__device__ __forceinline__ unsigned long long rank_key(int2 e)
 {
-    __shared__ int2 first[kMergeWarps][kMergeDepth][kMine * 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.x * kMergeWarps + warp;
+    if (e.y == kNoToken) return 0ull;
+    return static_cast<unsigned long long>(order_of(__int_as_float(e.x))) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(e.y));
+}
+
+template <int kRowThreads>
+__device__ __forceinline__ void row_sync()
+{
+    if constexpr (kRowThreads == 32)
+        __syncwarp();
+    else
+        __syncthreads();
+}
+
+// Joins the parts of a row: kRowThreads threads a row, a warp where there are at most 64 parts, else
+// one thread per part.  Only listed products at or above the row's bound can be among the best
+// `top`: a few dozen, which are collected and ranked by counting.
+template <int kRowThreads>
+__global__ void __launch_bounds__(kRowThreads == 32 ? 128 : kRowThreads) logprob_merge_kernel(const LogprobArgs a)
+{
+    constexpr int kRows = kRowThreads == 32 ? 4 : 1, kWarps = kRowThreads / 32;
+    constexpr int kMine = kRowThreads == 32 ? 2 : 1;
+    __shared__ unsigned long long cand_all[kRows][kMaxCand];
+    __shared__ unsigned long long best_all[kWarps];
+    __shared__ int count_all[kRows];
+    __shared__ float4 red[kWarps];
+    const int sub = threadIdx.x / kRowThreads, t = threadIdx.x % kRowThreads;
+    const int warp = t >> 5, lane = t & 31;
+    const int r = blockIdx.x * kRows + sub;
     ptx::grid_dep_wait();
-    if (r >= a.n) return;
+    if (r >= a.n) return;  // a whole warp, or the whole block
+    unsigned long long *cand = cand_all[sub];
     const int rt = r / a.plan.tile_rows;
     const int pass = min(rt / a.plan.group, a.plan.passes() - 1);
     const int g = a.plan.tiles_of(pass), lists = a.plan.chunks_of(pass) * kHalves;
     const int64_t cell0 = a.plan.first_cell(pass) + static_cast<int64_t>(rt - pass * a.plan.group) * a.plan.tile_rows +
                           r % a.plan.tile_rows;
     const int64_t step = static_cast<int64_t>(g) * a.plan.tile_rows;
-    const int top = a.top, stride = a.best_stride, depth = min(top, kMergeDepth);
+    const int top = a.top;
     const float nan = __int_as_float(0x7FC00000);
     const int target = a.targets ? __ldg(a.targets + r) : -1;
     const int hr = a.row_idx ? __ldg(a.row_idx + r) : r;
-    const int2 none = make_int2(__float_as_int(-INFINITY), kNoToken);
     float4 st[kMine];
-    int4 e01[kMine], e23[kMine];  // lists are 16-byte aligned and padded to kMergeDepth entries
+    int2 head[kMine];
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
-        const int l = lane + 32 * q;
-        const int64_t cell = cell0 + l * step;
-        st[q] = l < lists ? __ldcg(a.stat + cell) : make_float4(-INFINITY, 0.f, 0.f, nan);
-        if (top > 0 && l < lists) {
-            const int4 *p = reinterpret_cast<const int4 *>(a.best + cell * stride);
-            e01[q] = __ldcg(p);
-            e23[q] = __ldcg(p + 1);
-        }
+        const int l = t + q * kRowThreads;
+        st[q] = l < lists ? __ldcg(a.stat + cell0 + l * step) : make_float4(-INFINITY, 0.f, 0.f, nan);
+        head[q] = l < lists && top > 0 ? __ldcg(a.best + (cell0 + l * step) * top) : make_int2(0, kNoToken);
     }
+    // the smallest of the row's words (one per lane), as an order; 0: fewer than `top` products yet
+    uint32_t word = 0xFFFFFFFFu;
+    if (lane < top) word = __ldcg(a.bounds + static_cast<int64_t>(r) * kMaxTop + lane);
+    if (t == 0) count_all[sub] = 0;
+
     float m = -INFINITY, tz = -INFINITY;
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
@@ -645,68 +667,96 @@ __global__ void __launch_bounds__(kMergeWarps * 32) logprob_merge_kernel(const L
         tz = fmaxf(tz, __shfl_xor_sync(0xFFFFFFFFu, tz, o));
     }
     float s = 0.f, u = 0.f;
+    auto join = [&](float pm, float ps, float pu) {
+        const float d = pm == -INFINITY ? 0.f : pm - m, f = exp2f(d);  // an empty part, or one of NaN alone
+        s = fmaf(f, ps, s);
+        u = fmaf(f, fmaf(ps, d, pu), u);
+    };
 #pragma unroll
-    for (int q = 0; q < kMine; ++q) {
-        const float d = st[q].x == -INFINITY ? 0.f : st[q].x - m;  // an empty part, or one of NaN alone
-        const float f = exp2f(d);
-        s = fmaf(f, st[q].y, s);
-        u = fmaf(f, fmaf(st[q].y, d, st[q].z), u);
-    }
+    for (int q = 0; q < kMine; ++q) join(st[q].x, st[q].y, st[q].z);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
     }
+    if constexpr (kRowThreads > 32) {  // the warps' parts, joined by every thread in the same order
+        if (lane == 0) red[warp] = make_float4(m, s, u, tz);
+        __syncthreads();
+        m = -INFINITY;
+        for (int w = 0; w < kWarps; ++w) {
+            m = fmaxf(m, red[w].x);
+            tz = fmaxf(tz, red[w].w);
+        }
+        s = u = 0.f;
+        for (int w = 0; w < kWarps; ++w) join(red[w].x, red[w].y, red[w].z);
+    }
     const bool bad = hr < 0 || hr >= a.hidden_rows;
     const float l2s = log2f(s);
     const float l2 = bad ? nan : m + l2s;
-    if (lane == 0) {
+    if (t == 0) {
         if (bad || target < -1 || target >= a.V) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
         if (a.lse) a.lse[r] = l2 * kLn2;
         if (a.entropy) a.entropy[r] = bad ? nan : (l2s - u / s) * kLn2;
         if (a.logprob) a.logprob[r] = target >= 0 && target < a.V ? fmaf(tz, a.c, -l2) * kLn2 : nan;
     }
     if (top == 0) return;
-    uint32_t key[kMine];  // order of the first entry left of each list, its token, its place
-    int token[kMine], at[kMine];
+
+    auto put = [&](int place, unsigned long long key) {
+        const bool no = bad || key == 0ull;
+        a.top_ids[static_cast<int64_t>(r) * top + place] = no ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+        a.top_lp[static_cast<int64_t>(r) * top + place] =
+            no ? nan : fmaf(of_order(static_cast<uint32_t>(key >> 32)), a.c, -l2) * kLn2;
+    };
+    const unsigned long long bound = static_cast<unsigned long long>(__reduce_min_sync(0xFFFFFFFFu, word)) << 32;
+    row_sync<kRowThreads>();  // the count starts at zero
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
-        const int l = lane + 32 * q;
-        at[q] = 0;
-        key[q] = 0u;
-        token[q] = kNoToken;
-        if (l < lists) {
-            first[warp][1][l] = make_int2(e01[q].z, e01[q].w);
-            first[warp][2][l] = make_int2(e23[q].x, e23[q].y);
-            first[warp][3][l] = make_int2(e23[q].z, e23[q].w);
-            token[q] = e01[q].y;
-            key[q] = token[q] == kNoToken ? 0u : order_of(__int_as_float(e01[q].x));
+        const int l = t + q * kRowThreads;
+        unsigned long long key = rank_key(head[q]);
+        for (int j = 0; key != 0ull && key >= bound;) {
+            const int at = atomicAdd(&count_all[sub], 1);
+            if (at < kMaxCand) cand[at] = key;
+            if (++j == top) break;
+            key = rank_key(__ldcg(a.best + (cell0 + l * step) * top + j));
         }
     }
-    for (int k = 0; k < top; ++k) {
-        uint32_t bk = 0u;
-#pragma unroll
-        for (int q = 0; q < kMine; ++q) bk = max(bk, key[q]);
-        const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, bk);
-        int bt = kNoToken;
-#pragma unroll
-        for (int q = 0; q < kMine; ++q)
-            if (key[q] == best) bt = min(bt, token[q]);
-        const int tok = __reduce_min_sync(0xFFFFFFFFu, bt);
-        if (lane == 0) {
-            const bool no = bad || tok == kNoToken;
-            a.top_ids[static_cast<int64_t>(r) * top + k] = no ? -1 : tok;
-            a.top_lp[static_cast<int64_t>(r) * top + k] = no ? nan : fmaf(of_order(best), a.c, -l2) * kLn2;
+    row_sync<kRowThreads>();
+    const int count = count_all[sub];
+    if (count <= kMaxCand) {
+        for (int e = t; e < count; e += kRowThreads) {
+            const unsigned long long key = cand[e];
+            int place = 0;
+            for (int o = 0; o < count; ++o) place += cand[o] > key;  // tokens differ, so keys do
+            if (place < top) put(place, key);
         }
-        if (bt == tok && tok != kNoToken) {  // a token is in one list: one lane goes on in one list
+        for (int k = count + t; k < top; k += kRowThreads) put(k, 0ull);  // NaN logits left fewer than `top`
+        return;
+    }
+    // More products at or above the bound than the room (many equal ones): the best first entry,
+    // `top` times.
+    int next[kMine];
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) next[q] = 0;
+    for (int k = 0; k < top; ++k) {
+        unsigned long long mine = 0ull;
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) mine = max(mine, rank_key(head[q]));
+        unsigned long long best = mine;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+        if constexpr (kRowThreads > 32) {
+            if (lane == 0) best_all[warp] = best;
+            __syncthreads();
+            for (int w = 0; w < kWarps; ++w) best = max(best, best_all[w]);
+            __syncthreads();
+        }
+        if (t == 0) put(k, best);
+        if (mine == best && best != 0ull) {
 #pragma unroll
             for (int q = 0; q < kMine; ++q) {
-                if (token[q] == tok && key[q] == best) {
-                    const int j = ++at[q], l = lane + 32 * q;
-                    int2 e = none;
-                    if (j < top) e = j < depth ? first[warp][j][l] : __ldcg(a.best + (cell0 + l * step) * stride + j);
-                    token[q] = e.y;
-                    key[q] = e.y == kNoToken ? 0u : order_of(__int_as_float(e.x));
+                if (rank_key(head[q]) == best) {
+                    const int l = t + q * kRowThreads;
+                    head[q] = ++next[q] < top ? __ldcg(a.best + (cell0 + l * step) * top + next[q]) : make_int2(0, kNoToken);
                 }
             }
         }
@@ -717,17 +767,13 @@ struct WsLayout {
     size_t stat, best, bounds, rows, total;
 };
 
-// Entries of a list in memory: even, so that lists start at 16 bytes, and enough for the merge's
-// first loads.
-int best_stride(int top) { return top == 0 ? 0 : top <= 4 ? 4 : (top + 1) / 2 * 2; }
-
 WsLayout ws_layout(const LogprobPlan &p, int n, int H, int top)
 {
     WsLayout l{};
     const size_t cells = static_cast<size_t>(p.cells());
     l.stat = kHeaderBytes;
     l.best = l.stat + align_up(cells * sizeof(float4), 256);
-    l.bounds = l.best + align_up(cells * best_stride(top) * sizeof(int2), 256);
+    l.bounds = l.best + align_up(cells * top * sizeof(int2), 256);
     l.rows = l.bounds + (top > 0 ? static_cast<size_t>(n) * kMaxTop * sizeof(uint32_t) : 0);
     l.total = l.rows + align_up(static_cast<size_t>(n) * H * sizeof(uint16_t), 256);
     return l;
@@ -824,7 +870,6 @@ extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t h
     a.c = kLog2e / temperature;
     a.stat = reinterpret_cast<float4 *>(wsb + l.stat);
     a.best = reinterpret_cast<int2 *>(wsb + l.best);
-    a.best_stride = best_stride(top);
     a.logprob = d_logprob;
     a.entropy = d_entropy;
     a.lse = d_lse;
@@ -873,12 +918,13 @@ extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t h
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>((n + kMergeWarps - 1) / kMergeWarps));
-    cfg.blockDim = dim3(kMergeWarps * 32);
+    const bool wide = lists > 64;
+    cfg.gridDim = dim3(static_cast<unsigned>(wide ? n : (n + 3) / 4));
+    cfg.blockDim = dim3(wide ? kWideRow : 128);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto merge = lists <= 64 ? logprob_merge_kernel<2> : logprob_merge_kernel<(kMaxLists + 31) / 32>;
-    if (cudaLaunchKernelEx(&cfg, merge, a) != cudaSuccess) return BLINK_CUDA_ERROR;
+    if (cudaLaunchKernelEx(&cfg, wide ? logprob_merge_kernel<kWideRow> : logprob_merge_kernel<32>, a) != cudaSuccess)
+        return BLINK_CUDA_ERROR;
     return BLINK_OK;
 }

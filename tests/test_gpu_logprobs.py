@@ -192,3 +192,27 @@ def test_repeat_bitwise_own_stream_and_graph():
     torch.cuda.synchronize()
     for k in ("logprob", "entropy", "lse", "top_ids", "top_logprobs"):
         assert torch.equal(r[k], r2[k]) and torch.equal(r[k], r3[k]), k
+
+
+@pytest.mark.parametrize("n,V,top", [(1, 5000, 20), (3, 20001, 32), (130, 3000, 9), (600, 1500, 4)])
+def test_more_equal_best_logits_than_any_list_holds(n, V, top):
+    """Every logit equal, or thousands of equal best ones: the lowest ids, whatever the parts are."""
+    h = torch.ones(n, 64, dtype=BF, device="cuda")
+    W = torch.zeros(V, 64, dtype=BF, device="cuda")
+    r = blink.blink_token_logprobs(h, W, top=top)
+    assert torch.equal(r["top_ids"], torch.arange(top, dtype=torch.int32, device="cuda").expand(n, top))
+    W[V // 3:, 0] = 1.0
+    W[5, 0] = 2.0
+    r = blink.blink_token_logprobs(h, W, top=top)
+    want = torch.cat([torch.tensor([5]), V // 3 + torch.arange(top - 1)]).to(torch.int32).cuda()
+    assert torch.equal(r["top_ids"], want.expand(n, top))
+
+
+def test_fewer_numbers_than_alternatives():
+    """NaN rows of the unembedding: the other tokens are listed, then -1; the sums are NaN."""
+    h = torch.ones(2, 64, dtype=BF, device="cuda")
+    W = torch.full((700, 64), float("nan"), dtype=BF, device="cuda")
+    W[[650, 3, 300]] = torch.tensor([[0.5], [0.25], [0.5]], device="cuda").to(BF).expand(3, 64)
+    r = blink.blink_token_logprobs(h, W, top=6)
+    assert r["top_ids"].tolist() == [[300, 650, 3, -1, -1, -1]] * 2
+    assert bool(r["lse"].isnan().all()) and bool(r["entropy"].isnan().all())
