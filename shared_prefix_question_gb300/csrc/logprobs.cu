@@ -21,14 +21,18 @@
 //
 // Precision.  The tensor core's fp32 accumulator truncates: over a sum of H / 16 steps the loss grows
 // with H (measured against 64 bits, logits of 12: 2.7e-6 of the logit at H = 2560, 5.4e-6 at 5120, and
-// four times that where all products have one sign).  So a product runs over kPartBlocks * 64 of H
-// only, and the row's thread adds the parts in registers, rounded to nearest: the loss stays that of
+// four times that where all products have one sign).  So a product runs over at most 640 of H only, and the row's thread adds the parts in registers, rounded to nearest: the loss stays that of
 // one part whatever H is.
 //
-// Roles (384 threads a block): warps 0-7 the states (thread t and t + 128 share row t, 128 of a tile's
-// columns each), warp 8 TMA producer, warp 9 MMA issuer (of the even block).  Tensor memory: two
-// accumulators of 256 columns, so one part is read out and folded while the next is multiplied.  The
-// states take 232 registers a thread (128 of them the tile's logits), the other warps 40.
+// Roles (384 threads a block): warps 0-7 the states (threads t and t + 128 share row t, 128 of a tile's
+// columns each, held in registers: 232 a thread, 40 for the other warps), warp 8 TMA producer, warp 9
+// MMA issuer (of the even block).
+// Tensor memory: two accumulators of 256 columns, so one part is read out and folded while the next is
+// multiplied.  Warps 10 and 11 keep the rows' bounds (below) up to date in shared memory.
+//
+// Lists.  A thread's alternatives are in registers, sorted.  While the tensor core reads its operands
+// from shared memory, a dependent shared-memory access of another warp takes hundreds of cycles:
+// lists there cost 1,500 cycles per product inserted, whichever way they were worked on.
 #include <cstdint>
 
 #include "common.cuh"
@@ -43,18 +47,17 @@ constexpr int kMaxTop = BLINK_MAX_TOP_TOKENS;
 constexpr int kVocabTile = 256;
 constexpr int kBlockRows = 128;
 constexpr int kThreadsLP = 384;
+constexpr int kRegsNeeded = 256 * 232 + 128 * 40;
 constexpr int kStateWarps = 8;
 constexpr int kProducerLP = 8, kIssuerLP = 9;
-constexpr int kRegsNeeded = 256 * 232 + 128 * 40;
 constexpr int kHalves = 2;      // threads that share a row
 constexpr int kHalfCols = kVocabTile / kHalves;
-#ifndef KPB
-#define KPB 8
-#endif
-constexpr int kPartBlocks = KPB;  // 64-wide blocks of H per product
+constexpr int kPartBlocks = 10;  // at most this many 64-wide blocks of H per product
 constexpr int kNoToken = 0x7FFFFFFF;
 constexpr int kMaxWorkers = 160;
 constexpr int kMaxStages = 8;
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kBatchCols = 8;  // columns searched for alternatives at a time
 
 // How the rows and the vocabulary are shared out (computed on the host, walked by every role).
 struct LogprobPlan {
@@ -146,41 +149,49 @@ struct LogprobArgs {
     int *err;
     uint32_t *bounds;  // [n][kMaxTop]: see RowBound
     int prepared;      // a launch before gathered the hidden rows and cleared the bounds
+    // shared memory: the stages, with alternatives the rows' bounds, then the barriers
+    int stages, stage_bytes, a_bytes, bound_off, bar_off, smem_bytes;
 };
 
-template <int kCtas>
-struct LpLayout {
-    static constexpr int kABytes = kBlockRows * 128;               // 64 of H per stage
-    static constexpr int kBRows = kVocabTile / kCtas;
-    static constexpr int kBBytes = kBRows * 128;
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = kCtas == 1 ? 4 : 6;
-    static constexpr int kScoreOff = kStages * kStageBytes;        // [32][threads of the states] floats
-    static constexpr int kBarOff = kScoreOff + 32 * kStateWarps * 32 * 4;
-    static constexpr int kBytes = kBarOff + 256;
-};
+// Divides the shared memory of a block: as many stages as fit.
+void lay_out(LogprobArgs &a)
+{
+    const bool one = a.plan.blocks_per_worker == 1;
+    a.a_rows = a.n < kBlockRows ? (a.n + 7) / 8 * 8 : kBlockRows;
+    a.a_bytes = a.a_rows * 128;
+    a.stage_bytes = a.a_bytes + kVocabTile / (one ? 1 : 2) * 128;
+    const int bounds = a.top > 0 ? kBlockRows * static_cast<int>(sizeof(int2)) : 0;
+    a.stages = (kSmemMax - bounds - 256) / a.stage_bytes;
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    a.bound_off = a.stages * a.stage_bytes;
+    a.bar_off = a.bound_off + bounds;
+    a.smem_bytes = a.bar_off + 256;
+}
 
-// State of one row: running (m, s, u), the target's product and the best kTop products so far.
-// The list holds `top` entries in its last places; the places before them are +inf and never move.
+// State of one row: running (m, s, u), the target's product, the row's bound as last read (+inf where
+// the thread has no row) and the best products so far.  The list holds `top` entries in its last
+// places; the places before them are +inf and never move.
 template <int kTop>
 struct RowState {
-    float m, s, u, tz;
+    float m, s, u, tz, bound;
     float v[kTop > 0 ? kTop : 1];
     int32_t id[kTop > 0 ? kTop : 1];
-    __device__ __forceinline__ void clear(int top)
+    __device__ __forceinline__ void clear(int top, bool has_row)
     {
         m = -INFINITY;
         s = u = 0.f;
         tz = __int_as_float(0x7FC00000);
+        bound = has_row ? -INFINITY : INFINITY;
 #pragma unroll
         for (int j = 0; j < kTop; ++j) {
             v[j] = j < kTop - top ? INFINITY : -INFINITY;
             id[j] = kNoToken;
         }
     }
+    __device__ __forceinline__ float last() const { return v[kTop > 0 ? kTop - 1 : 0]; }
     // Tokens come in ascending id, so an equal product goes behind those already listed.  No entry
     // waits for another: the list is descending, so entry j moves one place down exactly when the one
-    // before it is below z (a chain of swaps took 500 cycles for 32 entries).
+    // before it is below z.  No change for a z that is not above the last.
     __device__ __forceinline__ void insert(float z, int32_t i)
     {
 #pragma unroll
@@ -200,17 +211,36 @@ __device__ __forceinline__ uint32_t order_of(float z)  // larger unsigned = larg
 }
 __device__ __forceinline__ float of_order(uint32_t o) { return __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o); }
 
-// A row's bound: `top` words, each the largest product seen so far in its own share of the vocabulary
-// (a thread's groups of 32 columns are dealt to the words), kept by every worker with atomic maxima.
-// `top` products are at least the smallest of them, so a product below it is no alternative
-// of the row and need not enter a list.  How far the others have come varies from run to run, and with
-// it what the lists hold, but not their best `top`: the result does not vary.
-template <int kTop>
+// A row's bound.  Each of kMaxTop words per row holds the largest product seen so far in its own share
+// of the vocabulary (a thread's groups of 32 columns are dealt to the words), kept by every worker with
+// atomic maxima.  So at least `top` products are no smaller than the top-th largest word, and a
+// product below that is no alternative of the row and need not enter a list.  With 20 of 32 words
+// about 31 products of the whole row are at or above it, where a thread's own list alone would let in
+// its first 20, about half of the next 20 and so on.  How far the others have come varies from run to
+// run, and with it what the lists hold, but not the best `top` of them: the result does not vary.
+
+// The k-th largest (k = 1..32) of one word per lane.
+__device__ __forceinline__ uint32_t kth_largest(uint32_t v, int k)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2) {
+#pragma unroll
+        for (int o = size / 2; o > 0; o /= 2) {
+            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            const bool first = (lane & o) == 0, down = (lane & size) == 0;  // descending runs
+            v = first == down ? max(v, other) : min(v, other);
+        }
+    }
+    return __shfl_sync(0xFFFFFFFFu, v, k - 1);
+}
+
+// A looser bound that one thread reads by itself: the smallest of the first `top` words.
 __device__ __forceinline__ float row_bound(const uint32_t *words, int top)
 {
     uint32_t lo = 0xFFFFFFFFu;
 #pragma unroll
-    for (int j = 0; j < kTop; j += 4) {
+    for (int j = 0; j < kMaxTop; j += 4) {
         if (j < top) {
             const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(words + j));
             lo = min(lo, w.x);
@@ -222,39 +252,60 @@ __device__ __forceinline__ float row_bound(const uint32_t *words, int top)
     return lo == 0u ? -INFINITY : of_order(lo);
 }
 
+// Where a row's bound is kept.
+struct BoundPlace {
+    uint32_t *words;  // of this thread's row
+    uint32_t kept;    // as warps 10 and 11 last saw it: tag, order (shared address)
+    int top, slot0, tag;
+};
+
+// The first of columns 8 b .. 8 b + 7 that is at least `least` and not in `done` (b the same in the warp).
+__device__ __forceinline__ void next_candidate(const float (&z)[kHalfCols], int b, float least, uint32_t done, float &zc,
+                                               int &jc)
+{
+    static_assert(kBatchCols == 8 && kHalfCols == 128, "sixteen batches of eight columns");
+    zc = -INFINITY;
+    jc = -1;
+#define BLINK_SEARCH(B)                                                                     \
+    case B:                                                                                 \
+        _Pragma("unroll") for (int j = 7; j >= 0; --j) if (z[8 * B + j] >= least && !(done >> j & 1u)) \
+            zc = z[8 * B + j], jc = j;                                                      \
+        break;
+    switch (b) {
+        BLINK_SEARCH(0) BLINK_SEARCH(1) BLINK_SEARCH(2) BLINK_SEARCH(3) BLINK_SEARCH(4) BLINK_SEARCH(5)
+        BLINK_SEARCH(6) BLINK_SEARCH(7) BLINK_SEARCH(8) BLINK_SEARCH(9) BLINK_SEARCH(10) BLINK_SEARCH(11)
+        BLINK_SEARCH(12) BLINK_SEARCH(13) BLINK_SEARCH(14) BLINK_SEARCH(15)
+    }
+#undef BLINK_SEARCH
+}
+
 // Folds a row's logits of a tile, tokens id0 .. id0 + kHalfCols - 1, into its state.
 template <int kTop>
 __device__ __forceinline__ void fold_tile(RowState<kTop> &r, float (&z)[kHalfCols], int id0, int V, float c, int target,
-                                          float *zs, uint32_t *words, int top, int slot0, float &bound)
+                                          const BoundPlace &bp)
 {
-    constexpr int kGroups = kHalfCols / 32, kZsStep = kStateWarps * 32;
+    constexpr int kBatches = kHalfCols / kBatchCols;
     const bool whole = id0 + kHalfCols <= V;
     if (!whole) {
 #pragma unroll
         for (int j = 0; j < kHalfCols; ++j)
             if (id0 + j >= V) z[j] = -INFINITY;
     }
-    float gmax[kGroups];
+    float bmax[kBatches];  // of eight columns
 #pragma unroll
-    for (int q = 0; q < kGroups; ++q) {
-        const float *y = z + 32 * q;
-        float m0 = fmaxf(y[0], y[1]), m1 = fmaxf(y[2], y[3]);
+    for (int b = 0; b < kBatches; ++b) {
+        const float *y = z + 8 * b;
+        bmax[b] = ptx::max3(ptx::max3(y[0], y[1], y[2]), ptx::max3(y[3], y[4], y[5]), fmaxf(y[6], y[7]));
+    }
+    float zmax = -INFINITY;
 #pragma unroll
-        for (int j = 4; j < 32; j += 4) {
-            m0 = ptx::max3(m0, y[j], y[j + 1]);
-            m1 = ptx::max3(m1, y[j + 2], y[j + 3]);
-        }
-        gmax[q] = fmaxf(m0, m1);
+    for (int q = 0; q < kHalfCols / 32; ++q) {
+        const float gmax = ptx::max3(bmax[4 * q], bmax[4 * q + 1], fmaxf(bmax[4 * q + 2], bmax[4 * q + 3]));
+        zmax = fmaxf(zmax, gmax);
         if constexpr (kTop > 0) {
-            if (gmax[q] > bound && gmax[q] > -INFINITY) {
-                int w = slot0 + q;
-                w = w >= top ? w % top : w;
-                atomicMax(words + w, order_of(gmax[q]));
-            }
+            if (gmax > r.bound) atomicMax(bp.words + bp.slot0 + q, order_of(gmax));
         }
     }
-    const float zmax = fmaxf(fmaxf(gmax[0], gmax[1]), fmaxf(gmax[2], gmax[3]));
-    static_assert(kGroups == 4, "four groups of 32 columns");
     const float ym = zmax * c;
     if (ym > r.m) {
         const float d = r.m == -INFINITY ? 0.f : r.m - ym, f = ptx::ex2(d);
@@ -263,23 +314,30 @@ __device__ __forceinline__ void fold_tile(RowState<kTop> &r, float (&z)[kHalfCol
         r.m = ym;
     }
     const float nm = r.m == -INFINITY ? 0.f : -r.m;  // all NaN so far
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, u0 = 0.f, u1 = 0.f, u2 = 0.f, u3 = 0.f;
     if (whole) {
+        // two columns an instruction for all but the exp2
+        const uint64_t cc = ptx::f32x2(c, c), mm = ptx::f32x2(nm, nm);
+        uint64_t s0 = 0ull, s1 = 0ull, u0 = 0ull, u1 = 0ull;
 #pragma unroll
         for (int j = 0; j < kHalfCols; j += 4) {
-            const float x0 = fmaf(z[j], c, nm), x1 = fmaf(z[j + 1], c, nm), x2 = fmaf(z[j + 2], c, nm),
-                        x3 = fmaf(z[j + 3], c, nm);
-            const float e0 = ptx::ex2(x0), e1 = ptx::ex2(x1), e2 = ptx::ex2(x2), e3 = ptx::ex2(x3);
-            s0 += e0;
-            s1 += e1;
-            s2 += e2;
-            s3 += e3;
-            u0 = fmaf(e0, x0, u0);
-            u1 = fmaf(e1, x1, u1);
-            u2 = fmaf(e2, x2, u2);
-            u3 = fmaf(e3, x3, u3);
+            const uint64_t x0 = ptx::fma_f32x2(ptx::f32x2(z[j], z[j + 1]), cc, mm);
+            const uint64_t x1 = ptx::fma_f32x2(ptx::f32x2(z[j + 2], z[j + 3]), cc, mm);
+            float a0, a1, a2, a3;
+            ptx::f32x2_split(x0, a0, a1);
+            ptx::f32x2_split(x1, a2, a3);
+            const uint64_t e0 = ptx::f32x2(ptx::ex2(a0), ptx::ex2(a1)), e1 = ptx::f32x2(ptx::ex2(a2), ptx::ex2(a3));
+            s0 = ptx::add_f32x2(s0, e0);
+            s1 = ptx::add_f32x2(s1, e1);
+            u0 = ptx::fma_f32x2(e0, x0, u0);
+            u1 = ptx::fma_f32x2(e1, x1, u1);
         }
+        float lo, hi;
+        ptx::f32x2_split(ptx::add_f32x2(s0, s1), lo, hi);
+        r.s += lo + hi;
+        ptx::f32x2_split(ptx::add_f32x2(u0, u1), lo, hi);
+        r.u += lo + hi;
     } else {
+        float s0 = 0.f, u0 = 0.f;
 #pragma unroll
         for (int j = 0; j < kHalfCols; ++j) {
             if (id0 + j < V) {
@@ -288,40 +346,39 @@ __device__ __forceinline__ void fold_tile(RowState<kTop> &r, float (&z)[kHalfCol
                 u0 = fmaf(e0, x0, u0);
             }
         }
+        r.s += s0;
+        r.u += u0;
     }
-    r.s += (s0 + s1) + (s2 + s3);
-    r.u += (u0 + u1) + (u2 + u3);
     if (__any_sync(0xFFFFFFFFu, static_cast<uint32_t>(target - id0) < static_cast<uint32_t>(kHalfCols))) {
 #pragma unroll
         for (int j = 0; j < kHalfCols; ++j)
             if (target == id0 + j) r.tz = z[j];
     }
     if constexpr (kTop > 0) {
-        if (__any_sync(0xFFFFFFFFu, zmax > r.v[kTop - 1] && zmax >= bound)) {
-            if (bound < INFINITY) bound = row_bound<kTop>(words, top);
+        int2 kept;
+        asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];" : "=r"(kept.x), "=r"(kept.y) : "r"(bp.kept) : "memory");
+        if (kept.x == bp.tag && kept.y != 0) r.bound = fmaxf(r.bound, of_order(static_cast<uint32_t>(kept.y)));
+        if (__any_sync(0xFFFFFFFFu, zmax > r.last() && zmax >= r.bound)) {
+            if (r.bound == -INFINITY) r.bound = row_bound(bp.words, bp.top);  // the first tile
+            uint32_t mine = 0u;  // this row's batches with a candidate
 #pragma unroll
-            for (int q = 0; q < kGroups; ++q) {
-                // Candidates: products above the list's last.  Each round every row takes its next one
-                // (through shared memory: the place varies by row), so the rounds are the largest count
-                // in the warp.
-                if (__any_sync(0xFFFFFFFFu, gmax[q] > r.v[kTop - 1] && gmax[q] >= bound)) {
-                    uint32_t cand = 0u;
-                    const float last = r.v[kTop - 1];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        zs[j * kZsStep] = z[32 * q + j];
-                        cand |= z[32 * q + j] > last && z[32 * q + j] >= bound ? 1u << j : 0u;
-                    }
-                    while (__any_sync(0xFFFFFFFFu, cand != 0u)) {
-                        float zc = -INFINITY;
-                        int j = 0;
-                        if (cand) {
-                            j = __ffs(cand) - 1;
-                            cand &= cand - 1;
-                            zc = zs[j * kZsStep];
-                        }
-                        r.insert(zc, id0 + 32 * q + j);  // no change unless above the last
-                    }
+            for (int b = 0; b < kBatches; ++b)
+                if (bmax[b] > r.last() && bmax[b] >= r.bound) mine |= 1u << b;
+            // Batch by batch, every row takes its next candidate in each round.  One copy of the insertion: it
+            // runs seldom (measured: for 1 to 2 batches of a warp's 16 in a tile, once the first tiles are
+            // done), and a copy for every column would miss the instruction cache every time.
+            uint32_t todo = __reduce_or_sync(0xFFFFFFFFu, mine);
+            while (todo != 0u) {
+                const int b = __ffs(todo) - 1;
+                todo &= todo - 1;
+                uint32_t done = 0u;
+                while (true) {
+                    float zc;
+                    int jc;
+                    next_candidate(z, b, fmaxf(r.bound, r.last()), done, zc, jc);  // one equal to the last changes nothing
+                    if (!__any_sync(0xFFFFFFFFu, jc >= 0)) break;
+                    if (jc >= 0) done |= 1u << jc;
+                    r.insert(zc, id0 + 8 * b + jc);
                 }
             }
         }
@@ -332,25 +389,28 @@ template <int kCtas, int kTop>
 __global__ void __launch_bounds__(kThreadsLP, 1)
     logprob_kernel(const __grid_constant__ CUtensorMap tm_h, const __grid_constant__ CUtensorMap tm_w, const LogprobArgs a)
 {
-    using L = LpLayout<kCtas>;
+    constexpr bool kList = kTop > 0;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + a.bar_off);
     uint64_t *full = bars, *empty = bars + kMaxStages;
     uint64_t *acc_full = bars + 2 * kMaxStages, *acc_empty = acc_full + 2;
     uint64_t *mma_done = acc_empty + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
     int *abort_word = reinterpret_cast<int *>(tmem_holder + 1);
     volatile int *abort_flag = abort_word;
+    volatile int *turn = abort_word + 1;  // pass + 1 the states are at; 0 before, -1 after
+    const uint32_t kept_bounds = ptx::smem_u32(smem + a.bound_off);  // [128][2]: pass + 1, order
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = kCtas == 2 ? ptx::cluster_rank() : 0u;
     const int worker = blockIdx.x / kCtas;
     const int passes = a.plan.passes();
     const int k_blocks = (a.H + 63) / 64;
+    const int n_parts = (k_blocks + kPartBlocks - 1) / kPartBlocks, part_blocks = (k_blocks + n_parts - 1) / n_parts;
     const bool aligned = (ptx::smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need it
     if (!aligned && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
 
     if (warp == kProducerLP && lane == 0) {
-        for (int i = 0; i < L::kStages; ++i) {
+        for (int i = 0; i < a.stages; ++i) {
             ptx::mbar_init(full + i, 1);
             ptx::mbar_init(empty + i, 1);
         }
@@ -361,9 +421,12 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
         ptx::mbar_init(mma_done, 1);
         ptx::fence_mbar_init();
         *abort_word = aligned ? 0 : 1;
+        *turn = 0;
         ptx::tma_prefetch_desc(&tm_h);
         ptx::tma_prefetch_desc(&tm_w);
     }
+    if (kList && threadIdx.x < kBlockRows)
+        reinterpret_cast<int2 *>(smem + a.bound_off)[threadIdx.x] = make_int2(0, 0);
     if (warp == 0) {
         if constexpr (kCtas == 2) {
             ptx::tmem_alloc_pair(tmem_holder, 512);
@@ -388,34 +451,32 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
         // nothing was started: straight to the end
     } else if (warp == kProducerLP) {
         if (lane == 0) {
-            const uint32_t a_bytes = static_cast<uint32_t>(a.a_rows) * 128u;
-            const uint32_t bytes = (a_bytes + L::kBBytes) * kCtas;  // of both blocks, counted on the even one
-            int it = 0;
+            const uint32_t bytes = static_cast<uint32_t>(a.stage_bytes) * kCtas;  // of both blocks, counted on the even one
+            int it = 0, st = 0;
+            uint32_t ph = 1u;
             bool ok = true, waited = a.prepared == 0;
             for (int ps = 0; ok && ps < passes; ++ps) {
                 const Share sh = share_of(a.plan, ps, worker);
                 if (!sh.any) continue;
                 const int row0 = sh.row_tile * a.plan.tile_rows + static_cast<int>(rank) * kBlockRows;
                 for (int vt = sh.v0; ok && vt < sh.v1; ++vt) {
-                    const int col0 = vt * kVocabTile + static_cast<int>(rank) * L::kBRows;
+                    const int col0 = vt * kVocabTile + static_cast<int>(rank) * (kVocabTile / kCtas);
                     for (int kb = 0; kb < k_blocks; ++kb, ++it) {
-                        const int st = it % L::kStages;
-                        if (!(ok = ptx::mbar_wait(empty + st, ((it / L::kStages) & 1) ^ 1, abort_flag, a.err,
-                                                  BLINK_DEVICE_TIMEOUT)))
-                            break;
-                        uint8_t *dst = smem + st * L::kStageBytes;
+                        if (!(ok = ptx::mbar_wait(empty + st, ph, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
+                        uint8_t *dst = smem + st * a.stage_bytes;
                         if constexpr (kCtas == 2) {
                             const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(full + st), 0);
                             if (rank == 0) ptx::mbar_arrive_expect_tx(full + st, bytes);
-                            ptx::tma_load_3d_pair(dst + L::kABytes, &tm_w, kb * 64, col0, 0, bar);
+                            ptx::tma_load_3d_pair(dst + a.a_bytes, &tm_w, kb * 64, col0, 0, bar);
                             if (!waited) ptx::grid_dep_wait(), waited = true;
                             ptx::tma_load_3d_pair(dst, &tm_h, kb * 64, row0, 0, bar);
                         } else {
                             ptx::mbar_arrive_expect_tx(full + st, bytes);
-                            ptx::tma_load_3d(dst + L::kABytes, &tm_w, kb * 64, col0, 0, full + st);
+                            ptx::tma_load_3d(dst + a.a_bytes, &tm_w, kb * 64, col0, 0, full + st);
                             if (!waited) ptx::grid_dep_wait(), waited = true;
                             ptx::tma_load_3d(dst, &tm_h, kb * 64, row0, 0, full + st);
                         }
+                        if (++st == a.stages) st = 0, ph ^= 1u;
                     }
                 }
             }
@@ -424,48 +485,42 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
             // on the even block, which the other waits for at the cluster barrier below.
             if (rank == 0) {
                 volatile int no_abort = 0;
-                for (int n = it > L::kStages ? it - L::kStages : 0; n < it; ++n, no_abort = 0)
-                    ptx::mbar_wait(full + n % L::kStages, (n / L::kStages) & 1, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
+                for (int n = it > a.stages ? it - a.stages : 0; n < it; ++n, no_abort = 0)
+                    ptx::mbar_wait(full + n % a.stages, (n / a.stages) & 1, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
             }
         }
     } else if (warp == kIssuerLP) {
         if (lane == 0 && rank == 0) {
             constexpr uint32_t idesc = ptx::idesc_bf16_f32(kBlockRows * kCtas, kVocabTile, false);
-            const uint32_t base = ptx::smem_u32(smem);
-            int it = 0, part = 0;
+            const uint64_t desc0 = ptx::smem_desc_sw128(ptx::smem_u32(smem), 16, 1024);  // in units of 16 bytes
+            const uint32_t stage16 = static_cast<uint32_t>(a.stage_bytes) >> 4, a16 = static_cast<uint32_t>(a.a_bytes) >> 4;
+            int st = 0, part = 0;
+            uint32_t ph = 0u;
             bool ok = true;
             for (int ps = 0; ok && ps < passes; ++ps) {
                 const Share sh = share_of(a.plan, ps, worker);
                 if (!sh.any) continue;
                 for (int vt = sh.v0; ok && vt < sh.v1; ++vt) {
-                    for (int k0 = 0; ok && k0 < k_blocks; k0 += kPartBlocks, ++part) {
+                    for (int k0 = 0; ok && k0 < k_blocks; k0 += part_blocks, ++part) {
                         const int buf = part & 1;
                         if (!(ok = ptx::mbar_wait(acc_empty + buf, ((part >> 1) & 1) ^ 1, abort_flag, a.err,
                                                   BLINK_DEVICE_TIMEOUT)))
                             break;
                         ptx::tc_fence_after();
                         const uint32_t d = tmem + buf * kVocabTile;
-                        const int kn = min(kPartBlocks, k_blocks - k0);
-                        for (int kb = 0; kb < kn; ++kb, ++it) {
-                            const int st = it % L::kStages;
-                            if (!(ok = ptx::mbar_wait(full + st, (it / L::kStages) & 1, abort_flag, a.err,
-                                                      BLINK_DEVICE_TIMEOUT)))
-                                break;
+                        const int kn = min(part_blocks, k_blocks - k0);
+                        for (int kb = 0; kb < kn; ++kb) {
+                            if (!(ok = ptx::mbar_wait(full + st, ph, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
                             ptx::tc_fence_after();
-                            const uint64_t ad = ptx::smem_desc_sw128(base + st * L::kStageBytes, 16, 1024);
-                            const uint64_t bd = ptx::smem_desc_sw128(base + st * L::kStageBytes + L::kABytes, 16, 1024);
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {  // 16 of H: 32 bytes, 2 in the descriptor's units
-                                const uint32_t acc = kb > 0 || kk > 0;
-                                if constexpr (kCtas == 2)
-                                    ptx::mma_ss_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, acc);
-                                else
-                                    ptx::mma_ss(d, ad + 2 * kk, bd + 2 * kk, idesc, acc);
-                            }
-                            if constexpr (kCtas == 2)
+                            const uint64_t ad = desc0 + st * stage16, bd = ad + a16;
+                            if constexpr (kCtas == 2) {
+                                ptx::mma_ss_pair_x4(d, ad, bd, idesc, kb > 0);
                                 ptx::mma_commit_pair(empty + st);
-                            else
+                            } else {
+                                ptx::mma_ss_x4(d, ad, bd, idesc, kb > 0);
                                 ptx::mma_commit(empty + st);
+                            }
+                            if (++st == a.stages) st = 0, ph ^= 1u;
                         }
                         if (!ok) break;
                         if constexpr (kCtas == 2)
@@ -488,9 +543,11 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int half = warp >> 2, lane_row = (warp & 3) * 32 + lane;
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * kHalfCols;
-        float *zs = reinterpret_cast<float *>(smem + L::kScoreOff) + threadIdx.x;  // this thread's column
         const float c = a.c;
-        if (kTop > 0) ptx::grid_dep_wait();  // the bounds have been cleared
+        BoundPlace bp;
+        bp.top = a.top;
+        bp.kept = kept_bounds + lane_row * 8;
+        if (kList) ptx::grid_dep_wait();  // the bounds have been cleared
         int part = 0;
         bool ok = true;
         for (int ps = 0; ok && ps < passes; ++ps) {
@@ -500,14 +557,17 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
             const int row = row_w + lane;
             const bool live = row_w < a.n;  // of the warp: it has rows at all
             const int target = a.targets && row < a.n ? __ldg(a.targets + row) : -1;
-            uint32_t *words = a.bounds + static_cast<int64_t>(min(row, a.n - 1)) * kMaxTop;
-            const int slot0 = kTop > 0 ? ((sh.chunk * kHalves + half) * (kHalfCols / 32)) % a.top : 0;
-            float bound = row < a.n ? -INFINITY : INFINITY;  // no row: nothing to publish or list
             RowState<kTop> r;
-            r.clear(a.top);
+            r.clear(a.top, row < a.n);
+            if (kList) {
+                bp.words = a.bounds + static_cast<int64_t>(min(row, a.n - 1)) * kMaxTop;
+                bp.slot0 = ((sh.chunk * kHalves + half) * (kHalfCols / 32)) % kMaxTop;
+                bp.tag = ps + 1;
+                if (threadIdx.x == 0) *turn = ps + 1;
+            }
             for (int vt = sh.v0; vt < sh.v1; ++vt) {
                 float z[kHalfCols];
-                for (int k0 = 0; k0 < k_blocks; k0 += kPartBlocks, ++part) {
+                for (int k0 = 0; k0 < k_blocks; k0 += part_blocks, ++part) {
                     const int buf = part & 1;
                     if (!(ok = ptx::mbar_wait(acc_full + buf, (part >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT)))
                         break;
@@ -538,23 +598,60 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
                 if (!ok) break;
                 const int first_id = vt * kVocabTile + half * kHalfCols;
                 if (live && first_id < a.V)
-                    fold_tile<kTop>(r, z, first_id, a.V, c, target, zs, words, a.top, slot0, bound);
+                    fold_tile<kTop>(r, z, first_id, a.V, c, target, bp);
             }
             if (!ok) break;
             if (row < a.n) {
                 const int64_t cell = sh.cell + half * sh.half_step + static_cast<int>(rank) * kBlockRows + lane_row;
                 a.stat[cell] = make_float4(r.m, r.s, r.u, r.tz);
-                if constexpr (kTop > 0) {
 #pragma unroll
-                    for (int j = 0; j < kTop; ++j) {
-                        const int o = j - (kTop - a.top);
-                        if (o >= 0) a.best[cell * a.top + o] = make_int2(__float_as_int(r.v[j]), r.id[j]);
-                    }
+                for (int j = 0; j < kTop; ++j) {
+                    const int o = j - (kTop - a.top);
+                    if (o >= 0) a.best[cell * a.top + o] = make_int2(__float_as_int(r.v[j]), r.id[j]);
                 }
             }
         }
-    } else {
-        // the two warps that fill the last warpgroup
+        if (threadIdx.x == 0) *turn = -1;
+    } else if (kList) {
+        // ------------------------------------------------------------ bounds: warps 10 and 11, 64 rows each
+        // Reads the words of the rows that the states are at, again and again, until they are done.  A value
+        // that comes late is only looser.
+        ptx::grid_dep_wait();
+        int seen = 0;
+        uint64_t since = ptx::globaltimer_ns();
+        while (true) {
+            const int now = *turn;
+            if (now < 0 || *abort_flag) break;
+            if (now != seen) {
+                seen = now;
+                since = ptx::globaltimer_ns();
+            } else if (ptx::globaltimer_ns() - since > 10000000000ull) {
+                break;  // the states' own waits end long before
+            }
+            if (now > 0) {
+                const Share sh = share_of(a.plan, now - 1, worker);
+                const int first = (warp - 10) * 64;
+                const int row0 = sh.row_tile * a.plan.tile_rows + static_cast<int>(rank) * kBlockRows + first;
+                for (int i = 0; i < 64 && row0 + i < a.n; i += 4) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = row0 + i + j < a.n ? __ldcg(a.bounds + static_cast<int64_t>(row0 + i + j) * kMaxTop + lane) : 0u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = kth_largest(w[j], a.top);
+                    if (lane < 4) {
+                        const uint32_t b = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
+                        // one 8-byte store: a reader sees a bound with its own tag
+                        asm volatile("st.volatile.shared.v2.b32 [%0], {%1, %2};" ::"r"(
+                                         kept_bounds + (first + i + lane) * 8),
+                                     "r"(now), "r"(b)
+                                     : "memory");
+                    }
+                }
+            }
+            __nanosleep(1000);
+        }
+        __syncwarp();
     }
     __syncwarp();
     if (aligned && rank == 1 && warp == 0 && lane == 0) {
@@ -650,9 +747,7 @@ __global__ void __launch_bounds__(kRowThreads == 32 ? 128 : kRowThreads) logprob
         st[q] = l < lists ? __ldcg(a.stat + cell0 + l * step) : make_float4(-INFINITY, 0.f, 0.f, nan);
         head[q] = l < lists && top > 0 ? __ldcg(a.best + (cell0 + l * step) * top) : make_int2(0, kNoToken);
     }
-    // the smallest of the row's words (one per lane), as an order; 0: fewer than `top` products yet
-    uint32_t word = 0xFFFFFFFFu;
-    if (lane < top) word = __ldcg(a.bounds + static_cast<int64_t>(r) * kMaxTop + lane);
+    uint32_t word = top > 0 ? __ldcg(a.bounds + static_cast<int64_t>(r) * kMaxTop + lane) : 0u;
     if (t == 0) count_all[sub] = 0;
 
     float m = -INFINITY, tz = -INFINITY;
@@ -707,7 +802,7 @@ __global__ void __launch_bounds__(kRowThreads == 32 ? 128 : kRowThreads) logprob
         a.top_lp[static_cast<int64_t>(r) * top + place] =
             no ? nan : fmaf(of_order(static_cast<uint32_t>(key >> 32)), a.c, -l2) * kLn2;
     };
-    const unsigned long long bound = static_cast<unsigned long long>(__reduce_min_sync(0xFFFFFFFFu, word)) << 32;
+    const unsigned long long bound = static_cast<unsigned long long>(kth_largest(word, top)) << 32;
     row_sync<kRowThreads>();  // the count starts at zero
 #pragma unroll
     for (int q = 0; q < kMine; ++q) {
@@ -797,7 +892,7 @@ cudaError_t launch_logprob(const CUtensorMap &tm_h, const CUtensorMap &tm_w, con
         return cudaFuncGetAttributes(&fa, kern) == cudaSuccess && fa.numRegs * kThreadsLP >= kRegsNeeded;
     }();
     if (!fits) return cudaErrorLaunchOutOfResources;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LpLayout<kCtas>::kBytes);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -814,7 +909,7 @@ cudaError_t launch_logprob(const CUtensorMap &tm_h, const CUtensorMap &tm_w, con
     }
     cfg.gridDim = dim3(static_cast<unsigned>(a.plan.workers * kCtas));
     cfg.blockDim = dim3(kThreadsLP);
-    cfg.dynamicSmemBytes = LpLayout<kCtas>::kBytes;
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.smem_bytes);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = static_cast<unsigned>(na);
@@ -863,7 +958,7 @@ extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t h
     a.H = H;
     a.n = n;
     a.top = top;
-    a.a_rows = n < kBlockRows ? (n + 7) / 8 * 8 : kBlockRows;
+    lay_out(a);
     a.row_idx = d_row_idx;
     a.hidden_rows = hidden_rows;
     a.targets = d_targets;
