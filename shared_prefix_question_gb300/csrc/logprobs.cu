@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
                 const Share sh = share_of(a.plan, now - 1, worker);
                 const int first = (warp - 10) * 64;
                 const int row0 = sh.row_tile * a.plan.tile_rows + static_cast<int>(rank) * kBlockRows + first;
-                for (int i = 0; i < 64 && row0 + i < a.n; i += 4) {
+                for (int i = 0; i < 64 && row0 + i < a.n && *turn == now; i += 4) {
                     uint32_t w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
                     }
                 }
             }
-            __nanosleep(1000);
+            if (*turn == now) __nanosleep(500);
         }
         __syncwarp();
     }
