@@ -3,24 +3,27 @@
 //
 // Mathematics.  With lse known there is no running maximum: a term is 2^(c s - b), c = scale log2(e),
 // b = lse log2(e), one fused multiply-add and one exp2 per score, and the result is a plain sum over
-// query columns.  The scores are computed transposed, S = K Q^T with the keys as the M rows, so that a
-// key is a tensor-memory lane: the sum over columns stays inside one thread and needs no exchange.
+// columns, a column being a (row, query head of the group) pair.
 //
-// Work.  A unit is 256 keys (two M = 128 tiles) of one kv head; a column is (row, query head of the
-// group), up to 256 of them per column tile.  The (unit, column tile) steps, unit-major, are cut into
+// Layout.  S = Q K^T with 128 columns as the M rows of the product and 256 keys as its N.  So a thread
+// holds one column: its b is a register, and it keeps one partial sum per key (128 of them, in
+// registers) over all the column tiles it works through; the 128 threads of a tile are added up once, at
+// the end.  (With the keys as the M rows the sum over columns stays in a thread, but every score needs
+// its b from shared memory, which the tensor core's operand reads keep busy: 18k 1.37 ms.)
+//
+// Work.  A unit is 256 keys of one kv head.  The (unit, column tile) steps, unit-major, are cut into
 // equal consecutive ranges, one per block (one block per SM): every block does the same number of
 // steps whatever the shape.  A unit that one block covers is written by it; the pieces of a unit
 // that a range boundary cuts go to the workspace, and a second launch adds them in block order.  So
 // the order of every sum is fixed by the shapes and the number of SMs.
 //
-// Roles (352 threads): warp 8 TMA producer (K tiles and column tiles into two rings), warp 9 MMA issuer,
-// warp 10 bias loader (lse of the columns, as -b, into a ring beside the column tiles), warps 0-3 /
-// 4-7 the sums of key tile 0 / 1, one key per thread.
-// Tensor memory (512 columns): two sets of [key tile 0, key tile 1] x 128 columns.
+// Roles (384 threads): warps 0-3 / 4-7 the sums of keys 0-127 / 128-255 (232 registers a thread), warp 8
+// TMA producer (two buffers of 256 keys and a ring of column tiles), warp 9 MMA issuer (40 registers).
+// Tensor memory: two score tiles of 256 columns.
 //
-// Columns that do not count have -b = -inf, so their term is 0: columns past the last row (Q is zero
-// there) and rows owned by no question.  Only the latter may hold NaN or infinities in q; column tiles
-// that have any are summed with a select per column.
+// A column that does not count has -b = -inf, so its term is 0: rows past the last (Q is zero there) and
+// rows owned by no question.  Only the latter may hold NaN or infinities in q; a warp with such a row
+// sums with a select.
 #include <cstdint>
 
 #include "common.cuh"
@@ -29,21 +32,27 @@
 namespace blink {
 namespace {
 
-constexpr int kKeysPerTile = 128;
-constexpr int kUnitKeys = 2 * kKeysPerTile;
-constexpr int kMaxCols = 256;   // columns of a column tile
-constexpr int kSubCols = 128;   // columns of one product
-constexpr int kQSlots = 2;
-constexpr int kMaxKSlots = 8;
-constexpr int kThreadsKW = 352;
-constexpr int kProducer = 8, kIssuer = 9, kBias = 10;
+constexpr int kUnitKeys = 256;
+constexpr int kHalfKeys = 128;  // keys of one thread
+constexpr int kTileCols = 128;  // columns of a column tile
+constexpr int kThreadsKW = 384;
+constexpr int kProducer = 8, kIssuer = 9;
+constexpr int kRegsNeeded = 256 * 232 + 128 * 40;
 constexpr int kMaxBlocks = 256;
 constexpr uint32_t kTmem = 512;
-constexpr int kRingBytes = 224 * 1024;
-constexpr int kBiasOff = kRingBytes;
-constexpr int kBarOff = kBiasOff + kQSlots * kMaxCols * 4;
-constexpr int kSmemBytes = kBarOff + 384;
 constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct KwLayout {
+    static constexpr int kPanels = D / 64;
+    static constexpr int kKPanel = kUnitKeys * 128, kQPanel = kTileCols * 128;
+    static constexpr int kKBytes = kPanels * kKPanel, kQBytes = kPanels * kQPanel;
+    static constexpr int kKSlots = 2, kQSlots = D == 128 ? 3 : 6;
+    static constexpr int kQOff = kKSlots * kKBytes;
+    static constexpr int kSumOff = kQOff + kQSlots * kQBytes;  // [2][2][128] floats
+    static constexpr int kBarOff = kSumOff + 4 * kHalfKeys * 4;
+    static constexpr int kBytes = kBarOff + 256;
+};
 
 struct KeyWeightArgs {
     const float *lse;
@@ -54,8 +63,7 @@ struct KeyWeightArgs {
     int64_t w_stride;
     float *part;  // [blocks][2][kUnitKeys]
     int *err;
-    int rows, P, g, tpt, n_tiles, n_pairs, cols;  // tpt: rows per column tile; cols: columns per tile
-    int k_slots, q_slot_bytes;
+    int rows, P, g, tpt, n_tiles, n_units_head;  // tpt: rows per column tile; n_units_head: units of a kv head
     int64_t total;  // steps: units x column tiles
     float c, decay;
 };
@@ -70,11 +78,11 @@ __host__ __device__ __forceinline__ int64_t first_step(int64_t b, int64_t total,
 // role walks the same sequence.
 struct Segment {
     int64_t at, end;
-    int n_tiles, n_pairs;
+    int n_tiles, n_units_head;
     int head, key0, tile0, tiles;
     bool first, new_q;  // new_q: the column tile is not the one already in shared memory
     bool last_use;      // of a single column tile that the next segment shares
-    __device__ Segment(int64_t begin, int64_t e, int nt, int np) : at(begin), end(e), n_tiles(nt), n_pairs(np), first(true)
+    __device__ Segment(int64_t begin, int64_t e, int nt, int np) : at(begin), end(e), n_tiles(nt), n_units_head(np), first(true)
     {
         head = -1;
         load();
@@ -83,12 +91,12 @@ struct Segment {
     {
         if (at >= end) return;
         const int64_t unit = at / n_tiles;
-        const int h = static_cast<int>(unit / n_pairs);
-        key0 = static_cast<int>(unit - static_cast<int64_t>(h) * n_pairs) * kUnitKeys;
+        const int h = static_cast<int>(unit / n_units_head);
+        key0 = static_cast<int>(unit - static_cast<int64_t>(h) * n_units_head) * kUnitKeys;
         tile0 = static_cast<int>(at - unit * n_tiles);
         tiles = static_cast<int>(min(static_cast<int64_t>(n_tiles - tile0), end - at));
         new_q = n_tiles > 1 || h != head;
-        last_use = n_tiles > 1 || at + 1 >= end || (unit + 1) / n_pairs != h;
+        last_use = n_tiles > 1 || at + 1 >= end || (unit + 1) / n_units_head != h;
         head = h;
     }
     __device__ bool more() const { return at < end; }
@@ -100,51 +108,57 @@ struct Segment {
     }
 };
 
+// Adds acc[0 .. 127] over the 32 threads of a warp; thread l is left with keys 4 l .. 4 l + 3 in
+// acc[0 .. 3].  Each step a thread hands half of what it has to its partner.
+__device__ __forceinline__ void warp_sum_scatter(float (&acc)[kHalfKeys], int lane)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < 4 * o; ++i) {
+            const float give = upper ? acc[i] : acc[i + 4 * o];
+            const float keep = upper ? acc[i + 4 * o] : acc[i];
+            acc[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreadsKW, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const KeyWeightArgs a)
 {
+    using L = KwLayout<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr int kPanels = D / 64;
-    constexpr int kKTileBytes = kKeysPerTile * D * 2;
-    constexpr int kKPanelBytes = kKeysPerTile * 128;
-    uint8_t *k_ring = smem;
-    uint8_t *q_ring = smem + a.k_slots * kKTileBytes;
-    float *bias = reinterpret_cast<float *>(smem + kBiasOff);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kBarOff);
-    uint64_t *k_full = bars, *k_empty = bars + kMaxKSlots;
-    uint64_t *q_full = bars + 2 * kMaxKSlots, *q_empty = q_full + kQSlots;
-    uint64_t *b_full = q_empty + kQSlots, *b_empty = b_full + kQSlots;
-    uint64_t *s_full = b_empty + kQSlots, *s_empty = s_full + 4;  // [set][key tile]
-    uint64_t *mma_done = s_empty + 4;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
-    int *abort_word = reinterpret_cast<int *>(tmem_holder + 1);
-    int *slow = abort_word + 1;  // [kQSlots]: the tile has rows owned by no question
-    volatile int *abort_flag = abort_word;
-
     if (ptx::smem_u32(smem) & 1023u) {  // the swizzled tiles need it; the whole block leaves
         if (threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
         return;
     }
+    uint8_t *q_ring = smem + L::kQOff;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
+    uint64_t *k_full = bars, *k_empty = bars + 2, *q_full = bars + 4, *q_empty = bars + 10;
+    uint64_t *s_full = bars + 16, *s_empty = bars + 18, *mma_done = bars + 20, *met = bars + 21;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(met + 2);
+    int *abort_word = reinterpret_cast<int *>(tmem_holder + 1);
+    volatile int *abort_flag = abort_word;
+
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t begin = first_step(blockIdx.x, a.total, gridDim.x), end = first_step(blockIdx.x + 1, a.total, gridDim.x);
-    const int q_panel = a.cols * 128;
+    const int cols_used = a.g * a.tpt;
+    const int live_warps = (cols_used + 31) / 32;  // of four: the others have no column in any tile
 
     if (warp == kProducer && lane == 0) {
-        for (int i = 0; i < a.k_slots; ++i) {
+        for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(k_full + i, 1);
             ptx::mbar_init(k_empty + i, 1);
+            ptx::mbar_init(s_full + i, 1);
+            ptx::mbar_init(s_empty + i, 2 * live_warps);
+            ptx::mbar_init(met + i, live_warps);
         }
-        for (int i = 0; i < kQSlots; ++i) {
+        for (int i = 0; i < L::kQSlots; ++i) {
             ptx::mbar_init(q_full + i, 1);
             ptx::mbar_init(q_empty + i, 1);
-            ptx::mbar_init(b_full + i, 32);
-            ptx::mbar_init(b_empty + i, 8);
-        }
-        for (int i = 0; i < 4; ++i) {
-            ptx::mbar_init(s_full + i, 1);
-            ptx::mbar_init(s_empty + i, 4);
         }
         ptx::mbar_init(mma_done, 1);
         ptx::fence_mbar_init();
@@ -156,12 +170,11 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
         ptx::tmem_alloc(tmem_holder, kTmem);
         ptx::tmem_relinquish();
     }
-    // Columns past g * tpt are never copied: zero once, so that their scores are 0.
-    const int cols_used = a.g * a.tpt;
-    if (warp < 8 && cols_used < a.cols) {
-        const int pad = (a.cols - cols_used) * 128;
-        for (int s = 0; s < kQSlots * kPanels; ++s) {
-            uint8_t *dst = q_ring + (s / kPanels) * a.q_slot_bytes + (s % kPanels) * q_panel + cols_used * 128;
+    // Columns of the last live warp past g * tpt are never copied: zero once, so that their scores are 0.
+    if (warp < 8 && cols_used < live_warps * 32) {
+        const int pad = (live_warps * 32 - cols_used) * 128;
+        for (int s = 0; s < L::kQSlots * L::kPanels; ++s) {
+            uint8_t *dst = q_ring + s * L::kQPanel + cols_used * 128;
             for (int off = threadIdx.x * 16; off < pad; off += 256 * 16)
                 *reinterpret_cast<uint4 *>(dst + off) = make_uint4(0, 0, 0, 0);
         }
@@ -171,198 +184,178 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
+    // Registers by role: 128 threads at 40 and 256 at 232 are the 384 at 168 of the launch.
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
 
     if (warp == kProducer) {
         if (lane == 0) {
             int nk = 0, nq = 0;
             bool ok = true;
-            const uint32_t q_bytes = static_cast<uint32_t>(kPanels) * 64u * cols_used * 2u;
-            for (Segment sg(begin, end, a.n_tiles, a.n_pairs); ok && sg.more(); sg.next()) {
-                for (int t = 0; ok && t < 2; ++t, ++nk) {
-                    const int slot = nk % a.k_slots;
-                    // freed at the end of an earlier segment: the limit grows with a segment's length
-                    if (!(ok = ptx::mbar_wait(k_empty + slot, ((nk / a.k_slots) & 1) ^ 1, abort_flag, a.err,
-                                              BLINK_DEVICE_TIMEOUT, 1000000000ull + 20000ull * a.n_tiles)))
-                        break;
-                    ptx::mbar_arrive_expect_tx(k_full + slot, kKTileBytes);
-                    for (int p = 0; p < kPanels; ++p)
-                        ptx::tma_load_3d(k_ring + slot * kKTileBytes + p * kKPanelBytes, &tm_k, p * 64, sg.head,
-                                         sg.key0 + t * kKeysPerTile, k_full + slot);
-                }
+            const uint32_t q_bytes = static_cast<uint32_t>(L::kPanels) * 128u * cols_used;
+            for (Segment sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next(), ++nk) {
+                const int ks = nk & 1;
+                // freed at the end of an earlier segment: the limit grows with a segment's length
+                if (!(ok = ptx::mbar_wait(k_empty + ks, ((nk >> 1) & 1) ^ 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT,
+                                          1000000000ull + 20000ull * a.n_tiles)))
+                    break;
+                ptx::mbar_arrive_expect_tx(k_full + ks, L::kKBytes);
+                for (int p = 0; p < L::kPanels; ++p)
+                    ptx::tma_load_3d(smem + ks * L::kKBytes + p * L::kKPanel, &tm_k, p * 64, sg.head, sg.key0, k_full + ks);
                 for (int i = 0; ok && sg.new_q && i < sg.tiles; ++i, ++nq) {
-                    const int slot = nq % kQSlots;
-                    if (!(ok = ptx::mbar_wait(q_empty + slot, ((nq / kQSlots) & 1) ^ 1, abort_flag, a.err,
+                    const int qs = nq % L::kQSlots;
+                    if (!(ok = ptx::mbar_wait(q_empty + qs, ((nq / L::kQSlots) & 1) ^ 1, abort_flag, a.err,
                                               BLINK_DEVICE_TIMEOUT)))
                         break;
-                    ptx::mbar_arrive_expect_tx(q_full + slot, q_bytes);
-                    for (int p = 0; p < kPanels; ++p)
-                        ptx::tma_load_3d(q_ring + slot * a.q_slot_bytes + p * q_panel, &tm_q, p * 64, sg.head * a.g,
-                                         (sg.tile0 + i) * a.tpt, q_full + slot);
+                    ptx::mbar_arrive_expect_tx(q_full + qs, q_bytes);
+                    for (int p = 0; p < L::kPanels; ++p)
+                        ptx::tma_load_3d(q_ring + qs * L::kQBytes + p * L::kQPanel, &tm_q, p * 64, sg.head * a.g,
+                                         (sg.tile0 + i) * a.tpt, q_full + qs);
                 }
             }
             ptx::grid_launch_dependents();
             // every copy issued must have landed before the block may exit
             volatile int no_abort = 0;
-            for (int n = nk > a.k_slots ? nk - a.k_slots : 0; n < nk; ++n, no_abort = 0)
-                ptx::mbar_wait(k_full + n % a.k_slots, (n / a.k_slots) & 1, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
-            for (int n = nq > kQSlots ? nq - kQSlots : 0; n < nq; ++n, no_abort = 0)
-                ptx::mbar_wait(q_full + n % kQSlots, (n / kQSlots) & 1, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
+            for (int n = nk > 2 ? nk - 2 : 0; n < nk; ++n, no_abort = 0)
+                ptx::mbar_wait(k_full + (n & 1), (n >> 1) & 1, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
+            for (int n = nq > L::kQSlots ? nq - L::kQSlots : 0; n < nq; ++n, no_abort = 0)
+                ptx::mbar_wait(q_full + n % L::kQSlots, (n / L::kQSlots) & 1, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
         }
     } else if (warp == kIssuer) {
         if (lane == 0) {
-            const uint32_t kb = ptx::smem_u32(k_ring), qb = ptx::smem_u32(q_ring);
-            const int n_sub = a.cols > kSubCols ? 2 : 1;
-            const uint32_t idesc[2] = {ptx::idesc_bf16_f32(kKeysPerTile, a.cols > kSubCols ? kSubCols : a.cols, false),
-                                       ptx::idesc_bf16_f32(kKeysPerTile, a.cols > kSubCols ? a.cols - kSubCols : 32, false)};
+            constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTileCols, kUnitKeys, false);
+            const uint64_t desc0 = ptx::smem_desc_sw128(ptx::smem_u32(smem), 16, 1024);  // in units of 16 bytes
             int nk = 0, nq = -1, st = 0;
             bool ok = true;
-            for (Segment sg(begin, end, a.n_tiles, a.n_pairs); ok && sg.more(); sg.next(), nk += 2) {
-                const int ks[2] = {nk % a.k_slots, (nk + 1) % a.k_slots};
-                uint64_t kd[2][D / 16];
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        kd[t][kk] = ptx::smem_desc_sw128(kb + ks[t] * kKTileBytes + (kk >> 2) * kKPanelBytes + (kk & 3) * 32,
-                                                         16, 1024);
-                for (int i = 0; ok && i < sg.tiles; ++i) {
+            for (Segment sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next(), ++nk) {
+                const int ks = nk & 1;
+                if (!(ok = ptx::mbar_wait(k_full + ks, (nk >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
+                const uint64_t kd = desc0 + (ks * L::kKBytes >> 4);
+                for (int i = 0; i < sg.tiles; ++i, ++st) {
                     if (sg.new_q) ++nq;
-                    const int qs = nq % kQSlots;
-                    if (sg.new_q && !(ok = ptx::mbar_wait(q_full + qs, (nq / kQSlots) & 1, abort_flag, a.err,
+                    const int qs = nq % L::kQSlots;
+                    if (sg.new_q && !(ok = ptx::mbar_wait(q_full + qs, (nq / L::kQSlots) & 1, abort_flag, a.err,
                                                           BLINK_DEVICE_TIMEOUT)))
                         break;
-                    for (int sub = 0; ok && sub < n_sub; ++sub, ++st) {
-                        uint64_t qd[D / 16];
+                    const int buf = st & 1;
+                    if (!(ok = ptx::mbar_wait(s_empty + buf, ((st >> 1) & 1) ^ 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT)))
+                        break;
+                    ptx::tc_fence_after();
+                    const uint64_t qd = desc0 + ((L::kQOff + qs * L::kQBytes) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            qd[kk] = ptx::smem_desc_sw128(qb + qs * a.q_slot_bytes + (kk >> 2) * q_panel + sub * kSubCols * 128 +
-                                                              (kk & 3) * 32,
-                                                          16, 1024);
-                        for (int t = 0; t < 2; ++t) {
-                            if (i == 0 && sub == 0 &&
-                                !(ok = ptx::mbar_wait(k_full + ks[t], ((nk + t) / a.k_slots) & 1, abort_flag, a.err,
-                                                      BLINK_DEVICE_TIMEOUT)))
-                                break;
-                            const int buf = (st & 1) * 2 + t;
-                            if (!(ok = ptx::mbar_wait(s_empty + buf, ((st >> 1) & 1) ^ 1, abort_flag, a.err,
-                                                      BLINK_DEVICE_TIMEOUT)))
-                                break;
-                            ptx::tc_fence_after();
-                            if constexpr (D == 128) {
-                                ptx::mma_ss_x8(tmem + buf * kSubCols, kd[t], qd, idesc[sub], 0u);
-                            } else {
-#pragma unroll
-                                for (int kk = 0; kk < D / 16; ++kk)
-                                    ptx::mma_ss(tmem + buf * kSubCols, kd[t][kk], qd[kk], idesc[sub], kk > 0 ? 1u : 0u);
-                            }
-                            ptx::mma_commit(s_full + buf);
-                            if (i == sg.tiles - 1 && sub == n_sub - 1) ptx::mma_commit(k_empty + ks[t]);
-                        }
-                    }
-                    if (ok && sg.last_use) ptx::mma_commit(q_empty + qs);
+                    for (int p = 0; p < L::kPanels; ++p)
+                        ptx::mma_ss_x4(tmem + buf * kUnitKeys, qd + (p * L::kQPanel >> 4), kd + (p * L::kKPanel >> 4), idesc,
+                                       p > 0);
+                    ptx::mma_commit(s_full + buf);
+                    if (sg.last_use) ptx::mma_commit(q_empty + qs);
                 }
+                if (ok) ptx::mma_commit(k_empty + ks);
             }
             ptx::mma_commit(mma_done);  // every product issued must be complete before tensor memory is released
             volatile int no_abort = 0;
             ptx::mbar_wait(mma_done, 0, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
         }
-    } else if (warp == kBias) {
-        int off_t[kMaxCols / 32], off_h[kMaxCols / 32];
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int half = warp >> 2, wq = warp & 3;
+        if (wq < live_warps) {
+            // -------------------------------------------------------- sums: one column per thread
+            const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16) + half * kHalfKeys;
+            float *sums = reinterpret_cast<float *>(smem + L::kSumOff) + half * 2 * kHalfKeys;
+            const int col = wq * 32 + lane;
+            const int tok = col < cols_used ? col / a.g : 0x40000000;  // past every row
+            const int head_off = col % a.g;
+            const uint64_t cc = ptx::f32x2(a.c, a.c);
+            int st = 0, meetings = 0;
+            bool ok = true;
+            for (Segment sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next()) {
+                const float *lse = a.lse + (sg.head * a.g + head_off) * a.lse_stride;
+                auto lse_of = [&](int tile) {
+                    const int t0 = tile * a.tpt;
+                    return tile < sg.tile0 + sg.tiles && tok < a.rows - t0 ? __ldg(lse + t0 + tok) : INFINITY;
+                };
+                float acc[kHalfKeys];
 #pragma unroll
-        for (int j = 0; j < kMaxCols / 32; ++j) {
-            const int c = lane + 32 * j;
-            off_t[j] = c < cols_used ? c / a.g : 0x40000000;  // past every row
-            off_h[j] = c % a.g;
-        }
-        int nq = 0;
-        bool ok = true;
-        for (Segment sg(begin, end, a.n_tiles, a.n_pairs); ok && sg.more(); sg.next()) {
-            for (int i = 0; ok && sg.new_q && i < sg.tiles; ++i, ++nq) {
-                const int t0 = (sg.tile0 + i) * a.tpt;
-                float v[kMaxCols / 32];
-                bool dead = false;
-#pragma unroll
-                for (int j = 0; j < kMaxCols / 32; ++j) {
-                    const bool valid = off_t[j] < a.rows - t0;
-                    v[j] = valid ? __ldg(a.lse + (sg.head * a.g + off_h[j]) * a.lse_stride + t0 + off_t[j]) : INFINITY;
-                }
-                const int slot = nq % kQSlots;
-                if (!(ok = ptx::mbar_wait(b_empty + slot, ((nq / kQSlots) & 1) ^ 1, abort_flag, a.err,
-                                          BLINK_DEVICE_TIMEOUT)))
-                    break;
-#pragma unroll
-                for (int j = 0; j < kMaxCols / 32; ++j) {
-                    dead = dead || v[j] == -INFINITY;
-                    bias[slot * kMaxCols + lane + 32 * j] = v[j] == -INFINITY ? -INFINITY : -v[j] * kLog2e;
-                }
-                const bool any = __any_sync(0xFFFFFFFFu, dead);
-                if (lane == 0) slow[slot] = any;
-                ptx::mbar_arrive(b_full + slot);
-            }
-        }
-    } else {
-        // ------------------------------------------------------------ sums: one key per thread
-        const int t = warp >> 2;
-        const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const int key_off = t * kKeysPerTile + (warp & 3) * 32 + lane;
-        const int n_sub = a.cols > kSubCols ? 2 : 1;
-        const float c = a.c;
-        int nq = -1, st = 0;
-        bool ok = true;
-        for (Segment sg(begin, end, a.n_tiles, a.n_pairs); ok && sg.more(); sg.next()) {
-            float sum = 0.f;
-            for (int i = 0; ok && i < sg.tiles; ++i) {
-                if (sg.new_q) ++nq;
-                const int slot = nq % kQSlots;
-                if (sg.new_q && !(ok = ptx::mbar_wait(b_full + slot, (nq / kQSlots) & 1, abort_flag, a.err,
-                                                      BLINK_DEVICE_TIMEOUT)))
-                    break;
-                const bool careful = slow[slot] != 0;
-                for (int sub = 0; sub < n_sub; ++sub, ++st) {
-                    const int buf = (st & 1) * 2 + t;
+                for (int i = 0; i < kHalfKeys; ++i) acc[i] = 0.f;
+                float next = lse_of(sg.tile0), after = lse_of(sg.tile0 + 1);  // two tiles ahead of their use
+                for (int i = 0; i < sg.tiles; ++i, ++st) {
+                    const float b = next;
+                    next = after;
+                    after = lse_of(sg.tile0 + i + 2);
+                    const bool dead = b == -INFINITY;  // owned by no question: q may hold anything
+                    const float nb = dead ? -INFINITY : -b * kLog2e;
+                    const bool careful = __any_sync(0xFFFFFFFFu, dead);
+                    const uint64_t nb2 = ptx::f32x2(nb, nb);
+                    const int buf = st & 1;
                     if (!(ok = ptx::mbar_wait(s_full + buf, (st >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
                     ptx::tc_fence_after();
-                    const float *bs = bias + slot * kMaxCols + sub * kSubCols;
-                    const int cols = min(kSubCols, a.cols - sub * kSubCols);
-                    float s0 = 0.f, s1 = 0.f;
-                    for (int c0 = 0; c0 < cols; c0 += 32) {
+#pragma unroll
+                    for (int q = 0; q < kHalfKeys / 32; ++q) {
                         uint32_t raw[32];
-                        ptx::tmem_ld32(trow + buf * kSubCols + c0, raw);
+                        ptx::tmem_ld32(trow + buf * kUnitKeys + q * 32, raw);
                         ptx::tmem_wait_ld();
+                        if (q == kHalfKeys / 32 - 1) {  // the tile is in registers: its buffer may be written
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(s_empty + buf);
+                        }
                         if (!careful) {
 #pragma unroll
                             for (int j = 0; j < 32; j += 2) {
-                                const float2 b = *reinterpret_cast<const float2 *>(bs + c0 + j);
-                                s0 += ptx::ex2(fmaf(__uint_as_float(raw[j]), c, b.x));
-                                s1 += ptx::ex2(fmaf(__uint_as_float(raw[j + 1]), c, b.y));
+                                float x0, x1;
+                                ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])),
+                                                                cc, nb2),
+                                                 x0, x1);
+                                const uint64_t s2 = ptx::add_f32x2(ptx::f32x2(acc[q * 32 + j], acc[q * 32 + j + 1]),
+                                                                   ptx::f32x2(ptx::ex2(x0), ptx::ex2(x1)));
+                                ptx::f32x2_split(s2, acc[q * 32 + j], acc[q * 32 + j + 1]);
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float b = bs[c0 + j];
-                                s0 += b == -INFINITY ? 0.f : ptx::ex2(fmaf(__uint_as_float(raw[j]), c, b));
-                            }
+                            for (int j = 0; j < 32; ++j)
+                                acc[q * 32 + j] += dead ? 0.f : ptx::ex2(fmaf(__uint_as_float(raw[j]), a.c, nb));
                         }
                     }
-                    sum += s0 + s1;
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(s_empty + buf);
                 }
-                __syncwarp();
-                if (ok && sg.last_use && lane == 0) ptx::mbar_arrive(b_empty + slot);
-            }
-            if (!ok) break;
-            const int key = sg.key0 + key_off;
-            if (sg.tiles == a.n_tiles) {
-                if (key < a.P)
-                    a.w[sg.head * a.w_stride + key] =
-                        a.decay > 0.f ? fmaf(a.decay, a.prev[sg.head * a.prev_stride + key], sum) : sum;
-            } else {
-                a.part[(static_cast<int64_t>(blockIdx.x) * 2 + (sg.first ? 0 : 1)) * kUnitKeys + key_off] = sum;
+                if (!ok) break;
+                warp_sum_scatter(acc, lane);
+                float4 s = make_float4(acc[0], acc[1], acc[2], acc[3]);  // keys 4 lane .. 4 lane + 3 of this half
+                if (live_warps > 1) {
+                    // ((w0 + w2) + (w1 + w3)): the live warps of the half, two at a time through shared memory
+                    auto meet = [&] {
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(met + half);
+                        ok = ok && ptx::mbar_wait(met + half, meetings & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT);
+                        ++meetings;
+                    };
+                    float4 *dst = reinterpret_cast<float4 *>(sums + (wq & 1) * kHalfKeys) + lane;
+                    auto add = [&](const float4 &o) { s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w; };
+                    if (wq >= 2) *dst = s;
+                    meet();
+                    if (wq < 2 && wq + 2 < live_warps) add(*dst);
+                    meet();
+                    if (wq == 1) *dst = s;
+                    meet();
+                    if (wq == 0) add(*(dst + kHalfKeys / 4));
+                    meet();  // the buffers are free again
+                }
+                if (ok && wq == 0) {
+                    const float v[4] = {s.x, s.y, s.z, s.w};
+                    const int key = sg.key0 + half * kHalfKeys + 4 * lane;
+                    if (sg.tiles == a.n_tiles) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (key + i < a.P)
+                                a.w[sg.head * a.w_stride + key + i] =
+                                    a.decay > 0.f ? fmaf(a.decay, a.prev[sg.head * a.prev_stride + key + i], v[i]) : v[i];
+                    } else {
+                        float *part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (sg.first ? 0 : 1)) * kUnitKeys;
+                        *reinterpret_cast<float4 *>(part + half * kHalfKeys + 4 * lane) = s;
+                    }
+                }
             }
         }
     }
+    __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -377,8 +370,8 @@ __global__ void __launch_bounds__(kUnitKeys) key_weights_join_kernel(const KeyWe
     const int b0 = static_cast<int>(((lo + 1) * blocks - 1) / a.total);  // the block that has step lo
     const int b1 = static_cast<int>((hi * blocks - 1) / a.total);        // and step hi - 1
     if (b0 == b1) return;
-    const int head = blockIdx.x / a.n_pairs;
-    const int key = (blockIdx.x - head * a.n_pairs) * kUnitKeys + threadIdx.x;
+    const int head = blockIdx.x / a.n_units_head;
+    const int key = (blockIdx.x - head * a.n_units_head) * kUnitKeys + threadIdx.x;
     if (key >= a.P) return;
     float sum = 0.f;
     for (int b = b0; b <= b1; ++b) {
@@ -394,6 +387,25 @@ int sm_count()
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
     return sms;
+}
+
+template <int D>
+cudaError_t launch_key_weights(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const KeyWeightArgs &a, unsigned blocks,
+                               cudaStream_t stream)
+{
+    auto kern = key_weights_kernel<D>;
+    // The split of registers by role has to fit the registers of the launch: checked once.
+    static const bool fits = [kern] {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, kern) == cudaSuccess && fa.numRegs * kThreadsKW >= kRegsNeeded;
+    }();
+    if (!fits) return cudaErrorLaunchOutOfResources;
+    // all 512 tensor-memory columns: one block per SM, which the shared memory keeps so for d = 64 too
+    constexpr int kSmem = KwLayout<D>::kBytes > 120 * 1024 ? KwLayout<D>::kBytes : 120 * 1024;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<blocks, kThreadsKW, kSmem, stream>>>(tm_q, tm_k, a);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -432,15 +444,10 @@ extern "C" blink_status blink_prefix_key_weights(const blink_bf16 *q, const blin
 
     KeyWeightArgs a{};
     a.g = Hq / Hkv;
-    a.tpt = kMaxCols / a.g < rows ? kMaxCols / a.g : rows;
+    a.tpt = kTileCols / a.g < rows ? kTileCols / a.g : rows;
     a.n_tiles = (rows + a.tpt - 1) / a.tpt;
-    a.n_pairs = (P + kUnitKeys - 1) / kUnitKeys;
-    a.cols = a.n_tiles > 1 ? kMaxCols : (a.g * a.tpt + 31) / 32 * 32;  // read from tensor memory 32 at a time
-    a.q_slot_bytes = a.cols * d * 2;
-    const int k_tile = kKeysPerTile * d * 2;
-    a.k_slots = (kRingBytes - kQSlots * a.q_slot_bytes) / k_tile;
-    if (a.k_slots > kMaxKSlots) a.k_slots = kMaxKSlots;
-    a.total = static_cast<int64_t>(Hkv) * a.n_pairs * a.n_tiles;
+    a.n_units_head = (P + kUnitKeys - 1) / kUnitKeys;
+    a.total = static_cast<int64_t>(Hkv) * a.n_units_head * a.n_tiles;
     const int sms = sm_count();
     if (sms < 1) return BLINK_CUDA_ERROR;
     int64_t blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
@@ -463,19 +470,17 @@ extern "C" blink_status blink_prefix_key_weights(const blink_bf16 *q, const blin
     const uint64_t e = 2;
     if (!encode_tmap_3d_bf16(&tm_q, q, d, Hq, rows, d * e, static_cast<uint64_t>(Hq) * d * e, 64, a.g, a.tpt) ||
         !encode_tmap_3d_bf16(&tm_k, k_pre, d, Hkv, P, d * e, static_cast<uint64_t>(pre_row_stride) * e, 64, 1,
-                             kKeysPerTile))
+                             kUnitKeys))
         return BLINK_CUDA_ERROR;
-    auto kern = d == 128 ? key_weights_kernel<128> : key_weights_kernel<64>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
-        return BLINK_CUDA_ERROR;
-    kern<<<static_cast<unsigned>(blocks), kThreadsKW, kSmemBytes, stream>>>(tm_q, tm_k, a);
-    if (cudaGetLastError() != cudaSuccess) return BLINK_CUDA_ERROR;
+    const cudaError_t err = d == 128 ? launch_key_weights<128>(tm_q, tm_k, a, static_cast<unsigned>(blocks), stream)
+                                     : launch_key_weights<64>(tm_q, tm_k, a, static_cast<unsigned>(blocks), stream);
+    if (err != cudaSuccess) return BLINK_CUDA_ERROR;
     if (a.n_tiles == 1) return BLINK_OK;  // a unit of one step is never cut
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(Hkv * a.n_pairs));
+    cfg.gridDim = dim3(static_cast<unsigned>(Hkv * a.n_units_head));
     cfg.blockDim = dim3(kUnitKeys);
     cfg.stream = stream;
     cfg.attrs = attr;
