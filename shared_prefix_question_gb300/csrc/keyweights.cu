@@ -6,7 +6,7 @@
 // columns, a column being a (row, query head of the group) pair.
 //
 // Layout.  S = Q K^T with 128 columns as the M rows of the product and 256 keys as its N.  So a thread
-// holds one column: its b is a register, and it keeps one partial sum per key (128 of them, in
+// holds one column: its b is a register, and it keeps one partial sum per key (64 of them, in
 // registers) over all the column tiles it works through; the 128 threads of a tile are added up once, at
 // the end.  (With the keys as the M rows the sum over columns stays in a thread, but every score needs
 // its b from shared memory, which the tensor core's operand reads keep busy: 18k 1.37 ms.)
@@ -17,9 +17,12 @@
 // that a range boundary cuts go to the workspace, and a second launch adds them in block order.  So
 // the order of every sum is fixed by the shapes and the number of SMs.
 //
-// Roles (384 threads): warps 0-3 / 4-7 the sums of keys 0-127 / 128-255 (232 registers a thread), warp 8
-// TMA producer (two buffers of 256 keys and a ring of column tiles), warp 9 MMA issuer (40 registers).
-// Tensor memory: two score tiles of 256 columns.
+// Roles (640 threads): warps 0-15 the sums, four warps (the 128 columns) for each 64 of the keys (112
+// registers a thread), warp 16 TMA producer (two buffers of 256 keys and a ring of column tiles), warp 17
+// MMA issuer (32 registers).  Tensor memory: two score tiles of 256 columns.
+// What bounds it: a tile is 1,024 cycles of the tensor core and 1,024 of the exp2 unit (8 lanes a clock on
+// each of the SM's four partitions, measured), so the four warps of a partition have to keep one
+// unit busy while others wait for scores.  Two warps with 128 keys each took 1,590 cycles a tile.
 //
 // A column that does not count has -b = -inf, so its term is 0: rows past the last (Q is zero there) and
 // rows owned by no question.  Only the latter may hold NaN or infinities in q; a warp with such a row
@@ -33,11 +36,12 @@ namespace blink {
 namespace {
 
 constexpr int kUnitKeys = 256;
-constexpr int kHalfKeys = 128;  // keys of one thread
+constexpr int kThreadKeys = 64;  // keys of one thread
+constexpr int kSumWarps = 16;
 constexpr int kTileCols = 128;  // columns of a column tile
-constexpr int kThreadsKW = 384;
-constexpr int kProducer = 8, kIssuer = 9;
-constexpr int kRegsNeeded = 256 * 232 + 128 * 40;
+constexpr int kThreadsKW = 640;
+constexpr int kProducer = 16, kIssuer = 17;
+constexpr int kRegsNeeded = 512 * 112 + 128 * 32;
 constexpr int kMaxBlocks = 256;
 constexpr uint32_t kTmem = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -49,8 +53,8 @@ struct KwLayout {
     static constexpr int kKBytes = kPanels * kKPanel, kQBytes = kPanels * kQPanel;
     static constexpr int kKSlots = 2, kQSlots = D == 128 ? 3 : 6;
     static constexpr int kQOff = kKSlots * kKBytes;
-    static constexpr int kSumOff = kQOff + kQSlots * kQBytes;  // [2][2][128] floats
-    static constexpr int kBarOff = kSumOff + 4 * kHalfKeys * 4;
+    static constexpr int kSumOff = kQOff + kQSlots * kQBytes;  // [4][2][64] floats
+    static constexpr int kBarOff = kSumOff + 8 * kThreadKeys * 4;
     static constexpr int kBytes = kBarOff + 256;
 };
 
@@ -108,17 +112,17 @@ struct Segment {
     }
 };
 
-// Adds acc[0 .. 127] over the 32 threads of a warp; thread l is left with keys 4 l .. 4 l + 3 in
-// acc[0 .. 3].  Each step a thread hands half of what it has to its partner.
-__device__ __forceinline__ void warp_sum_scatter(float (&acc)[kHalfKeys], int lane)
+// Adds acc[0 .. 63] over the 32 threads of a warp; thread l is left with keys 2 l and 2 l + 1 in acc[0]
+// and acc[1].  Each step a thread hands half of what it has to its partner.
+__device__ __forceinline__ void warp_sum_scatter(float (&acc)[kThreadKeys], int lane)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const bool upper = (lane & o) != 0;
 #pragma unroll
-        for (int i = 0; i < 4 * o; ++i) {
-            const float give = upper ? acc[i] : acc[i + 4 * o];
-            const float keep = upper ? acc[i + 4 * o] : acc[i];
+        for (int i = 0; i < 2 * o; ++i) {
+            const float give = upper ? acc[i] : acc[i + 2 * o];
+            const float keep = upper ? acc[i + 2 * o] : acc[i];
             acc[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
         }
     }
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
     uint64_t *k_full = bars, *k_empty = bars + 2, *q_full = bars + 4, *q_empty = bars + 10;
     uint64_t *s_full = bars + 16, *s_empty = bars + 18, *mma_done = bars + 20, *met = bars + 21;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(met + 2);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(met + 4);
     int *abort_word = reinterpret_cast<int *>(tmem_holder + 1);
     volatile int *abort_flag = abort_word;
 
@@ -153,9 +157,9 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
             ptx::mbar_init(k_full + i, 1);
             ptx::mbar_init(k_empty + i, 1);
             ptx::mbar_init(s_full + i, 1);
-            ptx::mbar_init(s_empty + i, 2 * live_warps);
-            ptx::mbar_init(met + i, live_warps);
+            ptx::mbar_init(s_empty + i, 4 * live_warps);
         }
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(met + i, live_warps);
         for (int i = 0; i < L::kQSlots; ++i) {
             ptx::mbar_init(q_full + i, 1);
             ptx::mbar_init(q_empty + i, 1);
@@ -171,11 +175,11 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
         ptx::tmem_relinquish();
     }
     // Columns of the last live warp past g * tpt are never copied: zero once, so that their scores are 0.
-    if (warp < 8 && cols_used < live_warps * 32) {
+    if (warp < kSumWarps && cols_used < live_warps * 32) {
         const int pad = (live_warps * 32 - cols_used) * 128;
         for (int s = 0; s < L::kQSlots * L::kPanels; ++s) {
             uint8_t *dst = q_ring + s * L::kQPanel + cols_used * 128;
-            for (int off = threadIdx.x * 16; off < pad; off += 256 * 16)
+            for (int off = threadIdx.x * 16; off < pad; off += kSumWarps * 32 * 16)
                 *reinterpret_cast<uint4 *>(dst + off) = make_uint4(0, 0, 0, 0);
         }
         ptx::fence_proxy_async_smem();
@@ -184,8 +188,8 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    // Registers by role: 128 threads at 40 and 256 at 232 are the 384 at 168 of the launch.
-    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    // Registers by role: 128 threads at 32 and 512 at 112 are the 640 at 96 of the launch.
+    if (warp >= kSumWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
 
     if (warp == kProducer) {
         if (lane == 0) {
@@ -254,13 +258,13 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
             volatile int no_abort = 0;
             ptx::mbar_wait(mma_done, 0, &no_abort, a.err, BLINK_DEVICE_TIMEOUT);
         }
-    } else if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        const int half = warp >> 2, wq = warp & 3;
+    } else if (warp < kSumWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+        const int quarter = warp >> 2, wq = warp & 3;  // of the unit's keys, of the tile's columns
         if (wq < live_warps) {
             // -------------------------------------------------------- sums: one column per thread
-            const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16) + half * kHalfKeys;
-            float *sums = reinterpret_cast<float *>(smem + L::kSumOff) + half * 2 * kHalfKeys;
+            const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16) + quarter * kThreadKeys;
+            float *sums = reinterpret_cast<float *>(smem + L::kSumOff) + quarter * 2 * kThreadKeys;
             const int col = wq * 32 + lane;
             const int tok = col < cols_used ? col / a.g : 0x40000000;  // past every row
             const int head_off = col % a.g;
@@ -273,9 +277,9 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                     const int t0 = tile * a.tpt;
                     return tile < sg.tile0 + sg.tiles && tok < a.rows - t0 ? __ldg(lse + t0 + tok) : INFINITY;
                 };
-                float acc[kHalfKeys];
+                float acc[kThreadKeys];
 #pragma unroll
-                for (int i = 0; i < kHalfKeys; ++i) acc[i] = 0.f;
+                for (int i = 0; i < kThreadKeys; ++i) acc[i] = 0.f;
                 float next = lse_of(sg.tile0), after = lse_of(sg.tile0 + 1);  // two tiles ahead of their use
                 for (int i = 0; i < sg.tiles; ++i, ++st) {
                     const float b = next;
@@ -289,11 +293,11 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                     if (!(ok = ptx::mbar_wait(s_full + buf, (st >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
                     ptx::tc_fence_after();
 #pragma unroll
-                    for (int q = 0; q < kHalfKeys / 32; ++q) {
+                    for (int q = 0; q < kThreadKeys / 32; ++q) {
                         uint32_t raw[32];
                         ptx::tmem_ld32(trow + buf * kUnitKeys + q * 32, raw);
                         ptx::tmem_wait_ld();
-                        if (q == kHalfKeys / 32 - 1) {  // the tile is in registers: its buffer may be written
+                        if (q == kThreadKeys / 32 - 1) {  // the tile is in registers: its buffer may be written
                             ptx::tc_fence_before();
                             __syncwarp();
                             if (lane == 0) ptx::mbar_arrive(s_empty + buf);
@@ -318,38 +322,38 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                 }
                 if (!ok) break;
                 warp_sum_scatter(acc, lane);
-                float4 s = make_float4(acc[0], acc[1], acc[2], acc[3]);  // keys 4 lane .. 4 lane + 3 of this half
+                float2 s = make_float2(acc[0], acc[1]);  // keys 2 lane and 2 lane + 1 of this quarter
                 if (live_warps > 1) {
-                    // ((w0 + w2) + (w1 + w3)): the live warps of the half, two at a time through shared memory
+                    // ((w0 + w2) + (w1 + w3)): the live warps of the quarter, two at a time through shared memory
                     auto meet = [&] {
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(met + half);
-                        ok = ok && ptx::mbar_wait(met + half, meetings & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT);
+                        if (lane == 0) ptx::mbar_arrive(met + quarter);
+                        ok = ok && ptx::mbar_wait(met + quarter, meetings & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT);
                         ++meetings;
                     };
-                    float4 *dst = reinterpret_cast<float4 *>(sums + (wq & 1) * kHalfKeys) + lane;
-                    auto add = [&](const float4 &o) { s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w; };
+                    float2 *dst = reinterpret_cast<float2 *>(sums + (wq & 1) * kThreadKeys) + lane;
+                    auto add = [&](const float2 &o) { s.x += o.x, s.y += o.y; };
                     if (wq >= 2) *dst = s;
                     meet();
                     if (wq < 2 && wq + 2 < live_warps) add(*dst);
                     meet();
                     if (wq == 1) *dst = s;
                     meet();
-                    if (wq == 0) add(*(dst + kHalfKeys / 4));
+                    if (wq == 0) add(*(dst + kThreadKeys / 2));
                     meet();  // the buffers are free again
                 }
                 if (ok && wq == 0) {
-                    const float v[4] = {s.x, s.y, s.z, s.w};
-                    const int key = sg.key0 + half * kHalfKeys + 4 * lane;
+                    const float v[2] = {s.x, s.y};
+                    const int key = sg.key0 + quarter * kThreadKeys + 2 * lane;
                     if (sg.tiles == a.n_tiles) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < 2; ++i)
                             if (key + i < a.P)
                                 a.w[sg.head * a.w_stride + key + i] =
                                     a.decay > 0.f ? fmaf(a.decay, a.prev[sg.head * a.prev_stride + key + i], v[i]) : v[i];
                     } else {
                         float *part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (sg.first ? 0 : 1)) * kUnitKeys;
-                        *reinterpret_cast<float4 *>(part + half * kHalfKeys + 4 * lane) = s;
+                        *reinterpret_cast<float2 *>(part + quarter * kThreadKeys + 2 * lane) = s;
                     }
                 }
             }
