@@ -367,7 +367,7 @@ blink_status blink_label_readout_noalloc(const blink_bf16 *hidden, int64_t hidde
  * weights of that kv head NaN.  lse must not be smaller than the scores it normalises by more than
  * 80 (an attention's own lse never is).
  *
- * q       [rows, Hq, d] bf16, rows >= 1 (one row: a single decoded token)
+ * q       [rows, Hq, d] bf16, rows in 1..2^30 (one row: a single decoded token)
  * k_pre   [P, Hkv, d]   bf16 rows pre_row_stride elements apart, as for the attention; P in 1..131072
  * lse     fp32 natural-log log-sum-exp, head h at lse + h * lse_stride (lse_stride >= rows), so the
  *         rows of one request can be passed as a slice of a larger launch

@@ -366,14 +366,13 @@ def blink_rotation_debias(logits, pass_off, key_of_pos, question_pass, raw_off, 
 INT32_MAX = 2**31 - 1
 
 
-def _need(name, t, dtype, shape=None, inner: int = 1):
-    """`t` is a CUDA tensor of `dtype` (and `shape`, where given: None leaves a size free) whose last
-    `inner` dimensions are contiguous."""
+def _refuse(name, t, dtype, shape, inner):
+    """Raises what is wrong with `t` (see _need)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape))):
+    if t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     want = 1
     for s, st in list(zip(t.shape, t.stride()))[::-1][:inner]:
@@ -382,9 +381,23 @@ def _need(name, t, dtype, shape=None, inner: int = 1):
         want *= s
 
 
+def _need(name, t, dtype, shape, inner: int = 1):
+    """`t` is a CUDA tensor of `dtype` and `shape` (None leaves a size free) whose last `inner`
+    dimensions are contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _refuse(name, t, dtype, shape, inner)
+
+
 def _row_stride(t) -> int:
     """Elements between the rows (first dimension) of `t`; a single row has any stride."""
-    return int(t.stride(0)) if t.shape[0] > 1 else int(t[0].numel())
+    return t.stride(0) if t.shape[0] > 1 else t[0].numel()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream's handle, without an object
 
 
 class _Launch:
@@ -392,42 +405,48 @@ class _Launch:
     current one.  What the call allocates belongs to that stream, and its inputs are marked as used on
     it, so a caller that passes another stream than its tensors' own may drop them after the call."""
 
-    def __init__(self, stream, *tensors):
-        ts = [t for t in tensors if t is not None]
-        self.device = ts[0].device
-        if any(t.device != self.device for t in ts):
-            raise ValueError("tensors passed to one call must be on one device")
-        self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if self.stream.device != self.device:
+    __slots__ = ("device", "handle", "_contexts")
+
+    def __init__(self, stream, first, *others):
+        index = first.get_device()
+        for t in others:
+            if t is not None and t.get_device() != index:
+                raise ValueError("tensors passed to one call must be on one device")
+        self.device = first.device
+        self._contexts = None
+        if stream is None and index == torch.cuda.current_device():
+            self.handle = _raw_stream(index) if _raw_stream else torch.cuda.current_stream().cuda_stream
+            return
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device != self.device:
             raise ValueError("the stream belongs to another device than the tensors")
-        self.tensors = ts
-        self.explicit = stream is not None
+        else:
+            with torch.cuda.stream(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+            for t in () if capturing else (first, *others):
+                if t is not None:
+                    t.record_stream(stream)
+        self.handle = stream.cuda_stream
+        self._contexts = (torch.cuda.device(self.device), torch.cuda.stream(stream))
 
     def __enter__(self):
-        self._dev = torch.cuda.device(self.device)
-        self._str = torch.cuda.stream(self.stream)
-        self._dev.__enter__()
-        self._str.__enter__()
-        if self.explicit and not torch.cuda.is_current_stream_capturing():
-            for t in self.tensors:
-                t.record_stream(self.stream)
+        for c in self._contexts or ():
+            c.__enter__()
         return self
 
     def __exit__(self, *exc):
-        self._str.__exit__(*exc)
-        self._dev.__exit__(*exc)
+        for c in reversed(self._contexts or ()):
+            c.__exit__(*exc)
 
-    def workspace(self, ws, nbytes: int):
-        """`ws`, or a new workspace whose header (all that has to start at zero) is cleared."""
-        if ws is None:
-            ws = torch.empty(max(256, (nbytes + 255) // 256 * 256), dtype=torch.uint8, device=self.device)
-            ws[:256].zero_()
+    def empty(self, dtype, *shape):
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, nbytes: int):
+        """A new workspace whose header (all that has to start at zero) is cleared."""
+        ws = self.empty(torch.uint8, max(256, (nbytes + 255) // 256 * 256))
+        ws[:256].zero_()
         return ws
-
-
-def _need_ws(ws):
-    if ws is not None:
-        _need("ws", ws, torch.uint8, (None,))
 
 
 def key_weights_workspace_bytes(rows, P, Hq, Hkv, d) -> int:
@@ -440,24 +459,26 @@ def blink_prefix_key_weights(q, k_pre, lse, prev=None, decay: float = 0.0, scale
     of k_pre may be strided: an arena region), lse [Hq, rows] fp32 from blink_prefix_tail_attention
     (a slice of a wider one is fine).  Returns (weights [Hkv, P] fp32, ws); with `prev` and `decay` > 0
     decay * prev is added (`out=prev` accumulates in place)."""
-    _need("q", q, torch.bfloat16, (None, None, None), inner=3)
+    _need("q", q, torch.bfloat16, q.shape if getattr(q, "ndim", 0) == 3 else (None,) * 3, inner=3)
     rows, Hq, d = q.shape
-    _need("k_pre", k_pre, torch.bfloat16, (None, None, d), inner=2)
-    P, Hkv = k_pre.shape[:2]
+    P, Hkv = k_pre.shape[:2] if getattr(k_pre, "ndim", 0) == 3 else (None, None)
+    _need("k_pre", k_pre, torch.bfloat16, (P, Hkv, d), inner=2)
     _need("lse", lse, torch.float32, (Hq, rows))
     if prev is not None:
         _need("prev", prev, torch.float32, (Hkv, P))
     if out is not None:
         _need("out", out, torch.float32, (Hkv, P))
-    _need_ws(ws)
+    if ws is not None:
+        _need("ws", ws, torch.uint8, (ws.numel(),))
     with _Launch(stream, q, k_pre, lse, prev, out, ws) as call:
         if out is None:
-            out = torch.empty(Hkv, P, dtype=torch.float32, device=q.device)
-        ws = call.workspace(ws, key_weights_workspace_bytes(rows, P, Hq, Hkv, d))
+            out = call.empty(torch.float32, Hkv, P)
+        if ws is None:
+            ws = call.workspace(key_weights_workspace_bytes(rows, P, Hq, Hkv, d))
         st = lib().blink_prefix_key_weights(
-            _ptr(q), _ptr(k_pre), _row_stride(k_pre), _ptr(lse), _row_stride(lse), int(rows), int(P), int(Hq), int(Hkv),
-            int(d), float(scale), float(decay), _ptr(prev), _row_stride(prev) if prev is not None else 0, _ptr(out),
-            _row_stride(out), _ptr(ws), ws.numel(), _stream(call.stream))
+            q.data_ptr(), k_pre.data_ptr(), _row_stride(k_pre) if P else 0, lse.data_ptr(), _row_stride(lse), rows, P, Hq, Hkv,
+            d, scale, decay, _addr(prev), 0 if prev is None else _row_stride(prev), out.data_ptr(), _row_stride(out),
+            ws.data_ptr(), ws.numel(), call.handle)
     _check(st, "blink_prefix_key_weights")
     return out, ws
 
@@ -473,10 +494,10 @@ def blink_kv_evict(weights, k, v, keep: int, pos=None, sink: int = 0, recent_fro
     Without k_dst / v_dst the regions are compacted in place into their first `keep` rows; with them the
     kept rows are written there.  weights_dst / pos_dst may be views of weights / pos (in place).
     Returns {"slots", "k", "v", "weights", "pos", "ws"}, all of `keep` keys per head."""
-    _need("weights", weights, torch.float32, (None, None))
-    Hkv, P = weights.shape
-    _need("k", k, torch.bfloat16, (P, Hkv, None), inner=2)
-    d = k.shape[2]
+    Hkv, P = weights.shape if getattr(weights, "ndim", 0) == 2 else (None, None)
+    _need("weights", weights, torch.float32, (Hkv, P))
+    d = k.shape[2] if getattr(k, "ndim", 0) == 3 else None
+    _need("k", k, torch.bfloat16, (P, Hkv, d), inner=2)
     _need("v", v, torch.bfloat16, (P, Hkv, d), inner=2)
     keep = int(keep)
     if not 1 <= keep <= P:
@@ -485,36 +506,42 @@ def blink_kv_evict(weights, k, v, keep: int, pos=None, sink: int = 0, recent_fro
         _need("pos", pos, torch.int32, (Hkv, P))
     if (k_dst is None) != (v_dst is None):
         raise ValueError("k_dst and v_dst go together")
-    if _row_stride(k) != _row_stride(v) and P > 1:
+    src_stride = _row_stride(k)
+    if P > 1 and v.stride(0) != src_stride:
         raise ValueError("k and v must have the same row stride")
-    k_out = k[:keep] if k_dst is None else k_dst
-    v_out = v[:keep] if v_dst is None else v_dst
-    _need("k_dst", k_out, torch.bfloat16, (keep, Hkv, d), inner=2)
-    _need("v_dst", v_out, torch.bfloat16, (keep, Hkv, d), inner=2)
-    dst_stride = _row_stride(k) if k_dst is None else _row_stride(k_out)
-    if k_dst is not None and keep > 1 and _row_stride(v_out) != dst_stride:
-        raise ValueError("k_dst and v_dst must have the same row stride")
-    for name, t, dt in (("weights_dst", weights_dst, torch.float32), ("pos_dst", pos_dst, torch.int32),
-                        ("slots", slots, torch.int32)):
-        if t is not None:
-            _need(name, t, dt, (Hkv, keep), inner=2 if name == "slots" else 1)
-    _need_ws(ws)
+    in_place = k_dst is None
+    if in_place:
+        k_dst, v_dst, dst_stride = k[:keep], v[:keep], src_stride
+    else:
+        _need("k_dst", k_dst, torch.bfloat16, (keep, Hkv, d), inner=2)
+        _need("v_dst", v_dst, torch.bfloat16, (keep, Hkv, d), inner=2)
+        dst_stride = _row_stride(k_dst)
+        if keep > 1 and v_dst.stride(0) != dst_stride:
+            raise ValueError("k_dst and v_dst must have the same row stride")
+    if weights_dst is not None:
+        _need("weights_dst", weights_dst, torch.float32, (Hkv, keep))
+    if pos_dst is not None:
+        _need("pos_dst", pos_dst, torch.int32, (Hkv, keep))
+    if slots is not None:
+        _need("slots", slots, torch.int32, (Hkv, keep), inner=2)
+    if ws is not None:
+        _need("ws", ws, torch.uint8, (ws.numel(),))
     with _Launch(stream, weights, k, v, pos, k_dst, v_dst, weights_dst, pos_dst, slots, ws) as call:
-        dev = weights.device
         if slots is None:
-            slots = torch.empty(Hkv, keep, dtype=torch.int32, device=dev)
+            slots = call.empty(torch.int32, Hkv, keep)
         if weights_dst is None:
-            weights_dst = torch.empty(Hkv, keep, dtype=torch.float32, device=dev)
+            weights_dst = call.empty(torch.float32, Hkv, keep)
         if pos_dst is None:
-            pos_dst = torch.empty(Hkv, keep, dtype=torch.int32, device=dev)
-        ws = call.workspace(ws, kv_evict_workspace_bytes(P, keep, Hkv))
+            pos_dst = call.empty(torch.int32, Hkv, keep)
+        if ws is None:
+            ws = call.workspace(kv_evict_workspace_bytes(P, keep, Hkv))
         st = lib().blink_kv_evict(
-            _ptr(weights), _row_stride(weights), _ptr(pos), _row_stride(pos) if pos is not None else 0, int(P), keep,
-            int(sink), INT32_MAX if recent_from is None else int(recent_from), int(Hkv), int(d), _ptr(k), _ptr(v),
-            _row_stride(k), _ptr(k_out), _ptr(v_out), dst_stride, _ptr(slots), _ptr(weights_dst),
-            _row_stride(weights_dst), _ptr(pos_dst), _row_stride(pos_dst), _ptr(ws), ws.numel(), _stream(call.stream))
+            weights.data_ptr(), _row_stride(weights), _addr(pos), 0 if pos is None else _row_stride(pos), P, keep, sink,
+            INT32_MAX if recent_from is None else recent_from, Hkv, d, k.data_ptr(), v.data_ptr(), src_stride,
+            k_dst.data_ptr(), v_dst.data_ptr(), dst_stride, slots.data_ptr(), weights_dst.data_ptr(), _row_stride(weights_dst),
+            pos_dst.data_ptr(), _row_stride(pos_dst), ws.data_ptr(), ws.numel(), call.handle)
     _check(st, "blink_kv_evict")
-    return {"slots": slots, "k": k_out, "v": v_out, "weights": weights_dst, "pos": pos_dst, "ws": ws}
+    return {"slots": slots, "k": k_dst, "v": v_dst, "weights": weights_dst, "pos": pos_dst, "ws": ws}
 
 
 # ------------------------------------------------------------------------------------------------ whole vocabulary
@@ -528,28 +555,29 @@ def blink_token_logprobs(hidden, unembed, targets=None, row_idx=None, temperatur
     against unembed [V, H] bf16.  Returns {"logprob" (of int32 `targets`, else None), "entropy", "lse",
     "top_ids", "top_logprobs" ([n, top], None for top = 0), "ws"}; nothing is copied to the host.
     Device-side problems (a bad row index or target) are read with blink_read_device_status(ws)."""
-    _need("hidden", hidden, torch.bfloat16, (None, None))
-    rows, H = hidden.shape
-    _need("unembed", unembed, torch.bfloat16, (None, H), inner=2)
-    V = unembed.shape[0]
+    rows, H = hidden.shape if getattr(hidden, "ndim", 0) == 2 else (None, None)
+    _need("hidden", hidden, torch.bfloat16, (rows, H))
+    V = unembed.shape[0] if getattr(unembed, "ndim", 0) == 2 else None
+    _need("unembed", unembed, torch.bfloat16, (V, H), inner=2)
+    n = rows
     if row_idx is not None:
-        _need("row_idx", row_idx, torch.int32, (None,))
-    n = rows if row_idx is None else row_idx.numel()
+        n = row_idx.numel()
+        _need("row_idx", row_idx, torch.int32, (n,))
     if targets is not None:
         _need("targets", targets, torch.int32, (n,))
-    _need_ws(ws)
+    if ws is not None:
+        _need("ws", ws, torch.uint8, (ws.numel(),))
     top = int(top)
     with _Launch(stream, hidden, unembed, targets, row_idx, ws) as call:
-        def new(dtype, *shape):
-            return torch.empty(*shape, dtype=dtype, device=hidden.device)
-        r = {"logprob": new(torch.float32, n) if targets is not None else None, "entropy": new(torch.float32, n),
-             "lse": new(torch.float32, n), "top_ids": new(torch.int32, n, top) if top > 0 else None,
-             "top_logprobs": new(torch.float32, n, top) if top > 0 else None}
-        ws = call.workspace(ws, token_logprobs_workspace_bytes(n, H, V, top))
+        f32 = torch.float32
+        logprob = None if targets is None else call.empty(f32, n)
+        entropy, lse = call.empty(f32, n), call.empty(f32, n)
+        ids, lps = (call.empty(torch.int32, n, top), call.empty(f32, n, top)) if top > 0 else (None, None)
+        if ws is None:
+            ws = call.workspace(token_logprobs_workspace_bytes(n, H, V, top))
         st = lib().blink_token_logprobs(
-            _ptr(hidden), _row_stride(hidden) if rows else int(H), int(rows), _ptr(row_idx), _ptr(unembed), int(V), int(H), _ptr(targets),
-            int(n), float(temperature), top, _ptr(r["logprob"]), _ptr(r["entropy"]), _ptr(r["lse"]), _ptr(r["top_ids"]),
-            _ptr(r["top_logprobs"]), _ptr(ws), ws.numel(), _stream(call.stream))
+            hidden.data_ptr(), _row_stride(hidden) if rows else H, rows, _addr(row_idx), unembed.data_ptr(), V, H,
+            _addr(targets), n, temperature, top, _addr(logprob), entropy.data_ptr(), lse.data_ptr(), _addr(ids), _addr(lps),
+            ws.data_ptr(), ws.numel(), call.handle)
     _check(st, "blink_token_logprobs")
-    r["ws"] = ws
-    return r
+    return {"logprob": logprob, "entropy": entropy, "lse": lse, "top_ids": ids, "top_logprobs": lps, "ws": ws}

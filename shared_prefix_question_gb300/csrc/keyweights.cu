@@ -26,7 +26,7 @@
 //
 // A column that does not count has -b = -inf, so its term is 0: rows past the last (Q is zero there) and
 // rows owned by no question.  Only the latter may hold NaN or infinities in q; a warp with such a row
-// sums with a select.
+// clears its scores first.
 #include <cstdint>
 
 #include "common.cuh"
@@ -266,25 +266,28 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
             const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16) + quarter * kThreadKeys;
             float *sums = reinterpret_cast<float *>(smem + L::kSumOff) + quarter * 2 * kThreadKeys;
             const int col = wq * 32 + lane;
-            const int tok = col < cols_used ? col / a.g : 0x40000000;  // past every row
+            const int tok = col / a.g;
             const int head_off = col % a.g;
             const uint64_t cc = ptx::f32x2(a.c, a.c);
             int st = 0, meetings = 0;
             bool ok = true;
             for (Segment sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next()) {
                 const float *lse = a.lse + (sg.head * a.g + head_off) * a.lse_stride;
-                auto lse_of = [&](int tile) {
-                    const int t0 = tile * a.tpt;
-                    return tile < sg.tile0 + sg.tiles && tok < a.rows - t0 ? __ldg(lse + t0 + tok) : INFINITY;
+                int at = sg.tile0 * a.tpt + tok;  // this column's row in the tile to be read next
+                const int last = col < cols_used ? min(a.rows, (sg.tile0 + sg.tiles) * a.tpt) : 0;  // 0: no column
+                auto lse_next = [&] {
+                    const float v = at < last ? __ldg(lse + at) : INFINITY;
+                    at += a.tpt;
+                    return v;
                 };
                 float acc[kThreadKeys];
 #pragma unroll
                 for (int i = 0; i < kThreadKeys; ++i) acc[i] = 0.f;
-                float next = lse_of(sg.tile0), after = lse_of(sg.tile0 + 1);  // two tiles ahead of their use
+                float next = lse_next(), after = lse_next();  // two tiles ahead of their use
                 for (int i = 0; i < sg.tiles; ++i, ++st) {
                     const float b = next;
                     next = after;
-                    after = lse_of(sg.tile0 + i + 2);
+                    after = lse_next();
                     const bool dead = b == -INFINITY;  // owned by no question: q may hold anything
                     const float nb = dead ? -INFINITY : -b * kLog2e;
                     const bool careful = __any_sync(0xFFFFFFFFu, dead);
@@ -302,21 +305,18 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                             __syncwarp();
                             if (lane == 0) ptx::mbar_arrive(s_empty + buf);
                         }
-                        if (!careful) {
+                        if (careful) {  // such a row's scores become 0, and with -b = -inf its terms
 #pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                float x0, x1;
-                                ptx::f32x2_split(ptx::fma_f32x2(ptx::f32x2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])),
-                                                                cc, nb2),
-                                                 x0, x1);
-                                const uint64_t s2 = ptx::add_f32x2(ptx::f32x2(acc[q * 32 + j], acc[q * 32 + j + 1]),
-                                                                   ptx::f32x2(ptx::ex2(x0), ptx::ex2(x1)));
-                                ptx::f32x2_split(s2, acc[q * 32 + j], acc[q * 32 + j + 1]);
-                            }
-                        } else {
+                            for (int j = 0; j < 32; ++j) raw[j] = dead ? 0u : raw[j];
+                        }
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                acc[q * 32 + j] += dead ? 0.f : ptx::ex2(fmaf(__uint_as_float(raw[j]), a.c, nb));
+                        for (int j = 0; j < 32; j += 2) {
+                            float x0, x1;
+                            ptx::f32x2_split(
+                                ptx::fma_f32x2(ptx::f32x2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])), cc, nb2), x0, x1);
+                            const uint64_t s2 = ptx::add_f32x2(ptx::f32x2(acc[q * 32 + j], acc[q * 32 + j + 1]),
+                                                               ptx::f32x2(ptx::ex2(x0), ptx::ex2(x1)));
+                            ptx::f32x2_split(s2, acc[q * 32 + j], acc[q * 32 + j + 1]);
                         }
                     }
                 }
@@ -432,7 +432,7 @@ extern "C" blink_status blink_prefix_key_weights(const blink_bf16 *q, const blin
     if (!q || !k_pre || !lse || !d_weights || !d_ws) return BLINK_INVALID_ARG;
     if (rows < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 128 || (d != 64 && d != 128))
         return BLINK_INVALID_ARG;
-    if (P < 1 || P > BLINK_MAX_INPUT_TOKENS || Hkv > 65535) return BLINK_OUT_OF_RANGE;
+    if (P < 1 || P > BLINK_MAX_INPUT_TOKENS || Hkv > 65535 || rows > (1 << 30)) return BLINK_OUT_OF_RANGE;
     if (!(decay >= 0.f) || !(decay < INFINITY) || (decay > 0.f && !d_prev)) return BLINK_INVALID_ARG;
     if (scale != scale || scale == INFINITY) return BLINK_INVALID_ARG;
     if (pre_row_stride < static_cast<int64_t>(Hkv) * d || pre_row_stride % 8 != 0) return BLINK_INVALID_ARG;
