@@ -414,8 +414,8 @@ blink_status blink_prefix_key_weights(const blink_bf16 *q, const blink_bf16 *k_p
  * d_weights_dst, d_pos_dst  optional outputs [Hkv][keep] (row strides wd_stride, pd_stride): weights
  *             and positions of the kept keys; each may be its input itself with the same stride, or
  *             memory that overlaps neither input
- * d_ws        workspace of blink_kv_evict_workspace(...) bytes; not shared by calls that may run at
- *             the same time
+ * d_ws        workspace of blink_kv_evict_workspace(...) bytes (the error word; nothing on the device
+ *             can fail in this call)
  * Errors: BLINK_INVALID_ARG (null, alignment, strides, overlap), BLINK_OUT_OF_RANGE (P, keep, Hkv, d),
  * BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR.
  * ------------------------------------------------------------------------------------------ */

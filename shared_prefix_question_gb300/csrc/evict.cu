@@ -1,18 +1,25 @@
-// evict.cu -- eviction of a cached prefix's lightest keys: per kv head the `keep` best of P keys are
-// selected by accumulated attention weight, and the arena region is compacted to slots [0, keep).
+// evict.cu -- eviction of a cached prefix's lightest keys (blink_kv_evict): per kv head the `keep` best of
+// P keys are selected by accumulated attention weight, and the arena region is compacted to slots
+// [0, keep).
 //
 // Selection.  Each weight becomes a 32-bit key whose unsigned order is the order of the keys
 // (protected keys above every weight, NaN below); the keep-th largest key T is found by a radix
-// select over 11 + 11 + 10 bits.  Kept are the keys above T and, of those equal to T, the lowest slots.
+// select over four digits of 8 bits, which stops early when all keys of the digit found are kept.  Kept
+// are the keys above T and, of those equal to T, the lowest slots.
 // One thread-block cluster per head, its blocks holding consecutive pieces of the head's keys in
 // shared memory: the weights are read once, the per-block histograms are summed through distributed
-// shared memory, and no global counter or atomic order enters the result.
+// shared memory, and no global counter or atomic order enters the result.  A few thousand keys take a
+// block microseconds either way, so what it costs is the chain of barriers and remote reads: digits
+// are small (with 2048 bins the blocks read 64 KB of one another's histograms a digit, 4 us), one warp
+// joins them, and there is nothing in global memory between the steps.
 //
 // Compaction.  Kept keys below slot `keep` stay; the r-th evicted slot below `keep` (a hole) takes the
 // r-th kept slot at `keep` or above (a survivor).  Sources are never destinations, so the moves of
-// an in-place compaction need no order among themselves.
+// an in-place compaction need no order among themselves.  The selection writes each slot's source; a second
+// launch, its programmatic dependent, moves keys, values, weights and positions.
 #include <cooperative_groups.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "common.cuh"
@@ -23,20 +30,21 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048;
+constexpr int kDigits = 4, kBins = 256;
 constexpr int kMaxPiece = (BLINK_MAX_INPUT_TOKENS + kMaxCluster - 1) / kMaxCluster;  // keys of one block
-constexpr int kMaxSteps = kMaxPiece / kSelThreads;                                    // 32-key steps of a warp
+constexpr int kClusterPiece = 8192;  // keys per block before a head gets more blocks (4096 and 16384 measure the same or slower)
+constexpr int kLoadAhead = 8;
 
 struct EvictArgs {
     const float *w;
     const int32_t *pos;  // or nullptr: slot = position
     int64_t w_stride, pos_stride;
-    int P, keep, sink, recent_from, Hkv, piece;  // piece: keys per block, a multiple of kSelThreads
-    int32_t *slots;                              // [Hkv][keep]
-    int32_t *holes, *survivors;                  // [Hkv][min(keep, P - keep)]
+    int P, keep, sink, recent_from;
+    int piece;       // keys per block, a multiple of kSelThreads
+    int32_t *slots;  // [Hkv][keep]
 };
 
 // Larger weight = larger unsigned; NaN = 1, so that 0 is below every key and ~0 above.
@@ -47,40 +55,42 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ bool is_protected(const EvictArgs &a, int head, int slot)
-{
-    const int p = a.pos ? __ldg(a.pos + head * a.pos_stride + slot) : slot;
-    return p < a.sink || p >= a.recent_from;
-}
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xFFFFFFFFu, v); }
 
-// Sum over the block of one value per thread (every thread gets it).
-__device__ __forceinline__ int block_sum(int v, int *warp_tot)
+// Sum of the lanes before this one.
+__device__ __forceinline__ int sum_before(int v, int lane)
 {
+    int run = v;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if ((threadIdx.x & 31) == 0) warp_tot[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int t = warp_tot[threadIdx.x & 31];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    __syncthreads();
-    return t;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, run, o);
+        if (lane >= o) run += up;
+    }
+    return run - v;
 }
 
 struct PieceCounts {  // of one block's or one warp's keys: above T and equal to T, slots below `keep` and not
     int gt_low, gt_high, eq_low, eq_high, n_low;
 };
 
+// With `eq_before` keys equal to T in lower slots: holes and survivors among the counted keys.
+__device__ __forceinline__ int2 holes_and_survivors(const PieceCounts &c, int eq_before, int need)
+{
+    const int take_low = max(0, min(c.eq_low, need - eq_before));
+    const int take_high = max(0, min(c.eq_high, need - eq_before - c.eq_low));
+    return make_int2(c.n_low - c.gt_low - take_low, c.gt_high + take_high);
+}
+
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictArgs a)
 {
-    extern __shared__ uint32_t keys[];  // [piece]
-    __shared__ uint32_t hist[3][kBins];
-    __shared__ int warp_tot[kSelWarps];
+    extern __shared__ uint32_t keys[];  // [piece], then the survivors' slots [piece]
+    __shared__ __align__(16) uint32_t hist[kDigits][kBins];
     __shared__ PieceCounts warp_cnt[kSelWarps];
     __shared__ PieceCounts block_cnt;
     __shared__ int n_protected;
     __shared__ uint32_t found_digit;
-    __shared__ int found_rest;
+    __shared__ int found_rest, found_count;
+    __shared__ bool too_many;
 
     cg::cluster_group cluster = cg::this_cluster();
     const int C = static_cast<int>(cluster.num_blocks());
@@ -90,146 +100,183 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     const int n = max(0, min(a.P - lo, a.piece));  // this block's keys: slots [lo, lo + n)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int steps = a.piece / kSelThreads;
-    // Warp w owns the consecutive keys [w * piece / 32, ...), 32 at a step, so ballots give slot order.
+    const uint32_t below = (1u << lane) - 1u;
+    int32_t *surv_list = reinterpret_cast<int32_t *>(keys + a.piece);
+    // Warp w owns the consecutive keys [w * piece / warps, ...), 32 at a step, so ballots give slot order.
     const int wbase = warp * (a.piece / kSelWarps);
+    auto sync_all = [&] {
+        if (C > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
+    ptx::grid_launch_dependents();
 
-    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0u;
     const float *w = a.w + head * a.w_stride;
-    uint32_t guard = 0u;
-    int n_guard = 0;
-    const bool guarded = a.sink > 0 || a.recent_from < 0x7FFFFFFF;
-    for (int s = 0; s < steps; ++s) {
-        const int i = wbase + s * 32 + lane;
-        uint32_t key = 0u;
-        if (i < n) {
-            key = weight_key(__ldg(w + lo + i));
-            if (guarded && is_protected(a, head, lo + i)) {
-                guard |= 1u << s;
-                ++n_guard;
+    const int32_t *pos = a.pos ? a.pos + head * a.pos_stride : nullptr;
+    const bool guarded = a.sink > 0 || a.recent_from < INT_MAX;
+    // Fills keys[]; returns how many of this thread's keys are protected.  `among_them`: only protected
+    // keys are candidates (there are more than `keep`); otherwise protected keys come before all others.
+    auto load_keys = [&](bool among_them) {
+        int n_guard = 0;
+        for (int s0 = 0; s0 < steps; s0 += kLoadAhead) {
+            float x[kLoadAhead];
+            int p[kLoadAhead];
+#pragma unroll
+            for (int u = 0; u < kLoadAhead; ++u) {
+                const int i = wbase + (s0 + u) * 32 + lane;
+                const bool in = s0 + u < steps && i < n;
+                x[u] = in ? __ldg(w + lo + i) : 0.f;
+                p[u] = in && guarded ? (pos ? __ldg(pos + lo + i) : lo + i) : INT_MAX;
+            }
+#pragma unroll
+            for (int u = 0; u < kLoadAhead; ++u) {
+                const int i = wbase + (s0 + u) * 32 + lane;
+                if (s0 + u >= steps) break;
+                const bool g = guarded && i < n && (p[u] < a.sink || p[u] >= a.recent_from);
+                n_guard += g;
+                uint32_t key = weight_key(x[u]);
+                if (among_them)
+                    key = g ? key : 0u;
+                else if (g)
+                    key = 0xFFFFFFFFu;
+                keys[i] = i < n ? key : 0u;
             }
         }
-        keys[i] = key;
-    }
-    if (guarded) {
-        n_guard = block_sum(n_guard, warp_tot);
-        if (tid == 0) n_protected = n_guard;
-        cluster.sync();
-        int total = 0;
-        for (int c = 0; c < C; ++c) total += *cluster.map_shared_rank(&n_protected, c);
-        // More protected keys than `keep`: the selection is among them alone.  Else they are all kept.
-        for (int s = 0; s < steps; ++s) {
-            const int i = wbase + s * 32 + lane;
-            const bool g = (guard >> s) & 1u;
-            if (total > a.keep) {
-                if (!g) keys[i] = 0u;
-            } else if (g) {
-                keys[i] = 0xFFFFFFFFu;
-            }
-        }
+        return n_guard;
+    };
+    auto zero_hists = [&] {
+        for (int i = tid; i < kDigits * kBins; i += kSelThreads) (&hist[0][0])[i] = 0u;
+    };
+
+    if (tid == 0) n_protected = 0;
+    zero_hists();
+    __syncthreads();
+    {
+        const int g = warp_sum(load_keys(false));
+        if (lane == 0 && g > 0) atomicAdd(&n_protected, g);
     }
     __syncthreads();
 
     // ---- radix select of the keep-th largest key
     uint32_t prefix = 0u, mask = 0u;
     int want = a.keep;  // rank of the key looked for among those that match the prefix
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t digit_mask = pass == 2 ? 1023u : 2047u;
-        uint32_t *h = hist[pass];
-        for (int s = 0; s < steps; ++s) {
-            const int i = wbase + s * 32 + lane;
-            const uint32_t key = keys[i];
-            const bool in = i < n && (key & mask) == prefix;
-            const uint32_t bin = (key >> shift) & digit_mask;
-            const uint32_t act = __ballot_sync(0xFFFFFFFFu, in);
-            if (act == 0u) continue;
-            // a whole step in one bin (equal weights): one atomic instead of 32 on one address
-            const uint32_t bin0 = __shfl_sync(0xFFFFFFFFu, bin, __ffs(act) - 1);
-            if (__all_sync(0xFFFFFFFFu, !in || bin == bin0)) {
-                if (lane == 0) atomicAdd(h + bin0, static_cast<uint32_t>(__popc(act)));
-            } else if (in) {
-                atomicAdd(h + bin, 1u);
+    bool among = false;
+    for (int pass = 0; pass < kDigits; ++pass) {
+        const int shift = 24 - 8 * pass;
+        for (int s0 = 0; s0 < steps; s0 += kLoadAhead) {
+            uint32_t key[kLoadAhead];
+#pragma unroll
+            for (int u = 0; u < kLoadAhead; ++u) key[u] = s0 + u < steps ? keys[wbase + (s0 + u) * 32 + lane] : 0u;
+#pragma unroll
+            for (int u = 0; u < kLoadAhead; ++u)  // no key in range is 0, and padding is
+                if (key[u] != 0u && (key[u] & mask) == prefix)
+                    atomicAdd(&hist[pass][(key[u] >> shift) & 255u], 1u);
+        }
+        sync_all();
+        if (warp == 0) {
+            // lane l: bins 255 - 8 l down to 248 - 8 l, summed over the blocks
+            const int b0 = kBins - 8 - 8 * lane;
+            uint4 part[kMaxCluster][2];
+            int guards = 0;
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) {
+                part[c][0] = part[c][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (c < C) {
+                    const uint4 *h = reinterpret_cast<const uint4 *>(cluster.map_shared_rank(hist[pass], c) + b0);
+                    part[c][0] = h[0];
+                    part[c][1] = h[1];
+                    if (pass == 0 && guarded) guards += *cluster.map_shared_rank(&n_protected, c);
+                }
             }
-        }
-        cluster.sync();
-        // bins in descending order, two per thread: cluster-wide counts and their running sum
-        const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
-        int c1 = 0, c0 = 0;
-        for (int c = 0; c < C; ++c) {
-            const uint32_t *rh = cluster.map_shared_rank(h, c);
-            const uint2 v = *reinterpret_cast<const uint2 *>(rh + b0);
-            c0 += static_cast<int>(v.x);
-            c1 += static_cast<int>(v.y);
-        }
-        int run = c0 + c1;
+            int cnt[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // of bins b0 + 7, ..., b0
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xFFFFFFFFu, run, o);
-            if (lane >= o) run += up;
-        }
-        if (lane == 31) warp_tot[warp] = run;
-        __syncthreads();
-        int before = lane < warp ? warp_tot[lane] : 0;
+            for (int c = 0; c < kMaxCluster; ++c) {
+                cnt[0] += static_cast<int>(part[c][1].w);
+                cnt[1] += static_cast<int>(part[c][1].z);
+                cnt[2] += static_cast<int>(part[c][1].y);
+                cnt[3] += static_cast<int>(part[c][1].x);
+                cnt[4] += static_cast<int>(part[c][0].w);
+                cnt[5] += static_cast<int>(part[c][0].z);
+                cnt[6] += static_cast<int>(part[c][0].y);
+                cnt[7] += static_cast<int>(part[c][0].x);
+            }
+            int mine = 0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-        run += before;                      // keys in bins >= b0
-        const int above1 = run - c0 - c1;   // keys in bins > b1
-        if (above1 < want && want <= above1 + c1) {
-            found_digit = static_cast<uint32_t>(b1);
-            found_rest = want - above1;
-        } else if (above1 + c1 < want && want <= run) {
-            found_digit = static_cast<uint32_t>(b0);
-            found_rest = want - above1 - c1;
+            for (int q = 0; q < 8; ++q) mine += cnt[q];
+            int above = sum_before(mine, lane);  // keys in the bins above this lane's
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (above < want && want <= above + cnt[q]) {
+                    found_digit = static_cast<uint32_t>(b0 + 7 - q);
+                    found_rest = want - above;
+                    found_count = cnt[q];
+                }
+                above += cnt[q];
+            }
+            if (lane == 0) too_many = !among && guards > a.keep;
         }
         __syncthreads();
+        if (pass == 0 && guarded && too_many) {
+            // More protected keys than `keep` (seldom): again, among them alone.
+            among = true;
+            sync_all();  // every block has read the histograms
+            zero_hists();
+            load_keys(true);
+            __syncthreads();
+            pass = -1;
+            continue;
+        }
         prefix |= found_digit << shift;
-        mask |= digit_mask << shift;
+        mask |= 255u << shift;
         want = found_rest;
-        __syncthreads();
+        const bool done = want == found_count;  // every key with this prefix is kept: T is the lowest it could be
+        if (done) {
+            want = INT_MAX;
+            break;
+        }
     }
     const uint32_t T = prefix;
     const int need = want;  // how many of the keys equal to T are kept: the lowest slots
 
     // ---- counts per warp and block, then every warp's place in the slot order
     PieceCounts my = {0, 0, 0, 0, 0};
+#pragma unroll 8
     for (int s = 0; s < steps; ++s) {
         const int i = wbase + s * 32 + lane;
         const uint32_t key = keys[i];
         const bool in = i < n, low = lo + i < a.keep;
-        my.gt_low += __popc(__ballot_sync(0xFFFFFFFFu, in && low && key > T));
-        my.gt_high += __popc(__ballot_sync(0xFFFFFFFFu, in && !low && key > T));
-        my.eq_low += __popc(__ballot_sync(0xFFFFFFFFu, in && low && key == T));
-        my.eq_high += __popc(__ballot_sync(0xFFFFFFFFu, in && !low && key == T));
-        my.n_low += __popc(__ballot_sync(0xFFFFFFFFu, in && low));
+        my.gt_low += in && low && key > T;
+        my.gt_high += in && !low && key > T;
+        my.eq_low += in && low && key == T;
+        my.eq_high += in && !low && key == T;
+        my.n_low += in && low;
     }
+    my = {warp_sum(my.gt_low), warp_sum(my.gt_high), warp_sum(my.eq_low), warp_sum(my.eq_high), warp_sum(my.n_low)};
     if (lane == 0) warp_cnt[warp] = my;
     __syncthreads();
-    if (tid == 0) {
-        PieceCounts t = {0, 0, 0, 0, 0};
-        for (int i = 0; i < kSelWarps; ++i) {
-            t.gt_low += warp_cnt[i].gt_low;
-            t.gt_high += warp_cnt[i].gt_high;
-            t.eq_low += warp_cnt[i].eq_low;
-            t.eq_high += warp_cnt[i].eq_high;
-            t.n_low += warp_cnt[i].n_low;
-        }
-        block_cnt = t;
+    const PieceCounts none = {0, 0, 0, 0, 0};
+    const PieceCounts wc = lane < kSelWarps ? warp_cnt[lane] : none;  // lane l: warp l
+    if (warp == 0) {
+        const PieceCounts t = {warp_sum(wc.gt_low), warp_sum(wc.gt_high), warp_sum(wc.eq_low), warp_sum(wc.eq_high),
+                               warp_sum(wc.n_low)};
+        if (lane == 0) block_cnt = t;
     }
-    cluster.sync();
-    int eq_before = 0, hole = 0, surv = 0;  // in the slots before this warp's
-    auto pass_over = [&](const PieceCounts &c) {
-        const int take_low = max(0, min(c.eq_low, need - eq_before));
-        const int take_high = max(0, min(c.eq_high, need - eq_before - c.eq_low));
-        hole += c.n_low - c.gt_low - take_low;
-        surv += c.gt_high + take_high;
-        eq_before += c.eq_low + c.eq_high;
-    };
-    for (int c = 0; c < rank; ++c) pass_over(*cluster.map_shared_rank(&block_cnt, c));
-    for (int i = 0; i < warp; ++i) pass_over(warp_cnt[i]);
+    sync_all();
+    const PieceCounts bc = lane < C ? *cluster.map_shared_rank(&block_cnt, lane) : none;  // lane l: block l
+    const int bc_eq_before = sum_before(bc.eq_low + bc.eq_high, lane);
+    const int2 bc_hs = holes_and_survivors(bc, bc_eq_before, need);
+    const int block_surv = sum_before(bc_hs.y, lane);  // lane l: survivors in the blocks before block l
+    int eq_before = __shfl_sync(0xFFFFFFFFu, bc_eq_before, rank);
+    int hole = warp_sum(lane < rank ? bc_hs.x : 0);
+    const int wc_eq_before = eq_before + sum_before(wc.eq_low + wc.eq_high, lane);
+    const int2 wc_hs = holes_and_survivors(wc, wc_eq_before, need);
+    eq_before = __shfl_sync(0xFFFFFFFFu, wc_eq_before, warp);
+    hole += warp_sum(lane < warp ? wc_hs.x : 0);
+    int surv = warp_sum(lane < warp ? wc_hs.y : 0);  // in this block's list
 
-    const int64_t list = static_cast<int64_t>(head) * min(a.keep, a.P - a.keep);
     int32_t *slots = a.slots + static_cast<int64_t>(head) * a.keep;
-    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
     for (int s = 0; s < steps; ++s) {
         const int i = wbase + s * 32 + lane;
         const int slot = lo + i;
@@ -240,23 +287,36 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
         eq_before += __popc(eq);
         const uint32_t hm = __ballot_sync(0xFFFFFFFFu, in && low && !kept);
         const uint32_t sm = __ballot_sync(0xFFFFFFFFu, kept && !low);
-        if (kept && low) slots[slot] = slot;
-        if (in && low && !kept) a.holes[list + hole + __popc(hm & below)] = slot;
-        if (kept && !low) a.survivors[list + surv + __popc(sm & below)] = slot;
+        if (kept && !low) surv_list[surv + __popc(sm & below)] = slot;
+        keys[i] = in && low && !kept ? static_cast<uint32_t>(hole + __popc(hm & below)) : kept && low ? ~1u : ~0u;
         hole += __popc(hm);
         surv += __popc(sm);
     }
-    // every block's lists are complete: the r-th hole takes the r-th survivor
-    cluster.sync();
-    int moved = 0, eqs = 0;
-    for (int c = 0; c < C; ++c) {
-        const PieceCounts bc = *cluster.map_shared_rank(&block_cnt, c);
-        moved += bc.gt_high + max(0, min(bc.eq_high, need - eqs - bc.eq_low));
-        eqs += bc.eq_low + bc.eq_high;
+    // every block's list is complete: the r-th hole takes the r-th survivor
+    sync_all();
+    int first[kMaxCluster];  // survivors in the blocks before block c
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) first[c] = __shfl_sync(0xFFFFFFFFu, block_surv, c);
+    for (int s0 = 0; s0 < steps; s0 += kLoadAhead) {
+        int from[kLoadAhead];
+#pragma unroll
+        for (int u = 0; u < kLoadAhead; ++u) {
+            const int i = wbase + (s0 + u) * 32 + lane;
+            const uint32_t r = s0 + u < steps ? keys[i] : ~0u;
+            from[u] = r == ~1u ? lo + i : -1;
+            if (r < ~1u) {
+                int owner = 0, base = 0;  // the block with survivor r
+#pragma unroll
+                for (int c = 1; c < kMaxCluster; ++c)
+                    if (c < C && static_cast<int>(r) >= first[c]) owner = c, base = first[c];
+                from[u] = cluster.map_shared_rank(surv_list, owner)[static_cast<int>(r) - base];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kLoadAhead; ++u)
+            if (from[u] >= 0) slots[lo + wbase + (s0 + u) * 32 + lane] = from[u];
     }
-    for (int r = rank * kSelThreads + tid; r < moved; r += C * kSelThreads)
-        slots[__ldcg(a.holes + list + r)] = __ldcg(a.survivors + list + r);
-    cluster.sync();  // no block leaves while another may still read its shared memory
+    sync_all();  // no block leaves while another may still read its shared memory
 }
 
 struct MoveArgs {
@@ -265,40 +325,59 @@ struct MoveArgs {
     int64_t row_stride, dst_stride;  // in 16-byte pieces
     const int32_t *slots;
     const float *w;
-    float *w_dst;
+    float *w_dst;  // or nullptr
     const int32_t *pos;
-    int32_t *pos_dst;
+    int32_t *pos_dst;  // or nullptr
     int64_t w_stride, wd_stride, pos_stride, pd_stride;
-    int keep, Hkv, pieces;  // pieces: 16-byte pieces of one key (d / 8)
-    int skip_k, skip_v, skip_w, skip_pos;  // in place: a key that stays is not copied
+    unsigned row_blocks;
+    int Hkv, keep, pieces, row_pieces;  // pieces: of one key (d / 8); row_pieces: of a row (Hkv d / 8)
+    int skip_k, skip_v;            // in place: a key that stays is not copied
 };
 
 constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 16;  // destination rows of a block
+constexpr int kMoveAhead = 4;
 
-// One thread per 16-byte piece of a destination row (pieces of a row contiguous), K and V together;
-// the first piece's thread also moves the key's weight and position.
+// A thread moves 16-byte pieces of destination rows, K and V, kMoveAhead of them in flight together.  The
+// blocks after those of the rows move the weights and positions, a key each thread (done by the thread of a
+// key's first piece they cost 5 us of the 12 that 18k rows take, in 4-byte writes all over).
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs a)
 {
     ptx::grid_dep_wait();
-    const int64_t row_pieces = static_cast<int64_t>(a.Hkv) * a.pieces;
-    const int64_t total = row_pieces * a.keep;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; t < total;
-         t += static_cast<int64_t>(gridDim.x) * kMoveThreads) {
-        const int64_t j = t / row_pieces;
-        const int64_t c = t - j * row_pieces;
-        const int head = static_cast<int>(c / a.pieces);
-        const int slot = __ldg(a.slots + static_cast<int64_t>(head) * a.keep + j);
-        const bool stays = slot == j;
-        const bool do_k = !(stays && a.skip_k), do_v = !(stays && a.skip_v);
-        uint4 kv, vv;
-        if (do_k) kv = __ldcs(a.k + slot * a.row_stride + c);
-        if (do_v) vv = __ldcs(a.v + slot * a.row_stride + c);
-        if (do_k) a.k_dst[j * a.dst_stride + c] = kv;
-        if (do_v) a.v_dst[j * a.dst_stride + c] = vv;
-        if (c == static_cast<int64_t>(head) * a.pieces) {
-            if (a.w_dst && !(stays && a.skip_w)) a.w_dst[head * a.wd_stride + j] = a.w[head * a.w_stride + slot];
-            if (a.pos_dst && !(stays && a.skip_pos))
-                a.pos_dst[head * a.pd_stride + j] = a.pos ? a.pos[head * a.pos_stride + slot] : slot;
+    if (blockIdx.x >= a.row_blocks) {
+        const int64_t t = static_cast<int64_t>(blockIdx.x - a.row_blocks) * kMoveThreads + threadIdx.x;
+        const int64_t head = t / a.keep, j = t - head * a.keep;
+        if (head >= a.Hkv) return;
+        const int slot = __ldg(a.slots + t);
+        if (a.w_dst) a.w_dst[head * a.wd_stride + j] = a.w[head * a.w_stride + slot];
+        if (a.pos_dst) a.pos_dst[head * a.pd_stride + j] = a.pos ? a.pos[head * a.pos_stride + slot] : slot;
+        return;
+    }
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kMoveRows;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kMoveRows), a.keep - j0));
+    const int total = rows * a.row_pieces;
+    for (int t0 = threadIdx.x; t0 < total; t0 += kMoveThreads * kMoveAhead) {
+        uint4 kv[kMoveAhead], vv[kMoveAhead];
+        int64_t dst[kMoveAhead];
+        bool do_k[kMoveAhead], do_v[kMoveAhead];
+#pragma unroll
+        for (int u = 0; u < kMoveAhead; ++u) {
+            const int t = t0 + u * kMoveThreads;
+            const int row = t / a.row_pieces, c = t - row * a.row_pieces;
+            const int64_t j = j0 + row;
+            int slot = 0;
+            if (t < total) slot = __ldg(a.slots + static_cast<int64_t>(c / a.pieces) * a.keep + j);
+            do_k[u] = t < total && !(slot == j && a.skip_k);
+            do_v[u] = t < total && !(slot == j && a.skip_v);
+            dst[u] = j * a.dst_stride + c;
+            const int64_t src = slot * a.row_stride + c;
+            if (do_k[u]) kv[u] = __ldcs(a.k + src);
+            if (do_v[u]) vv[u] = __ldcs(a.v + src);
+        }
+#pragma unroll
+        for (int u = 0; u < kMoveAhead; ++u) {
+            if (do_k[u]) a.k_dst[dst[u]] = kv[u];
+            if (do_v[u]) a.v_dst[dst[u]] = vv[u];
         }
     }
 }
@@ -322,9 +401,8 @@ bool rows_overlap(const void *a, int64_t sa, int64_t na, const void *b, int64_t 
 extern "C" size_t blink_kv_evict_workspace(int32_t P, int32_t keep, int32_t Hkv)
 {
     using namespace blink;
-    if (P < 1 || keep < 1 || keep > P || Hkv < 1) return kHeaderBytes;
-    const size_t list = static_cast<size_t>(keep < P - keep ? keep : P - keep) * Hkv * sizeof(int32_t);
-    return kHeaderBytes + 2 * align_up(list, 256);
+    (void)P, (void)keep, (void)Hkv;
+    return kHeaderBytes;
 }
 
 extern "C" blink_status blink_kv_evict(const float *d_weights, int64_t w_stride, const int32_t *d_pos,
@@ -382,18 +460,14 @@ extern "C" blink_status blink_kv_evict(const float *d_weights, int64_t w_stride,
     e.keep = keep;
     e.sink = sink;
     e.recent_from = recent_from;
-    e.Hkv = Hkv;
-    int C = 1;  // blocks per head: pieces of 1024 keys and more, at most kMaxCluster of them
-    while (C < kMaxCluster && P > C * kSelThreads) C *= 2;
+    int C = 1;  // blocks per head: pieces of kClusterPiece keys and more, at most kMaxCluster of them
+    while (C < kMaxCluster && P > C * kClusterPiece) C *= 2;
     e.piece = (P + C * kSelThreads - 1) / (C * kSelThreads) * kSelThreads;
     e.slots = d_slots;
-    const size_t list = align_up(static_cast<size_t>(keep < P - keep ? keep : P - keep) * Hkv * sizeof(int32_t), 256);
-    e.holes = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + kHeaderBytes);
-    e.survivors = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + kHeaderBytes + list);
 
-    const int smem = e.piece * static_cast<int>(sizeof(uint32_t));
+    const int smem = 2 * e.piece * static_cast<int>(sizeof(uint32_t));
     if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxPiece * static_cast<int>(sizeof(uint32_t))) != cudaSuccess)
+                             2 * kMaxPiece * static_cast<int>(sizeof(uint32_t))) != cudaSuccess)
         return BLINK_CUDA_ERROR;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -425,17 +499,24 @@ extern "C" blink_status blink_kv_evict(const float *d_weights, int64_t w_stride,
     m.wd_stride = wd_stride;
     m.pos_stride = pos_stride;
     m.pd_stride = pd_stride;
-    m.keep = keep;
+    m.row_blocks = static_cast<unsigned>((keep + kMoveRows - 1) / kMoveRows);
     m.Hkv = Hkv;
+    m.keep = keep;
     m.pieces = d / 8;
+    m.row_pieces = Hkv * (d / 8);
     m.skip_k = k_in;
     m.skip_v = v_in;
-    m.skip_w = w_in;
-    m.skip_pos = p_in;
-    const int64_t total = static_cast<int64_t>(keep) * Hkv * m.pieces;
-    const int64_t blocks = (total + kMoveThreads - 1) / kMoveThreads;
-    const unsigned grid = static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20));
-    evict_move_kernel<<<grid, kMoveThreads, 0, stream>>>(m);
-    if (cudaGetLastError() != cudaSuccess) return BLINK_CUDA_ERROR;
+    cudaLaunchConfig_t mc = {};
+    cudaLaunchAttribute ma[1];
+    ma[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    ma[0].val.programmaticStreamSerializationAllowed = 1;
+    const int64_t list_blocks =
+        d_weights_dst || d_pos_dst ? (static_cast<int64_t>(Hkv) * keep + kMoveThreads - 1) / kMoveThreads : 0;
+    mc.gridDim = dim3(m.row_blocks + static_cast<unsigned>(list_blocks));
+    mc.blockDim = dim3(kMoveThreads);
+    mc.stream = stream;
+    mc.attrs = ma;
+    mc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&mc, evict_move_kernel, m) != cudaSuccess) return BLINK_CUDA_ERROR;
     return BLINK_OK;
 }
