@@ -80,6 +80,7 @@ __host__ __device__ __forceinline__ int64_t first_step(int64_t b, int64_t total,
 
 // The steps of a block, segment by segment (a segment: consecutive column tiles of one unit).  Every
 // role walks the same sequence.
+template <bool kOneTile>
 struct Segment {
     int64_t at, end;
     int n_tiles, n_units_head;
@@ -108,7 +109,15 @@ struct Segment {
     {
         at += tiles;
         first = false;
-        load();
+        if constexpr (kOneTile) {  // the next unit, without a division
+            const int units = n_units_head * kUnitKeys;
+            key0 += kUnitKeys;
+            new_q = key0 == units;
+            if (new_q) key0 = 0, ++head;
+            last_use = at + 1 >= end || key0 + kUnitKeys == units;
+        } else {
+            load();
+        }
     }
 };
 
@@ -128,7 +137,9 @@ __device__ __forceinline__ void warp_sum_scatter(float (&acc)[kThreadKeys], int 
     }
 }
 
-template <int D>
+// kOneTile: all columns fit one tile (a decoded token, a short question): a unit is one step, and the tile and its
+// lse stay from unit to unit of a head.
+template <int D, bool kOneTile>
 __global__ void __launch_bounds__(kThreadsKW, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const KeyWeightArgs a)
@@ -196,7 +207,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
             int nk = 0, nq = 0;
             bool ok = true;
             const uint32_t q_bytes = static_cast<uint32_t>(L::kPanels) * 128u * cols_used;
-            for (Segment sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next(), ++nk) {
+            for (Segment<kOneTile> sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next(), ++nk) {
                 const int ks = nk & 1;
                 // freed at the end of an earlier segment: the limit grows with a segment's length
                 if (!(ok = ptx::mbar_wait(k_empty + ks, ((nk >> 1) & 1) ^ 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT,
@@ -230,7 +241,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
             const uint64_t desc0 = ptx::smem_desc_sw128(ptx::smem_u32(smem), 16, 1024);  // in units of 16 bytes
             int nk = 0, nq = -1, st = 0;
             bool ok = true;
-            for (Segment sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next(), ++nk) {
+            for (Segment<kOneTile> sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next(), ++nk) {
                 const int ks = nk & 1;
                 if (!(ok = ptx::mbar_wait(k_full + ks, (nk >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
                 const uint64_t kd = desc0 + (ks * L::kKBytes >> 4);
@@ -270,8 +281,9 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
             const int head_off = col % a.g;
             const uint64_t cc = ptx::f32x2(a.c, a.c);
             int st = 0, meetings = 0;
+            float single = 0.f;
             bool ok = true;
-            for (Segment sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next()) {
+            for (Segment<kOneTile> sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next()) {
                 const float *lse = a.lse + (sg.head * a.g + head_off) * a.lse_stride;
                 int at = sg.tile0 * a.tpt + tok;  // this column's row in the tile to be read next
                 const int last = col < cols_used ? min(a.rows, (sg.tile0 + sg.tiles) * a.tpt) : 0;  // 0: no column
@@ -283,11 +295,19 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                 float acc[kThreadKeys];
 #pragma unroll
                 for (int i = 0; i < kThreadKeys; ++i) acc[i] = 0.f;
-                float next = lse_next(), after = lse_next();  // two tiles ahead of their use
+                float next, after = INFINITY;  // two tiles ahead of their use
+                if constexpr (kOneTile) {
+                    if (sg.new_q) single = lse_next();
+                    next = single;
+                } else {
+                    next = lse_next(), after = lse_next();
+                }
                 for (int i = 0; i < sg.tiles; ++i, ++st) {
                     const float b = next;
-                    next = after;
-                    after = lse_next();
+                    if constexpr (!kOneTile) {
+                        next = after;
+                        after = lse_next();
+                    }
                     const bool dead = b == -INFINITY;  // owned by no question: q may hold anything
                     const float nb = dead ? -INFINITY : -b * kLog2e;
                     const bool careful = __any_sync(0xFFFFFFFFu, dead);
@@ -393,11 +413,11 @@ int sm_count()
     return sms;
 }
 
-template <int D>
+template <int D, bool kOneTile>
 cudaError_t launch_key_weights(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const KeyWeightArgs &a, unsigned blocks,
                                cudaStream_t stream)
 {
-    auto kern = key_weights_kernel<D>;
+    auto kern = key_weights_kernel<D, kOneTile>;
     // The split of registers by role has to fit the registers of the launch: checked once.
     static const bool fits = [kern] {
         cudaFuncAttributes fa;
@@ -476,8 +496,12 @@ extern "C" blink_status blink_prefix_key_weights(const blink_bf16 *q, const blin
         !encode_tmap_3d_bf16(&tm_k, k_pre, d, Hkv, P, d * e, static_cast<uint64_t>(pre_row_stride) * e, 64, 1,
                              kUnitKeys))
         return BLINK_CUDA_ERROR;
-    const cudaError_t err = d == 128 ? launch_key_weights<128>(tm_q, tm_k, a, static_cast<unsigned>(blocks), stream)
-                                     : launch_key_weights<64>(tm_q, tm_k, a, static_cast<unsigned>(blocks), stream);
+    const auto grid = static_cast<unsigned>(blocks);
+    const cudaError_t err =
+        a.n_tiles > 1 ? (d == 128 ? launch_key_weights<128, false>(tm_q, tm_k, a, grid, stream)
+                                  : launch_key_weights<64, false>(tm_q, tm_k, a, grid, stream))
+                      : (d == 128 ? launch_key_weights<128, true>(tm_q, tm_k, a, grid, stream)
+                                  : launch_key_weights<64, true>(tm_q, tm_k, a, grid, stream));
     if (err != cudaSuccess) return BLINK_CUDA_ERROR;
     if (a.n_tiles == 1) return BLINK_OK;  // a unit of one step is never cut
     cudaLaunchConfig_t cfg = {};
