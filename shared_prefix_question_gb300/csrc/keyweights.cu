@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
             const uint64_t cc = ptx::f32x2(a.c, a.c);
             int st = 0, meetings = 0;
             float single = 0.f;
+            float2 before = make_float2(0.f, 0.f);  // previous weights of this thread's keys
             bool ok = true;
             for (Segment<kOneTile> sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next()) {
                 const float *lse = a.lse + (sg.head * a.g + head_off) * a.lse_stride;
@@ -299,6 +300,12 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                 if constexpr (kOneTile) {
                     if (sg.new_q) single = lse_next();
                     next = single;
+                    if (a.decay > 0.f && wq == 0) {  // read now, a kilocycle before its use
+                        const int key = sg.key0 + quarter * kThreadKeys + 2 * lane;
+                        const float *prev = a.prev + sg.head * a.prev_stride;
+                        before.x = key < a.P ? prev[key] : 0.f;
+                        before.y = key + 1 < a.P ? prev[key + 1] : 0.f;
+                    }
                 } else {
                     next = lse_next(), after = lse_next();
                 }
@@ -368,9 +375,13 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                     if (sg.tiles == a.n_tiles) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            if (key + i < a.P)
-                                a.w[sg.head * a.w_stride + key + i] =
-                                    a.decay > 0.f ? fmaf(a.decay, a.prev[sg.head * a.prev_stride + key + i], v[i]) : v[i];
+                            if (key + i < a.P) {
+                                float *w = a.w + sg.head * a.w_stride + key + i;
+                                if constexpr (kOneTile)
+                                    *w = fmaf(a.decay, i ? before.y : before.x, v[i]);
+                                else
+                                    *w = a.decay > 0.f ? fmaf(a.decay, a.prev[sg.head * a.prev_stride + key + i], v[i]) : v[i];
+                            }
                     } else {
                         float *part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (sg.first ? 0 : 1)) * kUnitKeys;
                         *reinterpret_cast<float2 *>(part + quarter * kThreadKeys + 2 * lane) = s;
