@@ -137,13 +137,20 @@ __device__ __forceinline__ void warp_sum_scatter(float (&acc)[kThreadKeys], int 
     }
 }
 
-// kOneTile: all columns fit one tile (a decoded token, a short question): a unit is one step, and the tile and its
-// lse stay from unit to unit of a head.
-template <int D, bool kOneTile>
+// Forms.  kManyTiles: the columns take several tiles.  kOneTile: they fit one (a short question): a unit is one
+// step, and the tile and its lse stay from unit to unit of a head.  kFewColumns: they fit 32 rows of a tile
+// (a decoded token): the same 32 rows are copied to all four quarters of the tile, so that all 16
+// warps have them and each sums 16 of the keys (with the one warp that would have the columns otherwise, the
+// sums of a unit take 3,400 cycles against 1,700 for its keys to arrive).
+constexpr int kManyTiles = 0, kOneTileForm = 1, kFewColumns = 2;
+
+template <int D, int kForm>
 __global__ void __launch_bounds__(kThreadsKW, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const KeyWeightArgs a)
 {
+    constexpr bool kOneTile = kForm != kManyTiles;
+    constexpr bool kFew = kForm == kFewColumns;
     using L = KwLayout<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (ptx::smem_u32(smem) & 1023u) {  // the swizzled tiles need it; the whole block leaves
@@ -161,7 +168,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t begin = first_step(blockIdx.x, a.total, gridDim.x), end = first_step(blockIdx.x + 1, a.total, gridDim.x);
     const int cols_used = a.g * a.tpt;
-    const int live_warps = (cols_used + 31) / 32;  // of four: the others have no column in any tile
+    const int live_warps = kFew ? 4 : (cols_used + 31) / 32;  // of four: the others have no column in any tile
 
     if (warp == kProducer && lane == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -186,10 +193,10 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
         ptx::tmem_relinquish();
     }
     // Columns of the last live warp past g * tpt are never copied: zero once, so that their scores are 0.
-    if (warp < kSumWarps && cols_used < live_warps * 32) {
-        const int pad = (live_warps * 32 - cols_used) * 128;
-        for (int s = 0; s < L::kQSlots * L::kPanels; ++s) {
-            uint8_t *dst = q_ring + s * L::kQPanel + cols_used * 128;
+    if (warp < kSumWarps && (kFew ? cols_used < 32 : cols_used < live_warps * 32)) {
+        const int pad = ((kFew ? 32 : live_warps * 32) - cols_used) * 128;
+        for (int s = 0; s < L::kQSlots * L::kPanels * (kFew ? 4 : 1); ++s) {
+            uint8_t *dst = q_ring + s * (kFew ? 32 * 128 : L::kQPanel) + cols_used * 128;
             for (int off = threadIdx.x * 16; off < pad; off += kSumWarps * 32 * 16)
                 *reinterpret_cast<uint4 *>(dst + off) = make_uint4(0, 0, 0, 0);
         }
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
         if (lane == 0) {
             int nk = 0, nq = 0;
             bool ok = true;
-            const uint32_t q_bytes = static_cast<uint32_t>(L::kPanels) * 128u * cols_used;
+            const uint32_t q_bytes = static_cast<uint32_t>(L::kPanels) * 128u * cols_used * (kFew ? 4u : 1u);
             for (Segment<kOneTile> sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next(), ++nk) {
                 const int ks = nk & 1;
                 // freed at the end of an earlier segment: the limit grows with a segment's length
@@ -223,8 +230,9 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                         break;
                     ptx::mbar_arrive_expect_tx(q_full + qs, q_bytes);
                     for (int p = 0; p < L::kPanels; ++p)
-                        ptx::tma_load_3d(q_ring + qs * L::kQBytes + p * L::kQPanel, &tm_q, p * 64, sg.head * a.g,
-                                         (sg.tile0 + i) * a.tpt, q_full + qs);
+                        for (int r = 0; r < (kFew ? 4 : 1); ++r)
+                            ptx::tma_load_3d(q_ring + qs * L::kQBytes + p * L::kQPanel + r * 32 * 128, &tm_q, p * 64,
+                                             sg.head * a.g, (sg.tile0 + i) * a.tpt, q_full + qs);
                 }
             }
             ptx::grid_launch_dependents();
@@ -272,7 +280,50 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
     } else if (warp < kSumWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         const int quarter = warp >> 2, wq = warp & 3;  // of the unit's keys, of the tile's columns
-        if (wq < live_warps) {
+        if constexpr (kFew) {
+            // -------------------------------------------------------- sums: one column per thread, 16 keys a warp
+            constexpr int kKeys = 16;
+            const int offset = quarter * kThreadKeys + wq * kKeys;  // of the warp's keys in the unit
+            const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16) + offset;
+            const int row = lane / a.g;
+            const bool has = lane < cols_used && row < a.rows;
+            int st = 0;
+            float b = INFINITY;
+            bool ok = true;
+            for (Segment<kOneTile> sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next(), ++st) {
+                if (sg.new_q) b = has ? __ldg(a.lse + (sg.head * a.g + lane % a.g) * a.lse_stride + row) : INFINITY;
+                const bool dead = b == -INFINITY;  // owned by no question: q may hold anything
+                const float nb = dead ? -INFINITY : -b * kLog2e;
+                const int key = sg.key0 + offset + (lane >> 1);  // the key this thread writes, if its lane is even
+                const bool writes = (lane & 1) == 0 && key < a.P;
+                const float before = writes && a.decay > 0.f ? a.prev[sg.head * a.prev_stride + key] : 0.f;
+                const int buf = st & 1;
+                if (!(ok = ptx::mbar_wait(s_full + buf, (st >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
+                ptx::tc_fence_after();
+                uint32_t raw[kKeys];
+                ptx::tmem_ld16(trow + buf * kUnitKeys, raw);
+                ptx::tmem_wait_ld();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(s_empty + buf);
+                float acc[kKeys];
+#pragma unroll
+                for (int j = 0; j < kKeys; ++j) acc[j] = dead ? 0.f : ptx::ex2(fmaf(__uint_as_float(raw[j]), a.c, nb));
+                // over the warp's threads, each step handing half of the keys to the partner
+#pragma unroll
+                for (int o = 16; o > 1; o >>= 1) {
+                    const bool upper = (lane & o) != 0;
+#pragma unroll
+                    for (int j = 0; j < o / 2; ++j) {
+                        const float give = upper ? acc[j] : acc[j + o / 2];
+                        const float keep = upper ? acc[j + o / 2] : acc[j];
+                        acc[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                    }
+                }
+                const float sum = acc[0] + __shfl_xor_sync(0xFFFFFFFFu, acc[0], 1);
+                if (writes) a.w[sg.head * a.w_stride + key] = fmaf(a.decay, before, sum);
+            }
+        } else if (wq < live_warps) {
             // -------------------------------------------------------- sums: one column per thread
             const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16) + quarter * kThreadKeys;
             float *sums = reinterpret_cast<float *>(smem + L::kSumOff) + quarter * 2 * kThreadKeys;
@@ -424,11 +475,11 @@ int sm_count()
     return sms;
 }
 
-template <int D, bool kOneTile>
+template <int D, int kForm>
 cudaError_t launch_key_weights(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const KeyWeightArgs &a, unsigned blocks,
                                cudaStream_t stream)
 {
-    auto kern = key_weights_kernel<D, kOneTile>;
+    auto kern = key_weights_kernel<D, kForm>;
     // The split of registers by role has to fit the registers of the launch: checked once.
     static const bool fits = [kern] {
         cudaFuncAttributes fa;
@@ -508,11 +559,16 @@ extern "C" blink_status blink_prefix_key_weights(const blink_bf16 *q, const blin
                              kUnitKeys))
         return BLINK_CUDA_ERROR;
     const auto grid = static_cast<unsigned>(blocks);
-    const cudaError_t err =
-        a.n_tiles > 1 ? (d == 128 ? launch_key_weights<128, false>(tm_q, tm_k, a, grid, stream)
-                                  : launch_key_weights<64, false>(tm_q, tm_k, a, grid, stream))
-                      : (d == 128 ? launch_key_weights<128, true>(tm_q, tm_k, a, grid, stream)
-                                  : launch_key_weights<64, true>(tm_q, tm_k, a, grid, stream));
+    cudaError_t err;
+    if (a.n_tiles > 1)
+        err = d == 128 ? launch_key_weights<128, kManyTiles>(tm_q, tm_k, a, grid, stream)
+                       : launch_key_weights<64, kManyTiles>(tm_q, tm_k, a, grid, stream);
+    else if (a.g * a.tpt > 32)
+        err = d == 128 ? launch_key_weights<128, kOneTileForm>(tm_q, tm_k, a, grid, stream)
+                       : launch_key_weights<64, kOneTileForm>(tm_q, tm_k, a, grid, stream);
+    else
+        err = d == 128 ? launch_key_weights<128, kFewColumns>(tm_q, tm_k, a, grid, stream)
+                       : launch_key_weights<64, kFewColumns>(tm_q, tm_k, a, grid, stream);
     if (err != cudaSuccess) return BLINK_CUDA_ERROR;
     if (a.n_tiles == 1) return BLINK_OK;  // a unit of one step is never cut
     cudaLaunchConfig_t cfg = {};

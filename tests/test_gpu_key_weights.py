@@ -55,7 +55,7 @@ def check(got, q, k, lse, scale=None, add=None):
 
 @pytest.mark.parametrize("rows,P,Hq,Hkv,d", [
     (1, 1, 1, 1, 64), (1, 1, 4, 2, 128), (60, 64, 4, 2, 64), (1, 2048, 32, 8, 128), (5, 127, 8, 8, 64),
-    (3, 129, 6, 2, 128), (64, 256, 4, 1, 128), (65, 257, 4, 1, 128), (17, 1000, 40, 8, 128), (51, 511, 5, 1, 64),
+    (3, 129, 6, 2, 128), (4, 1300, 16, 2, 64), (8, 700, 8, 2, 128), (9, 700, 8, 2, 128), (32, 515, 3, 3, 128), (64, 256, 4, 1, 128), (65, 257, 4, 1, 128), (17, 1000, 40, 8, 128), (51, 511, 5, 1, 64),
     (2, 300, 128, 1, 64), (3, 300, 127, 1, 128), (700, 513, 7, 1, 128), (257, 3000, 2, 2, 64), (130, 5000, 28, 4, 128),
     (1000, 700, 16, 2, 64)])
 def test_against_formula(rows, P, Hq, Hkv, d):
