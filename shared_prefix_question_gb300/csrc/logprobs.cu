@@ -21,8 +21,9 @@
 //
 // Precision.  The tensor core's fp32 accumulator truncates: over a sum of H / 16 steps the loss grows
 // with H (measured against 64 bits, logits of 12: 2.7e-6 of the logit at H = 2560, 5.4e-6 at 5120, and
-// four times that where all products have one sign).  So a product runs over at most 640 of H only, and the row's thread adds the parts in registers, rounded to nearest: the loss stays that of
-// one part whatever H is.
+// four times that where all products have one sign).  So a product runs over at most 512 of H only,
+// and the row's thread adds the parts in registers, rounded to nearest: the loss stays that of one part
+// whatever H is.
 //
 // Roles (384 threads a block): warps 0-7 the states (threads t and t + 128 share row t, 128 of a tile's
 // columns each, held in registers: 232 a thread, 40 for the other warps), warp 8 TMA producer, warp 9
@@ -52,7 +53,14 @@ constexpr int kStateWarps = 8;
 constexpr int kProducerLP = 8, kIssuerLP = 9;
 constexpr int kHalves = 2;      // threads that share a row
 constexpr int kHalfCols = kVocabTile / kHalves;
-constexpr int kPartBlocks = 10;  // at most this many 64-wide blocks of H per product
+// At most this many 64-wide blocks of H per product.  Measured at H = 2560, entropy against 64 bits: 1.5e-6
+// off with 10 blocks, 0.95e-6 with 8, 0.7e-6 with 6; pairs take 4 % longer with 6 than with 8, and 1 % less
+// with 10.
+constexpr int kPartBlocks = 8;
+// 64-wide blocks of H per stage of the ring.  A pair's issuer loses some 120 cycles of the tensor core at every
+// barrier it waits for: with two blocks a stage 4096 tokens take 1.73 ms instead of 1.82.  One block alone
+// waits for memory, and more, smaller stages suit it.
+constexpr int kStageBlocksOne = 1, kStageBlocksPair = 2;  // 64-wide blocks of H per stage of the ring
 constexpr int kNoToken = 0x7FFFFFFF;
 constexpr int kMaxWorkers = 160;
 constexpr int kMaxStages = 8;
@@ -150,7 +158,7 @@ struct LogprobArgs {
     uint32_t *bounds;  // [n][kMaxTop]: see RowBound
     int prepared;      // a launch before gathered the hidden rows and cleared the bounds
     // shared memory: the stages, with alternatives the rows' bounds, then the barriers
-    int stages, stage_bytes, a_bytes, bound_off, bar_off, smem_bytes;
+    int stages, block_bytes, a_bytes, bound_off, bar_off, smem_bytes;
 };
 
 // Divides the shared memory of a block: as many stages as fit.
@@ -159,11 +167,12 @@ void lay_out(LogprobArgs &a)
     const bool one = a.plan.blocks_per_worker == 1;
     a.a_rows = a.n < kBlockRows ? (a.n + 7) / 8 * 8 : kBlockRows;
     a.a_bytes = a.a_rows * 128;
-    a.stage_bytes = a.a_bytes + kVocabTile / (one ? 1 : 2) * 128;
+    a.block_bytes = a.a_bytes + kVocabTile / (one ? 1 : 2) * 128;
+    const int stage_bytes = a.block_bytes * (one ? kStageBlocksOne : kStageBlocksPair);
     const int bounds = a.top > 0 ? kBlockRows * static_cast<int>(sizeof(int2)) : 0;
-    a.stages = (kSmemMax - bounds - 256) / a.stage_bytes;
+    a.stages = (kSmemMax - bounds - 256) / stage_bytes;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
-    a.bound_off = a.stages * a.stage_bytes;
+    a.bound_off = a.stages * stage_bytes;
     a.bar_off = a.bound_off + bounds;
     a.smem_bytes = a.bar_off + 256;
 }
@@ -405,7 +414,9 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
     const int worker = blockIdx.x / kCtas;
     const int passes = a.plan.passes();
     const int k_blocks = (a.H + 63) / 64;
-    const int n_parts = (k_blocks + kPartBlocks - 1) / kPartBlocks, part_blocks = (k_blocks + n_parts - 1) / n_parts;
+    constexpr int kStageBlocks = kCtas == 1 ? kStageBlocksOne : kStageBlocksPair;
+    const int n_parts = (k_blocks + kPartBlocks - 1) / kPartBlocks;
+    const int part_blocks = ((k_blocks + n_parts - 1) / n_parts + kStageBlocks - 1) / kStageBlocks * kStageBlocks;
     const bool aligned = (ptx::smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need it
     if (!aligned && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
 
@@ -451,7 +462,7 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
         // nothing was started: straight to the end
     } else if (warp == kProducerLP) {
         if (lane == 0) {
-            const uint32_t bytes = static_cast<uint32_t>(a.stage_bytes) * kCtas;  // of both blocks, counted on the even one
+            const uint32_t bytes = static_cast<uint32_t>(a.block_bytes) * kCtas;  // of both blocks, counted on the even one
             int it = 0, st = 0;
             uint32_t ph = 1u;
             bool ok = true, waited = a.prepared == 0;
@@ -461,20 +472,24 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
                 const int row0 = sh.row_tile * a.plan.tile_rows + static_cast<int>(rank) * kBlockRows;
                 for (int vt = sh.v0; ok && vt < sh.v1; ++vt) {
                     const int col0 = vt * kVocabTile + static_cast<int>(rank) * (kVocabTile / kCtas);
-                    for (int kb = 0; kb < k_blocks; ++kb, ++it) {
+                    for (int k0 = 0; k0 < k_blocks; k0 += kStageBlocks, ++it) {
                         if (!(ok = ptx::mbar_wait(empty + st, ph, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
-                        uint8_t *dst = smem + st * a.stage_bytes;
-                        if constexpr (kCtas == 2) {
-                            const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(full + st), 0);
-                            if (rank == 0) ptx::mbar_arrive_expect_tx(full + st, bytes);
-                            ptx::tma_load_3d_pair(dst + a.a_bytes, &tm_w, kb * 64, col0, 0, bar);
-                            if (!waited) ptx::grid_dep_wait(), waited = true;
-                            ptx::tma_load_3d_pair(dst, &tm_h, kb * 64, row0, 0, bar);
-                        } else {
-                            ptx::mbar_arrive_expect_tx(full + st, bytes);
-                            ptx::tma_load_3d(dst + a.a_bytes, &tm_w, kb * 64, col0, 0, full + st);
-                            if (!waited) ptx::grid_dep_wait(), waited = true;
-                            ptx::tma_load_3d(dst, &tm_h, kb * 64, row0, 0, full + st);
+                        const int kn = min(kStageBlocks, k_blocks - k0);
+                        const uint32_t bar = kCtas == 2 ? ptx::map_to_rank(ptx::smem_u32(full + st), 0) : 0u;
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(full + st, bytes * kn);
+#pragma unroll
+                        for (int kb = 0; kb < kStageBlocks; ++kb) {
+                            if (kb >= kn) break;
+                            uint8_t *dst = smem + (st * kStageBlocks + kb) * a.block_bytes;
+                            if constexpr (kCtas == 2) {
+                                ptx::tma_load_3d_pair(dst + a.a_bytes, &tm_w, (k0 + kb) * 64, col0, 0, bar);
+                                if (!waited) ptx::grid_dep_wait(), waited = true;
+                                ptx::tma_load_3d_pair(dst, &tm_h, (k0 + kb) * 64, row0, 0, bar);
+                            } else {
+                                ptx::tma_load_3d(dst + a.a_bytes, &tm_w, (k0 + kb) * 64, col0, 0, full + st);
+                                if (!waited) ptx::grid_dep_wait(), waited = true;
+                                ptx::tma_load_3d(dst, &tm_h, (k0 + kb) * 64, row0, 0, full + st);
+                            }
                         }
                         if (++st == a.stages) st = 0, ph ^= 1u;
                     }
@@ -493,7 +508,7 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
         if (lane == 0 && rank == 0) {
             constexpr uint32_t idesc = ptx::idesc_bf16_f32(kBlockRows * kCtas, kVocabTile, false);
             const uint64_t desc0 = ptx::smem_desc_sw128(ptx::smem_u32(smem), 16, 1024);  // in units of 16 bytes
-            const uint32_t stage16 = static_cast<uint32_t>(a.stage_bytes) >> 4, a16 = static_cast<uint32_t>(a.a_bytes) >> 4;
+            const uint32_t block16 = static_cast<uint32_t>(a.block_bytes) >> 4, a16 = static_cast<uint32_t>(a.a_bytes) >> 4;
             int st = 0, part = 0;
             uint32_t ph = 0u;
             bool ok = true;
@@ -509,12 +524,13 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
                         ptx::tc_fence_after();
                         const uint32_t d = tmem + buf * kVocabTile;
                         const int kn = min(part_blocks, k_blocks - k0);
-                        for (int kb = 0; kb < kn; ++kb) {
+                        for (int kb = 0; kb < kn; kb += kStageBlocks) {
                             if (!(ok = ptx::mbar_wait(full + st, ph, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
                             ptx::tc_fence_after();
-                            const uint64_t ad = desc0 + st * stage16, bd = ad + a16;
+                            const uint64_t ad = desc0 + st * kStageBlocks * block16, bd = ad + a16;
                             if constexpr (kCtas == 2) {
                                 ptx::mma_ss_pair_x4(d, ad, bd, idesc, kb > 0);
+                                if (kb + 1 < kn) ptx::mma_ss_pair_x4(d, ad + block16, bd + block16, idesc, 1u);
                                 ptx::mma_commit_pair(empty + st);
                             } else {
                                 ptx::mma_ss_x4(d, ad, bd, idesc, kb > 0);
