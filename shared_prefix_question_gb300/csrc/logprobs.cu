@@ -63,6 +63,7 @@ constexpr int kPartBlocks = 8;
 constexpr int kStageBlocksOne = 1, kStageBlocksPair = 2;  // 64-wide blocks of H per stage of the ring
 constexpr int kNoToken = 0x7FFFFFFF;
 constexpr int kMaxWorkers = 160;
+constexpr int kLaunchRows = 8192;  // rows of one launch: bounds the workspace (102 MB with 32 alternatives)
 constexpr int kMaxStages = 8;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kBatchCols = 8;  // columns searched for alternatives at a time
@@ -932,38 +933,12 @@ cudaError_t launch_logprob(const CUtensorMap &tm_h, const CUtensorMap &tm_w, con
     return cudaLaunchKernelEx(&cfg, kern, tm_h, tm_w, a);
 }
 
-}  // namespace
-}  // namespace blink
-
-extern "C" size_t blink_token_logprobs_workspace(int32_t n, int32_t H, int32_t V, int32_t top)
+// One launch sequence over at most kLaunchRows rows; the workspace serves one after the other.
+blink_status run_logprobs(const blink_bf16 *hidden, int64_t hidden_row_stride, int32_t hidden_rows, const int32_t *d_row_idx,
+                          const blink_bf16 *unembed, int32_t V, int32_t H, const int32_t *d_targets, int32_t n,
+                          float temperature, int32_t top, float *d_logprob, float *d_entropy, float *d_lse,
+                          int32_t *d_top_ids, float *d_top_logprobs, void *d_ws, cudaStream_t stream)
 {
-    using namespace blink;
-    if (n < 1 || n > BLINK_MAX_INPUT_TOKENS || H < 1 || H > 32768 || V < 1 || V > (1 << 24) || top < 0 || top > kMaxTop)
-        return kHeaderBytes;
-    const int sms = sm_count();
-    return ws_layout(make_plan(n, V, sms > 0 ? sms : 1), n, H, top).total;
-}
-
-extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t hidden_row_stride, int32_t hidden_rows,
-                                             const int32_t *d_row_idx, const blink_bf16 *unembed, int32_t V, int32_t H,
-                                             const int32_t *d_targets, int32_t n, float temperature, int32_t top,
-                                             float *d_logprob, float *d_entropy, float *d_lse, int32_t *d_top_ids,
-                                             float *d_top_logprobs, void *d_ws, size_t ws_bytes, cudaStream_t stream)
-{
-    using namespace blink;
-    if (!hidden || !unembed || !d_ws) return BLINK_INVALID_ARG;
-    if (!d_logprob && !d_entropy && !d_lse && !d_top_ids) return BLINK_INVALID_ARG;
-    if ((d_logprob && !d_targets) || (d_top_ids == nullptr) != (d_top_logprobs == nullptr)) return BLINK_INVALID_ARG;
-    if (!(temperature > 0.f) || !(temperature < INFINITY)) return BLINK_INVALID_ARG;
-    if (H < 8 || H % 8 != 0 || V < 1 || hidden_rows < 1 || hidden_row_stride < H || hidden_row_stride % 8 != 0)
-        return BLINK_INVALID_ARG;
-    if (!aligned16(hidden) || !aligned16(unembed)) return BLINK_INVALID_ARG;
-    if (top < 0 || top > kMaxTop || top > V || H > 32768 || V > (1 << 24)) return BLINK_OUT_OF_RANGE;
-    if ((top > 0) != (d_top_ids != nullptr)) return BLINK_INVALID_ARG;
-    if (n < 1 || n > BLINK_MAX_INPUT_TOKENS) return BLINK_OUT_OF_RANGE;
-    if (!d_row_idx && n > hidden_rows) return BLINK_INVALID_ARG;
-    if (ws_bytes < blink_token_logprobs_workspace(n, H, V, top)) return BLINK_WORKSPACE_TOO_SMALL;
-
     const int sms = sm_count();
     if (sms < 2) return BLINK_CUDA_ERROR;
     LogprobArgs a{};
@@ -1037,5 +1012,50 @@ extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t h
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, wide ? logprob_merge_kernel<kWideRow> : logprob_merge_kernel<32>, a) != cudaSuccess)
         return BLINK_CUDA_ERROR;
+    return BLINK_OK;
+}
+
+}  // namespace
+}  // namespace blink
+
+extern "C" size_t blink_token_logprobs_workspace(int32_t n, int32_t H, int32_t V, int32_t top)
+{
+    using namespace blink;
+    if (n < 1 || n > BLINK_MAX_INPUT_TOKENS || H < 1 || H > 32768 || V < 1 || V > (1 << 24) || top < 0 || top > kMaxTop)
+        return kHeaderBytes;
+    const int sms = sm_count();
+    const int rows = n < kLaunchRows ? n : kLaunchRows;
+    return ws_layout(make_plan(rows, V, sms > 0 ? sms : 1), rows, H, top).total;
+}
+
+extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t hidden_row_stride, int32_t hidden_rows,
+                                             const int32_t *d_row_idx, const blink_bf16 *unembed, int32_t V, int32_t H,
+                                             const int32_t *d_targets, int32_t n, float temperature, int32_t top,
+                                             float *d_logprob, float *d_entropy, float *d_lse, int32_t *d_top_ids,
+                                             float *d_top_logprobs, void *d_ws, size_t ws_bytes, cudaStream_t stream)
+{
+    using namespace blink;
+    if (!hidden || !unembed || !d_ws) return BLINK_INVALID_ARG;
+    if (!d_logprob && !d_entropy && !d_lse && !d_top_ids) return BLINK_INVALID_ARG;
+    if ((d_logprob && !d_targets) || (d_top_ids == nullptr) != (d_top_logprobs == nullptr)) return BLINK_INVALID_ARG;
+    if (!(temperature > 0.f) || !(temperature < INFINITY)) return BLINK_INVALID_ARG;
+    if (H < 8 || H % 8 != 0 || V < 1 || hidden_rows < 1 || hidden_row_stride < H || hidden_row_stride % 8 != 0)
+        return BLINK_INVALID_ARG;
+    if (!aligned16(hidden) || !aligned16(unembed)) return BLINK_INVALID_ARG;
+    if (top < 0 || top > kMaxTop || top > V || H > 32768 || V > (1 << 24)) return BLINK_OUT_OF_RANGE;
+    if ((top > 0) != (d_top_ids != nullptr)) return BLINK_INVALID_ARG;
+    if (n < 1 || n > BLINK_MAX_INPUT_TOKENS) return BLINK_OUT_OF_RANGE;
+    if (!d_row_idx && n > hidden_rows) return BLINK_INVALID_ARG;
+    if (ws_bytes < blink_token_logprobs_workspace(n, H, V, top)) return BLINK_WORKSPACE_TOO_SMALL;
+
+    for (int32_t r = 0; r < n; r += kLaunchRows) {
+        const int32_t rows = n - r < kLaunchRows ? n - r : kLaunchRows;
+        const blink_bf16 *h = d_row_idx ? hidden : hidden + r * hidden_row_stride;
+        auto at = [r](auto *p, int64_t width) { return p ? p + r * width : p; };
+        const blink_status st = run_logprobs(h, hidden_row_stride, d_row_idx ? hidden_rows : rows, at(d_row_idx, 1), unembed, V,
+                                             H, at(d_targets, 1), rows, temperature, top, at(d_logprob, 1), at(d_entropy, 1),
+                                             at(d_lse, 1), at(d_top_ids, top), at(d_top_logprobs, top), d_ws, stream);
+        if (st != BLINK_OK) return st;
+    }
     return BLINK_OK;
 }

@@ -208,6 +208,32 @@ def test_more_equal_best_logits_than_any_list_holds(n, V, top):
     assert torch.equal(r["top_ids"], want.expand(n, top))
 
 
+def test_more_rows_than_one_launch():
+    """8192 rows go in one launch: rows before and after the seam, gathered and direct."""
+    n, H, V = 8192 + 300, 64, 700
+    h, W, t = grid(n, H, V, seed=21)
+    want, _, zmax = ref(h, W, t, 1.0, 3)
+    r = blink.blink_token_logprobs(h, W, targets=t, top=3)
+    check(r, want, 0.0, zmax, H, V, True)
+    idx = torch.randperm(n, device="cuda").to(torch.int32)
+    r = blink.blink_token_logprobs(h, W, targets=t[idx.long()], row_idx=idx, top=3, ws=r["ws"])
+    check(r, {k: v[idx.long()] for k, v in want.items()}, 0.0, zmax, H, V, True)
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each: the same results as one after the other."""
+    a, b = normal(300, 512, 9000, seed=31), normal(40, 1024, 9000, seed=32)
+    want = [blink.blink_token_logprobs(h, W, targets=t, top=5) for h, W, t in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [blink.blink_token_logprobs(h, W, targets=t, top=5, stream=s) for (h, W, t), s in zip((a, b), streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for k in ("logprob", "entropy", "lse", "top_ids", "top_logprobs"):
+                assert torch.equal(g[k], w[k]), k
+
+
 def test_fewer_numbers_than_alternatives():
     """NaN rows of the unembedding: the other tokens are listed, then -1; the sums are NaN."""
     h = torch.ones(2, 64, dtype=BF, device="cuda")
