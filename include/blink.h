@@ -376,8 +376,8 @@ blink_status blink_label_readout_noalloc(const blink_bf16 *hidden, int64_t hidde
  * d_prev  fp32, head h at d_prev + h * prev_stride (stride >= P); may be d_weights itself with the
  *         same stride (accumulation in place), otherwise the two must not overlap
  * d_weights  fp32 output, head h at d_weights + h * w_stride (stride >= P)
- * d_ws    workspace of blink_prefix_key_weights_workspace(...) bytes, its first 256 zero-filled
- *         before its first use; not shared by calls that may run at the same time
+ * d_ws    workspace of blink_prefix_key_weights_workspace(...) bytes, 16-byte aligned, its first 256
+ *         zero-filled before its first use; not shared by calls that may run at the same time
  * The sum's order is fixed by the shapes and the GPU: repeated calls give the same bits.
  * Errors: BLINK_INVALID_ARG, BLINK_OUT_OF_RANGE, BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR;
  * device-side: BLINK_DEVICE_TIMEOUT.
@@ -414,8 +414,8 @@ blink_status blink_prefix_key_weights(const blink_bf16 *q, const blink_bf16 *k_p
  * d_weights_dst, d_pos_dst  optional outputs [Hkv][keep] (row strides wd_stride, pd_stride): weights
  *             and positions of the kept keys; each may be its input itself with the same stride, or
  *             memory that overlaps neither input
- * d_ws        workspace of blink_kv_evict_workspace(...) bytes (the error word; nothing on the device
- *             can fail in this call)
+ * d_ws        workspace of blink_kv_evict_workspace(...) bytes, 16-byte aligned; not shared by calls that
+ *             may run at the same time (its error word is never set: nothing on the device can fail here)
  * Errors: BLINK_INVALID_ARG (null, alignment, strides, overlap), BLINK_OUT_OF_RANGE (P, keep, Hkv, d),
  * BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR.
  * ------------------------------------------------------------------------------------------ */
@@ -447,8 +447,8 @@ blink_status blink_kv_evict(const float *d_weights, int64_t w_stride, const int3
  * temperature  > 0 and finite
  * top        0..BLINK_MAX_TOP_TOKENS alternatives per row, at most V
  * Outputs: each may be NULL, not all; d_top_ids and d_top_logprobs [n][top] together, when top > 0
- * d_ws       workspace of blink_token_logprobs_workspace(...) bytes (of the current device), its first
- *            256 zero-filled before its first use; not shared by calls that may run at the same time
+ * d_ws       workspace of blink_token_logprobs_workspace(...) bytes (of the current device), 16-byte aligned,
+ *            its first 256 zero-filled before its first use; not shared by calls that may run at the same time
  * A row index outside [0, hidden_rows) latches BLINK_DEVICE_FLAG and makes the row's outputs NaN and
  * -1; a target outside [-1, V) latches it and makes that log probability NaN.  A row with a NaN logit
  * gets NaN (ids: those of its other logits, then -1); logits must not be infinite.

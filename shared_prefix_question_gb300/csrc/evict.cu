@@ -9,14 +9,22 @@
 // One thread-block cluster per head, its blocks holding consecutive pieces of the head's keys in
 // shared memory: the weights are read once, the per-block histograms are summed through distributed
 // shared memory, and no global counter or atomic order enters the result.  A few thousand keys take a
-// block microseconds either way, so what it costs is the chain of barriers and remote reads: digits
-// are small (with 2048 bins the blocks read 64 KB of one another's histograms a digit, 4 us), one warp
-// joins them, and there is nothing in global memory between the steps.
+// block microseconds either way, so what it costs is the chain of barriers and remote reads, 3,400 cycles
+// a digit with 8 blocks of 2304 keys: digits are small (with 2048 bins the blocks read 64 KB of one
+// another's histograms a digit, 4 us), a thread sums a bin over the blocks, every warp finds the digit
+// for itself, and there is nothing in global memory between the steps.  The blocks hand each other their
+// counts by writing them before the last barrier, so that none has to wait for another's reads at its end.
 //
 // Compaction.  Kept keys below slot `keep` stay; the r-th evicted slot below `keep` (a hole) takes the
 // r-th kept slot at `keep` or above (a survivor).  Sources are never destinations, so the moves of
-// an in-place compaction need no order among themselves.  The selection writes each slot's source; a second
-// launch, its programmatic dependent, moves keys, values, weights and positions.
+// an in-place compaction need no order among themselves.  The selection writes each slot's source, or the
+// rank of its survivor, and the survivors' slots; a second launch, its programmatic dependent, joins the two
+// and moves keys, values, weights and positions.  (Joined in the selection, through the blocks' shared
+// memory, they cost it another 5 us of 32 at 131072 keys.)
+//
+// 8 kv heads of width 128, warm / with a cold L2: 9216 of 18432 keys 21 / 30 us (selection 10,
+// move 11), 32768 of 131072 keys 70 / 75 us (selection 25, move 42).  The move of the
+// largest runs at the copy rate; the selection's chain of barriers is what is left over it.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -35,16 +43,19 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kDigits = 4, kBins = 256;
 constexpr int kMaxPiece = (BLINK_MAX_INPUT_TOKENS + kMaxCluster - 1) / kMaxCluster;  // keys of one block
-constexpr int kClusterPiece = 8192;  // keys per block before a head gets more blocks (4096 and 16384 measure the same or slower)
+// Keys per block before a head gets more blocks.  18432 x 8: 22.5 us for the call with 4096, 26.1 with 8192
+// (2048 the same as 4096: the cluster is full).
+constexpr int kClusterPiece = 4096;
 constexpr int kLoadAhead = 8;
+constexpr int kFetchAhead = 16;  // weights and positions a thread has in flight (8: 131072 keys take 1 us more)
 
 struct EvictArgs {
     const float *w;
     const int32_t *pos;  // or nullptr: slot = position
     int64_t w_stride, pos_stride;
     int P, keep, sink, recent_from;
-    int piece;       // keys per block, a multiple of kSelThreads
-    int32_t *slots;  // [Hkv][keep]
+    int piece;                  // keys per block, a multiple of kSelThreads
+    int32_t *from, *survivors;  // [Hkv][keep]: a destination slot's source, or ~r for the head's r-th survivor; their slots
 };
 
 // Larger weight = larger unsigned; NaN = 1, so that 0 is below every key and ~0 above.
@@ -73,6 +84,9 @@ struct PieceCounts {  // of one block's or one warp's keys: above T and equal to
     int gt_low, gt_high, eq_low, eq_high, n_low;
 };
 
+// Bits [0, n) of a mask, n of any size.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // With `eq_before` keys equal to T in lower slots: holes and survivors among the counted keys.
 __device__ __forceinline__ int2 holes_and_survivors(const PieceCounts &c, int eq_before, int need)
 {
@@ -83,13 +97,12 @@ __device__ __forceinline__ int2 holes_and_survivors(const PieceCounts &c, int eq
 
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const EvictArgs a)
 {
-    extern __shared__ uint32_t keys[];  // [piece], then the survivors' slots [piece]
+    extern __shared__ uint32_t keys[];  // [piece]
     __shared__ __align__(16) uint32_t hist[kDigits][kBins];
     __shared__ PieceCounts warp_cnt[kSelWarps];
-    __shared__ PieceCounts block_cnt;
+    __shared__ PieceCounts block_cnt[kMaxCluster];  // written by the blocks themselves
     __shared__ int n_protected;
-    __shared__ uint32_t found_digit;
-    __shared__ int found_rest, found_count;
+    __shared__ __align__(16) int total[kBins];  // a digit's histogram over the blocks
     __shared__ bool too_many;
 
     cg::cluster_group cluster = cg::this_cluster();
@@ -101,7 +114,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int steps = a.piece / kSelThreads;
     const uint32_t below = (1u << lane) - 1u;
-    int32_t *surv_list = reinterpret_cast<int32_t *>(keys + a.piece);
     // Warp w owns the consecutive keys [w * piece / warps, ...), 32 at a step, so ballots give slot order.
     const int wbase = warp * (a.piece / kSelWarps);
     auto sync_all = [&] {
@@ -119,18 +131,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     // keys are candidates (there are more than `keep`); otherwise protected keys come before all others.
     auto load_keys = [&](bool among_them) {
         int n_guard = 0;
-        for (int s0 = 0; s0 < steps; s0 += kLoadAhead) {
-            float x[kLoadAhead];
-            int p[kLoadAhead];
+        for (int s0 = 0; s0 < steps; s0 += kFetchAhead) {
+            float x[kFetchAhead];
+            int p[kFetchAhead];
 #pragma unroll
-            for (int u = 0; u < kLoadAhead; ++u) {
+            for (int u = 0; u < kFetchAhead; ++u) {
                 const int i = wbase + (s0 + u) * 32 + lane;
                 const bool in = s0 + u < steps && i < n;
                 x[u] = in ? __ldg(w + lo + i) : 0.f;
                 p[u] = in && guarded ? (pos ? __ldg(pos + lo + i) : lo + i) : INT_MAX;
             }
 #pragma unroll
-            for (int u = 0; u < kLoadAhead; ++u) {
+            for (int u = 0; u < kFetchAhead; ++u) {
                 const int i = wbase + (s0 + u) * 32 + lane;
                 if (s0 + u >= steps) break;
                 const bool g = guarded && i < n && (p[u] < a.sink || p[u] >= a.recent_from);
@@ -161,7 +173,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     // ---- radix select of the keep-th largest key
     uint32_t prefix = 0u, mask = 0u;
     int want = a.keep;  // rank of the key looked for among those that match the prefix
-    bool among = false;
+    bool among = false, all_equal = false;
     for (int pass = 0; pass < kDigits; ++pass) {
         const int shift = 24 - 8 * pass;
         for (int s0 = 0; s0 < steps; s0 += kLoadAhead) {
@@ -174,49 +186,34 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
                     atomicAdd(&hist[pass][(key[u] >> shift) & 255u], 1u);
         }
         sync_all();
-        if (warp == 0) {
-            // lane l: bins 255 - 8 l down to 248 - 8 l, summed over the blocks
-            const int b0 = kBins - 8 - 8 * lane;
-            uint4 part[kMaxCluster][2];
-            int guards = 0;
-#pragma unroll
-            for (int c = 0; c < kMaxCluster; ++c) {
-                part[c][0] = part[c][1] = make_uint4(0u, 0u, 0u, 0u);
-                if (c < C) {
-                    const uint4 *h = reinterpret_cast<const uint4 *>(cluster.map_shared_rank(hist[pass], c) + b0);
-                    part[c][0] = h[0];
-                    part[c][1] = h[1];
-                    if (pass == 0 && guarded) guards += *cluster.map_shared_rank(&n_protected, c);
-                }
-            }
-            int cnt[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // of bins b0 + 7, ..., b0
-#pragma unroll
-            for (int c = 0; c < kMaxCluster; ++c) {
-                cnt[0] += static_cast<int>(part[c][1].w);
-                cnt[1] += static_cast<int>(part[c][1].z);
-                cnt[2] += static_cast<int>(part[c][1].y);
-                cnt[3] += static_cast<int>(part[c][1].x);
-                cnt[4] += static_cast<int>(part[c][0].w);
-                cnt[5] += static_cast<int>(part[c][0].z);
-                cnt[6] += static_cast<int>(part[c][0].y);
-                cnt[7] += static_cast<int>(part[c][0].x);
-            }
-            int mine = 0;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) mine += cnt[q];
-            int above = sum_before(mine, lane);  // keys in the bins above this lane's
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if (above < want && want <= above + cnt[q]) {
-                    found_digit = static_cast<uint32_t>(b0 + 7 - q);
-                    found_rest = want - above;
-                    found_count = cnt[q];
-                }
-                above += cnt[q];
-            }
+        if (tid < kBins) {
+            int sum = 0;
+#pragma unroll 8
+            for (int c = 0; c < C; ++c) sum += static_cast<int>(*cluster.map_shared_rank(&hist[pass][tid], c));
+            total[tid] = sum;
+        } else if (pass == 0 && guarded && warp == kBins / 32) {
+            const int guards = warp_sum(lane < C ? *cluster.map_shared_rank(&n_protected, lane) : 0);
             if (lane == 0) too_many = !among && guards > a.keep;
         }
         __syncthreads();
+        // every warp: lane l has the bins 255 - 8 l down to 248 - 8 l
+        const int b0 = kBins - 8 - 8 * lane;
+        const int4 t1 = *reinterpret_cast<const int4 *>(total + b0 + 4), t0 = *reinterpret_cast<const int4 *>(total + b0);
+        const int cnt[8] = {t1.w, t1.z, t1.y, t1.x, t0.w, t0.z, t0.y, t0.x};
+        const int mine = ((t1.w + t1.z) + (t1.y + t1.x)) + ((t0.w + t0.z) + (t0.y + t0.x));
+        int above = sum_before(mine, lane);  // keys in the bins above this lane's
+        const bool here = above < want && want <= above + mine;
+        uint32_t digit = 0u;
+        int rest = 0, count = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (above < want && want <= above + cnt[q]) {
+                digit = static_cast<uint32_t>(b0 + 7 - q);
+                rest = want - above;
+                count = cnt[q];
+            }
+            above += cnt[q];
+        }
         if (pass == 0 && guarded && too_many) {
             // More protected keys than `keep` (seldom): again, among them alone.
             among = true;
@@ -227,32 +224,32 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
             pass = -1;
             continue;
         }
-        prefix |= found_digit << shift;
+        const int from = __ffs(static_cast<int>(__ballot_sync(0xFFFFFFFFu, here))) - 1;
+        prefix |= __shfl_sync(0xFFFFFFFFu, digit, from) << shift;
         mask |= 255u << shift;
-        want = found_rest;
-        const bool done = want == found_count;  // every key with this prefix is kept: T is the lowest it could be
-        if (done) {
-            want = INT_MAX;
-            break;
-        }
+        want = __shfl_sync(0xFFFFFFFFu, rest, from);
+        // every key with this prefix is kept: T is the lowest it could be
+        all_equal = want == __shfl_sync(0xFFFFFFFFu, count, from);
+        if (all_equal) break;
     }
-    const uint32_t T = prefix;
-    const int need = want;  // how many of the keys equal to T are kept: the lowest slots
+    const uint32_t T = max(prefix, 1u);  // no key is 0: the padding is below T
+    const int need = want;  // unless all of them are: how many of the keys equal to T are kept, the lowest slots
+    auto above_T = [&](uint32_t key) { return all_equal ? key >= T : key > T; };
 
     // ---- counts per warp and block, then every warp's place in the slot order
-    PieceCounts my = {0, 0, 0, 0, 0};
+    const int left_low = min(n, a.keep - lo) - wbase;  // this warp's keys below `keep`
+    uint32_t seen = 0u;  // bytes: above T below `keep` and not, equal to T likewise; a thread has at most 32 keys
 #pragma unroll 8
     for (int s = 0; s < steps; ++s) {
         const int i = wbase + s * 32 + lane;
         const uint32_t key = keys[i];
-        const bool in = i < n, low = lo + i < a.keep;
-        my.gt_low += in && low && key > T;
-        my.gt_high += in && !low && key > T;
-        my.eq_low += in && low && key == T;
-        my.eq_high += in && !low && key == T;
-        my.n_low += in && low;
+        const uint32_t one = above_T(key) ? 1u : key == T ? 0x10000u : 0u;
+        seen += lo + i < a.keep ? one : one << 8;
     }
-    my = {warp_sum(my.gt_low), warp_sum(my.gt_high), warp_sum(my.eq_low), warp_sum(my.eq_high), warp_sum(my.n_low)};
+    static_assert(kMaxPiece / kSelThreads < 256, "a thread's counts are bytes");
+    const int in_low = static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, seen & 0x00FF00FFu));
+    const int in_high = static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, seen >> 8 & 0x00FF00FFu));
+    const PieceCounts my = {in_low & 0xFFFF, in_high & 0xFFFF, in_low >> 16, in_high >> 16, max(0, min(left_low, steps * 32))};
     if (lane == 0) warp_cnt[warp] = my;
     __syncthreads();
     const PieceCounts none = {0, 0, 0, 0, 0};
@@ -260,82 +257,66 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
     if (warp == 0) {
         const PieceCounts t = {warp_sum(wc.gt_low), warp_sum(wc.gt_high), warp_sum(wc.eq_low), warp_sum(wc.eq_high),
                                warp_sum(wc.n_low)};
-        if (lane == 0) block_cnt = t;
+        if (lane < C) *cluster.map_shared_rank(&block_cnt[rank], lane) = t;
     }
-    sync_all();
-    const PieceCounts bc = lane < C ? *cluster.map_shared_rank(&block_cnt, lane) : none;  // lane l: block l
+    sync_all();  // the last access to another block's memory is behind it
+    const PieceCounts bc = lane < C ? block_cnt[lane] : none;  // lane l: block l
     const int bc_eq_before = sum_before(bc.eq_low + bc.eq_high, lane);
     const int2 bc_hs = holes_and_survivors(bc, bc_eq_before, need);
-    const int block_surv = sum_before(bc_hs.y, lane);  // lane l: survivors in the blocks before block l
     int eq_before = __shfl_sync(0xFFFFFFFFu, bc_eq_before, rank);
-    int hole = warp_sum(lane < rank ? bc_hs.x : 0);
+    int hole = warp_sum(lane < rank ? bc_hs.x : 0), surv = warp_sum(lane < rank ? bc_hs.y : 0);
     const int wc_eq_before = eq_before + sum_before(wc.eq_low + wc.eq_high, lane);
     const int2 wc_hs = holes_and_survivors(wc, wc_eq_before, need);
     eq_before = __shfl_sync(0xFFFFFFFFu, wc_eq_before, warp);
     hole += warp_sum(lane < warp ? wc_hs.x : 0);
-    int surv = warp_sum(lane < warp ? wc_hs.y : 0);  // in this block's list
+    surv += warp_sum(lane < warp ? wc_hs.y : 0);
 
-    int32_t *slots = a.slots + static_cast<int64_t>(head) * a.keep;
+    int32_t *from = a.from + static_cast<int64_t>(head) * a.keep;
+    int32_t *survivors = a.survivors + static_cast<int64_t>(head) * a.keep;
 #pragma unroll 4
     for (int s = 0; s < steps; ++s) {
-        const int i = wbase + s * 32 + lane;
-        const int slot = lo + i;
-        const uint32_t key = keys[i];
-        const bool in = i < n, low = slot < a.keep;
-        const uint32_t eq = __ballot_sync(0xFFFFFFFFu, in && key == T);
-        const bool kept = in && (key > T || (key == T && eq_before + __popc(eq & below) < need));
-        eq_before += __popc(eq);
-        const uint32_t hm = __ballot_sync(0xFFFFFFFFu, in && low && !kept);
-        const uint32_t sm = __ballot_sync(0xFFFFFFFFu, kept && !low);
-        if (kept && !low) surv_list[surv + __popc(sm & below)] = slot;
-        keys[i] = in && low && !kept ? static_cast<uint32_t>(hole + __popc(hm & below)) : kept && low ? ~1u : ~0u;
-        hole += __popc(hm);
-        surv += __popc(sm);
-    }
-    // every block's list is complete: the r-th hole takes the r-th survivor
-    sync_all();
-    int first[kMaxCluster];  // survivors in the blocks before block c
-#pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) first[c] = __shfl_sync(0xFFFFFFFFu, block_surv, c);
-    for (int s0 = 0; s0 < steps; s0 += kLoadAhead) {
-        int from[kLoadAhead];
-#pragma unroll
-        for (int u = 0; u < kLoadAhead; ++u) {
-            const int i = wbase + (s0 + u) * 32 + lane;
-            const uint32_t r = s0 + u < steps ? keys[i] : ~0u;
-            from[u] = r == ~1u ? lo + i : -1;
-            if (r < ~1u) {
-                int owner = 0, base = 0;  // the block with survivor r
-#pragma unroll
-                for (int c = 1; c < kMaxCluster; ++c)
-                    if (c < C && static_cast<int>(r) >= first[c]) owner = c, base = first[c];
-                from[u] = cluster.map_shared_rank(surv_list, owner)[static_cast<int>(r) - base];
-            }
+        const int slot = lo + wbase + s * 32 + lane;
+        const uint32_t key = keys[wbase + s * 32 + lane];
+        const uint32_t low = low_bits(left_low - s * 32);
+        uint32_t kept = __ballot_sync(0xFFFFFFFFu, above_T(key));
+        if (!all_equal) {
+            const uint32_t eq = __ballot_sync(0xFFFFFFFFu, key == T);
+            kept |= __ballot_sync(0xFFFFFFFFu, key == T && eq_before + __popc(eq & below) < need);
+            eq_before += __popc(eq);
         }
-#pragma unroll
-        for (int u = 0; u < kLoadAhead; ++u)
-            if (from[u] >= 0) slots[lo + wbase + (s0 + u) * 32 + lane] = from[u];
+        const uint32_t holes = low & ~kept, moves = kept & ~low;
+        if (low >> lane & 1u) from[slot] = kept >> lane & 1u ? slot : ~(hole + __popc(holes & below));
+        if (moves >> lane & 1u) survivors[surv + __popc(moves & below)] = slot;
+        hole += __popc(holes);
+        surv += __popc(moves);
     }
-    sync_all();  // no block leaves while another may still read its shared memory
 }
 
 struct MoveArgs {
     const uint4 *k, *v;  // 16-byte pieces
     uint4 *k_dst, *v_dst;
     int64_t row_stride, dst_stride;  // in 16-byte pieces
-    const int32_t *slots;
+    const int32_t *from, *survivors;
+    int32_t *slots;
     const float *w;
     float *w_dst;  // or nullptr
     const int32_t *pos;
     int32_t *pos_dst;  // or nullptr
     int64_t w_stride, wd_stride, pos_stride, pd_stride;
-    unsigned row_blocks;
-    int Hkv, keep, pieces, row_pieces;  // pieces: of one key (d / 8); row_pieces: of a row (Hkv d / 8)
+    unsigned row_blocks, head_groups;
+    int Hkv, keep, pieces;  // pieces: of one key (d / 8)
     int skip_k, skip_v;            // in place: a key that stays is not copied
 };
 
+__device__ __forceinline__ int source_slot(const MoveArgs &a, int64_t head, int64_t j)
+{
+    const int f = __ldg(a.from + head * a.keep + j);
+    return f >= 0 ? f : __ldg(a.survivors + head * a.keep + ~f);
+}
+
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 16;  // destination rows of a block
+constexpr int kMoveRows = 16;  // destination rows of a block (32: 27 us instead of 22 for 18432 keys; 8 the same)
+constexpr int kMoveHeads = 64;  // and heads
 constexpr int kMoveAhead = 4;
 
 // A thread moves 16-byte pieces of destination rows, K and V, kMoveAhead of them in flight together.  The
@@ -348,14 +329,25 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
         const int64_t t = static_cast<int64_t>(blockIdx.x - a.row_blocks) * kMoveThreads + threadIdx.x;
         const int64_t head = t / a.keep, j = t - head * a.keep;
         if (head >= a.Hkv) return;
-        const int slot = __ldg(a.slots + t);
+        const int slot = source_slot(a, head, j);
+        a.slots[t] = slot;
         if (a.w_dst) a.w_dst[head * a.wd_stride + j] = a.w[head * a.w_stride + slot];
         if (a.pos_dst) a.pos_dst[head * a.pd_stride + j] = a.pos ? a.pos[head * a.pos_stride + slot] : slot;
         return;
     }
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * kMoveRows;
+    __shared__ int slot_of[kMoveRows * kMoveHeads];  // [head][row]
+    const unsigned tile = blockIdx.x / a.head_groups;
+    const int h0 = static_cast<int>(blockIdx.x - tile * a.head_groups) * kMoveHeads;
+    const int heads = min(kMoveHeads, a.Hkv - h0);
+    const int64_t j0 = static_cast<int64_t>(tile) * kMoveRows;
     const int rows = static_cast<int>(min(static_cast<int64_t>(kMoveRows), a.keep - j0));
-    const int total = rows * a.row_pieces;
+    for (int i = threadIdx.x; i < heads * kMoveRows; i += kMoveThreads) {
+        const int row = i % kMoveRows;
+        if (row < rows) slot_of[i] = source_slot(a, h0 + i / kMoveRows, j0 + row);
+    }
+    __syncthreads();
+    const int width = heads * a.pieces, total = rows * width;  // 16-byte pieces
+    const int64_t c0 = static_cast<int64_t>(h0) * a.pieces;
     for (int t0 = threadIdx.x; t0 < total; t0 += kMoveThreads * kMoveAhead) {
         uint4 kv[kMoveAhead], vv[kMoveAhead];
         int64_t dst[kMoveAhead];
@@ -363,14 +355,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
 #pragma unroll
         for (int u = 0; u < kMoveAhead; ++u) {
             const int t = t0 + u * kMoveThreads;
-            const int row = t / a.row_pieces, c = t - row * a.row_pieces;
+            const int row = t / width, c = t - row * width;
             const int64_t j = j0 + row;
-            int slot = 0;
-            if (t < total) slot = __ldg(a.slots + static_cast<int64_t>(c / a.pieces) * a.keep + j);
+            const int slot = t < total ? slot_of[c / a.pieces * kMoveRows + row] : 0;
             do_k[u] = t < total && !(slot == j && a.skip_k);
             do_v[u] = t < total && !(slot == j && a.skip_v);
-            dst[u] = j * a.dst_stride + c;
-            const int64_t src = slot * a.row_stride + c;
+            dst[u] = j * a.dst_stride + c0 + c;
+            const int64_t src = slot * a.row_stride + c0 + c;
             if (do_k[u]) kv[u] = __ldcs(a.k + src);
             if (do_v[u]) vv[u] = __ldcs(a.v + src);
         }
@@ -401,8 +392,9 @@ bool rows_overlap(const void *a, int64_t sa, int64_t na, const void *b, int64_t 
 extern "C" size_t blink_kv_evict_workspace(int32_t P, int32_t keep, int32_t Hkv)
 {
     using namespace blink;
-    (void)P, (void)keep, (void)Hkv;
-    return kHeaderBytes;
+    (void)P;
+    if (keep < 1 || Hkv < 1) return kHeaderBytes;
+    return kHeaderBytes + 2 * sizeof(int32_t) * static_cast<size_t>(Hkv) * static_cast<size_t>(keep);
 }
 
 extern "C" blink_status blink_kv_evict(const float *d_weights, int64_t w_stride, const int32_t *d_pos,
@@ -425,7 +417,8 @@ extern "C" blink_status blink_kv_evict(const float *d_weights, int64_t w_stride,
     if (d_pos && pos_stride < P && Hkv > 1) return BLINK_INVALID_ARG;
     if ((d_weights_dst && wd_stride < keep && Hkv > 1) || (d_pos_dst && pd_stride < keep && Hkv > 1))
         return BLINK_INVALID_ARG;
-    if (!aligned16(k) || !aligned16(v) || !aligned16(k_dst) || !aligned16(v_dst)) return BLINK_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_dst) || !aligned16(v_dst) || !aligned16(d_ws))
+        return BLINK_INVALID_ARG;
     const bool k_in = k_dst == k && dst_row_stride == row_stride, v_in = v_dst == v && dst_row_stride == row_stride;
     const int64_t rb = row * 2, sb = row_stride * 2, db = dst_row_stride * 2;
     if ((!k_in && rows_overlap(k, sb, P, k_dst, db, keep, rb)) || (!v_in && rows_overlap(v, sb, P, v_dst, db, keep, rb)) ||
@@ -463,11 +456,12 @@ extern "C" blink_status blink_kv_evict(const float *d_weights, int64_t w_stride,
     int C = 1;  // blocks per head: pieces of kClusterPiece keys and more, at most kMaxCluster of them
     while (C < kMaxCluster && P > C * kClusterPiece) C *= 2;
     e.piece = (P + C * kSelThreads - 1) / (C * kSelThreads) * kSelThreads;
-    e.slots = d_slots;
+    e.from = reinterpret_cast<int32_t *>(static_cast<char *>(d_ws) + kHeaderBytes);
+    e.survivors = e.from + static_cast<int64_t>(Hkv) * keep;
 
-    const int smem = 2 * e.piece * static_cast<int>(sizeof(uint32_t));
+    const int smem = e.piece * static_cast<int>(sizeof(uint32_t));
     if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             2 * kMaxPiece * static_cast<int>(sizeof(uint32_t))) != cudaSuccess)
+                             kMaxPiece * static_cast<int>(sizeof(uint32_t))) != cudaSuccess)
         return BLINK_CUDA_ERROR;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -490,6 +484,8 @@ extern "C" blink_status blink_kv_evict(const float *d_weights, int64_t w_stride,
     m.v_dst = reinterpret_cast<uint4 *>(v_dst);
     m.row_stride = row_stride / 8;
     m.dst_stride = dst_row_stride / 8;
+    m.from = e.from;
+    m.survivors = e.survivors;
     m.slots = d_slots;
     m.w = d_weights;
     m.w_dst = d_weights_dst;
@@ -499,19 +495,18 @@ extern "C" blink_status blink_kv_evict(const float *d_weights, int64_t w_stride,
     m.wd_stride = wd_stride;
     m.pos_stride = pos_stride;
     m.pd_stride = pd_stride;
-    m.row_blocks = static_cast<unsigned>((keep + kMoveRows - 1) / kMoveRows);
+    m.head_groups = static_cast<unsigned>((Hkv + kMoveHeads - 1) / kMoveHeads);
+    m.row_blocks = m.head_groups * static_cast<unsigned>((keep + kMoveRows - 1) / kMoveRows);
     m.Hkv = Hkv;
     m.keep = keep;
     m.pieces = d / 8;
-    m.row_pieces = Hkv * (d / 8);
     m.skip_k = k_in;
     m.skip_v = v_in;
     cudaLaunchConfig_t mc = {};
     cudaLaunchAttribute ma[1];
     ma[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     ma[0].val.programmaticStreamSerializationAllowed = 1;
-    const int64_t list_blocks =
-        d_weights_dst || d_pos_dst ? (static_cast<int64_t>(Hkv) * keep + kMoveThreads - 1) / kMoveThreads : 0;
+    const int64_t list_blocks = (static_cast<int64_t>(Hkv) * keep + kMoveThreads - 1) / kMoveThreads;
     mc.gridDim = dim3(m.row_blocks + static_cast<unsigned>(list_blocks));
     mc.blockDim = dim3(kMoveThreads);
     mc.stream = stream;

@@ -511,7 +511,7 @@ extern "C" blink_status blink_prefix_key_weights(const blink_bf16 *q, const blin
                                                  int64_t w_stride, void *d_ws, size_t ws_bytes, cudaStream_t stream)
 {
     using namespace blink;
-    if (!q || !k_pre || !lse || !d_weights || !d_ws) return BLINK_INVALID_ARG;
+    if (!q || !k_pre || !lse || !d_weights || !d_ws || !aligned16(d_ws)) return BLINK_INVALID_ARG;
     if (rows < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 128 || (d != 64 && d != 128))
         return BLINK_INVALID_ARG;
     if (P < 1 || P > BLINK_MAX_INPUT_TOKENS || Hkv > 65535 || rows > (1 << 30)) return BLINK_OUT_OF_RANGE;

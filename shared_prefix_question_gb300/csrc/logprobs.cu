@@ -1041,7 +1041,7 @@ extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t h
     if (!(temperature > 0.f) || !(temperature < INFINITY)) return BLINK_INVALID_ARG;
     if (H < 8 || H % 8 != 0 || V < 1 || hidden_rows < 1 || hidden_row_stride < H || hidden_row_stride % 8 != 0)
         return BLINK_INVALID_ARG;
-    if (!aligned16(hidden) || !aligned16(unembed)) return BLINK_INVALID_ARG;
+    if (!aligned16(hidden) || !aligned16(unembed) || !aligned16(d_ws)) return BLINK_INVALID_ARG;
     if (top < 0 || top > kMaxTop || top > V || H > 32768 || V > (1 << 24)) return BLINK_OUT_OF_RANGE;
     if ((top > 0) != (d_top_ids != nullptr)) return BLINK_INVALID_ARG;
     if (n < 1 || n > BLINK_MAX_INPUT_TOKENS) return BLINK_OUT_OF_RANGE;

@@ -130,3 +130,22 @@ def test_binding_refuses_host_tensors_and_shapes():
     blink._need("k", fake(torch.zeros(8, 4, 64, dtype=bf)[:, :2]), bf, (8, 2, 64), inner=2)  # strided rows are fine
     with pytest.raises(ValueError, match="contiguous"):
         blink._need("weights", fake(torch.zeros(8, 2).t()), f32, (2, 8))
+
+
+def test_workspaces_have_to_be_aligned(lib):
+    """The scratch behind a workspace's header holds 32-bit words and rows that copies of 16 bytes read."""
+    ws, n = _p(FAKE + 0x90008), 1 << 34
+    a, b, c = (_p(K + i * 0x1000000) for i in range(3))
+    assert lib.blink_prefix_key_weights(a, b, 128, c, 10, 10, 64, 4, 2, 64, 0.0, 0.0, None, 64, _p(FAKE + 0x80000), 64, ws, n,
+                                        None) == INVALID
+    assert lib.blink_kv_evict(a, 100, None, 100, 100, 40, 0, 2**31 - 1, 2, 64, _p(V), b, 128, _p(KD), _p(VD), 128, c, None, 40,
+                              None, 40, ws, n, None) == INVALID
+    assert lib.blink_token_logprobs(a, 256, 10, None, b, 1024, 256, None, 10, 1.0, 0, None, c, None, None, None, ws, n,
+                                    None) == INVALID
+
+
+def test_evict_workspace_grows_with_the_kept_keys(lib):
+    sizes = [blink.kv_evict_workspace_bytes(131072, keep, 8) for keep in (1, 1000, 131072)]
+    assert sizes == sorted(sizes) and sizes[-1] >= 2 * 4 * 8 * 131072
+    for bad in ((100, 0, 2), (100, 10, 0), (100, -1, 2)):
+        assert blink.kv_evict_workspace_bytes(*bad) >= 256

@@ -175,3 +175,27 @@ def test_repeat_bitwise_own_stream_and_graph():
     pos = np.tile(np.arange(30000, dtype=np.int32), (4, 1))
     assert np.array_equal(slots.cpu().numpy(), want_slots(wt.cpu().numpy(), pos, 7000, 0, 2**31 - 1))
     assert torch.equal(bits(kd), bits(k)[slots.long().t(), torch.arange(4, device="cuda")])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("P,keep,Hkv,d", [(40, 17, 64, 8), (300, 100, 65, 8), (300, 299, 130, 16), (4096, 2048, 2, 64),
+                                          (4097, 2049, 3, 64), (16385, 8000, 2, 64), (16896, 16000, 5, 64),
+                                          (32769, 5, 2, 64), (32768, 32767, 1, 64)])
+def test_many_heads_and_piece_edges(P, keep, Hkv, d, in_place):
+    """More heads than a moving block takes, and lengths at the edges of the blocks' pieces."""
+    w, k, v = inputs(P, Hkv, d, seed=P + Hkv, kind="zeros")
+    run_and_check(w, k, v, keep, in_place=in_place)
+
+
+def test_a_workspace_carries_nothing_over():
+    """Calls of other sizes with one workspace, its scratch full of other values: as with a new one."""
+    ws = torch.full((blink.kv_evict_workspace_bytes(9000, 4500, 4),), 0x5A, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    for P, keep, Hkv in ((9000, 4500, 4), (700, 33, 2), (9000, 100, 4), (5000, 4500, 1)):
+        w, k, v = inputs(P, Hkv, 64, seed=P + keep)
+        wt = torch.from_numpy(w).cuda()
+        kd, vd = (torch.zeros(keep, Hkv, 64, dtype=BF, device="cuda") for _ in range(2))
+        r = blink.blink_kv_evict(wt, k, v, keep, k_dst=kd, v_dst=vd, ws=ws)
+        assert np.array_equal(r["slots"].cpu().numpy(),
+                              want_slots(w, np.tile(np.arange(P, dtype=np.int32), (Hkv, 1)), keep, 0, 2**31 - 1))
+    assert blink.blink_read_device_status(ws) == blink.BLINK_OK
