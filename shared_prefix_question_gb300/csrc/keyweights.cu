@@ -448,23 +448,39 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
     if (warp == 0) ptx::tmem_dealloc(tmem, kTmem);
 }
 
-// One block per unit: adds the pieces of a unit that range boundaries cut, in block order.
-__global__ void __launch_bounds__(kUnitKeys) key_weights_join_kernel(const KeyWeightArgs a, int blocks)
+constexpr int kJoinThreads = kUnitKeys / 2;
+
+// One block per unit: adds the pieces of a unit that range boundaries cut, in block order.  128 threads of 32
+// registers are what the SM has left beside a block of the sums, so these are resident before that ends
+// and have their divisions and previous weights behind them.
+__global__ void __launch_bounds__(kJoinThreads) key_weights_join_kernel(const KeyWeightArgs a, int blocks)
 {
-    ptx::grid_dep_wait();
     const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.n_tiles, hi = lo + a.n_tiles;
     const int b0 = static_cast<int>(((lo + 1) * blocks - 1) / a.total);  // the block that has step lo
     const int b1 = static_cast<int>((hi * blocks - 1) / a.total);        // and step hi - 1
-    if (b0 == b1) return;
     const int head = blockIdx.x / a.n_units_head;
-    const int key = (blockIdx.x - head * a.n_units_head) * kUnitKeys + threadIdx.x;
-    if (key >= a.P) return;
-    float sum = 0.f;
-    for (int b = b0; b <= b1; ++b) {
-        const int piece = first_step(b, a.total, blocks) >= lo ? 0 : 1;
-        sum += __ldcg(a.part + (static_cast<int64_t>(b) * 2 + piece) * kUnitKeys + threadIdx.x);
+    const int key = (blockIdx.x - head * a.n_units_head) * kUnitKeys + 2 * threadIdx.x;
+    const bool cut = b0 != b1;
+    // the unit is the second piece of its first block, unless the block begins with it, and the first of all others
+    const float2 *part = reinterpret_cast<const float2 *>(a.part) + static_cast<int64_t>(b0) * kUnitKeys + threadIdx.x;
+    const int first_piece = first_step(b0, a.total, blocks) >= lo ? 0 : 1;
+    float before[2] = {0.f, 0.f};
+    if (cut && a.decay > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (key + i < a.P) before[i] = a.prev[head * a.prev_stride + key + i];
     }
-    a.w[head * a.w_stride + key] = a.decay > 0.f ? fmaf(a.decay, a.prev[head * a.prev_stride + key], sum) : sum;
+    ptx::grid_dep_wait();
+    if (!cut) return;
+    float2 sum = __ldcg(part + first_piece * kJoinThreads);
+#pragma unroll 4
+    for (int b = 1; b <= b1 - b0; ++b) {
+        const float2 v = __ldcg(part + static_cast<int64_t>(b) * kUnitKeys);
+        sum.x += v.x, sum.y += v.y;
+    }
+    float *w = a.w + head * a.w_stride + key;
+    if (key < a.P) w[0] = a.decay > 0.f ? fmaf(a.decay, before[0], sum.x) : sum.x;
+    if (key + 1 < a.P) w[1] = a.decay > 0.f ? fmaf(a.decay, before[1], sum.y) : sum.y;
 }
 
 int sm_count()
@@ -576,7 +592,7 @@ extern "C" blink_status blink_prefix_key_weights(const blink_bf16 *q, const blin
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(Hkv * a.n_units_head));
-    cfg.blockDim = dim3(kUnitKeys);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
