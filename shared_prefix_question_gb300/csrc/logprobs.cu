@@ -21,7 +21,7 @@
 //
 // Precision.  The tensor core's fp32 accumulator truncates: over a sum of H / 16 steps the loss grows
 // with H (measured against 64 bits, logits of 12: 2.7e-6 of the logit at H = 2560, 5.4e-6 at 5120, and
-// four times that where all products have one sign).  So a product runs over at most 512 of H only,
+// four times that where all products have one sign).  So a product runs over at most 512 of H only (256 for few rows),
 // and the row's thread adds the parts in registers, rounded to nearest: the loss stays that of one part
 // whatever H is.
 //
@@ -54,9 +54,11 @@ constexpr int kProducerLP = 8, kIssuerLP = 9;
 constexpr int kHalves = 2;      // threads that share a row
 constexpr int kHalfCols = kVocabTile / kHalves;
 // At most this many 64-wide blocks of H per product.  Measured at H = 2560, entropy against 64 bits: 1.5e-6
-// off with 10 blocks, 0.95e-6 with 8, 0.7e-6 with 6; pairs take 4 % longer with 6 than with 8, and 1 % less
-// with 10.
-constexpr int kPartBlocks = 8;
+// off with 10 blocks, 0.95e-6 with 8, 0.7e-6 with 6, 0.4e-6 with 4; pairs take 4 % longer with 6 than with 8,
+// and 1 % less with 10; one block with 64 rows takes 3 % longer with 4.  Up to 32 rows only a quarter of the
+// threads have a row and the shorter parts cost 0.5 %.
+constexpr int kPartBlocks = 8, kPartBlocksFew = 4;
+constexpr int kFewRows = 32;
 // 64-wide blocks of H per stage of the ring.  A pair's issuer loses some 120 cycles of the tensor core at every
 // barrier it waits for: with two blocks a stage 4096 tokens take 1.73 ms instead of 1.82.  One block alone
 // waits for memory, and more, smaller stages suit it.
@@ -416,7 +418,8 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
     const int passes = a.plan.passes();
     const int k_blocks = (a.H + 63) / 64;
     constexpr int kStageBlocks = kCtas == 1 ? kStageBlocksOne : kStageBlocksPair;
-    const int n_parts = (k_blocks + kPartBlocks - 1) / kPartBlocks;
+    const int most = kCtas == 1 && a.n <= kFewRows ? kPartBlocksFew : kPartBlocks;
+    const int n_parts = (k_blocks + most - 1) / most;
     const int part_blocks = ((k_blocks + n_parts - 1) / n_parts + kStageBlocks - 1) / kStageBlocks * kStageBlocks;
     const bool aligned = (ptx::smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need it
     if (!aligned && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
