@@ -22,7 +22,16 @@
 // MMA issuer (32 registers).  Tensor memory: two score tiles of 256 columns.
 // What bounds it: a tile is 1,024 cycles of the tensor core and 1,024 of the exp2 unit (8 lanes a clock on
 // each of the SM's four partitions, measured), so the four warps of a partition have to keep one
-// unit busy while others wait for scores.  Two warps with 128 keys each took 1,590 cycles a tile.
+// unit busy while others wait for scores.  Two warps with 128 keys each took 1,590 cycles a tile.  10240
+// rows, 18432 keys, 32/8 heads of 128: 950-965 us, 1,480 cycles a tile, both units 69 % busy (the products
+// alone, with nothing reading them, take 732 us); 1275 rows, 2048 keys: 26 us, of which the 17 tiles of a
+// block are 13 and the launch, the first loads and the join the rest.  Slower, at 18432 keys: a part of
+// the exponentials as a polynomial on the fused multiply-add units (1.01 ms with an eighth of them, 1.27
+// with three eighths), scores read two tiles ahead (1.3), halves of 128 keys (1.27), scalar instead of
+// paired adds (1.1).
+//
+// Short calls.  One row and 18432 keys read 38 MB: 12 us warm, 22 with a cold L2, where the floor is 5.6;
+// 60 rows and 64 keys 8 us, one launch.
 //
 // A column that does not count has -b = -inf, so its term is 0: rows past the last (Q is zero there) and
 // rows owned by no question.  Only the latter may hold NaN or infinities in q; a warp with such a row
