@@ -390,7 +390,7 @@ def _need(name, t, dtype, shape, inner: int = 1):
 
 def _row_stride(t) -> int:
     """Elements between the rows (first dimension) of `t`; a single row has any stride."""
-    return t.stride(0) if t.shape[0] > 1 else t[0].numel()
+    return t[0].numel() if t.shape[0] == 1 else t.stride(0)
 
 
 def _addr(t):
@@ -515,7 +515,7 @@ def blink_kv_evict(weights, k, v, keep: int, pos=None, sink: int = 0, recent_fro
     else:
         _need("k_dst", k_dst, torch.bfloat16, (keep, Hkv, d), inner=2)
         _need("v_dst", v_dst, torch.bfloat16, (keep, Hkv, d), inner=2)
-        dst_stride = _row_stride(k_dst)
+        dst_stride = _row_stride(k_dst) if keep > 1 else src_stride  # one row: so that it may be row 0 of k
         if keep > 1 and v_dst.stride(0) != dst_stride:
             raise ValueError("k_dst and v_dst must have the same row stride")
     if weights_dst is not None:

@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
 
     const float *w = a.w + head * a.w_stride;
     const int32_t *pos = a.pos ? a.pos + head * a.pos_stride : nullptr;
-    const bool guarded = a.sink > 0 || a.recent_from < INT_MAX;
+    const bool recent = a.recent_from < INT_MAX;
+    const bool guarded = a.sink > 0 || recent;
     // Fills keys[]; returns how many of this thread's keys are protected.  `among_them`: only protected
     // keys are candidates (there are more than `keep`); otherwise protected keys come before all others.
     auto load_keys = [&](bool among_them) {
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Evic
             for (int u = 0; u < kFetchAhead; ++u) {
                 const int i = wbase + (s0 + u) * 32 + lane;
                 if (s0 + u >= steps) break;
-                const bool g = guarded && i < n && (p[u] < a.sink || p[u] >= a.recent_from);
+                const bool g = guarded && i < n && (p[u] < a.sink || (recent && p[u] >= a.recent_from));
                 n_guard += g;
                 uint32_t key = weight_key(x[u]);
                 if (among_them)

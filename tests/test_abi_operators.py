@@ -149,3 +149,12 @@ def test_evict_workspace_grows_with_the_kept_keys(lib):
     assert sizes == sorted(sizes) and sizes[-1] >= 2 * 4 * 8 * 131072
     for bad in ((100, 0, 2), (100, 10, 0), (100, -1, 2)):
         assert blink.kv_evict_workspace_bytes(*bad) >= 256
+
+
+def test_binding_row_strides():
+    """Of tensors without rows too (the library refuses those by their sizes)."""
+    for shape in ((0, 4), (2, 0), (0, 2, 64), (3, 2, 64)):
+        t = torch.zeros(shape)
+        assert blink._row_stride(t) == t.stride(0)
+    assert blink._row_stride(torch.zeros(1, 7).expand(1, 7)) == 7
+    assert blink._row_stride(torch.zeros(4, 10)[:1, :6]) == 6

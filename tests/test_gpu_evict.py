@@ -199,3 +199,27 @@ def test_a_workspace_carries_nothing_over():
         assert np.array_equal(r["slots"].cpu().numpy(),
                               want_slots(w, np.tile(np.arange(P, dtype=np.int32), (Hkv, 1)), keep, 0, 2**31 - 1))
     assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+
+
+def test_no_recent_position_is_protected_by_default():
+    """Not even the largest there is, when the first positions are."""
+    w, k, v = inputs(500, 2, 64, seed=9)
+    pos = np.tile(np.arange(500, dtype=np.int32), (2, 1))
+    pos[:, 100:200] = 2**31 - 1
+    want = want_slots(w, pos.astype(np.int64), 60, 5, 2**31)
+    r = blink.blink_kv_evict(torch.from_numpy(w).cuda(), k, v, 60, pos=torch.from_numpy(pos).cuda(), sink=5)
+    assert np.array_equal(r["slots"].cpu().numpy(), want)
+
+
+def test_one_key_kept_in_its_strided_region():
+    """A destination that is row 0 of the source is in place whatever the rows' stride."""
+    w, k, v = inputs(70, 2, 64, seed=10)
+    arena = torch.zeros(70, 4, 64, dtype=BF, device="cuda")
+    arena[:, :2], arena[:, 2:] = k, v
+    r = blink.blink_kv_evict(torch.from_numpy(w).cuda(), arena[:, :2], arena[:, 2:], 1, k_dst=arena[:1, :2],
+                             v_dst=arena[:1, 2:])
+    best = torch.from_numpy(w.argmax(1)).cuda()
+    head = torch.arange(2, device="cuda")
+    assert torch.equal(r["slots"][:, 0].long(), best)
+    assert torch.equal(bits(arena[0, :2]), bits(k)[best, head]) and torch.equal(bits(arena[0, 2:]), bits(v)[best, head])
+    assert torch.equal(bits(arena[1:, :2]), bits(k)[1:]) and torch.equal(bits(arena[1:, 2:]), bits(v)[1:])
