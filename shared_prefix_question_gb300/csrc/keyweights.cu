@@ -23,12 +23,13 @@
 // What bounds it: a tile is 1,024 cycles of the tensor core and 1,024 of the exp2 unit (8 lanes a clock on
 // each of the SM's four partitions, measured), so the four warps of a partition have to keep one
 // unit busy while others wait for scores.  Two warps with 128 keys each took 1,590 cycles a tile.  10240
-// rows, 18432 keys, 32/8 heads of 128: 950-965 us, 1,480 cycles a tile, both units 69 % busy (the products
-// alone, with nothing reading them, take 732 us); 1275 rows, 2048 keys: 26 us, of which the 17 tiles of a
+// rows, 18432 keys, 32/8 heads of 128: 900 us, 1,400 cycles a tile, both units 73 % busy (the products
+// alone, with nothing reading them, take 732 us; the sums alone, in a loop of their own, 1,034 cycles a
+// tile, and 1,245 with the reads of the scores); 1275 rows, 2048 keys: 26 us, of which the 17 tiles of a
 // block are 13 and the launch, the first loads and the join the rest.  Slower, at 18432 keys: a part of
-// the exponentials as a polynomial on the fused multiply-add units (1.01 ms with an eighth of them, 1.27
-// with three eighths), scores read two tiles ahead (1.3), halves of 128 keys (1.27), scalar instead of
-// paired adds (1.1).
+// the exponentials as a polynomial on the fused multiply-add units (6 % with an eighth of them, 30 with
+// three eighths), scores read 16 at a time (11 %) or ahead of their use (14), halves of 128 keys (30), scalar
+// instead of paired adds (12).
 //
 // Short calls.  One row and 18432 keys read 38 MB: 12 us warm, 22 with a cold L2, where the floor is 5.6;
 // 60 rows and 64 keys 8 us, one launch.
@@ -345,18 +346,19 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
             float2 before = make_float2(0.f, 0.f);  // previous weights of this thread's keys
             bool ok = true;
             for (Segment<kOneTile> sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next()) {
-                const float *lse = a.lse + (sg.head * a.g + head_off) * a.lse_stride;
-                int at = sg.tile0 * a.tpt + tok;  // this column's row in the tile to be read next
-                const int last = col < cols_used ? min(a.rows, (sg.tile0 + sg.tiles) * a.tpt) : 0;  // 0: no column
+                const float *lse = a.lse + (sg.head * a.g + head_off) * a.lse_stride + (sg.tile0 * a.tpt + tok);
+                // rows from there to the last of the segment, if the thread has a column
+                int left = col < cols_used ? min(a.rows, (sg.tile0 + sg.tiles) * a.tpt) - (sg.tile0 * a.tpt + tok) : 0;
                 auto lse_next = [&] {
-                    const float v = at < last ? __ldg(lse + at) : INFINITY;
-                    at += a.tpt;
+                    const float v = left > 0 ? __ldg(lse) : INFINITY;
+                    lse += a.tpt;
+                    left -= a.tpt;
                     return v;
                 };
                 float acc[kThreadKeys];
 #pragma unroll
                 for (int i = 0; i < kThreadKeys; ++i) acc[i] = 0.f;
-                float next, after = INFINITY;  // two tiles ahead of their use
+                float next;  // a tile ahead of its use
                 if constexpr (kOneTile) {
                     if (sg.new_q) single = lse_next();
                     next = single;
@@ -367,16 +369,13 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                         before.y = key + 1 < a.P ? prev[key + 1] : 0.f;
                     }
                 } else {
-                    next = lse_next(), after = lse_next();
+                    next = lse_next();
                 }
-                for (int i = 0; i < sg.tiles; ++i, ++st) {
-                    const float b = next;
-                    if constexpr (!kOneTile) {
-                        next = after;
-                        after = lse_next();
-                    }
-                    const bool dead = b == -INFINITY;  // owned by no question: q may hold anything
-                    const float nb = dead ? -INFINITY : -b * kLog2e;
+                // two tiles a trip: 905 us instead of 940 for 18432 keys (four the same, eight 1010)
+#pragma unroll(kOneTile ? 1 : 2)
+                for (int i = sg.tiles; i > 0; --i, ++st) {
+                    const bool dead = next == -INFINITY;  // owned by no question: q may hold anything
+                    const float nb = dead ? -INFINITY : -next * kLog2e;
                     const bool careful = __any_sync(0xFFFFFFFFu, dead);
                     const uint64_t nb2 = ptx::f32x2(nb, nb);
                     const int buf = st & 1;
@@ -391,6 +390,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                             ptx::tc_fence_before();
                             __syncwarp();
                             if (lane == 0) ptx::mbar_arrive(s_empty + buf);
+                            if constexpr (!kOneTile) next = lse_next();
                         }
                         if (careful) {  // such a row's scores become 0, and with -b = -inf its terms
 #pragma unroll
