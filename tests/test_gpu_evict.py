@@ -223,3 +223,37 @@ def test_one_key_kept_in_its_strided_region():
     assert torch.equal(r["slots"][:, 0].long(), best)
     assert torch.equal(bits(arena[0, :2]), bits(k)[best, head]) and torch.equal(bits(arena[0, 2:]), bits(v)[best, head])
     assert torch.equal(bits(arena[1:, :2]), bits(k)[1:]) and torch.equal(bits(arena[1:, 2:]), bits(v)[1:])
+
+
+def test_two_graphs_of_one_workspace_and_two_streams():
+    """Replays in turn share a workspace; calls at the same time have one each."""
+    cases = []
+    for P, keep, seed in ((6000, 2500, 21), (20000, 900, 22)):
+        w, k, v = inputs(P, 3, 64, seed=seed)
+        kd, vd = (torch.zeros(keep, 3, 64, dtype=BF, device="cuda") for _ in range(2))
+        slots = torch.empty(3, keep, dtype=torch.int32, device="cuda")
+        want = want_slots(w, np.tile(np.arange(P, dtype=np.int32), (3, 1)), keep, 0, 2**31 - 1)
+        cases.append((torch.from_numpy(w).cuda(), k, v, keep, kd, vd, slots, want))
+    ws = blink.new_workspace(max(blink.kv_evict_workspace_bytes(w.shape[1], keep, 3) for w, _, _, keep, *_ in cases), "cuda")
+    graphs = []
+    for w, k, v, keep, kd, vd, slots, _ in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            blink.blink_kv_evict(w, k, v, keep, k_dst=kd, v_dst=vd, slots=slots, ws=ws)
+        graphs.append(graph)
+    for _ in range(3):
+        for graph, (*_, slots, want) in zip(graphs, cases):
+            slots.fill_(-1)
+            graph.replay()
+            assert np.array_equal(slots.cpu().numpy(), want)
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (w, k, v, keep, kd, vd, slots, _) in zip(streams, cases):
+            blink.blink_kv_evict(w, k, v, keep, k_dst=kd, v_dst=vd, slots=slots, stream=s)
+    torch.cuda.synchronize()
+    head = torch.arange(3, device="cuda")
+    for w, k, v, keep, kd, vd, slots, want in cases:
+        assert np.array_equal(slots.cpu().numpy(), want)
+        st = slots.long().t()
+        assert torch.equal(bits(kd), bits(k)[st, head]) and torch.equal(bits(vd), bits(v)[st, head])

@@ -170,3 +170,34 @@ def test_own_stream_and_graph_replay():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.allclose(acc, 3 * want, rtol=1e-6)
+
+
+def test_two_graphs_of_one_workspace_and_two_streams():
+    """Replays in turn share a workspace; calls at the same time have one each."""
+    cases = [make(700, 513, 8, 2, 128, seed=31), make(90, 3000, 16, 4, 64, seed=32)]
+    want = [blink.blink_prefix_key_weights(*c)[0].clone() for c in cases]
+    for c, w in zip(cases, want):
+        check(w, *c)
+    ws = blink.new_workspace(max(blink.key_weights_workspace_bytes(c[0].shape[0], c[1].shape[0], c[0].shape[1], c[1].shape[1],
+                                                                   c[0].shape[2]) for c in cases), "cuda")
+    outs = [torch.empty_like(w) for w in want]
+    graphs = []
+    for c, out in zip(cases, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            blink.blink_prefix_key_weights(*c, out=out, ws=ws)
+        graphs.append(graph)
+    for _ in range(3):
+        for graph, out, w in zip(graphs, outs, want):
+            out.fill_(-1.0)
+            graph.replay()
+            assert torch.equal(out, w)
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, c, out in zip(streams, cases, outs):
+            blink.blink_prefix_key_weights(*c, out=out, stream=s)
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert torch.equal(out, w)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_OK
