@@ -639,24 +639,32 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
     } else if (kList) {
         // ------------------------------------------------------------ bounds: warps 10 and 11, 64 rows each
         // Reads the words of the rows that the states are at, again and again, until they are done.  A value
-        // that comes late is only looser.
+        // that comes late is only looser.  The states change *turn at any time, so lane 0 reads it for the
+        // whole warp: kth_largest needs all lanes, at the same rows.
         ptx::grid_dep_wait();
+        constexpr unsigned kAll = 0xFFFFFFFFu;
+        const auto still_at = [&](int now) { return __shfl_sync(kAll, lane == 0 ? *turn : 0, 0) == now; };
         int seen = 0;
         uint64_t since = ptx::globaltimer_ns();
         while (true) {
-            const int now = *turn;
-            if (now < 0 || *abort_flag) break;
-            if (now != seen) {
-                seen = now;
-                since = ptx::globaltimer_ns();
-            } else if (ptx::globaltimer_ns() - since > 10000000000ull) {
-                break;  // the states' own waits end long before
+            int now = 0;
+            if (lane == 0) {
+                now = *turn;
+                if (now != seen) {
+                    seen = now;
+                    since = ptx::globaltimer_ns();
+                } else if (ptx::globaltimer_ns() - since > 10000000000ull) {
+                    now = -1;  // the states' own waits end long before
+                }
+                if (*abort_flag) now = -1;
             }
+            now = __shfl_sync(kAll, now, 0);
+            if (now < 0) break;
             if (now > 0) {
                 const Share sh = share_of(a.plan, now - 1, worker);
                 const int first = (warp - 10) * 64;
                 const int row0 = sh.row_tile * a.plan.tile_rows + static_cast<int>(rank) * kBlockRows + first;
-                for (int i = 0; i < 64 && row0 + i < a.n && *turn == now; i += 4) {
+                for (int i = 0; i < 64 && row0 + i < a.n && still_at(now); i += 4) {
                     uint32_t w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -671,9 +679,11 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
                                      "r"(now), "r"(b)
                                      : "memory");
                     }
+                    __syncwarp();
                 }
             }
-            if (*turn == now) __nanosleep(500);
+            if (still_at(now)) __nanosleep(500);
+            __syncwarp();
         }
         __syncwarp();
     }
