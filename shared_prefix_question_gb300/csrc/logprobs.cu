@@ -176,7 +176,7 @@ void lay_out(LogprobArgs &a)
     a.a_bytes = a.a_rows * 128;
     a.block_bytes = a.a_bytes + kVocabTile / (one ? 1 : 2) * 128;
     const int stage_bytes = a.block_bytes * (one ? kStageBlocksOne : kStageBlocksPair);
-    const int bounds = a.top > 0 ? kBlockRows * static_cast<int>(sizeof(int2)) : 0;
+    const int bounds = a.top > 0 ? kBlockRows * static_cast<int>(sizeof(uint64_t)) : 0;
     a.stages = (kSmemMax - bounds - 256) / stage_bytes;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     a.bound_off = a.stages * stage_bytes;
@@ -271,9 +271,25 @@ __device__ __forceinline__ float row_bound(const uint32_t *words, int top)
 // Where a row's bound is kept.
 struct BoundPlace {
     uint32_t *words;  // of this thread's row
-    uint32_t kept;    // as warps 10 and 11 last saw it: tag, order (shared address)
+    uint32_t kept;    // as warps 10 and 11 last saw it: tag << 32 | order (shared address)
     int top, slot0, tag;
 };
+
+// The tag (pass + 1) and the order of a bound are one scalar of 8 bytes, which a reader sees whole: a bound never
+// comes with the tag of another pass, whose row is another.  (Of a vector access each element is one by itself.)
+__device__ __forceinline__ void publish_bound(uint32_t place, int tag, uint32_t order)
+{
+    const uint64_t word = static_cast<uint64_t>(static_cast<uint32_t>(tag)) << 32 | order;
+    asm volatile("st.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(place), "l"(word) : "memory");
+}
+
+// 0: none yet in this pass.
+__device__ __forceinline__ uint32_t published_bound(uint32_t place, int tag)
+{
+    uint64_t word;
+    asm volatile("ld.relaxed.cta.shared::cta.b64 %0, [%1];" : "=l"(word) : "r"(place) : "memory");
+    return static_cast<int>(word >> 32) == tag ? static_cast<uint32_t>(word) : 0u;
+}
 
 // The first of columns 8 b .. 8 b + 7 that is at least `least` and not in `done` (b the same in the warp).
 __device__ __forceinline__ void next_candidate(const float (&z)[kHalfCols], int b, float least, uint32_t done, float &zc,
@@ -371,9 +387,8 @@ __device__ __forceinline__ void fold_tile(RowState<kTop> &r, float (&z)[kHalfCol
             if (target == id0 + j) r.tz = z[j];
     }
     if constexpr (kTop > 0) {
-        int2 kept;
-        asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];" : "=r"(kept.x), "=r"(kept.y) : "r"(bp.kept) : "memory");
-        if (kept.x == bp.tag && kept.y != 0) r.bound = fmaxf(r.bound, of_order(static_cast<uint32_t>(kept.y)));
+        const uint32_t kept = published_bound(bp.kept, bp.tag);
+        if (kept != 0u) r.bound = fmaxf(r.bound, of_order(kept));
         if (__any_sync(0xFFFFFFFFu, zmax > r.last() && zmax >= r.bound)) {
             if (r.bound == -INFINITY) r.bound = row_bound(bp.words, bp.top);  // the first tile
             uint32_t mine = 0u;  // this row's batches with a candidate
@@ -415,7 +430,7 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
     int *abort_word = reinterpret_cast<int *>(tmem_holder + 1);
     volatile int *abort_flag = abort_word;
     volatile int *turn = abort_word + 1;  // pass + 1 the states are at; 0 before, -1 after
-    const uint32_t kept_bounds = ptx::smem_u32(smem + a.bound_off);  // [128][2]: pass + 1, order
+    const uint32_t kept_bounds = ptx::smem_u32(smem + a.bound_off);  // [128]: see publish_bound
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = kCtas == 2 ? ptx::cluster_rank() : 0u;
     const int worker = blockIdx.x / kCtas;
@@ -445,7 +460,7 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
         ptx::tma_prefetch_desc(&tm_w);
     }
     if (kList && threadIdx.x < kBlockRows)
-        reinterpret_cast<int2 *>(smem + a.bound_off)[threadIdx.x] = make_int2(0, 0);
+        reinterpret_cast<uint64_t *>(smem + a.bound_off)[threadIdx.x] = 0ull;
     if (warp == 0) {
         if constexpr (kCtas == 2) {
             ptx::tmem_alloc_pair(tmem_holder, 512);
@@ -673,11 +688,7 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
                     for (int j = 0; j < 4; ++j) w[j] = kth_largest(w[j], a.top);
                     if (lane < 4) {
                         const uint32_t b = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
-                        // one 8-byte store: a reader sees a bound with its own tag
-                        asm volatile("st.volatile.shared.v2.b32 [%0], {%1, %2};" ::"r"(
-                                         kept_bounds + (first + i + lane) * 8),
-                                     "r"(now), "r"(b)
-                                     : "memory");
+                        publish_bound(kept_bounds + (first + i + lane) * 8, now, b);
                     }
                     __syncwarp();
                 }

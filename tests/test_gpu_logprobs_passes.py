@@ -35,3 +35,16 @@ def test_alternatives_of_many_short_passes(n, V, top):
         ws = r["ws"]
         assert torch.equal(r["top_ids"], want)
     assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+
+
+@pytest.mark.parametrize("top", [5, 20, 32])
+def test_a_bound_of_one_pass_does_not_reach_the_next(top):
+    """Every logit of every second 1024 rows is 128 lower than all logits of the others: with the bound of a row
+    of the pass before, such a row would lose its alternatives."""
+    n, H, V = 8192, 64, 3000
+    h, W = grid(n, H, V, seed=top)
+    W[:, 0] = 1.0
+    h[:, 0] = torch.where(torch.arange(n, device="cuda") // 1024 % 2 == 0, 64.0, -64.0).to(BF)
+    want = best(h, W, top)
+    for _ in range(5):
+        assert torch.equal(blink.blink_token_logprobs(h, W, top=top)["top_ids"], want)
