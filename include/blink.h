@@ -447,7 +447,8 @@ blink_status blink_kv_evict(const float *d_weights, int64_t w_stride, const int3
  * temperature  > 0 and finite
  * top        0..BLINK_MAX_TOP_TOKENS alternatives per row, at most V
  * Outputs: each may be NULL, not all; d_top_ids and d_top_logprobs [n][top] together, when top > 0
- * d_ws       workspace of blink_token_logprobs_workspace(...) bytes (of the current device), 16-byte aligned,
+ * d_ws       workspace of blink_token_logprobs_workspace(...) bytes (of the current device; one for n rows
+ *            serves calls of fewer), 16-byte aligned,
  *            its first 256 zero-filled before its first use; not shared by calls that may run at the same time
  * A row index outside [0, hidden_rows) latches BLINK_DEVICE_FLAG and makes the row's outputs NaN and
  * -1; a target outside [-1, V) latches it and makes that log probability NaN.  A row with a NaN logit
@@ -458,6 +459,11 @@ blink_status blink_kv_evict(const float *d_weights, int64_t w_stride, const int3
 #define BLINK_MAX_TOP_TOKENS 32
 
 size_t blink_token_logprobs_workspace(int32_t n, int32_t H, int32_t V, int32_t top);
+
+/* The workspace of a call on a GPU with `sms` SMs (host computation only): *ws_bytes is what the query above gives
+ * there, which is never less for more rows, and *used the most that a launch of the call lays out. */
+blink_status blink_token_logprobs_workspace_plan(int32_t n, int32_t H, int32_t V, int32_t top, int32_t sms,
+                                                 size_t *ws_bytes, size_t *used);
 
 blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t hidden_row_stride, int32_t hidden_rows,
                                   const int32_t *d_row_idx, const blink_bf16 *unembed, int32_t V, int32_t H,

@@ -74,6 +74,7 @@ _SIGNATURES = {
     "blink_kv_evict": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _vp, _i64,
                               _vp, _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
     "blink_token_logprobs_workspace": (_sz, [_i32] * 4),
+    "blink_token_logprobs_workspace_plan": (_i32, [_i32] * 5 + [_vp, _vp]),
     "blink_token_logprobs": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _f32, _i32] + [_vp] * 6 +
                              [_sz, _vp]),
 }
@@ -547,6 +548,16 @@ def blink_kv_evict(weights, k, v, keep: int, pos=None, sink: int = 0, recent_fro
 # ------------------------------------------------------------------------------------------------ whole vocabulary
 def token_logprobs_workspace_bytes(n, H, V, top) -> int:
     return int(lib().blink_token_logprobs_workspace(int(n), int(H), int(V), int(top)))
+
+
+def blink_token_logprobs_workspace_plan(n: int, H: int, V: int, top: int, sms: int):
+    """(bytes of the workspace, most bytes a launch of the call lays out) on a GPU with `sms` SMs (host
+    computation only)."""
+    ws, used = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    st = lib().blink_token_logprobs_workspace_plan(int(n), int(H), int(V), int(top), int(sms), ctypes.byref(ws),
+                                                   ctypes.byref(used))
+    _check(st, "blink_token_logprobs_workspace_plan")
+    return int(ws.value), int(used.value)
 
 
 def blink_token_logprobs(hidden, unembed, targets=None, row_idx=None, temperature: float = 1.0, top: int = 0, ws=None,

@@ -69,7 +69,7 @@ constexpr int kFewRows = 32;
 constexpr int kStageBlocksOne = 1, kStageBlocksPair = 2;  // 64-wide blocks of H per stage of the ring
 constexpr int kNoToken = 0x7FFFFFFF;
 constexpr int kMaxWorkers = 160;
-constexpr int kLaunchRows = 8192;  // rows of one launch: bounds the workspace (102 MB with 32 alternatives)
+constexpr int kLaunchRows = 8192;  // rows of one launch: bounds the workspace (86 MB with 32 alternatives, and 16 KB x H of rows)
 constexpr int kMaxStages = 8;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kBatchCols = 8;  // columns searched for alternatives at a time
@@ -120,6 +120,18 @@ __host__ __device__ inline Share share_of(const LogprobPlan &p, int pass, int wo
     return s;
 }
 
+// Row tiles per full pass: the count of 2..6 that leaves the fewest workers idle, the larger of
+// equals (fewer passes over the unembedding); all of them when there are no more than that.
+int full_group(int workers)
+{
+    int best = 1, best_used = 0;
+    for (int g = 2; g <= 6 && g <= workers; ++g) {
+        const int used = workers / g * g;
+        if (used >= best_used) best = g, best_used = used;
+    }
+    return best;
+}
+
 LogprobPlan make_plan(int n, int V, int sms)
 {
     LogprobPlan p{};
@@ -134,13 +146,7 @@ LogprobPlan make_plan(int n, int V, int sms)
         const int c = p.workers / tiles;
         return c < p.vocab_tiles ? c : p.vocab_tiles;
     };
-    // Row tiles per full pass: the count of 2..6 that leaves the fewest workers idle, the larger of
-    // equals (fewer passes over the unembedding); all of them when there are no more than that.
-    int best = 1, best_used = 0;
-    for (int g = 2; g <= 6 && g <= p.workers; ++g) {
-        const int used = p.workers / g * g;
-        if (used >= best_used) best = g, best_used = used;
-    }
+    const int best = full_group(p.workers);
     p.group = best < p.row_tiles ? best : p.row_tiles;
     p.full_passes = p.row_tiles / p.group;
     p.chunks = chunks_for(p.group);
@@ -907,16 +913,43 @@ struct WsLayout {
     size_t stat, best, bounds, rows, total;
 };
 
-WsLayout ws_layout(const LogprobPlan &p, int n, int H, int top)
+WsLayout ws_layout(int64_t n_cells, int n, int H, int top)
 {
     WsLayout l{};
-    const size_t cells = static_cast<size_t>(p.cells());
+    const size_t cells = static_cast<size_t>(n_cells);
     l.stat = kHeaderBytes;
     l.best = l.stat + align_up(cells * sizeof(float4), 256);
     l.bounds = l.best + align_up(cells * top * sizeof(int2), 256);
     l.rows = l.bounds + (top > 0 ? static_cast<size_t>(n) * kMaxTop * sizeof(uint32_t) : 0);
     l.total = l.rows + align_up(static_cast<size_t>(n) * H * sizeof(uint16_t), 256);
     return l;
+}
+
+// No fewer cells than the plan of any launch of up to n rows has, and never fewer for more rows: a pass has at
+// most a cell per worker and tile row (256 rows for each of two workers where pairs work), and no more
+// than the row tiles and the vocabulary tiles make.  The plans' own counts go up and down with n, as
+// the workers that a pass leaves idle do.
+int64_t most_cells(int n, int V, int sms)
+{
+    const int blocks = sms < 2 * kMaxWorkers ? sms : 2 * kMaxWorkers;
+    const int64_t row_tiles = (n + 2 * kBlockRows - 1) / (2 * kBlockRows), vocab_tiles = (V + kVocabTile - 1) / kVocabTile;
+    const int workers = blocks / 2 < 1 ? 1 : blocks / 2 < kMaxWorkers ? blocks / 2 : kMaxWorkers;
+    const int group = full_group(workers);
+    const int64_t by_workers = (row_tiles + group - 1) / group * (blocks < 2 ? 2 : blocks), by_tiles = 2 * row_tiles * vocab_tiles;
+    return (by_workers < by_tiles ? by_workers : by_tiles) * kHalves * kBlockRows;
+}
+
+// Bytes that serve every launch of a call of n rows, and those of a call of fewer.
+size_t ws_bytes_needed(int n, int H, int V, int top, int sms)
+{
+    const int rows = n < kLaunchRows ? n : kLaunchRows;
+    return ws_layout(most_cells(rows, V, sms > 0 ? sms : 1), rows, H, top).total;
+}
+
+// The sizes that workspaces are given out for.
+bool ws_sizes_ok(int n, int H, int V, int top)
+{
+    return n >= 1 && n <= BLINK_MAX_INPUT_TOKENS && H >= 1 && H <= 32768 && V >= 1 && V <= (1 << 24) && top >= 0 && top <= kMaxTop;
 }
 
 int sm_count()
@@ -971,7 +1004,7 @@ blink_status run_logprobs(const blink_bf16 *hidden, int64_t hidden_row_stride, i
     if (sms < 2) return BLINK_CUDA_ERROR;
     LogprobArgs a{};
     a.plan = make_plan(n, V, sms);
-    const WsLayout l = ws_layout(a.plan, n, H, top);
+    const WsLayout l = ws_layout(a.plan.cells(), n, H, top);
     auto *wsb = static_cast<uint8_t *>(d_ws);
     a.V = V;
     a.H = H;
@@ -1049,11 +1082,23 @@ blink_status run_logprobs(const blink_bf16 *hidden, int64_t hidden_row_stride, i
 extern "C" size_t blink_token_logprobs_workspace(int32_t n, int32_t H, int32_t V, int32_t top)
 {
     using namespace blink;
-    if (n < 1 || n > BLINK_MAX_INPUT_TOKENS || H < 1 || H > 32768 || V < 1 || V > (1 << 24) || top < 0 || top > kMaxTop)
-        return kHeaderBytes;
-    const int sms = sm_count();
-    const int rows = n < kLaunchRows ? n : kLaunchRows;
-    return ws_layout(make_plan(rows, V, sms > 0 ? sms : 1), rows, H, top).total;
+    return ws_sizes_ok(n, H, V, top) ? ws_bytes_needed(n, H, V, top, sm_count()) : static_cast<size_t>(kHeaderBytes);
+}
+
+extern "C" blink_status blink_token_logprobs_workspace_plan(int32_t n, int32_t H, int32_t V, int32_t top, int32_t sms,
+                                                            size_t *ws_bytes, size_t *used)
+{
+    using namespace blink;
+    if (!ws_bytes || !used) return BLINK_INVALID_ARG;
+    if (sms < 2 || !ws_sizes_ok(n, H, V, top)) return BLINK_OUT_OF_RANGE;
+    *ws_bytes = ws_bytes_needed(n, H, V, top, sms);
+    *used = 0;
+    for (int32_t r = 0; r < n; r += kLaunchRows) {
+        const int32_t rows = n - r < kLaunchRows ? n - r : kLaunchRows;
+        const size_t total = ws_layout(make_plan(rows, V, sms).cells(), rows, H, top).total;
+        if (total > *used) *used = total;
+    }
+    return BLINK_OK;
 }
 
 extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t hidden_row_stride, int32_t hidden_rows,
