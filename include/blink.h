@@ -363,8 +363,9 @@ blink_status blink_label_readout_noalloc(const blink_bf16 *hidden, int64_t hidde
  *             of exp(scale * q[i][h g + j] . k_pre[p][h] - lse[h g + j][i])
  * i.e. the softmax weights blink_prefix_tail_attention gave that key, summed over the rows and the
  * query heads that share it, when lse is that call's output.  A row whose lse is -inf (a row owned
- * by no question) adds nothing, whatever its q holds; a NaN in any other row or its lse makes the
- * weights of that kv head NaN.  lse must not be smaller than the scores it normalises by more than
+ * by no question) adds nothing, whatever its q or the keys hold; a NaN in any other row or its lse makes
+ * the weights of that kv head NaN, a NaN or an infinity in a key what the formula gives for that key
+ * alone.  lse must not be smaller than the scores it normalises by more than
  * 80 (an attention's own lse never is).
  *
  * q       [rows, Hq, d] bf16, rows in 1..2^30 (one row: a single decoded token)

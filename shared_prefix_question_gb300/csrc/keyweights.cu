@@ -34,9 +34,10 @@
 // Short calls.  One row and 18432 keys read 38 MB: 12 us warm, 22 with a cold L2, where the floor is 5.6;
 // 60 rows and 64 keys 8 us, one launch.
 //
-// A column that does not count has -b = -inf, so its term is 0: rows past the last (Q is zero there) and
-// rows owned by no question.  Only the latter may hold NaN or infinities in q; a warp with such a row
-// clears its scores first.
+// A column that does not count has -b = -inf, so its term is 0 once its score is finite.  It need not be: a row
+// owned by no question may hold NaN or infinities in q, and the zeros of a row past the last make NaN with an
+// infinite key.  A warp with such a row clears its scores first.  The columns past g * tpt, which no
+// tile has, are cleared once per unit instead, in the sums.
 #include <cstdint>
 
 #include "common.cuh"
@@ -298,11 +299,11 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
             const int row = lane / a.g;
             const bool has = lane < cols_used && row < a.rows;
             int st = 0;
-            float b = INFINITY;
+            float b = -INFINITY;
             bool ok = true;
             for (Segment<kOneTile> sg(begin, end, a.n_tiles, a.n_units_head); ok && sg.more(); sg.next(), ++st) {
-                if (sg.new_q) b = has ? __ldg(a.lse + (sg.head * a.g + lane % a.g) * a.lse_stride + row) : INFINITY;
-                const bool dead = b == -INFINITY;  // owned by no question: q may hold anything
+                if (sg.new_q) b = has ? __ldg(a.lse + (sg.head * a.g + lane % a.g) * a.lse_stride + row) : -INFINITY;
+                const bool dead = b == -INFINITY;  // no row, or owned by no question: the score may be anything
                 const float nb = dead ? -INFINITY : -b * kLog2e;
                 const int key = sg.key0 + offset + (lane >> 1);  // the key this thread writes, if its lane is even
                 const bool writes = (lane & 1) == 0 && key < a.P;
@@ -349,8 +350,9 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                 const float *lse = a.lse + (sg.head * a.g + head_off) * a.lse_stride + (sg.tile0 * a.tpt + tok);
                 // rows from there to the last of the segment, if the thread has a column
                 int left = col < cols_used ? min(a.rows, (sg.tile0 + sg.tiles) * a.tpt) - (sg.tile0 * a.tpt + tok) : 0;
+                // -inf: a row past the last.  A thread without a column has +inf: its sums are cleared at the end.
                 auto lse_next = [&] {
-                    const float v = left > 0 ? __ldg(lse) : INFINITY;
+                    const float v = left > 0 ? __ldg(lse) : col < cols_used ? -INFINITY : INFINITY;
                     lse += a.tpt;
                     left -= a.tpt;
                     return v;
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                 // two tiles a trip: 905 us instead of 940 for 18432 keys (four the same, eight 1010)
 #pragma unroll(kOneTile ? 1 : 2)
                 for (int i = sg.tiles; i > 0; --i, ++st) {
-                    const bool dead = next == -INFINITY;  // owned by no question: q may hold anything
+                    const bool dead = next == -INFINITY;  // no row, or owned by no question: the score may be anything
                     const float nb = dead ? -INFINITY : -next * kLog2e;
                     const bool careful = __any_sync(0xFFFFFFFFu, dead);
                     const uint64_t nb2 = ptx::f32x2(nb, nb);
@@ -408,6 +410,10 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                     }
                 }
                 if (!ok) break;
+                if (col >= cols_used) {  // zeros times an infinite key
+#pragma unroll
+                    for (int i = 0; i < kThreadKeys; ++i) acc[i] = 0.f;
+                }
                 warp_sum_scatter(acc, lane);
                 float2 s = make_float2(acc[0], acc[1]);  // keys 2 lane and 2 lane + 1 of this quarter
                 if (live_warps > 1) {
