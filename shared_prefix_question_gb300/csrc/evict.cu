@@ -309,10 +309,11 @@ struct MoveArgs {
     int skip_k, skip_v;            // in place: a key that stays is not copied
 };
 
+// Coherent loads: the selection writes both lists while this kernel is resident already.
 __device__ __forceinline__ int source_slot(const MoveArgs &a, int64_t head, int64_t j)
 {
-    const int f = __ldg(a.from + head * a.keep + j);
-    return f >= 0 ? f : __ldg(a.survivors + head * a.keep + ~f);
+    const int f = __ldcg(a.from + head * a.keep + j);
+    return f >= 0 ? f : __ldcg(a.survivors + head * a.keep + ~f);
 }
 
 constexpr int kMoveThreads = 256;
