@@ -69,8 +69,9 @@ blink_status blink_read_device_status(void *d_ws, int32_t clear, cudaStream_t st
 /* Self-test of the failure path every kernel relies on (no counterpart on the pages): one
  * thread waits, with the library's bounded wait, on a barrier that nothing arrives at; after
  * limit_us microseconds (1..1000000) the wait gives up and latches BLINK_DEVICE_TIMEOUT in the
- * workspace's error word, exactly as a kernel whose copy or peer never arrived would.  Returns
- * that status (BLINK_DEVICE_TIMEOUT when the path works), after clearing the word.  Nothing
+ * workspace's error word, exactly as a kernel whose copy or peer never arrived would.  A warp then
+ * waits together on it, half of its lanes for a phase that is complete: all have to give up.  Returns
+ * the status (BLINK_DEVICE_TIMEOUT when both work), after clearing the word.  Nothing
  * faults or traps and the context stays usable.  d_ws: a workspace of at least 256 bytes.
  * Synchronises `stream`. */
 blink_status blink_selftest_wait_timeout(uint32_t limit_us, void *d_ws, size_t ws_bytes, cudaStream_t stream);

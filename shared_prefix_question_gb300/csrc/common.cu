@@ -78,16 +78,21 @@ namespace blink {
 namespace {
 
 // One thread waits, with the same bounded wait every kernel uses, on a barrier that nothing
-// arrives at; the wait gives up after limit_ns and latches BLINK_DEVICE_TIMEOUT.
+// arrives at; the wait gives up after limit_ns and latches BLINK_DEVICE_TIMEOUT.  Then the warp waits
+// together, its even lanes for a phase that is complete: all lanes have to get the odd ones' answer.
 __global__ void selftest_wait_kernel(int *err, uint64_t limit_ns)
 {
     __shared__ uint64_t bar;
     __shared__ int abort_flag;
-    if (threadIdx.x != 0) return;
-    abort_flag = 0;
-    ptx::mbar_init(&bar, 1);
-    ptx::fence_mbar_init();
-    ptx::mbar_wait(&bar, 0, &abort_flag, err, BLINK_DEVICE_TIMEOUT, limit_ns);
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        ptx::mbar_init(&bar, 1);
+        ptx::fence_mbar_init();
+        ptx::mbar_wait(&bar, 0, &abort_flag, err, BLINK_DEVICE_TIMEOUT, limit_ns);
+    }
+    __syncwarp();
+    const uint32_t parity = threadIdx.x & 1 ? 0u : 1u;
+    if (ptx::mbar_wait_warp(&bar, parity, &abort_flag, err, BLINK_DEVICE_TIMEOUT, limit_ns)) atomicExch(err, BLINK_DEVICE_FLAG);
 }
 
 }  // namespace

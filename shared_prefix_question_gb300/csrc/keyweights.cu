@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                 const bool writes = (lane & 1) == 0 && key < a.P;
                 const float before = writes && a.decay > 0.f ? a.prev[sg.head * a.prev_stride + key] : 0.f;
                 const int buf = st & 1;
-                if (!(ok = ptx::mbar_wait(s_full + buf, (st >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
+                if (!(ok = ptx::mbar_wait_warp(s_full + buf, (st >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
                 ptx::tc_fence_after();
                 uint32_t raw[kKeys];
                 ptx::tmem_ld16(trow + buf * kUnitKeys, raw);
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                     const bool careful = __any_sync(0xFFFFFFFFu, dead);
                     const uint64_t nb2 = ptx::f32x2(nb, nb);
                     const int buf = st & 1;
-                    if (!(ok = ptx::mbar_wait(s_full + buf, (st >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
+                    if (!(ok = ptx::mbar_wait_warp(s_full + buf, (st >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
                     ptx::tc_fence_after();
 #pragma unroll
                     for (int q = 0; q < kThreadKeys / 32; ++q) {
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                     auto meet = [&] {
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(met + quarter);
-                        ok = ok && ptx::mbar_wait(met + quarter, meetings & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT);
+                        ok = ok && ptx::mbar_wait_warp(met + quarter, meetings & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT);
                         ++meetings;
                     };
                     float2 *dst = reinterpret_cast<float2 *>(sums + (wq & 1) * kThreadKeys) + lane;

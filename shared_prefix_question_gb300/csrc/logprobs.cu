@@ -614,7 +614,8 @@ __global__ void __launch_bounds__(kThreadsLP, 1)
                 float z[kHalfCols];
                 for (int k0 = 0; k0 < k_blocks; k0 += part_blocks, ++part) {
                     const int buf = part & 1;
-                    if (!(ok = ptx::mbar_wait(acc_full + buf, (part >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT)))
+                    if (!(ok = ptx::mbar_wait_warp(acc_full + buf, (part >> 1) & 1, abort_flag, a.err,
+                                                   BLINK_DEVICE_TIMEOUT)))
                         break;
                     ptx::tc_fence_after();
                     if (live) {

@@ -106,6 +106,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
+// The same by a whole warp that goes on to warp-wide instructions (tensor-memory reads, votes, shuffles): true in all
+// lanes or in none.  When a wait gives up, a lane may have seen the phase complete and another the abort.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, int timeout_code,
+                                               uint64_t limit_ns = 1000000000ull)
+{
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, err, timeout_code, limit_ns)) != 0;
+}
+
 // ---------------------------------------------------------------------------------------------
 // TMA (tiled tensor copies, global -> shared, completion counted on an mbarrier)
 // ---------------------------------------------------------------------------------------------
