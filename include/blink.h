@@ -446,7 +446,8 @@ blink_status blink_kv_evict(const float *d_weights, int64_t w_stride, const int3
  * unembed [V, H] bf16 row-major; H a multiple of 8, 16-byte aligned; H in 8..32768, V in 1..2^24
  * n          1..131072 rows (one row: a single decoded token)
  * d_targets  int32 [n]; -1: the row has no target (its log probability is NaN).  NULL without d_logprob
- * temperature  > 0 and finite
+ * temperature  > 0, finite, and not so small that log2(e) / temperature is not (4.3e-39); logits divided by it
+ *            have to stay within 1e38
  * top        0..BLINK_MAX_TOP_TOKENS alternatives per row, at most V
  * Outputs: each may be NULL, not all; d_top_ids and d_top_logprobs [n][top] together, when top > 0
  * d_ws       workspace of blink_token_logprobs_workspace(...) bytes (of the current device; one for n rows

@@ -1,12 +1,15 @@
 // logprobs.cu -- log probabilities of given tokens, entropy and top alternatives over the whole
 // vocabulary (blink_token_logprobs), without writing the logits.
 //
-// Mathematics.  With y = z log2(e) / T for the raw product z = h . w, a part of the vocabulary is
-// summarised by m = max y, s = sum 2^(y - m) and u = sum 2^(y - m) (y - m); two parts merge by
-// rescaling to the larger m:  s = a s1 + b s2,  u = a (u1 + s1 (m1 - m)) + b (u2 + s2 (m2 - m)) with
-// a = 2^(m1 - m), b = 2^(m2 - m).  Then lse = ln2 (m + log2 s) and entropy = ln2 (log2 s - u / s),
-// whose two terms are both small when the distribution is peaked.  Alternatives and the target keep
-// the raw z, which the temperature does not reorder.
+// Mathematics.  With c = log2(e) / T and the raw product z = h . w, a part of the vocabulary is
+// summarised by m = max z, s = sum 2^x and u = sum 2^x x, x = c (z - m); two parts merge by
+// rescaling to the larger m:  s = a s1 + b s2,  u = a (u1 + s1 d1) + b (u2 + s2 d2) with
+// d1 = c (m1 - m), a = 2^d1 and so on.  Then lse = ln2 (c m + log2 s), entropy = ln2 (log2 s - u / s),
+// whose two terms are both small when the distribution is peaked, and a log probability is
+// ln2 (c (z - m) - log2 s).  The difference is taken before the scaling: c z itself may have lost its
+// digits (at T = 10^-6 its last place is a whole unit), and a fused c z - c m leaves what the rounding of c m
+// did, 2^80 at T = 10^-30.  It is one instruction more for two logits.  Alternatives and the target
+// keep the raw z, which the temperature does not reorder.
 //
 // Work.  Hidden rows are the M rows of the product (a tensor-memory lane, so a thread, holds one row
 // and folds the logits into its state without any exchange), vocabulary rows the N columns, 256 per
@@ -163,7 +166,7 @@ struct LogprobArgs {
     int hidden_rows;
     const int32_t *targets;
     float c;       // log2(e) / T
-    float4 *stat;  // [cells]: m, s, u, target's raw product (NaN: not in this part)
+    float4 *stat;  // [cells]: m (a raw product), s, u, target's raw product (NaN: not in this part)
     int2 *best;    // [cells][top]: raw product (as bits) and token, descending
     float *logprob, *entropy, *lse, *top_lp;
     int32_t *top_ids;
@@ -344,12 +347,11 @@ __device__ __forceinline__ void fold_tile(RowState<kTop> &r, float (&z)[kHalfCol
             if (gmax > r.bound) atomicMax(bp.words + bp.slot0 + q, order_of(gmax));
         }
     }
-    const float ym = zmax * c;
-    if (ym > r.m) {
-        const float d = r.m == -INFINITY ? 0.f : r.m - ym, f = ptx::ex2(d);
-        r.u = f * fmaf(r.s, d, r.u);
+    if (zmax > r.m) {
+        const float d = r.m == -INFINITY ? 0.f : (r.m - zmax) * c, f = ptx::ex2(d);
+        r.u = f == 0.f ? 0.f : f * fmaf(r.s, d, r.u);  // s d may overflow
         r.s *= f;
-        r.m = ym;
+        r.m = zmax;
     }
     const float nm = r.m == -INFINITY ? 0.f : -r.m;  // all NaN so far
     if (whole) {
@@ -358,8 +360,8 @@ __device__ __forceinline__ void fold_tile(RowState<kTop> &r, float (&z)[kHalfCol
         uint64_t s0 = 0ull, s1 = 0ull, u0 = 0ull, u1 = 0ull;
 #pragma unroll
         for (int j = 0; j < kHalfCols; j += 4) {
-            const uint64_t x0 = ptx::fma_f32x2(ptx::f32x2(z[j], z[j + 1]), cc, mm);
-            const uint64_t x1 = ptx::fma_f32x2(ptx::f32x2(z[j + 2], z[j + 3]), cc, mm);
+            const uint64_t x0 = ptx::mul_f32x2(ptx::add_f32x2(ptx::f32x2(z[j], z[j + 1]), mm), cc);
+            const uint64_t x1 = ptx::mul_f32x2(ptx::add_f32x2(ptx::f32x2(z[j + 2], z[j + 3]), mm), cc);
             float a0, a1, a2, a3;
             ptx::f32x2_split(x0, a0, a1);
             ptx::f32x2_split(x1, a2, a3);
@@ -379,7 +381,7 @@ __device__ __forceinline__ void fold_tile(RowState<kTop> &r, float (&z)[kHalfCol
 #pragma unroll
         for (int j = 0; j < kHalfCols; ++j) {
             if (id0 + j < V) {
-                const float x0 = fmaf(z[j], c, nm), e0 = ptx::ex2(x0);
+                const float x0 = (z[j] + nm) * c, e0 = ptx::ex2(x0);
                 s0 += e0;
                 u0 = fmaf(e0, x0, u0);
             }
@@ -815,9 +817,9 @@ __global__ void __launch_bounds__(kRowThreads == 32 ? 128 : kRowThreads) logprob
     }
     float s = 0.f, u = 0.f;
     auto join = [&](float pm, float ps, float pu) {
-        const float d = pm == -INFINITY ? 0.f : pm - m, f = exp2f(d);  // an empty part, or one of NaN alone
+        const float d = pm == -INFINITY ? 0.f : (pm - m) * a.c, f = exp2f(d);  // an empty part, or one of NaN alone
         s = fmaf(f, ps, s);
-        u = fmaf(f, fmaf(ps, d, pu), u);
+        if (f != 0.f) u = fmaf(f, fmaf(ps, d, pu), u);  // s d may overflow
     };
 #pragma unroll
     for (int q = 0; q < kMine; ++q) join(st[q].x, st[q].y, st[q].z);
@@ -839,12 +841,11 @@ __global__ void __launch_bounds__(kRowThreads == 32 ? 128 : kRowThreads) logprob
     }
     const bool bad = hr < 0 || hr >= a.hidden_rows;
     const float l2s = log2f(s);
-    const float l2 = bad ? nan : m + l2s;
     if (t == 0) {
         if (bad || target < -1 || target >= a.V) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
-        if (a.lse) a.lse[r] = l2 * kLn2;
+        if (a.lse) a.lse[r] = bad ? nan : fmaf(m, a.c, l2s) * kLn2;
         if (a.entropy) a.entropy[r] = bad ? nan : (l2s - u / s) * kLn2;
-        if (a.logprob) a.logprob[r] = target >= 0 && target < a.V ? fmaf(tz, a.c, -l2) * kLn2 : nan;
+        if (a.logprob) a.logprob[r] = !bad && target >= 0 && target < a.V ? fmaf(tz - m, a.c, -l2s) * kLn2 : nan;
     }
     if (top == 0) return;
 
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__(kRowThreads == 32 ? 128 : kRowThreads) logprob
         const bool no = bad || key == 0ull;
         a.top_ids[static_cast<int64_t>(r) * top + place] = no ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
         a.top_lp[static_cast<int64_t>(r) * top + place] =
-            no ? nan : fmaf(of_order(static_cast<uint32_t>(key >> 32)), a.c, -l2) * kLn2;
+            no ? nan : fmaf(of_order(static_cast<uint32_t>(key >> 32)) - m, a.c, -l2s) * kLn2;
     };
     const unsigned long long bound = static_cast<unsigned long long>(kth_largest(word, top)) << 32;
     row_sync<kRowThreads>();  // the count starts at zero
@@ -1112,7 +1113,7 @@ extern "C" blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t h
     if (!hidden || !unembed || !d_ws) return BLINK_INVALID_ARG;
     if (!d_logprob && !d_entropy && !d_lse && !d_top_ids) return BLINK_INVALID_ARG;
     if ((d_logprob && !d_targets) || (d_top_ids == nullptr) != (d_top_logprobs == nullptr)) return BLINK_INVALID_ARG;
-    if (!(temperature > 0.f) || !(temperature < INFINITY)) return BLINK_INVALID_ARG;
+    if (!(temperature > 0.f) || !(temperature < INFINITY) || !(kLog2e / temperature < INFINITY)) return BLINK_INVALID_ARG;
     if (H < 8 || H % 8 != 0 || V < 1 || hidden_rows < 1 || hidden_row_stride < H || hidden_row_stride % 8 != 0)
         return BLINK_INVALID_ARG;
     if (!aligned16(hidden) || !aligned16(unembed) || !aligned16(d_ws)) return BLINK_INVALID_ARG;

@@ -158,3 +158,11 @@ def test_binding_row_strides():
         assert blink._row_stride(t) == t.stride(0)
     assert blink._row_stride(torch.zeros(1, 7).expand(1, 7)) == 7
     assert blink._row_stride(torch.zeros(4, 10)[:1, :6]) == 6
+
+
+@pytest.mark.parametrize("T,status", [(1e-40, INVALID), (4.2e-39, INVALID), (4.3e-39, SMALL), (1e-30, SMALL), (3e38, SMALL)])
+def test_logprobs_temperature_without_a_reciprocal(lib, T, status):
+    """log2(e) / temperature has to be a number; what passes that check is refused for its workspace here."""
+    st = lib.blink_token_logprobs(_p(FAKE), 256, 10, None, _p(FAKE), 1024, 256, _p(FAKE), 10, T, 0, _p(FAKE), None, None, None,
+                                  None, _p(FAKE), 256, None)
+    assert st == status
