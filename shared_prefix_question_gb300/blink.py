@@ -8,6 +8,7 @@ device every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -389,6 +390,20 @@ def _need(name, t, dtype, shape, inner: int = 1):
         _refuse(name, t, dtype, shape, inner)
 
 
+def _int32(name, x) -> int:
+    """`x` for a 32-bit argument: ctypes would drop the bits above without a word."""
+    x = operator.index(x)
+    if not -INT32_MAX - 1 <= x <= INT32_MAX:
+        raise ValueError(f"{name} must fit 32 bits, not {x}")
+    return x
+
+
+def _sizes(*sizes):
+    """Sizes of tensors, passed in 32 bits."""
+    if max(sizes) > INT32_MAX:
+        raise ValueError(f"sizes must fit 32 bits: {max(sizes)}")
+
+
 def _row_stride(t) -> int:
     """Elements between the rows (first dimension) of `t`; a single row has any stride."""
     return t[0].numel() if t.shape[0] == 1 else t.stride(0)
@@ -465,6 +480,7 @@ def blink_prefix_key_weights(q, k_pre, lse, prev=None, decay: float = 0.0, scale
     P, Hkv = k_pre.shape[:2] if getattr(k_pre, "ndim", 0) == 3 else (None, None)
     _need("k_pre", k_pre, torch.bfloat16, (P, Hkv, d), inner=2)
     _need("lse", lse, torch.float32, (Hq, rows))
+    _sizes(rows, P, Hq, Hkv)
     if prev is not None:
         _need("prev", prev, torch.float32, (Hkv, P))
     if out is not None:
@@ -503,6 +519,9 @@ def blink_kv_evict(weights, k, v, keep: int, pos=None, sink: int = 0, recent_fro
     keep = int(keep)
     if not 1 <= keep <= P:
         raise ValueError(f"keep must be in 1..{P}, not {keep}")
+    _sizes(P, Hkv, d)
+    sink = _int32("sink", sink)
+    recent_from = INT32_MAX if recent_from is None else _int32("recent_from", recent_from)
     if pos is not None:
         _need("pos", pos, torch.int32, (Hkv, P))
     if (k_dst is None) != (v_dst is None):
@@ -538,7 +557,7 @@ def blink_kv_evict(weights, k, v, keep: int, pos=None, sink: int = 0, recent_fro
             ws = call.workspace(kv_evict_workspace_bytes(P, keep, Hkv))
         st = lib().blink_kv_evict(
             weights.data_ptr(), _row_stride(weights), _addr(pos), 0 if pos is None else _row_stride(pos), P, keep, sink,
-            INT32_MAX if recent_from is None else recent_from, Hkv, d, k.data_ptr(), v.data_ptr(), src_stride,
+            recent_from, Hkv, d, k.data_ptr(), v.data_ptr(), src_stride,
             k_dst.data_ptr(), v_dst.data_ptr(), dst_stride, slots.data_ptr(), weights_dst.data_ptr(), _row_stride(weights_dst),
             pos_dst.data_ptr(), _row_stride(pos_dst), ws.data_ptr(), ws.numel(), call.handle)
     _check(st, "blink_kv_evict")
@@ -578,7 +597,8 @@ def blink_token_logprobs(hidden, unembed, targets=None, row_idx=None, temperatur
         _need("targets", targets, torch.int32, (n,))
     if ws is not None:
         _need("ws", ws, torch.uint8, (ws.numel(),))
-    top = int(top)
+    _sizes(n, rows, V, H)
+    top = _int32("top", int(top))
     with _Launch(stream, hidden, unembed, targets, row_idx, ws) as call:
         f32 = torch.float32
         logprob = None if targets is None else call.empty(f32, n)

@@ -166,3 +166,24 @@ def test_logprobs_temperature_without_a_reciprocal(lib, T, status):
     st = lib.blink_token_logprobs(_p(FAKE), 256, 10, None, _p(FAKE), 1024, 256, _p(FAKE), 10, T, 0, _p(FAKE), None, None, None,
                                   None, _p(FAKE), 256, None)
     assert st == status
+
+
+def test_binding_refuses_what_32_bits_do_not_hold():
+    """ctypes drops the bits above 32 of a number: 2^32 + 5 would be passed as 5."""
+    class Fake(torch.Tensor):  # a host tensor that says it is on a GPU: the checks of the arguments come first
+        is_cuda = True
+
+    def fake(*shape, dtype=torch.bfloat16):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(Fake)
+    w, k, v = fake(2, 8, dtype=torch.float32), fake(8, 2, 64), fake(8, 2, 64)
+    for kw in (dict(sink=2**32), dict(recent_from=2**32 + 5), dict(recent_from=2**31), dict(sink=-2**31 - 1)):
+        with pytest.raises(ValueError, match="must fit 32 bits"):
+            blink.blink_kv_evict(w, k, v, 4, **kw)
+    with pytest.raises(TypeError):
+        blink.blink_kv_evict(w, k, v, 4, sink=1.5)
+    h, u = fake(2, 8), fake(9, 8)
+    with pytest.raises(ValueError, match="must fit 32 bits"):
+        blink.blink_token_logprobs(h, u, top=2**32 + 1)
+    long = fake(8).as_strided((2**32 + 4, 8), (0, 1))
+    with pytest.raises(ValueError, match="must fit 32 bits"):
+        blink.blink_token_logprobs(long, u)
