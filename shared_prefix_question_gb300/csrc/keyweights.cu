@@ -34,10 +34,11 @@
 // Short calls.  One row and 18432 keys read 38 MB: 12 us warm, 22 with a cold L2, where the floor is 5.6;
 // 60 rows and 64 keys 8 us, one launch.
 //
-// A column that does not count has -b = -inf, so its term is 0 once its score is finite.  It need not be: a row
-// owned by no question may hold NaN or infinities in q, and the zeros of a row past the last make NaN with an
-// infinite key.  A warp with such a row clears its scores first.  The columns past g * tpt, which no
-// tile has, are cleared once per unit instead, in the sums.
+// A column that does not count has lse -inf here and -b = -inf, so its term is 0 once its score is finite.  It need
+// not be: a row owned by no question may hold NaN or infinities in q, and the zeros of a row past the last or of a
+// column past g * tpt make NaN with an infinite key.  A warp with such a column clears its scores first (where g does
+// not divide 128 the last warp has some in every tile: 4 % with g = 5; clearing their sums at the end of a unit
+// instead takes 1.5 % there and 1 % of the time of all other shapes).
 #include <cstdint>
 
 #include "common.cuh"
@@ -350,9 +351,8 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                 const float *lse = a.lse + (sg.head * a.g + head_off) * a.lse_stride + (sg.tile0 * a.tpt + tok);
                 // rows from there to the last of the segment, if the thread has a column
                 int left = col < cols_used ? min(a.rows, (sg.tile0 + sg.tiles) * a.tpt) - (sg.tile0 * a.tpt + tok) : 0;
-                // -inf: a row past the last.  A thread without a column has +inf: its sums are cleared at the end.
                 auto lse_next = [&] {
-                    const float v = left > 0 ? __ldg(lse) : col < cols_used ? -INFINITY : INFINITY;
+                    const float v = left > 0 ? __ldg(lse) : -INFINITY;
                     lse += a.tpt;
                     left -= a.tpt;
                     return v;
@@ -378,10 +378,16 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                 for (int i = sg.tiles; i > 0; --i, ++st) {
                     const bool dead = next == -INFINITY;  // no row, or owned by no question: the score may be anything
                     const float nb = dead ? -INFINITY : -next * kLog2e;
-                    const bool careful = __any_sync(0xFFFFFFFFu, dead);
                     const uint64_t nb2 = ptx::f32x2(nb, nb);
                     const int buf = st & 1;
-                    if (!(ok = ptx::mbar_wait_warp(s_full + buf, (st >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT))) break;
+                    ok = ptx::mbar_wait(s_full + buf, (st >> 1) & 1, abort_flag, a.err, BLINK_DEVICE_TIMEOUT);
+                    // one vote for both: a column that does not count, and a wait that gave up, which all lanes have to take
+                    // the same way (a vote for each: 1005 us instead of 996 for 18432 keys)
+                    const bool careful = !__all_sync(0xFFFFFFFFu, ok && !dead);
+                    if (careful && !__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        break;
+                    }
                     ptx::tc_fence_after();
 #pragma unroll
                     for (int q = 0; q < kThreadKeys / 32; ++q) {
@@ -410,10 +416,6 @@ __global__ void __launch_bounds__(kThreadsKW, 1)
                     }
                 }
                 if (!ok) break;
-                if (col >= cols_used) {  // zeros times an infinite key
-#pragma unroll
-                    for (int i = 0; i < kThreadKeys; ++i) acc[i] = 0.f;
-                }
                 warp_sum_scatter(acc, lane);
                 float2 s = make_float2(acc[0], acc[1]);  // keys 2 lane and 2 lane + 1 of this quarter
                 if (live_warps > 1) {
