@@ -23,9 +23,9 @@
 // What bounds it: a tile is 1,024 cycles of the tensor core and 1,024 of the exp2 unit (8 lanes a clock on
 // each of the SM's four partitions, measured), so the four warps of a partition have to keep one
 // unit busy while others wait for scores.  Two warps with 128 keys each took 1,590 cycles a tile.  10240
-// rows, 18432 keys, 32/8 heads of 128: 900 us, 1,400 cycles a tile, both units 73 % busy (the products
+// rows, 18432 keys, 32/8 heads of 128: 905 us alone, 1,400 cycles a tile, both units 73 % busy (the products
 // alone, with nothing reading them, take 732 us; the sums alone, in a loop of their own, 1,034 cycles a
-// tile, and 1,245 with the reads of the scores); 1275 rows, 2048 keys: 26 us, of which the 17 tiles of a
+// tile, and 1,245 with the reads of the scores), and 1.0 ms for calls in a row, under the power limit; 1275 rows, 2048 keys: 26 us, of which the 17 tiles of a
 // block are 13 and the launch, the first loads and the join the rest.  Slower, at 18432 keys: a part of
 // the exponentials as a polynomial on the fused multiply-add units (6 % with an eighth of them, 30 with
 // three eighths), scores read 16 at a time (11 %) or ahead of their use (14), halves of 128 keys (30), scalar

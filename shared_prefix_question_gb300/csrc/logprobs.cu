@@ -35,8 +35,8 @@
 // multiplied.  Warps 10 and 11 keep the rows' bounds (below) up to date in shared memory.
 //
 // What bounds it.  Up to 128 rows the unembedding is read once: 151936 x 2560 takes 122 us for one row or 64
-// (6.4 TB/s), 127 with the merge.  Above, the tensor core: 512 rows of 5120 take 500 us (83 % busy), 4096 rows
-// of 2560 1.8 ms alone and 2.0 in a row, where the power limit lowers the clock.
+// (6.4 TB/s), 127 with the merge.  Above, the tensor core: 512 rows of 5120 take 490 us alone (82 % busy), 4096 rows
+// of 2560 1.75 ms (88 %); in a row, where the power limit lowers the clock, 570 us and 2.05 ms.
 //
 // Lists.  A thread's alternatives are in registers, sorted.  While the tensor core reads its operands
 // from shared memory, a dependent shared-memory access of another warp takes hundreds of cycles:
