@@ -474,6 +474,159 @@ blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t hidden_row_s
                                   float *d_logprob, float *d_entropy, float *d_lse, int32_t *d_top_ids,
                                   float *d_top_logprobs, void *d_ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Rotary positions -- the step before the path, whose calls take rotated queries and keys: pair i
+ * of each head turns by position * theta_i, theta_i = base^(-2 i / rot).
+ *
+ * blink_rope_table computes the frequencies on the host, once per model: h_turns [rot/2] gets
+ * theta_i / (2 pi) as a fraction of a turn times 2^64 (copy it to the device for the calls below), and
+ * *h_amplitude the factor of the rotated values that belongs to the scaling (1 but for BY_DIM).
+ *   rot        even, 2..BLINK_MAX_ROPE_DIM: values of a head that turn
+ *   base       > 1
+ *   scaling    for contexts longer than the model was trained on (`original` tokens), by `factor` >= 1:
+ *     PLAIN      theta_i as above (the other arguments are not read)
+ *     LINEAR     theta_i / factor
+ *     BASE       base * factor^(rot / (rot - 2)) in place of base (rot >= 4)
+ *     BY_DIM     pairs below lo keep theta_i, pairs from hi on get theta_i / factor, a linear ramp over i
+ *                between: lo = floor(i(high)), hi = ceil(i(low)), where pair i(n) = rot ln(original /
+ *                (2 pi n)) / (2 ln base) turns n times over the original context (lo >= 0, hi <= rot - 1);
+ *                the amplitude is 0.1 ln(factor) + 1
+ *     BY_TURNS   with n_i = original theta_i / (2 pi) turns over the original context, the share
+ *                (n_i - low) / (high - low), clipped to 0..1, of theta_i and the rest of theta_i / factor
+ *   low, high  0 < low < high, in turns over the original context (BY_DIM, BY_TURNS)
+ *
+ * blink_rope turns the first `rot` values of every head of q and, if given, k, and copies the others:
+ * (y0, y1) = amplitude (x0 cos - x1 sin, x0 sin + x1 cos), in 32 bits, rounded once.
+ *   q [rows, Hq, d], k [rows, Hkv, d]  bf16, heads d apart, rows *_stride elements apart (slices of one
+ *               projection's rows are fine); k NULL: q alone.  16-byte pieces are used where bases and
+ *               strides are 16-byte aligned, d is a multiple of 8 and (halves) rot one of 16
+ *   d_positions [rows]   any int32 values (negative ones turn back)
+ *   d           2..BLINK_MAX_ROPE_DIM;  rows 0..2^30 (0: nothing is done)
+ *   interleaved 0: pair i is values (i, i + rot/2); 1: values (2 i, 2 i + 1)
+ *   q_out, k_out  as q and k: the same memory with the same stride (in place), or memory that overlaps
+ *               neither input nor the other output
+ * Errors: BLINK_INVALID_ARG, BLINK_OUT_OF_RANGE, BLINK_CUDA_ERROR.
+ * ------------------------------------------------------------------------------------------ */
+#define BLINK_MAX_ROPE_DIM 512
+#define BLINK_ROPE_PLAIN 0
+#define BLINK_ROPE_LINEAR 1
+#define BLINK_ROPE_BASE 2
+#define BLINK_ROPE_BY_DIM 3
+#define BLINK_ROPE_BY_TURNS 4
+
+blink_status blink_rope_table(int32_t rot, double base, int32_t scaling, double factor, int32_t original, double low,
+                              double high, uint64_t *h_turns, float *h_amplitude);
+
+blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const blink_bf16 *k, int64_t k_stride,
+                        const int32_t *d_positions, int32_t rows, int32_t Hq, int32_t Hkv, int32_t d, int32_t rot,
+                        const uint64_t *d_turns, float amplitude, int32_t interleaved, blink_bf16 *q_out,
+                        int64_t q_out_stride, blink_bf16 *k_out, int64_t k_out_stride, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The 8-bit paged cache -- half the bytes of the arena, in pages that sequences take as they grow and
+ * requests with a common prefix share.  The caller owns it:
+ *
+ * k_codes, v_codes  pages of `page_tokens` (16, 32, 64 or 128) tokens, [Hkv][page_tokens][d] e4m3 codes
+ *                   each, page_stride bytes apart (>= Hkv * page_tokens * d, a multiple of 16; 16-byte
+ *                   aligned), d in {64, 128}, Hkv 1..BLINK_MAX_PAGED_HEADS
+ * k_scale, v_scale  [Hkv] e8m0 scales each (a byte b stands for 2^(b - 127)), scale_stride bytes apart:
+ *                   a value is its code times the scale of its page and head
+ * d_page_table      int32, sequence s's pages at d_page_table + s * table_stride, table_width of them:
+ *                   token p lies in slot p % page_tokens of page p / page_tokens
+ *
+ * blink_paged_append writes the next tokens of S sequences and turns their keys on the way.  With m the
+ * largest finite magnitude of the tokens that a page gets for a head, the scale is the smallest 2^e with
+ * m <= 448 * 2^e, e in BLINK_PAGED_SCALE_MIN..MAX; a code is value / scale rounded to the nearest (ties to
+ * even) and at most 448, a NaN stays one.  A page that holds tokens of the sequence already (start is
+ * not a multiple of page_tokens) keeps its scale if that is larger; if the scale grows, its tokens' codes
+ * are rounded again, which changes only those that become subnormal.  Slots that get no token keep
+ * their codes.
+ * k [n, Hkv, d], v  bf16, rows *_stride elements apart (multiples of 8, 16-byte aligned); keys not yet rotated
+ * d_cu_new [S+1]    sequence s's tokens are rows cu[s] - cu[0] .. of k and v (none is fine)
+ * d_start [S]       tokens that the sequence holds; its new ones follow them
+ * S, max_new        1..BLINK_MAX_PLAN_SEQUENCES; upper bound of the new tokens of a sequence, checked on the
+ *                   device (at most 131072)
+ * d_positions [n]   positions of the rows, or NULL: start + 0, 1, ...
+ * d_turns, rot, amplitude, interleaved  as for blink_rope; rot 0: the keys are rotated already
+ * d_ws              blink_paged_append_workspace() bytes: the error word
+ * A page that two sequences share must not be written (sharers append to pages of their own).  A bad length,
+ * a page index outside [0, n_pages) or past table_width latches BLINK_DEVICE_FLAG; those pages are not written.
+ * Errors: BLINK_INVALID_ARG, BLINK_OUT_OF_RANGE, BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR.
+ * ------------------------------------------------------------------------------------------ */
+#define BLINK_MAX_PAGED_HEADS 1024
+#define BLINK_MAX_PAGED_TOKENS 64
+#define BLINK_PAGED_SCALE_MIN (-48)
+#define BLINK_PAGED_SCALE_MAX 32
+
+size_t blink_paged_append_workspace(void);
+
+blink_status blink_paged_append(const blink_bf16 *k, int64_t k_stride, const blink_bf16 *v, int64_t v_stride, int32_t n,
+                                int32_t Hkv, int32_t d, uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_scale,
+                                uint8_t *v_scale, int64_t page_stride, int64_t scale_stride, int32_t n_pages,
+                                int32_t page_tokens, const int32_t *d_page_table, int64_t table_stride,
+                                int32_t table_width, const int32_t *d_cu_new, const int32_t *d_start, int32_t S,
+                                int32_t max_new, const int32_t *d_positions, const uint64_t *d_turns, int32_t rot,
+                                float amplitude, int32_t interleaved, void *d_ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Attention of each sequence's last tokens over its pages -- the single-token form (T = 1), or a few
+ * tokens at once (a draft to verify).  The tokens' own keys and values are in the pages already.
+ *
+ * For sequence s with len cached tokens, token t of T, query head h (kv head h / (Hq/Hkv)):
+ *   out = softmax(scale * q . K[0 .. len - T + t]^T) V[0 .. len - T + t]
+ * q, out [S, T, Hq, d] bf16; lse [Hq, S * T] optional (may be NULL), fp32 natural log
+ * d_len [S]      cached tokens, on the device, so that a captured graph follows a growing cache; a token
+ *                that sees no key (len < T - t) gets zeros and -inf
+ * max_len        upper bound of d_len (0..131072), which decides how the work is cut
+ * S, T           1..BLINK_MAX_PLAN_SEQUENCES, 1..BLINK_MAX_PAGED_TOKENS; Hq/Hkv <= 128, and
+ *                Hkv * ceil(T Hq/Hkv / 16) <= 65535
+ * scale          softmax scale; <= 0 selects 1/sqrt(d)
+ * d_ws           blink_paged_token_attention_workspace(...) bytes (of the current device), 16-byte aligned, its first
+ *                256 zero-filled before its first use; not shared by calls that may run at the same time
+ * Scores are exact products of the 8-bit values in 32-bit sums; weights enter the second product in fp16.
+ * Keys that a token does not see have no influence, whatever their slots hold.  The same call gives the same bits.
+ * A length outside 0..max_len or past the table is cut to that, a page index outside [0, n_pages) counts as
+ * absent; both latch BLINK_DEVICE_FLAG.
+ * Errors: BLINK_INVALID_ARG, BLINK_OUT_OF_RANGE, BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR.
+ * ------------------------------------------------------------------------------------------ */
+size_t blink_paged_token_attention_workspace(int32_t S, int32_t T, int32_t max_len, int32_t Hq, int32_t Hkv, int32_t d);
+
+blink_status blink_paged_token_attention(const blink_bf16 *q, const uint8_t *k_codes, const uint8_t *v_codes,
+                                         const uint8_t *k_scale, const uint8_t *v_scale, int64_t page_stride,
+                                         int64_t scale_stride, int32_t n_pages, int32_t page_tokens,
+                                         const int32_t *d_page_table, int64_t table_stride, int32_t table_width,
+                                         const int32_t *d_len, int32_t S, int32_t T, int32_t max_len, int32_t Hq,
+                                         int32_t Hkv, int32_t d, float scale, blink_bf16 *out, float *lse, void *d_ws,
+                                         size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Prefix-tail attention with the prefixes in pages -- blink_prefix_tail_attention (one request) and
+ * blink_prefix_tail_attention_multi (several) for a prefix held in 8 bits.  Request r owns the tail rows
+ * [h_req_rows[r], h_req_rows[r+1]) (whole questions) and attends to the first h_prefix_len[r] tokens of row r
+ * of the page table; tails are bf16, as there.  Requests may share pages.
+ *
+ * h_req_rows [n_req+1], h_prefix_len [n_req]  host arrays; lengths 0..131072, n_req 1..64
+ * d_ws   blink_paged_prefix_tail_workspace(...) bytes (of the current device), 32-byte aligned, its first 256
+ *        zero-filled before its first use; not shared by calls that may run at the same time.  It holds the
+ *        prefixes as bf16 rows for the time of the call: one such workspace serves the caches of all layers
+ * Other arguments as there.  A page index outside [0, n_pages) latches BLINK_DEVICE_FLAG (its values count as 0).
+ * Errors: BLINK_INVALID_ARG, BLINK_OUT_OF_RANGE, BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR; device-side:
+ * BLINK_DEVICE_FLAG, BLINK_DEVICE_TIMEOUT.
+ * ------------------------------------------------------------------------------------------ */
+size_t blink_paged_prefix_tail_workspace(const int32_t *h_req_rows, const int32_t *h_prefix_len, int32_t n_req, int32_t B,
+                                         int32_t Hq, int32_t Hkv, int32_t d);
+
+blink_status blink_paged_prefix_tail_attention(const blink_bf16 *q, const uint8_t *k_codes, const uint8_t *v_codes,
+                                               const uint8_t *k_scale, const uint8_t *v_scale, int64_t page_stride,
+                                               int64_t scale_stride, int32_t n_pages, int32_t page_tokens,
+                                               const int32_t *d_page_table, int64_t table_stride, int32_t table_width,
+                                               const blink_bf16 *k_tail, const blink_bf16 *v_tail,
+                                               const int32_t *d_cu_seqlens, const int32_t *d_seq_start, int32_t B,
+                                               int32_t rows, int32_t n_req, const int32_t *h_req_rows,
+                                               const int32_t *h_prefix_len, int32_t max_tail, int32_t Hq, int32_t Hkv,
+                                               int32_t d, float scale, blink_bf16 *out, float *lse, void *d_ws,
+                                               size_t ws_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

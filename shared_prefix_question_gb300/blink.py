@@ -43,6 +43,7 @@ _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 _sz = ctypes.c_size_t
 
 _SIGNATURES = {
@@ -78,6 +79,18 @@ _SIGNATURES = {
     "blink_token_logprobs_workspace_plan": (_i32, [_i32] * 5 + [_vp, _vp]),
     "blink_token_logprobs": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _f32, _i32] + [_vp] * 6 +
                              [_sz, _vp]),
+    "blink_rope_table": (_i32, [_i32, _f64, _i32, _f64, _i32, _f64, _f64, _vp, _vp]),
+    "blink_rope": (_i32, [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _f32, _i32, _vp, _i64, _vp, _i64, _vp]),
+    "blink_paged_append_workspace": (_sz, []),
+    "blink_paged_append": (_i32, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _i64,
+                                  _i32, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _f32, _i32, _vp, _sz, _vp]),
+    "blink_paged_token_attention_workspace": (_sz, [_i32] * 6),
+    "blink_paged_token_attention": (_i32, [_vp] * 5 + [_i64, _i64, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _i32, _i32, _i32,
+                                                       _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "blink_paged_prefix_tail_workspace": (_sz, [_vp, _vp, _i32, _i32, _i32, _i32, _i32]),
+    "blink_paged_prefix_tail_attention": (_i32, [_vp] * 5 + [_i64, _i64, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i32,
+                                                             _i32, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp,
+                                                             _sz, _vp]),
 }
 
 
@@ -612,3 +625,235 @@ def blink_token_logprobs(hidden, unembed, targets=None, row_idx=None, temperatur
             ws.data_ptr(), ws.numel(), call.handle)
     _check(st, "blink_token_logprobs")
     return {"logprob": logprob, "entropy": entropy, "lse": lse, "top_ids": ids, "top_logprobs": lps, "ws": ws}
+
+
+# ------------------------------------------------------------------------------------------------ rotary positions
+ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "by_dim": 3, "by_turns": 4}
+_ROPE_TURNS = {"by_dim": (1.0, 32.0), "by_turns": (1.0, 4.0)}  # low and high where the caller gives none
+
+
+def blink_rope_table(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0, original: int = 0,
+                     low: float | None = None, high: float | None = None, device="cuda"):
+    """Frequencies of the `rot` / 2 pairs that turn: (turns int64 [rot/2] on `device`, amplitude), to be kept for the
+    calls that rotate.  `scaling`: None, "linear", "base", "by_dim" or "by_turns", for contexts `factor` times the
+    `original` ones (include/blink.h has the formulas; `low` and `high` are turns over the original context)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}, not {scaling!r}")
+    rot = _int32("rot", rot)
+    default = _ROPE_TURNS.get(scaling, (0.0, 0.0))
+    turns = torch.empty(max(1, min(rot, 512) // 2), dtype=torch.int64)
+    amplitude = ctypes.c_float(0.0)
+    st = lib().blink_rope_table(rot, float(base), ROPE_SCALINGS[scaling], float(factor), _int32("original", original),
+                                float(default[0] if low is None else low), float(default[1] if high is None else high),
+                                turns.data_ptr(), ctypes.byref(amplitude))
+    _check(st, "blink_rope_table")
+    return turns.to(device), float(amplitude.value)
+
+
+def _turns_of(turns, d):
+    n = turns.numel() if isinstance(turns, torch.Tensor) else None
+    _need("turns", turns, torch.int64, (n,))
+    if not 1 <= n <= d // 2:
+        raise ValueError(f"turns must have 1..{d // 2} values (those of rot / 2 pairs), not {n}")
+    return 2 * n
+
+
+def blink_rope(q, k, positions, turns, interleaved: bool = False, amplitude: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Turn the heads of q [rows, Hq, d] and k [rows, Hkv, d] (None: q alone) bf16 by int32 `positions` [rows]: pairs
+    (i, i + rot/2), or (2 i, 2 i + 1) if `interleaved`, with blink_rope_table's `turns` and amplitude.  Rows may be
+    strided (slices of one projection).  q_out / k_out: None for new tensors, q / k themselves for in place.
+    Returns (q_out, k_out)."""
+    rows, Hq, d = q.shape if getattr(q, "ndim", 0) == 3 else (None,) * 3
+    _need("q", q, torch.bfloat16, (rows, Hq, d), inner=2)
+    Hkv = k.shape[1] if getattr(k, "ndim", 0) == 3 else None
+    if k is not None:
+        _need("k", k, torch.bfloat16, (rows, Hkv, d), inner=2)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _need("positions", positions, torch.int32, (rows,))
+    rot = _turns_of(turns, d)
+    _sizes(rows, Hq, Hkv or 0, d)
+    if q_out is not None:
+        _need("q_out", q_out, torch.bfloat16, (rows, Hq, d), inner=2)
+    if k_out is not None:
+        _need("k_out", k_out, torch.bfloat16, (rows, Hkv, d), inner=2)
+    with _Launch(stream, q, k, positions, turns, q_out, k_out) as call:
+        if q_out is None:
+            q_out = call.empty(torch.bfloat16, rows, Hq, d)
+        if k_out is None and k is not None:
+            k_out = call.empty(torch.bfloat16, rows, Hkv, d)
+        if rows:
+            st = lib().blink_rope(q.data_ptr(), _row_stride(q), _addr(k), 0 if k is None else _row_stride(k), positions.data_ptr(),
+                                  rows, Hq, Hkv or 0, d, rot, turns.data_ptr(), amplitude, 1 if interleaved else 0,
+                                  q_out.data_ptr(), _row_stride(q_out), _addr(k_out), 0 if k is None else _row_stride(k_out),
+                                  call.handle)
+            _check(st, "blink_rope")
+    return q_out, k_out
+
+
+# ------------------------------------------------------------------------------------------------ 8-bit paged cache
+def blink_paged_cache(n_pages: int, page_tokens: int, Hkv: int, d: int, device="cuda") -> dict:
+    """An empty cache of `n_pages` pages of `page_tokens` (16, 32, 64 or 128) tokens: {"k", "v": float8_e4m3fn
+    [n_pages, Hkv, page_tokens, d], "k_scale", "v_scale": float8_e8m0fnu [n_pages, Hkv]}.  Any dict of such tensors is
+    a cache: pages may be strided (K and V as halves of one tensor)."""
+    zeros = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=device)  # noqa: E731
+    return {"k": zeros(n_pages, Hkv, page_tokens, d).view(torch.float8_e4m3fn),
+            "v": zeros(n_pages, Hkv, page_tokens, d).view(torch.float8_e4m3fn),
+            "k_scale": zeros(n_pages, Hkv).view(torch.float8_e8m0fnu), "v_scale": zeros(n_pages, Hkv).view(torch.float8_e8m0fnu)}
+
+
+def _cache_of(cache, Hkv, d):
+    """The tensors of a cache and its arguments of the C calls, checked."""
+    k, v, ks, vs = (cache[x] for x in ("k", "v", "k_scale", "v_scale"))
+    n, page = (k.shape[0], k.shape[2]) if getattr(k, "ndim", 0) == 4 else (None, None)
+    _need("cache k", k, torch.float8_e4m3fn, (n, Hkv, page, d), inner=3)
+    _need("cache v", v, torch.float8_e4m3fn, (n, Hkv, page, d), inner=3)
+    _need("cache k_scale", ks, torch.float8_e8m0fnu, (n, Hkv))
+    _need("cache v_scale", vs, torch.float8_e8m0fnu, (n, Hkv))
+    _sizes(n, Hkv, page, d)
+    if n < 1:
+        raise ValueError("a cache has at least one page")
+    if n > 1 and (k.stride(0) != v.stride(0) or ks.stride(0) != vs.stride(0)):
+        raise ValueError("k and v of a cache, and their scales, must have the same page strides")
+    return (k, v, ks, vs), (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), _row_stride(k), _row_stride(ks), n, page)
+
+
+def _table_of(table):
+    rows, width = table.shape if getattr(table, "ndim", 0) == 2 else (None, None)
+    _need("page_table", table, torch.int32, (rows, width))
+    _sizes(rows, width)
+    return rows, (table.data_ptr(), _row_stride(table), width)
+
+
+def _bytes(name, ws):
+    if ws is not None:
+        _need(name, ws, torch.uint8, (ws.numel(),))
+
+
+def paged_append_workspace_bytes() -> int:
+    return int(lib().blink_paged_append_workspace())
+
+
+def blink_paged_append(k, v, cache: dict, page_table, cu_new, start, max_new: int, positions=None, turns=None,
+                       interleaved: bool = False, amplitude: float = 1.0, ws=None, stream=None):
+    """Write the new tokens k, v [n, Hkv, d] bf16 (rows may be strided) of S sequences into their pages: sequence s's
+    rows [cu_new[s], cu_new[s+1]) follow its start[s] tokens; page_table [S, width], cu_new [S+1], start [S] int32.
+    Keys are turned by `positions` (int32 [n]; None: start + 0, 1, ...) with blink_rope_table's `turns` and amplitude
+    (turns None: they are rotated already).  max_new: upper bound of a sequence's new tokens.  Returns ws; device-side
+    problems (a bad length or page) are read with blink_read_device_status(ws)."""
+    n, Hkv, d = k.shape if getattr(k, "ndim", 0) == 3 else (None,) * 3
+    _need("k", k, torch.bfloat16, (n, Hkv, d), inner=2)
+    _need("v", v, torch.bfloat16, (n, Hkv, d), inner=2)
+    tensors, args = _cache_of(cache, Hkv, d)
+    S, table = _table_of(page_table)
+    _need("cu_new", cu_new, torch.int32, (S + 1,))
+    _need("start", start, torch.int32, (S,))
+    if positions is not None:
+        _need("positions", positions, torch.int32, (n,))
+    rot = 0 if turns is None else _turns_of(turns, d)
+    _bytes("ws", ws)
+    _sizes(n, S)
+    max_new = _int32("max_new", max_new)
+    with _Launch(stream, k, v, *tensors, page_table, cu_new, start, positions, turns, ws) as call:
+        if ws is None:
+            ws = call.workspace(paged_append_workspace_bytes())
+        if n:
+            st = lib().blink_paged_append(k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), n, Hkv, d, *args, *table,
+                                          cu_new.data_ptr(), start.data_ptr(), S, max_new, _addr(positions), _addr(turns), rot,
+                                          amplitude, 1 if interleaved else 0, ws.data_ptr(), ws.numel(), call.handle)
+            _check(st, "blink_paged_append")
+    return ws
+
+
+def paged_token_attention_workspace_bytes(S, T, max_len, Hq, Hkv, d) -> int:
+    return int(lib().blink_paged_token_attention_workspace(int(S), int(T), int(max_len), int(Hq), int(Hkv), int(d)))
+
+
+def blink_paged_token_attention(q, cache: dict, page_table, length, max_len: int, scale: float = 0.0, out=None, lse=None,
+                                want_lse: bool = False, ws=None, stream=None):
+    """Attention of the last T tokens of S sequences, q [S, T, Hq, d] bf16, over the pages that hold them: sequence s
+    has length[s] (int32, on the device) tokens in row s of page_table, and token t sees the first length - T + 1 + t.
+    max_len: upper bound of `length`.  Returns (out [S, T, Hq, d], lse [Hq, S * T] or None, ws)."""
+    S, T, Hq, d = q.shape if getattr(q, "ndim", 0) == 4 else (None,) * 4
+    _need("q", q, torch.bfloat16, (S, T, Hq, d), inner=4)
+    Hkv = cache["k"].shape[1] if getattr(cache["k"], "ndim", 0) == 4 else None
+    tensors, args = _cache_of(cache, Hkv, d)
+    rows, table = _table_of(page_table)
+    if rows != S:
+        raise ValueError(f"page_table must have a row for each of {S} sequences, not {rows}")
+    _need("length", length, torch.int32, (S,))
+    if out is not None:
+        _need("out", out, torch.bfloat16, (S, T, Hq, d), inner=4)
+    if lse is not None:
+        _need("lse", lse, torch.float32, (Hq, S * T), inner=2)
+    _bytes("ws", ws)
+    _sizes(S, T, Hq)
+    max_len = _int32("max_len", max_len)
+    with _Launch(stream, q, *tensors, page_table, length, out, lse, ws) as call:
+        if out is None:
+            out = call.empty(torch.bfloat16, S, T, Hq, d)
+        if lse is None and want_lse:
+            lse = call.empty(torch.float32, Hq, S * T)
+        if ws is None:
+            ws = call.workspace(paged_token_attention_workspace_bytes(S, T, max_len, Hq, Hkv, d))
+        st = lib().blink_paged_token_attention(q.data_ptr(), *args, *table, length.data_ptr(), S, T, max_len, Hq, Hkv, d, scale,
+                                               out.data_ptr(), _addr(lse), ws.data_ptr(), ws.numel(), call.handle)
+    _check(st, "blink_paged_token_attention")
+    return out, lse, ws
+
+
+def _int32s(name, values):
+    """A host list as a C array of int32."""
+    return (ctypes.c_int32 * len(values))(*[_int32(name, x) for x in values])
+
+
+def paged_prefix_tail_workspace_bytes(req_rows, prefix_len, B, Hq, Hkv, d) -> int:
+    if len(req_rows) != len(prefix_len) + 1:
+        raise ValueError("req_rows must have one value more than prefix_len")
+    return int(lib().blink_paged_prefix_tail_workspace(_int32s("req_rows", req_rows), _int32s("prefix_len", prefix_len),
+                                                       len(prefix_len), int(B), int(Hq), int(Hkv), int(d)))
+
+
+def blink_paged_prefix_tail_attention(q, cache: dict, page_table, prefix_len, k_tail, v_tail, cu_seqlens, B: int, max_tail: int,
+                                      req_rows=None, seq_start=None, scale: float = 0.0, out=None, lse=None,
+                                      want_lse: bool = False, ws=None, stream=None):
+    """Prefix-tail attention with the prefixes in pages: request r owns rows [req_rows[r], req_rows[r+1]) of q
+    [rows, Hq, d] and k_tail / v_tail [rows, Hkv, d] bf16 (req_rows None: one request has them all) and attends to the
+    first prefix_len[r] tokens of row r of page_table.  prefix_len and req_rows are host lists; the rest as
+    blink_prefix_tail_attention.  Returns (out, lse, ws)."""
+    rows, Hq, d = q.shape if getattr(q, "ndim", 0) == 3 else (None,) * 3
+    _need("q", q, torch.bfloat16, (rows, Hq, d), inner=3)
+    Hkv = k_tail.shape[1] if getattr(k_tail, "ndim", 0) == 3 else None
+    _need("k_tail", k_tail, torch.bfloat16, (rows, Hkv, d), inner=3)
+    _need("v_tail", v_tail, torch.bfloat16, (rows, Hkv, d), inner=3)
+    tensors, args = _cache_of(cache, Hkv, d)
+    n_req, table = _table_of(page_table)
+    if req_rows is None:
+        req_rows = [0, rows]
+    if len(prefix_len) != n_req or len(req_rows) != n_req + 1:
+        raise ValueError(f"page_table has {n_req} requests: prefix_len needs as many values, req_rows one more")
+    B, max_tail = _int32("B", B), _int32("max_tail", max_tail)
+    if seq_start is None:
+        _need("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+    else:
+        _need("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+        _need("seq_start", seq_start, torch.int32, (B,))
+    if out is not None:
+        _need("out", out, torch.bfloat16, (rows, Hq, d), inner=3)
+    if lse is not None:
+        _need("lse", lse, torch.float32, (Hq, rows), inner=2)
+    _bytes("ws", ws)
+    _sizes(rows, Hq, n_req)
+    h_rows, h_len = _int32s("req_rows", req_rows), _int32s("prefix_len", prefix_len)
+    with _Launch(stream, q, *tensors, page_table, k_tail, v_tail, cu_seqlens, seq_start, out, lse, ws) as call:
+        if out is None:
+            out = call.empty(torch.bfloat16, rows, Hq, d)
+        if lse is None and want_lse:
+            lse = call.empty(torch.float32, Hq, rows)
+        if ws is None:
+            ws = call.workspace(paged_prefix_tail_workspace_bytes(req_rows, prefix_len, B, Hq, Hkv, d))
+        st = lib().blink_paged_prefix_tail_attention(
+            q.data_ptr(), *args, *table, k_tail.data_ptr(), v_tail.data_ptr(), cu_seqlens.data_ptr(), _addr(seq_start), B, rows,
+            n_req, h_rows, h_len, max_tail, Hq, Hkv, d, scale, out.data_ptr(), _addr(lse), ws.data_ptr(), ws.numel(), call.handle)
+    _check(st, "blink_paged_prefix_tail_attention")
+    return out, lse, ws

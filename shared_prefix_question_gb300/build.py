@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libblink.so")
 SOURCES = ["common.cu", "plan.cu", "readout.cu", "attention.cu", "prefix.cu", "debias.cu",
-           "keyweights.cu", "evict.cu", "logprobs.cu"]
+           "keyweights.cu", "evict.cu", "logprobs.cu", "rope.cu", "paged.cu", "pagedattn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

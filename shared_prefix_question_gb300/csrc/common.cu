@@ -42,6 +42,25 @@ bool encode_tmap_3d_bf16(CUtensorMap *map, const void *base, uint64_t d0, uint64
     return r == CUDA_SUCCESS;
 }
 
+bool strided_overlap(const void *a, int64_t sa, int64_t na, const void *b, int64_t sb, int64_t nb, int64_t width_a,
+                     int64_t width_b)
+{
+    if (na < 1 || nb < 1) return false;
+    const int64_t pa = static_cast<int64_t>(reinterpret_cast<uintptr_t>(a));
+    const int64_t pb = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b));
+    if (pa + (na - 1) * sa + width_a <= pb || pb + (nb - 1) * sb + width_b <= pa) return false;
+    if (na == 1 || nb == 1 || sa != sb || sa < 1) return true;
+    const int64_t ahead = ((pb - pa) % sa + sa) % sa;  // where b's rows begin within a's
+    return ahead < width_a || sa - ahead < width_b;
+}
+
+int current_sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
+}
+
 }  // namespace blink
 
 extern "C" const char *blink_status_string(blink_status s)

@@ -28,4 +28,11 @@ bool encode_tmap_3d_bf16(CUtensorMap *map, const void *base, uint64_t d0, uint64
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether rows of `width` bytes, `na` of them `sa` bytes apart from `a`, share a byte with those of `b`.  Rows of
+// one stride may interleave (slices of one wider row); with other strides touching extents count as shared.
+bool strided_overlap(const void *a, int64_t sa, int64_t na, const void *b, int64_t sb, int64_t nb, int64_t width_a,
+                     int64_t width_b);
+
+int current_sm_count();  // of the current device; 0 if it cannot be asked
+
 }  // namespace blink

@@ -1,0 +1,62 @@
+// paged.cuh -- the 8-bit paged cache: its layout, and the conversions between its codes and other types.
+//
+// A page holds `page` tokens of every kv head, head by head: codes[page][head][token][d] in e4m3, and one scale per
+// (page, head), a power of two in e8m0 (the biased exponent alone).  A value is its code times its scale, which is
+// exact in 16 and in 32 bits: a scale moves no bit of a code, so it can be applied to a score or an exponent instead
+// of to each value, and a page whose scale grows loses only what falls below the smallest code.
+#pragma once
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace blink {
+
+constexpr int kScaleBias = 127;
+constexpr int kScaleMin = BLINK_PAGED_SCALE_MIN, kScaleMax = BLINK_PAGED_SCALE_MAX;
+
+struct PagedCache {
+    const uint8_t *k, *v;              // codes
+    const uint8_t *k_scale, *v_scale;  // biased exponents
+    int64_t page_stride, scale_stride; // bytes between pages
+    int n_pages;
+    int log2_page;
+};
+
+// Checks what every call that takes a cache checks, and fills `c`.
+blink_status check_cache(PagedCache &c, const void *k, const void *v, const void *ks, const void *vs, int64_t page_stride,
+                         int64_t scale_stride, int32_t n_pages, int32_t page_tokens, int32_t Hkv, int32_t d);
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ float scale_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + kScaleBias) << 23); }
+
+// Two e4m3 codes (the lower byte first) as two fp16 values, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+// The same for a word's upper two codes.
+__device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t four)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}" : "=r"(r) : "r"(four));
+    return r;
+}
+__device__ __forceinline__ void f16x2_split(uint32_t v, float &lo, float &hi)
+{
+    asm("{\n\t.reg .b16 t, u;\n\tmov.b32 {t, u}, %2;\n\tcvt.f32.f16 %0, t;\n\tcvt.f32.f16 %1, u;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(v));
+}
+// Two values as e4m3 codes: nearest, ties to even, larger ones at the largest code, NaN stays NaN.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+#endif
+}  // namespace blink

@@ -1,0 +1,565 @@
+// pagedattn.cu -- attention of the last tokens of each sequence over its 8-bit pages.
+//
+// One pass over the keys with a running maximum and sum.  A step is 16 keys of one kv head, always within a page; a
+// warp's M tile is 16 of the (token, query head) rows that share that head.  Codes become fp16 values exactly, queries
+// keep their 8 bits in fp16 too (each row moved by a power of two so that its largest value fits), and the scales
+// never touch a value: K's is a factor of the step's scores, V's goes into the weights.
+//
+// Bound by HBM: 2 bytes a key, head and channel against 4 rows' products.  A lane's operands of the products are its
+// own bytes of memory: both products allow any order of the summed index and of the output columns, so a lane takes 16
+// consecutive bytes of a key for four product steps, and 16 consecutive channels of four keys for sixteen output
+// columns.  Each lane therefore copies what it will read (16 bytes at a time, asynchronously, several steps ahead)
+// into a place of its own in shared memory: no barrier, no bank conflicts, no registers held while loads fly.
+#include <cmath>
+
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace blink {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStep = 16;                        // keys
+constexpr int kDepth = 6;                        // steps whose copies are in flight in a warp
+constexpr int kRound = kStep * kWarps;           // keys of a block per step of its warps
+constexpr int kMaxChunk = 32 * kRound;           // a lane holds the page of one step of its warp
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -1e37f;                 // below any score
+constexpr float kHead = 6.f, kSlack = 8.f;       // weights start at 2^kHead and may grow by 2^kSlack before the maximum moves
+
+struct TokenArgs {
+    PagedCache c;
+    const uint16_t *q;
+    const int32_t *table;
+    int64_t table_stride;
+    int table_width;
+    const int32_t *len;
+    int max_len, S, T, Hq, Hkv, g, tiles;  // tiles: M tiles of a sequence and kv head
+    int chunk, chunks;                     // keys of a block, blocks of a sequence, head and tile
+    float scale_log2;
+    uint16_t *out;
+    float *lse;
+    float *part_lse, *part_o;              // [S][Hkv][T g][chunks] and the same with [D] behind
+    int *err;
+};
+
+// A sequence's cached length, inside what the call allows; `bad`: it was not.
+__device__ __forceinline__ int length_of(const TokenArgs &a, int seq, bool &bad)
+{
+    const int n = __ldg(a.len + seq);
+    const int64_t room = static_cast<int64_t>(a.table_width) << a.c.log2_page;
+    const int most = room < a.max_len ? static_cast<int>(room) : a.max_len;
+    bad = n < 0 || n > most;
+    return n < 0 ? 0 : n > most ? most : n;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int D>
+struct Shape {
+    static constexpr int kPieces = D / 64;                 // 16-byte pieces of a key for one lane
+    static constexpr int kCols = D / 8;                    // consecutive channels of a lane in the second product
+    static constexpr int kKBytes = 2 * kPieces * 16;       // of a lane and step
+    static constexpr int kVBytes = 4 * kCols;
+    static constexpr int kStage = 32 * (kKBytes + kVBytes);
+    static constexpr int kRing = kWarps * kDepth * kStage;
+    static constexpr int kPad = D + 4;                     // floats of a row where the warps' sums are joined
+    static constexpr int kJoin = kWarps * 16 * kPad * 4 + 2 * kWarps * 16 * 4;
+    static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __grid_constant__ TokenArgs a)
+{
+    using Sh = Shape<D>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = lane >> 2, quad = lane & 3;  // rows r and r + 8 of the tile, columns 2 quad, 2 quad + 1 of each product
+    const int seq = blockIdx.z, h = blockIdx.y / a.tiles, tile = blockIdx.y - h * a.tiles;
+    const int Tg = a.T * a.g, rho0 = tile * 16, rows = min(16, Tg - rho0);
+
+    ptx::grid_launch_dependents();
+    bool bad;
+    const int len = length_of(a, seq, bad);
+    if (bad && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+    const int k0 = blockIdx.x * a.chunk, k1 = min(len, k0 + a.chunk);
+    if (k0 >= k1 && a.chunks > 1) return;  // the join knows the length too
+
+    // The pages of this warp's steps, one a lane; -1: past the end, or not a page (its keys are masked).
+    const int steps = max(0, (k1 - k0 + kStep - 1) / kStep);
+    const int mine = steps > warp ? (steps - warp + kWarps - 1) / kWarps : 0;
+    int page = -1, scales = 0;
+    if (lane < mine) {
+        const int key = k0 + (warp + lane * kWarps) * kStep;
+        page = __ldg(a.table + seq * a.table_stride + (key >> a.c.log2_page));
+        if (page < 0 || page >= a.c.n_pages) {
+            atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+            page = -1;
+        } else {
+            scales = static_cast<int>(__ldg(a.c.k_scale + page * a.c.scale_stride + h)) |
+                     static_cast<int>(__ldg(a.c.v_scale + page * a.c.scale_stride + h)) << 8;
+        }
+    }
+    const uint32_t ring = ptx::smem_u32(smem) + warp * kDepth * Sh::kStage;
+    const uint8_t *ring_ptr = smem + warp * kDepth * Sh::kStage;
+
+    auto issue = [&](int i) {
+        const int id = __shfl_sync(0xFFFFFFFFu, page, i & 31);
+        if (i < mine) {
+            const int key = k0 + (warp + i * kWarps) * kStep;
+            const uint32_t full = id >= 0 ? 1u : 0u;  // no page: zeros
+            const int64_t at = full ? id * a.c.page_stride + ((static_cast<int64_t>(h) << a.c.log2_page) +
+                                                              (key & ((1 << a.c.log2_page) - 1))) * D
+                                    : 0;
+            const uint32_t slot = ring + (i % kDepth) * Sh::kStage;
+            const uint8_t *k = a.c.k + at + r * D + quad * 16, *v = a.c.v + at + 2 * quad * D + r * Sh::kCols;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int p = 0; p < Sh::kPieces; ++p)
+                    copy16(slot + (t * Sh::kPieces + p) * 512 + lane * 16, full ? k + t * 8 * D + p * 64 : a.c.k, full * 16);
+            const uint32_t vs = slot + 32 * Sh::kKBytes;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // keys 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9
+                const uint8_t *src = full ? v + ((e & 1) + (e >> 1) * 8) * D : a.c.v;
+                if constexpr (Sh::kCols == 16)
+                    copy16(vs + e * 512 + lane * 16, src, full * 16);
+                else
+                    copy8(vs + e * 256 + lane * 8, src, full * 8);
+            }
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) issue(i);
+
+    // Queries as the first operand, in the order of the key bytes: product step 4 p + w takes channels
+    // 64 p + 16 quad + 4 w .. + 3 of this lane.
+    uint32_t qa[4 * Sh::kPieces][4];
+    float base[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int rho = rho0 + r + 8 * u, t = rho / a.g, j = rho - t * a.g;
+        uint4 w[2 * Sh::kPieces];
+#pragma unroll
+        for (int p = 0; p < Sh::kPieces; ++p) {
+            w[2 * p] = w[2 * p + 1] = make_uint4(0, 0, 0, 0);
+            if (rho < Tg) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.q + ((static_cast<int64_t>(seq) * a.T + t) * a.Hq + h * a.g + j) * D + p * 64 + quad * 16);
+                w[2 * p] = __ldg(src);
+                w[2 * p + 1] = __ldg(src + 1);
+            }
+        }
+        const uint32_t *x = reinterpret_cast<const uint32_t *>(w);
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8 * Sh::kPieces; ++e)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        // the row's largest value between 2^9 and 2^10: values 2^-33 of it and smaller lose bits, none overflows
+        int move = 9 - (static_cast<int>(__float_as_uint(m) >> 23) - 127);
+        move = !(m > 0.f) || m == INFINITY ? 0 : min(move, 126);
+        const float f = scale_of(move);
+        base[u] = a.scale_log2 * scale_of(-move);
+#pragma unroll
+        for (int e = 0; e < 8 * Sh::kPieces; ++e) {  // word e: channels 2 e, 2 e + 1 of the lane's 16 of a piece
+            const int step = e / 2;
+            qa[step][u + 2 * (e & 1)] = pack_f16x2(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xFFFF0000u) * f);
+        }
+    }
+    // Keys that rows r and r + 8 see, and the fewest that a row of the tile sees.
+    int see[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) see[u] = len - (a.T - 1 - min(rho0 + r + 8 * u, Tg - 1) / a.g);
+    const int t_first = rho0 / a.g, t_last = (rho0 + rows - 1) / a.g;
+    const int see_least = len - (a.T - 1 - t_first);
+
+    float o[Sh::kCols][4];
+#pragma unroll
+    for (int j = 0; j < Sh::kCols; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    float most[2] = {kNoMax, kNoMax}, sum[2] = {0.f, 0.f};
+    int unit = 0;  // o is in units of 2^unit
+    bool begun = false;
+
+    for (int i = 0; i < mine; ++i) {
+        issue(i + kDepth - 1);
+        copies_wait<kDepth - 1>();
+        const int key = k0 + (warp + i * kWarps) * kStep;
+        const int id = __shfl_sync(0xFFFFFFFFu, page, i), both = __shfl_sync(0xFFFFFFFFu, scales, i);
+        const int ek = (both & 0xFF) - kScaleBias, ev = (both >> 8) - kScaleBias;
+        const uint8_t *slot = ring_ptr + (i % kDepth) * Sh::kStage;
+
+        float s[2][2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[t][p][e] = 0.f;
+#pragma unroll
+            for (int p = 0; p < Sh::kPieces; ++p) {
+                const uint4 k = *reinterpret_cast<const uint4 *>(slot + (t * Sh::kPieces + p) * 512 + lane * 16);
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(&k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mma16816(s[t][(p + e) & 1], qa[4 * p + e], e4m3x2_to_f16x2(w[e]), e4m3x2_hi_to_f16x2(w[e]));
+            }
+        }
+        const bool edge = key + kStep > see_least || id < 0;  // warp-uniform
+        const float fk = scale_of(ek);
+        float x[2][4];  // [row u][key 8 t + 2 quad + c as 2 t + c]
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float f = base[u] * fk;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) x[u][2 * t + c] = (s[t][0][2 * u + c] + s[t][1][2 * u + c]) * f;
+        }
+        if (edge) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (key + 8 * (e >> 1) + 2 * quad + (e & 1) >= see[u] || id < 0) x[u][e] = -INFINITY;
+        }
+        float m[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            m[u] = fmaxf(fmaxf(x[u][0], x[u][1]), fmaxf(x[u][2], x[u][3]));
+            m[u] = fmaxf(m[u], __shfl_xor_sync(0xFFFFFFFFu, m[u], 1));
+            m[u] = fmaxf(m[u], __shfl_xor_sync(0xFFFFFFFFu, m[u], 2));
+        }
+        // The maximum moves only when a weight would pass 2^(kHead + kSlack), the unit when a page's V scale is above
+        // it (a weight might overflow fp16) or far below (weights would lose bits).
+        const bool grow = m[0] > most[0] + kSlack + kHead || m[1] > most[1] + kSlack + kHead;
+        const bool shift = !begun || ev > unit || ev < unit - 6;
+        if (__any_sync(0xFFFFFFFFu, grow) || shift) {
+            const float fu = begun && shift ? scale_of(unit - ev) : 1.f;
+            if (shift) unit = ev;
+            begun = true;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float f = 1.f;
+                if (m[u] > most[u] + kSlack + kHead) {
+                    const float now = m[u] - kHead;
+                    f = ptx::ex2(most[u] - now);
+                    most[u] = now;
+                    sum[u] *= f;
+                }
+                f *= fu;
+#pragma unroll
+                for (int j = 0; j < Sh::kCols; ++j) {
+                    o[j][2 * u] *= f;
+                    o[j][2 * u + 1] *= f;
+                }
+            }
+        }
+        const float fv = scale_of(ev - unit);
+        uint32_t pa[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(x[u][e] - most[u]);
+            sum[u] += (p[0] + p[1]) + (p[2] + p[3]);
+            pa[u] = pack_f16x2(p[0] * fv, p[1] * fv);
+            pa[u + 2] = pack_f16x2(p[2] * fv, p[3] * fv);
+        }
+        uint32_t v[4][Sh::kCols / 4];
+        const uint8_t *vs = slot + 32 * Sh::kKBytes;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (Sh::kCols == 16) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(vs + e * 512 + lane * 16);
+                v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2 *>(vs + e * 256 + lane * 8);
+                v[e][0] = w.x, v[e][1] = w.y;
+            }
+        }
+        if (!edge) {
+#pragma unroll
+            for (int w = 0; w < Sh::kCols / 4; ++w) {
+                const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+                const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+                mma16816(o[4 * w], pa, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
+                mma16816(o[4 * w + 1], pa, e4m3x2_hi_to_f16x2(a0), e4m3x2_hi_to_f16x2(b0));
+                mma16816(o[4 * w + 2], pa, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
+                mma16816(o[4 * w + 3], pa, e4m3x2_hi_to_f16x2(a1), e4m3x2_hi_to_f16x2(b1));
+            }
+        } else {
+            // Keys that a row does not see may hold anything, a NaN times its zero weight too: for each token of the tile
+            // the products run on the keys that it sees, and its rows take them.
+            for (int t = t_first; t <= t_last; ++t) {
+                const int limit = len - (a.T - 1 - t);
+                uint32_t keep[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) keep[e] = key + 2 * quad + (e & 1) + (e >> 1) * 8 < limit ? 0xFFFFFFFFu : 0u;
+                const bool mine0 = (rho0 + r) / a.g == t, mine1 = (rho0 + r + 8) / a.g == t;
+#pragma unroll
+                for (int w = 0; w < Sh::kCols / 4; ++w) {
+                    const uint32_t v0 = v[0][w] & keep[0], v1 = v[1][w] & keep[1], v2 = v[2][w] & keep[2], v3 = v[3][w] & keep[3];
+                    const uint32_t a0 = __byte_perm(v0, v1, 0x5140), a1 = __byte_perm(v0, v1, 0x7362);
+                    const uint32_t b0 = __byte_perm(v2, v3, 0x5140), b1 = __byte_perm(v2, v3, 0x7362);
+                    float d[4][4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d[c][e] = 0.f;
+                    mma16816(d[0], pa, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
+                    mma16816(d[1], pa, e4m3x2_hi_to_f16x2(a0), e4m3x2_hi_to_f16x2(b0));
+                    mma16816(d[2], pa, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
+                    mma16816(d[3], pa, e4m3x2_hi_to_f16x2(a1), e4m3x2_hi_to_f16x2(b1));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        o[4 * w + c][0] += mine0 ? d[c][0] : 0.f;
+                        o[4 * w + c][1] += mine0 ? d[c][1] : 0.f;
+                        o[4 * w + c][2] += mine1 ? d[c][2] : 0.f;
+                        o[4 * w + c][3] += mine1 ? d[c][3] : 0.f;
+                    }
+                }
+            }
+        }
+    }
+
+    // The warps' sums joined through shared memory, over the ring (every copy of this block has landed by the barrier).
+    copies_wait<0>();
+    __syncthreads();
+    float *so = reinterpret_cast<float *>(smem);
+    float *sm = so + kWarps * 16 * Sh::kPad, *sl = sm + kWarps * 16;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        sum[u] += __shfl_xor_sync(0xFFFFFFFFu, sum[u], 1);
+        sum[u] += __shfl_xor_sync(0xFFFFFFFFu, sum[u], 2);
+        if (quad == 0) {
+            sm[warp * 16 + r + 8 * u] = most[u];
+            sl[warp * 16 + r + 8 * u] = sum[u];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int row = r + 8 * u;
+        if (row >= rows) continue;
+        float top = kNoMax;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * 16 + row]);
+        const float f = ptx::ex2(most[u] - top + static_cast<float>(unit));
+        float *dst = so + (warp * 16 + row) * Sh::kPad + 2 * quad * Sh::kCols;  // channels 2 quad kCols ..
+#pragma unroll
+        for (int j = 0; j < Sh::kCols; j += 4) {
+            *reinterpret_cast<float4 *>(dst + j) = make_float4(o[j][2 * u] * f, o[j + 1][2 * u] * f, o[j + 2][2 * u] * f, o[j + 3][2 * u] * f);
+            *reinterpret_cast<float4 *>(dst + Sh::kCols + j) =
+                make_float4(o[j][2 * u + 1] * f, o[j + 1][2 * u + 1] * f, o[j + 2][2 * u + 1] * f, o[j + 3][2 * u + 1] * f);
+        }
+    }
+    __syncthreads();
+    constexpr int kVec = D / 4;
+    for (int e = threadIdx.x; e < rows * kVec; e += kThreads) {
+        const int row = e / kVec, col = (e - row * kVec) * 4;
+        float top = kNoMax, total = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * 16 + row]);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            total += sl[w * 16 + row] * ptx::ex2(sm[w * 16 + row] - top);
+            const float4 p = *reinterpret_cast<const float4 *>(so + (w * 16 + row) * Sh::kPad + col);
+            v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+        }
+        const bool none = total == 0.f;  // no key: zeros, and -inf
+        const float inv = none ? 0.f : 1.f / total, l2 = none ? -INFINITY : top + log2f(total);
+        v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+        const int rho = rho0 + row;
+        if (a.chunks > 1) {
+            const int64_t at = ((static_cast<int64_t>(seq) * a.Hkv + h) * Tg + rho) * a.chunks + blockIdx.x;
+            *reinterpret_cast<float4 *>(a.part_o + at * D + col) = v;
+            if (col == 0) a.part_lse[at] = l2;
+        } else {
+            const int t = rho / a.g, head = h * a.g + rho - t * a.g;
+            const int64_t tok = static_cast<int64_t>(seq) * a.T + t;
+            *reinterpret_cast<uint2 *>(a.out + (tok * a.Hq + head) * D + col) =
+                make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
+            if (col == 0 && a.lse) a.lse[head * static_cast<int64_t>(a.S) * a.T + tok] = l2 * kLn2;
+        }
+    }
+}
+
+constexpr int kJoinThreads = 128;
+
+// The chunks of a row joined by their log-sum-exp, a warp a row: a lane holds four channels (or two).
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const __grid_constant__ TokenArgs a)
+{
+    constexpr int kVec = D / 32;
+    const int lane = threadIdx.x & 31, Tg = a.T * a.g;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    if (row >= static_cast<int64_t>(a.S) * a.Hkv * Tg) return;
+    const int rho = static_cast<int>(row % Tg), h = static_cast<int>(row / Tg % a.Hkv), seq = static_cast<int>(row / Tg / a.Hkv);
+    bool bad;
+    const int len = length_of(a, seq, bad), n = (len + a.chunk - 1) / a.chunk;
+    ptx::grid_dep_wait();
+    const float *pl = a.part_lse + row * a.chunks, *po = a.part_o + row * a.chunks * D + lane * kVec;
+    float top = -INFINITY;
+    for (int c = lane; c < n; c += 32) top = fmaxf(top, pl[c]);
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    float v[kVec] = {}, total = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
+        const float l = pl[c];
+        const float w = l == -INFINITY ? 0.f : ptx::ex2(l - top);  // a NaN stays
+        total += w;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] += w * po[static_cast<int64_t>(c) * D + e];
+    }
+    const bool none = total == 0.f;
+    const float inv = none ? 0.f : 1.f / total;
+    const int t = rho / a.g, head = h * a.g + rho - t * a.g;
+    const int64_t tok = static_cast<int64_t>(seq) * a.T + t;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (tok * a.Hq + head) * D + lane * kVec);
+#pragma unroll
+    for (int e = 0; e < kVec; e += 2) dst[e / 2] = ptx::pack_bf16x2(v[e] * inv, v[e + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[head * static_cast<int64_t>(a.S) * a.T + tok] = none ? -INFINITY : (top + log2f(total)) * kLn2;
+}
+
+struct TokenPlan {
+    int chunk, chunks;
+    size_t lse, o, total;  // offsets of the partial results in the workspace
+};
+
+// Keys of a block: one block a SM runs at a time, so the keys of all (sequence, head, tile) units are cut into about
+// one chunk a SM; a chunk is whole rounds of the block's warps, and at most what the lanes can hold pages for.
+TokenPlan token_plan(int64_t S, int64_t T, int64_t max_len, int64_t Hkv, int64_t g, int d)
+{
+    TokenPlan p{};
+    const int64_t tiles = (T * g + 15) / 16, units = S * Hkv * tiles;
+    const int sms = current_sm_count() > 0 ? current_sm_count() : 1;
+    int64_t chunk = (max_len * units + sms - 1) / sms;
+    chunk = (chunk + kRound - 1) / kRound * kRound;
+    if (chunk > kMaxChunk) chunk = kMaxChunk;
+    if (chunk < kRound) chunk = kRound;
+    p.chunk = static_cast<int>(chunk);
+    p.chunks = static_cast<int>(max_len > 0 ? (max_len + chunk - 1) / chunk : 1);
+    p.lse = kHeaderBytes;
+    p.o = p.total = kHeaderBytes;
+    if (p.chunks > 1) {
+        const size_t parts = static_cast<size_t>(S) * Hkv * T * g * p.chunks;
+        p.o = p.lse + align_up(parts * sizeof(float), 256);
+        p.total = p.o + parts * d * sizeof(float);
+    }
+    return p;
+}
+
+bool token_sizes(int32_t S, int32_t T, int32_t max_len, int32_t Hq, int32_t Hkv, int32_t d, blink_status &st)
+{
+    st = BLINK_INVALID_ARG;
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128) || T < 1 || max_len < 0) return false;
+    st = BLINK_OUT_OF_RANGE;
+    if (S < 1 || S > BLINK_MAX_PLAN_SEQUENCES || T > BLINK_MAX_PAGED_TOKENS || max_len > BLINK_MAX_INPUT_TOKENS) return false;
+    if (Hkv > BLINK_MAX_PAGED_HEADS || Hq / Hkv > 128) return false;
+    if (static_cast<int64_t>(Hkv) * ((static_cast<int64_t>(T) * (Hq / Hkv) + 15) / 16) > 65535) return false;
+    st = BLINK_OK;
+    return true;
+}
+
+}  // namespace
+}  // namespace blink
+
+extern "C" size_t blink_paged_token_attention_workspace(int32_t S, int32_t T, int32_t max_len, int32_t Hq, int32_t Hkv, int32_t d)
+{
+    using namespace blink;
+    blink_status st;
+    if (!token_sizes(S, T, max_len, Hq, Hkv, d, st)) return kHeaderBytes;
+    return token_plan(S, T, max_len, Hkv, Hq / Hkv, d).total;
+}
+
+extern "C" blink_status blink_paged_token_attention(
+    const blink_bf16 *q, const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t *k_scale, const uint8_t *v_scale,
+    int64_t page_stride, int64_t scale_stride, int32_t n_pages, int32_t page_tokens, const int32_t *d_page_table,
+    int64_t table_stride, int32_t table_width, const int32_t *d_len, int32_t S, int32_t T, int32_t max_len, int32_t Hq,
+    int32_t Hkv, int32_t d, float scale, blink_bf16 *out, float *lse, void *d_ws, size_t ws_bytes, cudaStream_t stream)
+{
+    using namespace blink;
+    TokenArgs a{};
+    blink_status st = check_cache(a.c, k_codes, v_codes, k_scale, v_scale, page_stride, scale_stride, n_pages, page_tokens, Hkv, d);
+    if (st != BLINK_OK) return st;
+    if (!token_sizes(S, T, max_len, Hq, Hkv, d, st)) return st;
+    if (!q || !d_page_table || !d_len || !out || !d_ws) return BLINK_INVALID_ARG;
+    if (table_width < 1 || (S > 1 && table_stride < table_width) || std::isnan(scale) || std::isinf(scale)) return BLINK_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(d_ws)) return BLINK_INVALID_ARG;
+    const TokenPlan plan = token_plan(S, T, max_len, Hkv, Hq / Hkv, d);
+    if (ws_bytes < plan.total) return BLINK_WORKSPACE_TOO_SMALL;
+    auto *ws = static_cast<uint8_t *>(d_ws);
+    a.q = q;
+    a.table = d_page_table;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.len = d_len;
+    a.max_len = max_len;
+    a.S = S;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.g = Hq / Hkv;
+    a.tiles = (T * a.g + 15) / 16;
+    a.chunk = plan.chunk;
+    a.chunks = plan.chunks;
+    a.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(d))) * kLog2e;
+    a.out = out;
+    a.lse = lse;
+    a.part_lse = reinterpret_cast<float *>(ws + plan.lse);
+    a.part_o = reinterpret_cast<float *>(ws + plan.o);
+    a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
+    const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(Hkv * a.tiles), static_cast<unsigned>(S));
+    const int smem = d == 128 ? Shape<128>::kSmem : Shape<64>::kSmem;
+    auto kern = d == 128 ? token_attention_kernel<128> : token_attention_kernel<64>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BLINK_CUDA_ERROR;
+    kern<<<grid, kThreads, smem, stream>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return BLINK_CUDA_ERROR;
+    if (a.chunks == 1) return BLINK_OK;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const int64_t n = static_cast<int64_t>(S) * Hkv * T * a.g;
+    cfg.gridDim = dim3(static_cast<unsigned>((n + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = d == 128 ? cudaLaunchKernelEx(&cfg, token_join_kernel<128>, a) : cudaLaunchKernelEx(&cfg, token_join_kernel<64>, a);
+    return e == cudaSuccess ? BLINK_OK : BLINK_CUDA_ERROR;
+}
