@@ -1,4 +1,5 @@
 // common.cu -- status strings, the device error word, tensor-map encoding.
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -56,9 +57,13 @@ bool strided_overlap(const void *a, int64_t sa, int64_t na, const void *b, int64
 
 int current_sm_count()
 {
+    static std::atomic<int> known[64];  // by device: the count does not change, and asking costs a small call's time
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 }  // namespace blink

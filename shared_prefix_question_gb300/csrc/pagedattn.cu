@@ -1,15 +1,18 @@
 // pagedattn.cu -- attention of the last tokens of each sequence over its 8-bit pages.
 //
-// One pass over the keys with a running maximum and sum.  A step is 16 keys of one kv head, always within a page; a
-// warp's M tile is 16 of the (token, query head) rows that share that head.  Codes become fp16 values exactly, queries
-// keep their 8 bits in fp16 too (each row moved by a power of two so that its largest value fits), and the scales
-// never touch a value: K's is a factor of the step's scores, V's goes into the weights.
+// One pass over the keys with a running maximum and sum.  A step is 16 keys of one kv head, always within a page.  Keys
+// are the rows of the first product (S^T = K Q^T) and channels those of the second (O^T = V^T P^T); the columns of both
+// are 8 of the (token, query head) rows that share the kv head, so that four rows waste half of the products and not
+// three quarters.  Codes become fp16 values exactly, queries keep their 8 bits in fp16 too (each row moved by a power
+// of two so that its largest value fits), and the scales never touch a value: K's is a factor of the step's scores,
+// V's goes into the weights.
 //
 // Bound by HBM: 2 bytes a key, head and channel against 4 rows' products.  A lane's operands of the products are its
-// own bytes of memory: both products allow any order of the summed index and of the output columns, so a lane takes 16
-// consecutive bytes of a key for four product steps, and 16 consecutive channels of four keys for sixteen output
-// columns.  Each lane therefore copies what it will read (16 bytes at a time, asynchronously, several steps ahead)
-// into a place of its own in shared memory: no barrier, no bank conflicts, no registers held while loads fly.
+// own bytes of memory: both products allow any order of the summed index and of the output's channels, so a lane takes
+// 16 consecutive bytes of a key for four product steps, and 16 consecutive channels of four keys for eight products.
+// Each lane therefore copies what it will read (16 bytes at a time, asynchronously, some steps ahead) into a place of
+// its own in shared memory: no barrier, no bank conflicts, no registers held while loads fly.  A warp's step is a chain
+// of products, exponentials and products again, so it takes warps to hide it: blocks of four, several an SM.
 #include <cmath>
 
 #include "paged.cuh"
@@ -18,10 +21,9 @@
 namespace blink {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;                        // keys
-constexpr int kDepth = 6;                        // steps whose copies are in flight in a warp
 constexpr int kRound = kStep * kWarps;           // keys of a block per step of its warps
 constexpr int kMaxChunk = 32 * kRound;           // a lane holds the page of one step of its warp
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -83,8 +85,19 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
-template <int D>
+__device__ __forceinline__ uint32_t transposed(uint32_t v)  // of an 8 x 8 matrix of 16-bit values over the warp
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// NT: 8-row column tiles of a block.
+template <int D, int NT>
 struct Shape {
+    static constexpr int kResident = NT == 1 ? 4 : 3;      // blocks of an SM, as far as registers go
+    static constexpr int kDepth = NT == 1 ? 3 : 4;         // steps of a warp in shared memory, one of them in use
+    static constexpr int kRows = 8 * NT;
     static constexpr int kPieces = D / 64;                 // 16-byte pieces of a key for one lane
     static constexpr int kCols = D / 8;                    // consecutive channels of a lane in the second product
     static constexpr int kKBytes = 2 * kPieces * 16;       // of a lane and step
@@ -92,19 +105,20 @@ struct Shape {
     static constexpr int kStage = 32 * (kKBytes + kVBytes);
     static constexpr int kRing = kWarps * kDepth * kStage;
     static constexpr int kPad = D + 4;                     // floats of a row where the warps' sums are joined
-    static constexpr int kJoin = kWarps * 16 * kPad * 4 + 2 * kWarps * 16 * 4;
+    static constexpr int kJoin = kWarps * kRows * kPad * 4 + 2 * kWarps * kRows * 4;
     static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __grid_constant__ TokenArgs a)
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_attention_kernel(const __grid_constant__ TokenArgs a)
 {
-    using Sh = Shape<D>;
+    using Sh = Shape<D, NT>;
+    constexpr int kDepth = Sh::kDepth;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = lane >> 2, quad = lane & 3;  // rows r and r + 8 of the tile, columns 2 quad, 2 quad + 1 of each product
+    const int r = lane >> 2, quad = lane & 3;  // products: rows r and r + 8, columns 2 quad and 2 quad + 1
     const int seq = blockIdx.z, h = blockIdx.y / a.tiles, tile = blockIdx.y - h * a.tiles;
-    const int Tg = a.T * a.g, rho0 = tile * 16, rows = min(16, Tg - rho0);
+    const int Tg = a.T * a.g, rho0 = tile * Sh::kRows, rows = min(Sh::kRows, Tg - rho0);
 
     ptx::grid_launch_dependents();
     bool bad;
@@ -116,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __gr
     // The pages of this warp's steps, one a lane; -1: past the end, or not a page (its keys are masked).
     const int steps = max(0, (k1 - k0 + kStep - 1) / kStep);
     const int mine = steps > warp ? (steps - warp + kWarps - 1) / kWarps : 0;
-    int page = -1, scales = 0;
+    int page = -1, scales = kScaleBias | kScaleBias << 8;
     if (lane < mine) {
         const int key = k0 + (warp + lane * kWarps) * kStep;
         page = __ldg(a.table + seq * a.table_stride + (key >> a.c.log2_page));
@@ -131,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __gr
     const uint32_t ring = ptx::smem_u32(smem) + warp * kDepth * Sh::kStage;
     const uint8_t *ring_ptr = smem + warp * kDepth * Sh::kStage;
 
-    auto issue = [&](int i) {
+    auto issue = [&](int i, int stage) {
         const int id = __shfl_sync(0xFFFFFFFFu, page, i & 31);
         if (i < mine) {
             const int key = k0 + (warp + i * kWarps) * kStep;
@@ -139,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __gr
             const int64_t at = full ? id * a.c.page_stride + ((static_cast<int64_t>(h) << a.c.log2_page) +
                                                               (key & ((1 << a.c.log2_page) - 1))) * D
                                     : 0;
-            const uint32_t slot = ring + (i % kDepth) * Sh::kStage;
+            const uint32_t slot = ring + stage * Sh::kStage;
             const uint8_t *k = a.c.k + at + r * D + quad * 16, *v = a.c.v + at + 2 * quad * D + r * Sh::kCols;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -159,15 +173,16 @@ __global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __gr
         copies_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) issue(i);
+    for (int i = 0; i < kDepth - 1; ++i) issue(i, i);
 
-    // Queries as the first operand, in the order of the key bytes: product step 4 p + w takes channels
-    // 64 p + 16 quad + 4 w .. + 3 of this lane.
-    uint32_t qa[4 * Sh::kPieces][4];
-    float base[2];
+    // Queries as the second operand, in the order of the key bytes: product step 4 p + w takes channels
+    // 64 p + 16 quad + 4 w .. + 3 of this lane; the lane holds row r of each tile.
+    uint32_t qb[NT][4 * Sh::kPieces][2];
+    float base[NT][2];  // of rows 2 quad and 2 quad + 1: the factor of their scores
+    int see[NT][2];     // keys that they see
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int rho = rho0 + r + 8 * u, t = rho / a.g, j = rho - t * a.g;
+    for (int y = 0; y < NT; ++y) {
+        const int rho = rho0 + 8 * y + r, t = rho / a.g, j = rho - t * a.g;
         uint4 w[2 * Sh::kPieces];
 #pragma unroll
         for (int p = 0; p < Sh::kPieces; ++p) {
@@ -189,114 +204,116 @@ __global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __gr
         // the row's largest value between 2^9 and 2^10: values 2^-33 of it and smaller lose bits, none overflows
         int move = 9 - (static_cast<int>(__float_as_uint(m) >> 23) - 127);
         move = !(m > 0.f) || m == INFINITY ? 0 : min(move, 126);
-        const float f = scale_of(move);
-        base[u] = a.scale_log2 * scale_of(-move);
+        const float f = scale_of(move), back = a.scale_log2 * scale_of(-move);
 #pragma unroll
-        for (int e = 0; e < 8 * Sh::kPieces; ++e) {  // word e: channels 2 e, 2 e + 1 of the lane's 16 of a piece
-            const int step = e / 2;
-            qa[step][u + 2 * (e & 1)] = pack_f16x2(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xFFFF0000u) * f);
+        for (int e = 0; e < 8 * Sh::kPieces; ++e)  // word e: channels 2 e, 2 e + 1 of the lane's 16 of a piece
+            qb[y][e / 2][e & 1] = pack_f16x2(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xFFFF0000u) * f);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            base[y][c] = __shfl_sync(0xFFFFFFFFu, back, (2 * quad + c) * 4);
+            see[y][c] = len - (a.T - 1 - min(rho0 + 8 * y + 2 * quad + c, Tg - 1) / a.g);
         }
     }
-    // Keys that rows r and r + 8 see, and the fewest that a row of the tile sees.
-    int see[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) see[u] = len - (a.T - 1 - min(rho0 + r + 8 * u, Tg - 1) / a.g);
     const int t_first = rho0 / a.g, t_last = (rho0 + rows - 1) / a.g;
-    const int see_least = len - (a.T - 1 - t_first);
+    const int see_least = len - (a.T - 1 - t_first);  // the fewest keys that a row sees
 
-    float o[Sh::kCols][4];
+    float o[NT][Sh::kCols / 2][4];  // channels kCols r + 2 j (first two) and + 1, rows 2 quad and 2 quad + 1
 #pragma unroll
-    for (int j = 0; j < Sh::kCols; ++j)
+    for (int y = 0; y < NT; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    float most[2] = {kNoMax, kNoMax}, sum[2] = {0.f, 0.f};
-    int unit = 0;  // o is in units of 2^unit
-    bool begun = false;
+        for (int j = 0; j < Sh::kCols / 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[y][j][e] = 0.f;
+    float most[NT][2], sum[NT][2];
+#pragma unroll
+    for (int y = 0; y < NT; ++y) most[y][0] = most[y][1] = kNoMax, sum[y][0] = sum[y][1] = 0.f;
+    int unit = kScaleMin - 1;  // o is in units of 2^unit
 
+    int stage = 0;
     for (int i = 0; i < mine; ++i) {
-        issue(i + kDepth - 1);
+        issue(i + kDepth - 1, stage == 0 ? kDepth - 1 : stage - 1);
         copies_wait<kDepth - 1>();
         const int key = k0 + (warp + i * kWarps) * kStep;
         const int id = __shfl_sync(0xFFFFFFFFu, page, i), both = __shfl_sync(0xFFFFFFFFu, scales, i);
         const int ek = (both & 0xFF) - kScaleBias, ev = (both >> 8) - kScaleBias;
-        const uint8_t *slot = ring_ptr + (i % kDepth) * Sh::kStage;
+        const uint8_t *slot = ring_ptr + stage * Sh::kStage;
+        stage = stage + 1 == kDepth ? 0 : stage + 1;
 
-        float s[2][2][4];
+        float s[NT][2][4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int y = 0; y < NT; ++y)
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[t][p][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[y][b][e] = 0.f;
 #pragma unroll
-            for (int p = 0; p < Sh::kPieces; ++p) {
-                const uint4 k = *reinterpret_cast<const uint4 *>(slot + (t * Sh::kPieces + p) * 512 + lane * 16);
-                const uint32_t *w = reinterpret_cast<const uint32_t *>(&k);
+        for (int p = 0; p < Sh::kPieces; ++p) {
+            const uint4 klo = *reinterpret_cast<const uint4 *>(slot + p * 512 + lane * 16);                   // key r
+            const uint4 khi = *reinterpret_cast<const uint4 *>(slot + (Sh::kPieces + p) * 512 + lane * 16);  // key r + 8
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(&klo), *x = reinterpret_cast<const uint32_t *>(&khi);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    mma16816(s[t][(p + e) & 1], qa[4 * p + e], e4m3x2_to_f16x2(w[e]), e4m3x2_hi_to_f16x2(w[e]));
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t ka[4] = {e4m3x2_to_f16x2(w[e]), e4m3x2_to_f16x2(x[e]), e4m3x2_hi_to_f16x2(w[e]),
+                                        e4m3x2_hi_to_f16x2(x[e])};
+#pragma unroll
+                for (int y = 0; y < NT; ++y) mma16816(s[y][e & 1], ka, qb[y][4 * p + e][0], qb[y][4 * p + e][1]);
             }
         }
         const bool edge = key + kStep > see_least || id < 0;  // warp-uniform
         const float fk = scale_of(ek);
-        float x[2][4];  // [row u][key 8 t + 2 quad + c as 2 t + c]
+        float x[NT][4];  // keys r (first two) and r + 8, rows 2 quad and 2 quad + 1
+        bool grow = false;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const float f = base[u] * fk;
+        for (int y = 0; y < NT; ++y) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) x[u][2 * t + c] = (s[t][0][2 * u + c] + s[t][1][2 * u + c]) * f;
-        }
-        if (edge) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int e = 0; e < 4; ++e) x[y][e] = (s[y][0][e] + s[y][1][e]) * (base[y][e & 1] * fk);
+            if (edge) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (key + 8 * (e >> 1) + 2 * quad + (e & 1) >= see[u] || id < 0) x[u][e] = -INFINITY;
-        }
-        float m[2];
+                    if (key + r + 8 * (e >> 1) >= see[y][e & 1] || id < 0) x[y][e] = -INFINITY;
+            }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            m[u] = fmaxf(fmaxf(x[u][0], x[u][1]), fmaxf(x[u][2], x[u][3]));
-            m[u] = fmaxf(m[u], __shfl_xor_sync(0xFFFFFFFFu, m[u], 1));
-            m[u] = fmaxf(m[u], __shfl_xor_sync(0xFFFFFFFFu, m[u], 2));
+            for (int c = 0; c < 2; ++c) grow = grow || fmaxf(x[y][c], x[y][c + 2]) > most[y][c] + (kSlack + kHead);
         }
         // The maximum moves only when a weight would pass 2^(kHead + kSlack), the unit when a page's V scale is above
         // it (a weight might overflow fp16) or far below (weights would lose bits).
-        const bool grow = m[0] > most[0] + kSlack + kHead || m[1] > most[1] + kSlack + kHead;
-        const bool shift = !begun || ev > unit || ev < unit - 6;
+        const bool shift = ev > unit || ev < unit - 6;
         if (__any_sync(0xFFFFFFFFu, grow) || shift) {
-            const float fu = begun && shift ? scale_of(unit - ev) : 1.f;
+            const float fu = unit < kScaleMin || !shift ? 1.f : scale_of(unit - ev);
             if (shift) unit = ev;
-            begun = true;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float f = 1.f;
-                if (m[u] > most[u] + kSlack + kHead) {
-                    const float now = m[u] - kHead;
-                    f = ptx::ex2(most[u] - now);
-                    most[u] = now;
-                    sum[u] *= f;
-                }
-                f *= fu;
+            for (int y = 0; y < NT; ++y)
 #pragma unroll
-                for (int j = 0; j < Sh::kCols; ++j) {
-                    o[j][2 * u] *= f;
-                    o[j][2 * u + 1] *= f;
+                for (int c = 0; c < 2; ++c) {
+                    float m = fmaxf(x[y][c], x[y][c + 2]);
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+                    float f = 1.f;
+                    if (m > most[y][c] + (kSlack + kHead)) {
+                        const float now = m - kHead;
+                        f = ptx::ex2(most[y][c] - now);
+                        most[y][c] = now;
+                        sum[y][c] *= f;
+                    }
+                    f *= fu;
+#pragma unroll
+                    for (int j = 0; j < Sh::kCols / 2; ++j) {
+                        o[y][j][c] *= f;
+                        o[y][j][c + 2] *= f;
+                    }
                 }
-            }
         }
         const float fv = scale_of(ev - unit);
-        uint32_t pa[4];
+        uint32_t pb[NT][2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int y = 0; y < NT; ++y) {
             float p[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(x[u][e] - most[u]);
-            sum[u] += (p[0] + p[1]) + (p[2] + p[3]);
-            pa[u] = pack_f16x2(p[0] * fv, p[1] * fv);
-            pa[u + 2] = pack_f16x2(p[2] * fv, p[3] * fv);
+            for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(x[y][e] - most[y][e & 1]);
+            sum[y][0] += p[0] + p[2];
+            sum[y][1] += p[1] + p[3];
+            pb[y][0] = transposed(pack_f16x2(p[0] * fv, p[1] * fv));
+            pb[y][1] = transposed(pack_f16x2(p[2] * fv, p[3] * fv));
         }
         uint32_t v[4][Sh::kCols / 4];
         const uint8_t *vs = slot + 32 * Sh::kKBytes;
@@ -310,15 +327,21 @@ __global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __gr
                 v[e][0] = w.x, v[e][1] = w.y;
             }
         }
+        auto operand = [](uint32_t (&va)[4], uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3, uint32_t pick) {
+            const uint32_t lo = __byte_perm(v0, v1, pick), hi = __byte_perm(v2, v3, pick);  // two channels of two keys each
+            va[0] = e4m3x2_to_f16x2(lo);
+            va[1] = e4m3x2_hi_to_f16x2(lo);
+            va[2] = e4m3x2_to_f16x2(hi);
+            va[3] = e4m3x2_hi_to_f16x2(hi);
+        };
         if (!edge) {
 #pragma unroll
-            for (int w = 0; w < Sh::kCols / 4; ++w) {
-                const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-                const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-                mma16816(o[4 * w], pa, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
-                mma16816(o[4 * w + 1], pa, e4m3x2_hi_to_f16x2(a0), e4m3x2_hi_to_f16x2(b0));
-                mma16816(o[4 * w + 2], pa, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
-                mma16816(o[4 * w + 3], pa, e4m3x2_hi_to_f16x2(a1), e4m3x2_hi_to_f16x2(b1));
+            for (int j = 0; j < Sh::kCols / 2; ++j) {
+                const int w = j / 2;
+                uint32_t va[4];
+                operand(va, v[0][w], v[1][w], v[2][w], v[3][w], j & 1 ? 0x7362u : 0x5140u);
+#pragma unroll
+                for (int y = 0; y < NT; ++y) mma16816(o[y][j], va, pb[y][0], pb[y][1]);
             }
         } else {
             // Keys that a row does not see may hold anything, a NaN times its zero weight too: for each token of the tile
@@ -328,27 +351,18 @@ __global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __gr
                 uint32_t keep[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) keep[e] = key + 2 * quad + (e & 1) + (e >> 1) * 8 < limit ? 0xFFFFFFFFu : 0u;
-                const bool mine0 = (rho0 + r) / a.g == t, mine1 = (rho0 + r + 8) / a.g == t;
 #pragma unroll
-                for (int w = 0; w < Sh::kCols / 4; ++w) {
-                    const uint32_t v0 = v[0][w] & keep[0], v1 = v[1][w] & keep[1], v2 = v[2][w] & keep[2], v3 = v[3][w] & keep[3];
-                    const uint32_t a0 = __byte_perm(v0, v1, 0x5140), a1 = __byte_perm(v0, v1, 0x7362);
-                    const uint32_t b0 = __byte_perm(v2, v3, 0x5140), b1 = __byte_perm(v2, v3, 0x7362);
-                    float d[4][4];
+                for (int j = 0; j < Sh::kCols / 2; ++j) {
+                    const int w = j / 2;
+                    uint32_t va[4];
+                    operand(va, v[0][w] & keep[0], v[1][w] & keep[1], v[2][w] & keep[2], v[3][w] & keep[3], j & 1 ? 0x7362u : 0x5140u);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int y = 0; y < NT; ++y) {
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma16816(d, va, pb[y][0], pb[y][1]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) d[c][e] = 0.f;
-                    mma16816(d[0], pa, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
-                    mma16816(d[1], pa, e4m3x2_hi_to_f16x2(a0), e4m3x2_hi_to_f16x2(b0));
-                    mma16816(d[2], pa, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
-                    mma16816(d[3], pa, e4m3x2_hi_to_f16x2(a1), e4m3x2_hi_to_f16x2(b1));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        o[4 * w + c][0] += mine0 ? d[c][0] : 0.f;
-                        o[4 * w + c][1] += mine0 ? d[c][1] : 0.f;
-                        o[4 * w + c][2] += mine1 ? d[c][2] : 0.f;
-                        o[4 * w + c][3] += mine1 ? d[c][3] : 0.f;
+                        for (int e = 0; e < 4; ++e)
+                            o[y][j][e] += (rho0 + 8 * y + 2 * quad + (e & 1)) / a.g == t ? d[e] : 0.f;
                     }
                 }
             }
@@ -359,45 +373,47 @@ __global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __gr
     copies_wait<0>();
     __syncthreads();
     float *so = reinterpret_cast<float *>(smem);
-    float *sm = so + kWarps * 16 * Sh::kPad, *sl = sm + kWarps * 16;
+    float *sm = so + kWarps * Sh::kRows * Sh::kPad, *sl = sm + kWarps * Sh::kRows;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        sum[u] += __shfl_xor_sync(0xFFFFFFFFu, sum[u], 1);
-        sum[u] += __shfl_xor_sync(0xFFFFFFFFu, sum[u], 2);
-        if (quad == 0) {
-            sm[warp * 16 + r + 8 * u] = most[u];
-            sl[warp * 16 + r + 8 * u] = sum[u];
+    for (int y = 0; y < NT; ++y)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) sum[y][c] += __shfl_xor_sync(0xFFFFFFFFu, sum[y][c], d);
+            if (r == 0) {
+                sm[warp * Sh::kRows + 8 * y + 2 * quad + c] = most[y][c];
+                sl[warp * Sh::kRows + 8 * y + 2 * quad + c] = sum[y][c];
+            }
         }
-    }
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int row = r + 8 * u;
-        if (row >= rows) continue;
-        float top = kNoMax;
+    for (int y = 0; y < NT; ++y)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * 16 + row]);
-        const float f = ptx::ex2(most[u] - top + static_cast<float>(unit));
-        float *dst = so + (warp * 16 + row) * Sh::kPad + 2 * quad * Sh::kCols;  // channels 2 quad kCols ..
+        for (int c = 0; c < 2; ++c) {
+            const int row = 8 * y + 2 * quad + c;
+            if (row >= rows) continue;
+            float top = kNoMax;
 #pragma unroll
-        for (int j = 0; j < Sh::kCols; j += 4) {
-            *reinterpret_cast<float4 *>(dst + j) = make_float4(o[j][2 * u] * f, o[j + 1][2 * u] * f, o[j + 2][2 * u] * f, o[j + 3][2 * u] * f);
-            *reinterpret_cast<float4 *>(dst + Sh::kCols + j) =
-                make_float4(o[j][2 * u + 1] * f, o[j + 1][2 * u + 1] * f, o[j + 2][2 * u + 1] * f, o[j + 3][2 * u + 1] * f);
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * Sh::kRows + row]);
+            const float f = ptx::ex2(most[y][c] - top + static_cast<float>(unit));
+            float *dst = so + (warp * Sh::kRows + row) * Sh::kPad + r * Sh::kCols;
+#pragma unroll
+            for (int j = 0; j < Sh::kCols / 2; j += 2)
+                *reinterpret_cast<float4 *>(dst + 2 * j) =
+                    make_float4(o[y][j][c] * f, o[y][j][c + 2] * f, o[y][j + 1][c] * f, o[y][j + 1][c + 2] * f);
         }
-    }
     __syncthreads();
     constexpr int kVec = D / 4;
     for (int e = threadIdx.x; e < rows * kVec; e += kThreads) {
         const int row = e / kVec, col = (e - row * kVec) * 4;
         float top = kNoMax, total = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * 16 + row]);
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * Sh::kRows + row]);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            total += sl[w * 16 + row] * ptx::ex2(sm[w * 16 + row] - top);
-            const float4 p = *reinterpret_cast<const float4 *>(so + (w * 16 + row) * Sh::kPad + col);
+            total += sl[w * Sh::kRows + row] * ptx::ex2(sm[w * Sh::kRows + row] - top);
+            const float4 p = *reinterpret_cast<const float4 *>(so + (w * Sh::kRows + row) * Sh::kPad + col);
             v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
         }
         const bool none = total == 0.f;  // no key: zeros, and -inf
@@ -418,16 +434,18 @@ __global__ void __launch_bounds__(kThreads, 1) token_attention_kernel(const __gr
     }
 }
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = 4;
+constexpr int kJoinThreads = kJoinWarps * 32;
 
-// The chunks of a row joined by their log-sum-exp, a warp a row: a lane holds four channels (or two).
+// The chunks of a row joined by their log-sum-exp, a block a row: its warps share the chunks out, a lane holds D / 32
+// channels.  Bound by latency: all loads of eight chunks are in flight at once.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const __grid_constant__ TokenArgs a)
 {
     constexpr int kVec = D / 32;
-    const int lane = threadIdx.x & 31, Tg = a.T * a.g;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
-    if (row >= static_cast<int64_t>(a.S) * a.Hkv * Tg) return;
+    __shared__ float so[kJoinWarps][D], sw[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Tg = a.T * a.g;
+    const int64_t row = blockIdx.x;
     const int rho = static_cast<int>(row % Tg), h = static_cast<int>(row / Tg % a.Hkv), seq = static_cast<int>(row / Tg / a.Hkv);
     bool bad;
     const int len = length_of(a, seq, bad), n = (len + a.chunk - 1) / a.chunk;
@@ -437,16 +455,30 @@ __global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const __grid_c
     for (int c = lane; c < n; c += 32) top = fmaxf(top, pl[c]);
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     float v[kVec] = {}, total = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) {
+#pragma unroll 8
+    for (int c = warp; c < n; c += kJoinWarps) {
         const float l = pl[c];
         const float w = l == -INFINITY ? 0.f : ptx::ex2(l - top);  // a NaN stays
         total += w;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) v[e] += w * po[static_cast<int64_t>(c) * D + e];
     }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) so[warp][lane * kVec + e] = v[e];
+    if (lane == 0) sw[warp] = total;
+    __syncthreads();
+    if (warp != 0) return;
+    total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) total += sw[w];
     const bool none = total == 0.f;
     const float inv = none ? 0.f : 1.f / total;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+        v[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) v[e] += so[w][lane * kVec + e];
+    }
     const int t = rho / a.g, head = h * a.g + rho - t * a.g;
     const int64_t tok = static_cast<int64_t>(seq) * a.T + t;
     uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (tok * a.Hq + head) * D + lane * kVec);
@@ -456,18 +488,22 @@ __global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const __grid_c
 }
 
 struct TokenPlan {
-    int chunk, chunks;
+    int wide;              // column tiles of a block: two where the rows of a head need them
+    int tiles, chunk, chunks;
     size_t lse, o, total;  // offsets of the partial results in the workspace
 };
 
-// Keys of a block: one block a SM runs at a time, so the keys of all (sequence, head, tile) units are cut into about
-// one chunk a SM; a chunk is whole rounds of the block's warps, and at most what the lanes can hold pages for.
+// Keys of a block: the keys of all (sequence, head, tile) units are cut into about as many chunks as blocks run at a
+// time; a chunk is whole rounds of the block's warps, and at most what the lanes can hold pages for.
 TokenPlan token_plan(int64_t S, int64_t T, int64_t max_len, int64_t Hkv, int64_t g, int d)
 {
     TokenPlan p{};
-    const int64_t tiles = (T * g + 15) / 16, units = S * Hkv * tiles;
-    const int sms = current_sm_count() > 0 ? current_sm_count() : 1;
-    int64_t chunk = (max_len * units + sms - 1) / sms;
+    p.wide = T * g > 8 ? 2 : 1;
+    p.tiles = static_cast<int>((T * g + 8 * p.wide - 1) / (8 * p.wide));
+    const int64_t units = S * Hkv * p.tiles;
+    const int64_t at_once = static_cast<int64_t>(current_sm_count() > 0 ? current_sm_count() : 1) *
+                            (p.wide == 1 ? Shape<128, 1>::kResident : Shape<128, 2>::kResident);
+    int64_t chunk = (max_len * units + at_once - 1) / at_once;
     chunk = (chunk + kRound - 1) / kRound * kRound;
     if (chunk > kMaxChunk) chunk = kMaxChunk;
     if (chunk < kRound) chunk = kRound;
@@ -521,6 +557,8 @@ extern "C" blink_status blink_paged_token_attention(
     if (table_width < 1 || (S > 1 && table_stride < table_width) || std::isnan(scale) || std::isinf(scale)) return BLINK_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(d_ws)) return BLINK_INVALID_ARG;
     const TokenPlan plan = token_plan(S, T, max_len, Hkv, Hq / Hkv, d);
+    const int64_t joined = static_cast<int64_t>(S) * T * Hq;  // rows of the second launch
+    if (joined > 0x7FFFFFFF) return BLINK_OUT_OF_RANGE;
     if (ws_bytes < plan.total) return BLINK_WORKSPACE_TOO_SMALL;
     auto *ws = static_cast<uint8_t *>(d_ws);
     a.q = q;
@@ -534,7 +572,7 @@ extern "C" blink_status blink_paged_token_attention(
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.g = Hq / Hkv;
-    a.tiles = (T * a.g + 15) / 16;
+    a.tiles = plan.tiles;
     a.chunk = plan.chunk;
     a.chunks = plan.chunks;
     a.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(d))) * kLog2e;
@@ -544,18 +582,22 @@ extern "C" blink_status blink_paged_token_attention(
     a.part_o = reinterpret_cast<float *>(ws + plan.o);
     a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
     const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(Hkv * a.tiles), static_cast<unsigned>(S));
-    const int smem = d == 128 ? Shape<128>::kSmem : Shape<64>::kSmem;
-    auto kern = d == 128 ? token_attention_kernel<128> : token_attention_kernel<64>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BLINK_CUDA_ERROR;
-    kern<<<grid, kThreads, smem, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return BLINK_CUDA_ERROR;
+    auto launch = [&](auto kern, int smem) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+        kern<<<grid, kThreads, smem, stream>>>(a);
+        return cudaGetLastError() == cudaSuccess;
+    };
+    const bool launched = d == 128 ? (plan.wide == 1 ? launch(token_attention_kernel<128, 1>, Shape<128, 1>::kSmem)
+                                                     : launch(token_attention_kernel<128, 2>, Shape<128, 2>::kSmem))
+                                   : (plan.wide == 1 ? launch(token_attention_kernel<64, 1>, Shape<64, 1>::kSmem)
+                                                     : launch(token_attention_kernel<64, 2>, Shape<64, 2>::kSmem));
+    if (!launched) return BLINK_CUDA_ERROR;
     if (a.chunks == 1) return BLINK_OK;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    const int64_t n = static_cast<int64_t>(S) * Hkv * T * a.g;
-    cfg.gridDim = dim3(static_cast<unsigned>((n + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    cfg.gridDim = dim3(static_cast<unsigned>(joined));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
