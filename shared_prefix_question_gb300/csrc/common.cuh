@@ -26,6 +26,10 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool encode_tmap_3d_bf16(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
                          uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1, uint32_t b2);
 
+// The same over bytes, with `swizzle` (128 or 64) bytes of swizzle.
+bool encode_tmap_3d_bytes(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1_bytes,
+                          uint64_t stride2_bytes, uint32_t b0, uint32_t b1, uint32_t b2, int swizzle);
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Whether rows of `width` bytes, `na` of them `sa` bytes apart from `a`, share a byte with those of `b`.  Rows of

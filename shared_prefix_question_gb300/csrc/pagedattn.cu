@@ -10,9 +10,10 @@
 // Bound by HBM: 2 bytes a key, head and channel against 4 rows' products.  A lane's operands of the products are its
 // own bytes of memory: both products allow any order of the summed index and of the output's channels, so a lane takes
 // 16 consecutive bytes of a key for four product steps, and 16 consecutive channels of four keys for eight products.
-// Each lane therefore copies what it will read (16 bytes at a time, asynchronously, some steps ahead) into a place of
-// its own in shared memory: no barrier, no bank conflicts, no registers held while loads fly.  A warp's step is a chain
-// of products, exponentials and products again, so it takes warps to hide it: blocks of four, several an SM.
+// A step's keys and values are two tensor copies of 16 rows into the warp's own ring in shared memory, a few steps ahead;
+// swizzled rows make the lanes' reads free of bank conflicts.  (The same bytes fetched by 16-byte asynchronous copies
+// of each lane came at 5.2 TB/s with no arithmetic at all.)  A warp's step is a chain of products, exponentials and
+// products again, so it takes warps to hide it: blocks of four, several an SM, no barrier between a block's warps.
 #include <cmath>
 
 #include "paged.cuh"
@@ -56,21 +57,6 @@ __device__ __forceinline__ int length_of(const TokenArgs &a, int seq, bool &bad)
     return n < 0 ? 0 : n > most ? most : n;
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -100,21 +86,31 @@ struct Shape {
     static constexpr int kRows = 8 * NT;
     static constexpr int kPieces = D / 64;                 // 16-byte pieces of a key for one lane
     static constexpr int kCols = D / 8;                    // consecutive channels of a lane in the second product
-    static constexpr int kKBytes = 2 * kPieces * 16;       // of a lane and step
-    static constexpr int kVBytes = 4 * kCols;
-    static constexpr int kStage = 32 * (kKBytes + kVBytes);
+    static constexpr int kTile = kStep * D;                // bytes of a step's keys, and of its values
+    static constexpr int kStage = 2 * kTile;
     static constexpr int kRing = kWarps * kDepth * kStage;
     static constexpr int kPad = D + 4;                     // floats of a row where the warps' sums are joined
     static constexpr int kJoin = kWarps * kRows * kPad * 4 + 2 * kWarps * kRows * 4;
-    static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+    static constexpr int kBars = kRing > kJoin ? kRing : kJoin;         // where the barriers lie
+    static constexpr int kSmem = 1024 + kBars + kWarps * kDepth * 8 + 16;  // the ring is 1024-byte aligned
 };
 
+// Byte offset of a 16-byte piece of a row in a swizzled tile of D-byte rows.
+template <int D>
+__device__ __forceinline__ int piece_at(int row, int piece)
+{
+    return row * D + ((D == 128 ? piece ^ (row & 7) : piece ^ (row >> 1 & 3)) << 4);
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_attention_kernel(const __grid_constant__ TokenArgs a)
+__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ TokenArgs a)
 {
     using Sh = Shape<D, NT>;
     constexpr int kDepth = Sh::kDepth;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);
+    int *abort_flag = reinterpret_cast<int *>(smem + Sh::kBars + kWarps * kDepth * 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, quad = lane & 3;  // products: rows r and r + 8, columns 2 quad and 2 quad + 1
     const int seq = blockIdx.z, h = blockIdx.y / a.tiles, tile = blockIdx.y - h * a.tiles;
@@ -142,41 +138,36 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
                      static_cast<int>(__ldg(a.c.v_scale + page * a.c.scale_stride + h)) << 8;
         }
     }
-    const uint32_t ring = ptx::smem_u32(smem) + warp * kDepth * Sh::kStage;
-    const uint8_t *ring_ptr = smem + warp * kDepth * Sh::kStage;
+    uint8_t *ring = smem + warp * kDepth * Sh::kStage;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Sh::kBars) + warp * kDepth;
+    if (lane == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < kDepth; ++i) ptx::mbar_init(&bars[i], 1);
+        ptx::fence_mbar_init();
+    }
+    __syncwarp();
 
+    // Copies of step i into its slot, which all lanes have read before.
     auto issue = [&](int i, int stage) {
         const int id = __shfl_sync(0xFFFFFFFFu, page, i & 31);
-        if (i < mine) {
+        if (i < mine && lane == 0) {
             const int key = k0 + (warp + i * kWarps) * kStep;
-            const uint32_t full = id >= 0 ? 1u : 0u;  // no page: zeros
-            const int64_t at = full ? id * a.c.page_stride + ((static_cast<int64_t>(h) << a.c.log2_page) +
-                                                              (key & ((1 << a.c.log2_page) - 1))) * D
-                                    : 0;
-            const uint32_t slot = ring + stage * Sh::kStage;
-            const uint8_t *k = a.c.k + at + r * D + quad * 16, *v = a.c.v + at + 2 * quad * D + r * Sh::kCols;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int p = 0; p < Sh::kPieces; ++p)
-                    copy16(slot + (t * Sh::kPieces + p) * 512 + lane * 16, full ? k + t * 8 * D + p * 64 : a.c.k, full * 16);
-            const uint32_t vs = slot + 32 * Sh::kKBytes;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {  // keys 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9
-                const uint8_t *src = full ? v + ((e & 1) + (e >> 1) * 8) * D : a.c.v;
-                if constexpr (Sh::kCols == 16)
-                    copy16(vs + e * 512 + lane * 16, src, full * 16);
-                else
-                    copy8(vs + e * 256 + lane * 8, src, full * 8);
+            uint8_t *slot = ring + stage * Sh::kStage;
+            if (id >= 0) {
+                const int row = (h << a.c.log2_page) + (key & ((1 << a.c.log2_page) - 1));
+                ptx::mbar_arrive_expect_tx(&bars[stage], Sh::kStage);
+                ptx::tma_load_3d(slot, &tm_k, 0, row, id, &bars[stage]);
+                ptx::tma_load_3d(slot + Sh::kTile, &tm_v, 0, row, id, &bars[stage]);
+            } else {
+                ptx::mbar_arrive(&bars[stage]);  // no page: the slot holds anything, and nothing reads it as a key
             }
         }
-        copies_commit();
     };
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) issue(i, i);
 
     // Queries as the second operand, in the order of the key bytes: product step 4 p + w takes channels
-    // 64 p + 16 quad + 4 w .. + 3 of this lane; the lane holds row r of each tile.
+    // 16 kPieces quad + 16 p + 4 w .. + 3 of this lane; the lane holds row r of each tile.
     uint32_t qb[NT][4 * Sh::kPieces][2];
     float base[NT][2];  // of rows 2 quad and 2 quad + 1: the factor of their scores
     int see[NT][2];     // keys that they see
@@ -189,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
             w[2 * p] = w[2 * p + 1] = make_uint4(0, 0, 0, 0);
             if (rho < Tg) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(
-                    a.q + ((static_cast<int64_t>(seq) * a.T + t) * a.Hq + h * a.g + j) * D + p * 64 + quad * 16);
+                    a.q + ((static_cast<int64_t>(seq) * a.T + t) * a.Hq + h * a.g + j) * D + quad * 16 * Sh::kPieces + p * 16);
                 w[2 * p] = __ldg(src);
                 w[2 * p + 1] = __ldg(src + 1);
             }
@@ -230,14 +221,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
     int unit = kScaleMin - 1;  // o is in units of 2^unit
 
     int stage = 0;
+    uint32_t parity = 0;
+    bool fine = true;
     for (int i = 0; i < mine; ++i) {
+        __syncwarp();
         issue(i + kDepth - 1, stage == 0 ? kDepth - 1 : stage - 1);
-        copies_wait<kDepth - 1>();
+        fine = ptx::mbar_wait_warp(&bars[stage], parity, abort_flag, a.err, BLINK_DEVICE_TIMEOUT);
+        if (!fine) {  // the copies in flight still land in this block's memory: wait for them, again with a limit
+            int other = 0;
+            for (int n = i; n < min(mine, i + kDepth); ++n) {
+                ptx::mbar_wait(&bars[stage], parity, &other, a.err, BLINK_DEVICE_TIMEOUT);
+                other = 0;
+                if (++stage == kDepth) stage = 0, parity ^= 1;
+            }
+            break;
+        }
         const int key = k0 + (warp + i * kWarps) * kStep;
         const int id = __shfl_sync(0xFFFFFFFFu, page, i), both = __shfl_sync(0xFFFFFFFFu, scales, i);
         const int ek = (both & 0xFF) - kScaleBias, ev = (both >> 8) - kScaleBias;
-        const uint8_t *slot = ring_ptr + stage * Sh::kStage;
-        stage = stage + 1 == kDepth ? 0 : stage + 1;
+        const uint8_t *slot = ring + stage * Sh::kStage;
+        if (++stage == kDepth) stage = 0, parity ^= 1;
 
         float s[NT][2][4];
 #pragma unroll
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
                 for (int e = 0; e < 4; ++e) s[y][b][e] = 0.f;
 #pragma unroll
         for (int p = 0; p < Sh::kPieces; ++p) {
-            const uint4 klo = *reinterpret_cast<const uint4 *>(slot + p * 512 + lane * 16);                   // key r
-            const uint4 khi = *reinterpret_cast<const uint4 *>(slot + (Sh::kPieces + p) * 512 + lane * 16);  // key r + 8
+            const uint4 klo = *reinterpret_cast<const uint4 *>(slot + piece_at<D>(r, quad * Sh::kPieces + p));      // key r
+            const uint4 khi = *reinterpret_cast<const uint4 *>(slot + piece_at<D>(r + 8, quad * Sh::kPieces + p));  // key r + 8
             const uint32_t *w = reinterpret_cast<const uint32_t *>(&klo), *x = reinterpret_cast<const uint32_t *>(&khi);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -316,14 +319,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
             pb[y][1] = transposed(pack_f16x2(p[2] * fv, p[3] * fv));
         }
         uint32_t v[4][Sh::kCols / 4];
-        const uint8_t *vs = slot + 32 * Sh::kKBytes;
+        const uint8_t *vs = slot + Sh::kTile;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4; ++e) {  // keys 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9
+            const int row = 2 * quad + (e & 1) + (e >> 1) * 8;
             if constexpr (Sh::kCols == 16) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(vs + e * 512 + lane * 16);
+                const uint4 w = *reinterpret_cast<const uint4 *>(vs + piece_at<D>(row, r));
                 v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
             } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(vs + e * 256 + lane * 8);
+                const uint2 w = *reinterpret_cast<const uint2 *>(vs + piece_at<D>(row, r >> 1) + (r & 1) * 8);
                 v[e][0] = w.x, v[e][1] = w.y;
             }
         }
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
                 const int limit = len - (a.T - 1 - t);
                 uint32_t keep[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) keep[e] = key + 2 * quad + (e & 1) + (e >> 1) * 8 < limit ? 0xFFFFFFFFu : 0u;
+                for (int e = 0; e < 4; ++e) keep[e] = id >= 0 && key + 2 * quad + (e & 1) + (e >> 1) * 8 < limit ? 0xFFFFFFFFu : 0u;
 #pragma unroll
                 for (int j = 0; j < Sh::kCols / 2; ++j) {
                     const int w = j / 2;
@@ -369,9 +373,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
         }
     }
 
-    // The warps' sums joined through shared memory, over the ring (every copy of this block has landed by the barrier).
-    copies_wait<0>();
-    __syncthreads();
+    // The warps' sums joined through shared memory, over the ring: every copy of this block has landed by the barrier.
+    if (__syncthreads_or(!fine)) return;
     float *so = reinterpret_cast<float *>(smem);
     float *sm = so + kWarps * Sh::kRows * Sh::kPad, *sl = sm + kWarps * Sh::kRows;
 #pragma unroll
@@ -582,9 +585,15 @@ extern "C" blink_status blink_paged_token_attention(
     a.part_o = reinterpret_cast<float *>(ws + plan.o);
     a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
     const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(Hkv * a.tiles), static_cast<unsigned>(S));
+    // A page is rows of d bytes, head by head; a step's 16 keys are rows of one page.
+    CUtensorMap tm_k, tm_v;
+    const uint64_t page_rows = static_cast<uint64_t>(Hkv) * page_tokens;
+    if (!encode_tmap_3d_bytes(&tm_k, k_codes, d, page_rows, n_pages, d, page_stride, d, kStep, 1, d) ||
+        !encode_tmap_3d_bytes(&tm_v, v_codes, d, page_rows, n_pages, d, page_stride, d, kStep, 1, d))
+        return BLINK_CUDA_ERROR;
     auto launch = [&](auto kern, int smem) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
-        kern<<<grid, kThreads, smem, stream>>>(a);
+        kern<<<grid, kThreads, smem, stream>>>(tm_k, tm_v, a);
         return cudaGetLastError() == cudaSuccess;
     };
     const bool launched = d == 128 ? (plan.wide == 1 ? launch(token_attention_kernel<128, 1>, Shape<128, 1>::kSmem)
