@@ -650,6 +650,16 @@ def blink_rope_table(rot: int, base: float = 10000.0, scaling: str | None = None
     return turns.to(device), float(amplitude.value)
 
 
+def _need_rows(name, t, n, H, d) -> int:
+    """`t` is a bf16 CUDA tensor of shape (n, H, d) whose rows may be strided; returns their stride."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.bfloat16 and t.shape == (n, H, d):
+        row, head, one = t.stride()
+        if one == 1 and head == d and n > 1:
+            return row
+    _refuse(name, t, torch.bfloat16, (n, H, d), 2)
+    return t.stride(0) if n > 1 else H * d
+
+
 def _turns_of(turns, d):
     n = turns.numel() if isinstance(turns, torch.Tensor) else None
     _need("turns", turns, torch.int64, (n,))
@@ -664,29 +674,28 @@ def blink_rope(q, k, positions, turns, interleaved: bool = False, amplitude: flo
     strided (slices of one projection).  q_out / k_out: None for new tensors, q / k themselves for in place.
     Returns (q_out, k_out)."""
     rows, Hq, d = q.shape if getattr(q, "ndim", 0) == 3 else (None,) * 3
-    _need("q", q, torch.bfloat16, (rows, Hq, d), inner=2)
-    Hkv = k.shape[1] if getattr(k, "ndim", 0) == 3 else None
+    q_stride = _need_rows("q", q, rows, Hq, d)
+    Hkv = k_stride = k_out_stride = 0
     if k is not None:
-        _need("k", k, torch.bfloat16, (rows, Hkv, d), inner=2)
+        Hkv = k.shape[1] if getattr(k, "ndim", 0) == 3 else None
+        k_stride = _need_rows("k", k, rows, Hkv, d)
     elif k_out is not None:
         raise ValueError("k_out without k")
     _need("positions", positions, torch.int32, (rows,))
     rot = _turns_of(turns, d)
-    _sizes(rows, Hq, Hkv or 0, d)
-    if q_out is not None:
-        _need("q_out", q_out, torch.bfloat16, (rows, Hq, d), inner=2)
-    if k_out is not None:
-        _need("k_out", k_out, torch.bfloat16, (rows, Hkv, d), inner=2)
+    _sizes(rows, Hq, Hkv, d)
+    q_out_stride = Hq * d if q_out is None else _need_rows("q_out", q_out, rows, Hq, d)
+    if k is not None:
+        k_out_stride = Hkv * d if k_out is None else _need_rows("k_out", k_out, rows, Hkv, d)
     with _Launch(stream, q, k, positions, turns, q_out, k_out) as call:
         if q_out is None:
             q_out = call.empty(torch.bfloat16, rows, Hq, d)
         if k_out is None and k is not None:
             k_out = call.empty(torch.bfloat16, rows, Hkv, d)
         if rows:
-            st = lib().blink_rope(q.data_ptr(), _row_stride(q), _addr(k), 0 if k is None else _row_stride(k), positions.data_ptr(),
-                                  rows, Hq, Hkv or 0, d, rot, turns.data_ptr(), amplitude, 1 if interleaved else 0,
-                                  q_out.data_ptr(), _row_stride(q_out), _addr(k_out), 0 if k is None else _row_stride(k_out),
-                                  call.handle)
+            st = lib().blink_rope(q.data_ptr(), q_stride, _addr(k), k_stride, positions.data_ptr(), rows, Hq, Hkv, d, rot,
+                                  turns.data_ptr(), amplitude, 1 if interleaved else 0, q_out.data_ptr(), q_out_stride, _addr(k_out),
+                                  k_out_stride, call.handle)
             _check(st, "blink_rope")
     return q_out, k_out
 
@@ -704,25 +713,27 @@ def blink_paged_cache(n_pages: int, page_tokens: int, Hkv: int, d: int, device="
 
 def _cache_of(cache, Hkv, d):
     """The tensors of a cache and its arguments of the C calls, checked."""
-    k, v, ks, vs = (cache[x] for x in ("k", "v", "k_scale", "v_scale"))
+    k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     n, page = (k.shape[0], k.shape[2]) if getattr(k, "ndim", 0) == 4 else (None, None)
     _need("cache k", k, torch.float8_e4m3fn, (n, Hkv, page, d), inner=3)
     _need("cache v", v, torch.float8_e4m3fn, (n, Hkv, page, d), inner=3)
     _need("cache k_scale", ks, torch.float8_e8m0fnu, (n, Hkv))
     _need("cache v_scale", vs, torch.float8_e8m0fnu, (n, Hkv))
-    _sizes(n, Hkv, page, d)
     if n < 1:
         raise ValueError("a cache has at least one page")
-    if n > 1 and (k.stride(0) != v.stride(0) or ks.stride(0) != vs.stride(0)):
+    if n > INT32_MAX:
+        _sizes(n)
+    stride, scale_stride = (k.stride(0), ks.stride(0)) if n > 1 else (Hkv * page * d, Hkv)
+    if n > 1 and (v.stride(0) != stride or vs.stride(0) != scale_stride):
         raise ValueError("k and v of a cache, and their scales, must have the same page strides")
-    return (k, v, ks, vs), (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), _row_stride(k), _row_stride(ks), n, page)
+    return (k, v, ks, vs), (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), stride, scale_stride, n, page)
 
 
 def _table_of(table):
     rows, width = table.shape if getattr(table, "ndim", 0) == 2 else (None, None)
     _need("page_table", table, torch.int32, (rows, width))
     _sizes(rows, width)
-    return rows, (table.data_ptr(), _row_stride(table), width)
+    return rows, (table.data_ptr(), table.stride(0) if rows > 1 else width, width)
 
 
 def _bytes(name, ws):
@@ -742,8 +753,7 @@ def blink_paged_append(k, v, cache: dict, page_table, cu_new, start, max_new: in
     (turns None: they are rotated already).  max_new: upper bound of a sequence's new tokens.  Returns ws; device-side
     problems (a bad length or page) are read with blink_read_device_status(ws)."""
     n, Hkv, d = k.shape if getattr(k, "ndim", 0) == 3 else (None,) * 3
-    _need("k", k, torch.bfloat16, (n, Hkv, d), inner=2)
-    _need("v", v, torch.bfloat16, (n, Hkv, d), inner=2)
+    k_stride, v_stride = _need_rows("k", k, n, Hkv, d), _need_rows("v", v, n, Hkv, d)
     tensors, args = _cache_of(cache, Hkv, d)
     S, table = _table_of(page_table)
     _need("cu_new", cu_new, torch.int32, (S + 1,))
@@ -758,7 +768,7 @@ def blink_paged_append(k, v, cache: dict, page_table, cu_new, start, max_new: in
         if ws is None:
             ws = call.workspace(paged_append_workspace_bytes())
         if n:
-            st = lib().blink_paged_append(k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v), n, Hkv, d, *args, *table,
+            st = lib().blink_paged_append(k.data_ptr(), k_stride, v.data_ptr(), v_stride, n, Hkv, d, *args, *table,
                                           cu_new.data_ptr(), start.data_ptr(), S, max_new, _addr(positions), _addr(turns), rot,
                                           amplitude, 1 if interleaved else 0, ws.data_ptr(), ws.numel(), call.handle)
             _check(st, "blink_paged_append")

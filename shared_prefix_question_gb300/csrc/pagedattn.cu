@@ -117,26 +117,23 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
     const int Tg = a.T * a.g, rho0 = tile * Sh::kRows, rows = min(Sh::kRows, Tg - rho0);
 
     ptx::grid_launch_dependents();
+    // The pages of this warp's steps, one a lane, read before the length is known.
+    const int k0 = blockIdx.x * a.chunk;
+    const int64_t index = (static_cast<int64_t>(k0) + (warp + lane * kWarps) * kStep) >> a.c.log2_page;
+    int page = index < a.table_width ? __ldg(a.table + seq * a.table_stride + index) : -1;
     bool bad;
-    const int len = length_of(a, seq, bad);
+    const int len = length_of(a, seq, bad), k1 = min(len, k0 + a.chunk);
     if (bad && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
-    const int k0 = blockIdx.x * a.chunk, k1 = min(len, k0 + a.chunk);
     if (k0 >= k1 && a.chunks > 1) return;  // the join knows the length too
-
-    // The pages of this warp's steps, one a lane; -1: past the end, or not a page (its keys are masked).
     const int steps = max(0, (k1 - k0 + kStep - 1) / kStep);
     const int mine = steps > warp ? (steps - warp + kWarps - 1) / kWarps : 0;
-    int page = -1, scales = kScaleBias | kScaleBias << 8;
-    if (lane < mine) {
-        const int key = k0 + (warp + lane * kWarps) * kStep;
-        page = __ldg(a.table + seq * a.table_stride + (key >> a.c.log2_page));
-        if (page < 0 || page >= a.c.n_pages) {
-            atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
-            page = -1;
-        } else {
-            scales = static_cast<int>(__ldg(a.c.k_scale + page * a.c.scale_stride + h)) |
-                     static_cast<int>(__ldg(a.c.v_scale + page * a.c.scale_stride + h)) << 8;
-        }
+    int scales = kScaleBias | kScaleBias << 8;
+    if (page < 0 || page >= a.c.n_pages || lane >= mine) {
+        if (lane < mine) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+        page = -1;  // past the end, or not a page: its keys are masked
+    } else {
+        scales = static_cast<int>(__ldg(a.c.k_scale + page * a.c.scale_stride + h)) |
+                 static_cast<int>(__ldg(a.c.v_scale + page * a.c.scale_stride + h)) << 8;
     }
     uint8_t *ring = smem + warp * kDepth * Sh::kStage;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Sh::kBars) + warp * kDepth;
@@ -437,51 +434,77 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
     }
 }
 
-constexpr int kJoinWarps = 4;
-constexpr int kJoinThreads = kJoinWarps * 32;
+constexpr int kJoinWarps = 16;
+constexpr int kJoinBatch = 8;  // chunks of a warp whose loads are in flight at once
 
 // The chunks of a row joined by their log-sum-exp, a block a row: its warps share the chunks out, a lane holds D / 32
-// channels.  Bound by latency: all loads of eight chunks are in flight at once.
+// channels.  Bound by latency: a warp loads eight chunks at once, knows nothing of the others' maxima before the end,
+// and there are warps for all chunks up to 128.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const __grid_constant__ TokenArgs a)
+__global__ void __launch_bounds__(kJoinWarps * 32) token_join_kernel(const __grid_constant__ TokenArgs a)
 {
     constexpr int kVec = D / 32;
-    __shared__ float so[kJoinWarps][D], sw[kJoinWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Tg = a.T * a.g;
+    __shared__ float so[kJoinWarps][D], sw[kJoinWarps], st[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, Tg = a.T * a.g;
     const int64_t row = blockIdx.x;
     const int rho = static_cast<int>(row % Tg), h = static_cast<int>(row / Tg % a.Hkv), seq = static_cast<int>(row / Tg / a.Hkv);
     bool bad;
     const int len = length_of(a, seq, bad), n = (len + a.chunk - 1) / a.chunk;
     ptx::grid_dep_wait();
     const float *pl = a.part_lse + row * a.chunks, *po = a.part_o + row * a.chunks * D + lane * kVec;
-    float top = -INFINITY;
-    for (int c = lane; c < n; c += 32) top = fmaxf(top, pl[c]);
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    float v[kVec] = {}, total = 0.f;
-#pragma unroll 8
-    for (int c = warp; c < n; c += kJoinWarps) {
-        const float l = pl[c];
-        const float w = l == -INFINITY ? 0.f : ptx::ex2(l - top);  // a NaN stays
-        total += w;
+    float top = -INFINITY, total = 0.f, v[kVec] = {};
+    for (int c0 = warp; c0 < n; c0 += warps * kJoinBatch) {
+        float l[kJoinBatch], x[kJoinBatch][kVec];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] += w * po[static_cast<int64_t>(c) * D + e];
+        for (int i = 0; i < kJoinBatch; ++i) {
+            const int c = c0 + i * warps;
+            l[i] = -INFINITY;
+            if (c < n) {
+                l[i] = pl[c];
+                if constexpr (kVec == 4) {
+                    const float4 w = *reinterpret_cast<const float4 *>(po + static_cast<int64_t>(c) * D);
+                    x[i][0] = w.x, x[i][1] = w.y, x[i][2] = w.z, x[i][3] = w.w;
+                } else {
+                    const float2 w = *reinterpret_cast<const float2 *>(po + static_cast<int64_t>(c) * D);
+                    x[i][0] = w.x, x[i][1] = w.y;
+                }
+            }
+        }
+        float now = top;
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) now = fmaxf(now, l[i]);
+        const float f = top == -INFINITY ? 0.f : ptx::ex2(top - now);
+        top = now;
+        total *= f;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] *= f;
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            if (l[i] == -INFINITY) continue;  // no chunk, or one without keys; a NaN counts
+            const float w = ptx::ex2(l[i] - top);
+            total += w;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) v[e] += w * x[i][e];
+        }
     }
 #pragma unroll
     for (int e = 0; e < kVec; ++e) so[warp][lane * kVec + e] = v[e];
-    if (lane == 0) sw[warp] = total;
+    if (lane == 0) sw[warp] = total, st[warp] = top;
     __syncthreads();
     if (warp != 0) return;
+    for (int w = 1; w < warps; ++w) top = fmaxf(top, st[w]);
     total = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) total += sw[w];
+    for (int e = 0; e < kVec; ++e) v[e] = 0.f;
+    for (int w = 0; w < warps; ++w) {
+        if (sw[w] == 0.f) continue;
+        const float f = st[w] == -INFINITY ? 1.f : ptx::ex2(st[w] - top);  // all NaN: no maximum
+        total += f * sw[w];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] += f * so[w][lane * kVec + e];
+    }
     const bool none = total == 0.f;
     const float inv = none ? 0.f : 1.f / total;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-        v[e] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) v[e] += so[w][lane * kVec + e];
-    }
     const int t = rho / a.g, head = h * a.g + rho - t * a.g;
     const int64_t tok = static_cast<int64_t>(seq) * a.T + t;
     uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (tok * a.Hq + head) * D + lane * kVec);
@@ -607,7 +630,8 @@ extern "C" blink_status blink_paged_token_attention(
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(joined));
-    cfg.blockDim = dim3(kJoinThreads);
+    const int warps = (a.chunks + kJoinBatch - 1) / kJoinBatch;
+    cfg.blockDim = dim3(static_cast<unsigned>(warps < kJoinWarps ? warps : kJoinWarps) * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
