@@ -70,28 +70,68 @@ __device__ __forceinline__ uint2 requantised(uint2 w, float f)
     return w;
 }
 
-// The largest of the block's values, the same in all threads.  `part` has a place per warp; calls alternate between
-// two of them, so that one barrier a call is enough.
-__device__ __forceinline__ float block_max(float m, float *part)
+// The largest of the block's values of K and of V (none negative), the same in all threads.  `part` has a place per warp
+// and value; calls alternate between two of them, so that one barrier a call is enough.
+__device__ __forceinline__ void block_max(uint32_t &k, uint32_t &v, uint32_t (*part)[32])
 {
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    k = __reduce_max_sync(0xFFFFFFFFu, k);
+    v = __reduce_max_sync(0xFFFFFFFFu, v);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) part[0][warp] = k, part[1][warp] = v;
     __syncthreads();
-    m = part[0];
-    for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) m = fmaxf(m, part[w]);
-    return m;
+    const bool on = lane < static_cast<int>(blockDim.x >> 5);
+    k = __reduce_max_sync(0xFFFFFFFFu, on ? part[0][lane] : 0u);
+    v = __reduce_max_sync(0xFFFFFFFFu, on ? part[1][lane] : 0u);
 }
 
-// A block owns one page of a sequence and goes over some of its heads, K then V of each; a thread owns 16 values of
-// one of the page's token slots, as two 16-byte pieces (a pair of halves that turn together).  The largest magnitude
-// needs all of a page's new tokens before the first code is written, so the values wait in registers; those of the
-// next (head, K or V) are loaded meanwhile.  Bound by HBM: 2 bytes read and 1 written a value.  The angles belong to
-// the slot, so a thread computes its own once for all heads.
+// |32-bit rotation - the exact one| <= kTurnError * (the sizes of the two rotated values).  In half steps of 32 bits, and
+// relative to |x0| + |x1| <= sqrt(2) (|y0| + |y1|) / amplitude: cos and sin are off by 2, the amplitude and a product add
+// one each; the sum adds one of y itself.
+constexpr float kTurnError = 7.f * 5.9604645e-8f;
+
+// Rotated values that the 32-bit rotation leaves between two codes (bit e of `mask`: value e of the thread's 16, eight
+// from place j0 and eight from j1 of a head): computed to some 40 bits, and the nearer code written.  `factor`: the
+// amplitude over the scale.
+template <bool INTERLEAVED>
+__device__ __noinline__ void write_nearer_codes(uint32_t mask, uint8_t *codes, const uint16_t *k, int j0, int j1, int half,
+                                                const uint64_t *turns, int32_t pos, float factor)
+{
+    for (; mask; mask &= mask - 1) {
+        const int e = __ffs(mask) - 1, j = e < 8 ? j0 + e : j1 + e - 8;
+        const bool second = INTERLEAVED ? j & 1 : j >= half;
+        const int i = INTERLEAVED ? j / 2 : second ? j - half : j;
+        const float x0 = bf16_lo(k[INTERLEAVED ? 2 * i : i]), x1 = bf16_lo(k[INTERLEAVED ? 2 * i + 1 : i + half]);
+        Two s, c;
+        turn_cos_sin(__ldg(turns + i), pos, c, s);
+        const Two f = {factor, 0.f};
+        const Two y = mul(f, second ? add(mul({x0, 0.f}, s), mul({x1, 0.f}, c)) : add(mul({x0, 0.f}, c), mul({-x1, 0.f}, s)));
+        const uint32_t two = f32x2_to_e4m3x2(y.h * (1.f - 0x1p-20f), y.h * (1.f + 0x1p-20f));
+        float l, h;
+        f16x2_split(e4m3x2_to_f16x2(two), l, h);
+        const float middle = 0.5f * (l + h), past = (y.h - middle) + y.l;  // an exact difference, as the two are so near
+        const bool up = past == 0.f ? two & 1u : (past > 0.f) == (y.h > 0.f);  // the second is the larger one
+        codes[j] = static_cast<uint8_t>(up ? two >> 8 : two);
+    }
+}
+
+constexpr int kStages = 2;        // heads whose keys and values are in shared memory, one of them in use
+constexpr int kMaxBlockHeads = 8;
+
+// A block owns one page of a sequence and goes over some of its heads; a thread owns 16 values of one of the page's
+// token slots, as two 16-byte pieces (a pair of halves that turn together), of K and of V.  The largest magnitude needs
+// all of a page's new tokens before the first code is written: one barrier a head, for K and V together.  Bound by
+// HBM: 2 bytes read and 1 written a value; each thread copies its own pieces of the next heads into its own places
+// in shared memory meanwhile (no registers, no barrier).  The angles belong to the slot, so a thread computes its own
+// once for all heads.
+// Codes are those of the exact rotation: where the 32-bit one is too near the border of two codes to tell (one value of
+// some 10,000), a bit remembers it, and when the block's heads are done those values are computed to 40 bits.
 template <int D, int LAYOUT>
-__global__ void __launch_bounds__(D * 8) append_kernel(const __grid_constant__ AppendArgs a)
+__global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_constant__ AppendArgs a)
 {
     constexpr int kLanes = D / 16;  // threads of a token slot
-    __shared__ float part[2][32];
+    extern __shared__ uint4 ring[];
+    __shared__ uint32_t part[2][2][32];
+    __shared__ int16_t k_exponents[kMaxBlockHeads];
     const int seq = blockIdx.z;
     const int c0 = __ldg(a.cu + seq) - __ldg(a.cu), n = __ldg(a.cu + seq + 1) - __ldg(a.cu + seq), start = __ldg(a.start + seq);
     if (n == 0) return;
@@ -102,10 +142,6 @@ __global__ void __launch_bounds__(D * 8) append_kernel(const __grid_constant__ A
     const int64_t index = (start >> a.log2_page) + static_cast<int64_t>(blockIdx.x), base = index << a.log2_page;
     if (base >= static_cast<int64_t>(start) + n) return;
     const int id = index < a.table_width ? __ldg(a.table + seq * a.table_stride + index) : -1;
-    if (id < 0 || id >= a.n_pages) {
-        if (threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
-        return;
-    }
     const int filled = static_cast<int>(max(start - base, static_cast<int64_t>(0)));  // tokens the page holds already
     const int slot = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int64_t token = base + slot - start;  // among the sequence's new ones
@@ -120,120 +156,234 @@ __global__ void __launch_bounds__(D * 8) append_kernel(const __grid_constant__ A
         p0 = turn ? lane : a.rot / 8 + lane - a.rot / 16;
         p1 = p0 + (turn ? a.rot / 16 : (D - a.rot) / 16);
     }
+    const int h_begin = blockIdx.y * a.heads_per_block, h_end = min(a.Hkv, h_begin + a.heads_per_block);
+    const uint16_t *k_row = a.k + (c0 + token) * a.k_stride, *v_row = a.v + (c0 + token) * a.v_stride;
+    const uint32_t mine = ptx::smem_u32(ring) + threadIdx.x * 16;
+    const uint32_t plane = blockDim.x * 16;  // bytes of one piece of all threads; a stage is four
+    uint16_t *unsure = reinterpret_cast<uint16_t *>(ring + kStages * 4 * blockDim.x) + threadIdx.x;  // a mask per head
+    uint32_t any_unsure = 0;
+    auto copy = [&](int h, int stage) {
+        if (fresh && h < h_end) {
+            const uint16_t *k = k_row + static_cast<int64_t>(h) * D, *v = v_row + static_cast<int64_t>(h) * D;
+            const uint32_t to = mine + stage * 4 * plane;
+            ptx::cp_async16(to, k + p0 * 8);
+            ptx::cp_async16(to + plane, k + p1 * 8);
+            ptx::cp_async16(to + 2 * plane, v + p0 * 8);
+            ptx::cp_async16(to + 3 * plane, v + p1 * 8);
+        }
+        ptx::cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) copy(h_begin + i, i);
+    if (id < 0 || id >= a.n_pages) {
+        if (threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+        ptx::cp_async_wait<0>();
+        return;
+    }
+
     const int32_t pos = !fresh ? 0 : a.pos ? __ldg(a.pos + c0 + token) : static_cast<int32_t>(start + token);
-    float c[8], s[8];
+    uint64_t c[4], minus_s[4];  // of eight pairs
+    auto pair_of = [&](int e) { return LAYOUT == kHalves ? p0 * 8 + e : e < 4 ? p0 * 4 + e : p1 * 4 + e - 4; };
     if constexpr (LAYOUT == kHalves || LAYOUT == kInterleaved) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int i = LAYOUT == kHalves ? p0 * 8 + e : (e < 4 ? p0 * 4 + e : p1 * 4 + e - 4);
-            c[e] = 1.f;
-            s[e] = 0.f;
-            if (fresh && turn && i < half) turn_cos_sin(__ldg(a.turns + i), pos, a.amplitude, c[e], s[e]);
+        for (int e = 0; e < 4; ++e) {
+            float cc[2] = {1.f, 1.f}, ss[2] = {0.f, 0.f};
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                if (fresh && turn && pair_of(2 * e + b) < half)
+                    turn_cos_sin(__ldg(a.turns + pair_of(2 * e + b)), pos, a.amplitude, cc[b], ss[b]);
+            c[e] = ptx::f32x2(cc[0], cc[1]);
+            minus_s[e] = ptx::f32x2(-ss[0], -ss[1]);
         }
     }
 
-    const int h_begin = blockIdx.y * a.heads_per_block, h_end = min(a.Hkv, h_begin + a.heads_per_block);
-    const int64_t row = c0 + token;
-    uint4 next[2];
-    auto load = [&](int h, int t) {
-        if (!fresh) return;
-        const uint16_t *x = t ? a.v + row * a.v_stride : a.k + row * a.k_stride;
-        const uint4 *q = reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(h) * D);
-        next[0] = __ldcs(q + p0);
-        next[1] = __ldcs(q + p1);
-    };
-    load(h_begin, 0);
-    int flip = 0;
+    int flip = 0, stage = 0;
     for (int h = h_begin; h < h_end; ++h) {
+        copy(h + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+        uint8_t *k_scale = a.ks + id * a.scale_stride + h, *v_scale = a.vs + id * a.scale_stride + h;
+        int ek_old = kScaleMin, ev_old = kScaleMin;
+        if (filled > 0) {
+            ek_old = min(static_cast<int>(*reinterpret_cast<volatile uint8_t *>(k_scale)) - kScaleBias, kScaleMax);
+            ev_old = min(static_cast<int>(*reinterpret_cast<volatile uint8_t *>(v_scale)) - kScaleBias, kScaleMax);
+        }
+        ptx::cp_async_wait<kStages - 1>();
+        const uint4 *own = ring + stage * 4 * blockDim.x + threadIdx.x;
+        if (++stage == kStages) stage = 0;
+
+        // The rotated keys as pairs of 32-bit values: x[e] holds values 2 e and 2 e + 1 of the thread's 16.
+        uint64_t x[8];
+        uint32_t mk = 0, mv = 0;
+        const uint16_t *k = k_row + static_cast<int64_t>(h) * D;
+        if (fresh) {
+            {
+                const uint4 u0 = own[0], u1 = own[blockDim.x];
+                const uint32_t u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            uint8_t *scale = (t ? a.vs : a.ks) + id * a.scale_stride + h;
-            uint8_t *codes = (t ? a.vc : a.kc) + id * a.page_stride + (static_cast<int64_t>(h) << a.log2_page) * D +
-                             slot * D;
-            int e_old = kScaleMin;
-            if (filled > 0) e_old = min(static_cast<int>(*reinterpret_cast<volatile uint8_t *>(scale)) - kScaleBias, kScaleMax);
-            float x[16];
-            float m = 0.f;
-            if (fresh) {
-                const uint32_t *u = reinterpret_cast<const uint32_t *>(next);
+                for (int e = 0; e < 8; ++e) x[e] = ptx::f32x2(bf16_lo(u[e]), bf16_hi(u[e]));
+            }
+            if constexpr (LAYOUT == kHalves) {
+                if (turn) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[2 * e] = bf16_lo(u[e]);
-                    x[2 * e + 1] = bf16_hi(u[e]);
-                }
-                if (t == 0) {
-                    if constexpr (LAYOUT == kHalves) {
-                        if (turn) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float y = x[e], z = x[8 + e];
-                                x[e] = y * c[e] - z * s[e];
-                                x[8 + e] = y * s[e] + z * c[e];
-                            }
-                        }
-                    } else if constexpr (LAYOUT == kInterleaved) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int i = e < 4 ? p0 * 4 + e : p1 * 4 + e - 4;
-                            const float y = x[2 * e], z = x[2 * e + 1];
-                            if (i < half) {  // pairs past rot stay as they are, whatever they hold
-                                x[2 * e] = y * c[e] - z * s[e];
-                                x[2 * e + 1] = y * s[e] + z * c[e];
-                            }
-                        }
-                    } else if constexpr (LAYOUT == kHalvesByElement) {
-                        const uint16_t *k = a.k + row * a.k_stride + static_cast<int64_t>(h) * D;
-#pragma unroll 1
-                        for (int e = 0; e < 16; ++e) {
-                            const int j = (e < 8 ? p0 : p1) * 8 + (e & 7);
-                            if (j >= a.rot) continue;
-                            const int i = j < half ? j : j - half;
-                            float cc, ss;
-                            turn_cos_sin(__ldg(a.turns + i), pos, a.amplitude, cc, ss);
-                            const float y = __uint_as_float(static_cast<uint32_t>(k[i]) << 16);
-                            const float z = __uint_as_float(static_cast<uint32_t>(k[i + half]) << 16);
-                            const float r = j < half ? y * cc - z * ss : y * ss + z * cc;
-#pragma unroll
-                            for (int f = 0; f < 16; ++f)
-                                if (f == e) x[f] = r;
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const uint64_t y = x[e], z = x[4 + e];
+                        x[e] = ptx::fma_f32x2(z, minus_s[e], ptx::mul_f32x2(y, c[e]));
+                        x[4 + e] = ptx::fma_f32x2(z, c[e], ptx::mul_f32x2(y, minus_s[e] ^ 0x8000000080000000ull));
                     }
                 }
+            } else if constexpr (LAYOUT == kInterleaved) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));  // a NaN counts as nothing
-            }
-            if (t == 0)
-                load(h, 1);
-            else if (h + 1 < h_end)
-                load(h + 1, 0);
-            m = block_max(m, part[flip]);
-            flip ^= 1;
-            if (m == INFINITY) {  // the scale is that of the finite values; infinities take the largest code
-                m = 0.f;
-                if (fresh) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]) < INFINITY ? fabsf(x[e]) : 0.f);
+                for (int e = 0; e < 8; ++e) {
+                    float y, z, cc0, cc1, ss0, ss1;
+                    ptx::f32x2_split(x[e], y, z);
+                    ptx::f32x2_split(c[e / 2], cc0, cc1);
+                    ptx::f32x2_split(minus_s[e / 2], ss0, ss1);
+                    const float cc = e & 1 ? cc1 : cc0, ss = e & 1 ? ss1 : ss0;
+                    if (pair_of(e) < half) x[e] = ptx::f32x2(y * cc + z * ss, z * cc - y * ss);  // others stay, whatever they hold
                 }
-                m = block_max(m, part[flip]);
-                flip ^= 1;
+            } else if constexpr (LAYOUT == kHalvesByElement) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = (e < 8 ? p0 : p1) * 8 + (e & 7), i = j < half ? j : j - half;
+                    if (j < a.rot) {
+                        float cc, ss, lo, hi;
+                        turn_cos_sin(__ldg(a.turns + i), pos, a.amplitude, cc, ss);
+                        const float y = bf16_lo(k[i]), z = bf16_lo(k[i + half]), r = j < half ? y * cc - z * ss : y * ss + z * cc;
+                        ptx::f32x2_split(x[e / 2], lo, hi);
+                        x[e / 2] = e & 1 ? ptx::f32x2(lo, r) : ptx::f32x2(r, hi);
+                    }
+                }
             }
-            const int e = filled > 0 ? max(scale_exponent(m), e_old) : scale_exponent(m);
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float lo, hi;
+                ptx::f32x2_split(x[e], lo, hi);
+                m = ptx::max3(m, fabsf(lo), fabsf(hi));  // a NaN counts as nothing
+            }
+            mk = __float_as_uint(m);
+            const uint4 w0 = own[2 * blockDim.x], w1 = own[3 * blockDim.x];
+            const uint32_t v[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            uint32_t w = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w = max_bf16x2(w, v[e] & 0x7FFF7FFFu);
+            mv = max(w << 16, w & 0xFFFF0000u);
+        }
+        block_max(mk, mv, part[flip]);
+        flip ^= 1;
+        const bool infinite = mk == 0x7F800000u || mv == 0x7F800000u;
+        if (infinite) {  // the scale is that of the finite values; infinities take the largest code
+            mk = mv = 0;
             if (fresh) {
-                const float f = scale_of(-e);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t b = static_cast<uint32_t>(x[e / 2] >> 32 * (e & 1)) & 0x7FFFFFFFu;
+                    const uint32_t y = (reinterpret_cast<const uint32_t *>(own + (2 + e / 8) * blockDim.x)[e / 2 & 3] << (e & 1 ? 0 : 16)) &
+                                       0x7FFF0000u;
+                    mk = b < 0x7F800000u ? max(mk, b) : mk;
+                    mv = y < 0x7F800000u ? max(mv, y) : mv;
+                }
+            }
+            block_max(mk, mv, part[flip]);
+            flip ^= 1;
+        }
+        int ek = scale_exponent(__uint_as_float(mk)), ev = scale_exponent(__uint_as_float(mv));
+        if (filled > 0) ek = max(ek, ek_old), ev = max(ev, ev_old);
+        const int64_t at = id * a.page_stride + (((static_cast<int64_t>(h) << a.log2_page) + slot) * D);
+        uint2 *kc = reinterpret_cast<uint2 *>(a.kc + at), *vc = reinterpret_cast<uint2 *>(a.vc + at);
+        if (fresh) {
+            {
+                const uint64_t f = ptx::f32x2(scale_of(-ev), scale_of(-ev));
+                const uint4 w0 = own[2 * blockDim.x], w1 = own[3 * blockDim.x];
+                const uint32_t v[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    w[i] = f32x2_to_e4m3x2(x[4 * i] * f, x[4 * i + 1] * f) |
-                           f32x2_to_e4m3x2(x[4 * i + 2] * f, x[4 * i + 3] * f) << 16;
-                reinterpret_cast<uint2 *>(codes)[p0] = make_uint2(w[0], w[1]);
-                reinterpret_cast<uint2 *>(codes)[p1] = make_uint2(w[2], w[3]);
-            } else if (kept && e > e_old) {
-                const float f = scale_of(e_old - e);
-                uint2 *w = reinterpret_cast<uint2 *>(codes);
-                w[p0] = requantised(w[p0], f);
-                w[p1] = requantised(w[p1], f);
+                    w[i] = f32x4_to_e4m3x4(ptx::mul_f32x2(ptx::f32x2(bf16_lo(v[2 * i]), bf16_hi(v[2 * i])), f),
+                                           ptx::mul_f32x2(ptx::f32x2(bf16_lo(v[2 * i + 1]), bf16_hi(v[2 * i + 1])), f));
+                vc[p0] = make_uint2(w[0], w[1]);
+                vc[p1] = make_uint2(w[2], w[3]);
             }
-            if (threadIdx.x == 0) *scale = static_cast<uint8_t>(e + kScaleBias);
+            const float fk = scale_of(-ek);
+            const uint64_t f = ptx::f32x2(fk, fk);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = ptx::mul_f32x2(x[e], f);
+            uint32_t w[4];
+            if (LAYOUT == kNoRotation || infinite) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = f32x4_to_e4m3x4(x[2 * i], x[2 * i + 1]);
+                kc[p0] = make_uint2(w[0], w[1]);
+                kc[p1] = make_uint2(w[2], w[3]);
+            } else {
+                // Codes of the least and the most that each exact value can be.
+                const float error = turn ? kTurnError : 0.f;
+                const uint64_t more = ptx::f32x2(error, error), less = ptx::f32x2(-error, -error);
+                uint32_t differ[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint64_t l[2], u[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int e = 2 * i + q;
+                        uint64_t size;  // what the error is relative to, for values 2 e and 2 e + 1
+                        float y0, y1, z0, z1;
+                        ptx::f32x2_split(x[e], y0, y1);
+                        if constexpr (LAYOUT == kHalves) {
+                            ptx::f32x2_split(x[e ^ 4], z0, z1);
+                            size = ptx::f32x2(fabsf(y0) + fabsf(z0), fabsf(y1) + fabsf(z1));
+                        } else if constexpr (LAYOUT == kInterleaved) {
+                            const float t = pair_of(e) < half ? fabsf(y0) + fabsf(y1) : 0.f;
+                            size = ptx::f32x2(t, t);
+                        } else {
+                            float t[2];
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                const int j = (i < 2 ? p0 : p1) * 8 + (2 * e & 7) + b, n = j < half ? j : j - half;
+                                t[b] = j < a.rot ? fabsf(a.amplitude) * (fabsf(bf16_lo(k[n])) + fabsf(bf16_lo(k[n + half]))) * fk : 0.f;
+                            }
+                            size = ptx::f32x2(t[0], t[1]);
+                        }
+                        l[q] = ptx::fma_f32x2(size, less, x[e]);
+                        u[q] = ptx::fma_f32x2(size, more, x[e]);
+                    }
+                    w[i] = f32x4_to_e4m3x4(l[0], l[1]);
+                    differ[i] = w[i] ^ f32x4_to_e4m3x4(u[0], u[1]);
+                }
+                kc[p0] = make_uint2(w[0], w[1]);
+                kc[p1] = make_uint2(w[2], w[3]);
+                if (differ[0] | differ[1] | differ[2] | differ[3]) {
+                    uint32_t mask = 0;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) mask |= (differ[e / 4] >> 8 * (e & 3) & 0xFFu) ? 1u << e : 0u;
+                    any_unsure |= 1u << (h - h_begin);
+                    unsure[(h - h_begin) * blockDim.x] = static_cast<uint16_t>(mask);
+                }
+            }
+        } else if (kept) {
+            if (ek > ek_old) {
+                const float f = scale_of(ek_old - ek);
+                kc[p0] = requantised(kc[p0], f);
+                kc[p1] = requantised(kc[p1], f);
+            }
+            if (ev > ev_old) {
+                const float f = scale_of(ev_old - ev);
+                vc[p0] = requantised(vc[p0], f);
+                vc[p1] = requantised(vc[p1], f);
+            }
+        }
+        if (threadIdx.x == 0) {
+            *k_scale = static_cast<uint8_t>(ek + kScaleBias);
+            *v_scale = static_cast<uint8_t>(ev + kScaleBias);
+            k_exponents[h - h_begin] = static_cast<int16_t>(ek);
+        }
+    }
+    if constexpr (LAYOUT != kNoRotation) {
+        if (!__syncthreads_or(static_cast<int>(any_unsure))) return;
+        for (; any_unsure; any_unsure &= any_unsure - 1) {
+            const int n_head = __ffs(any_unsure) - 1, h = h_begin + n_head;
+            write_nearer_codes<LAYOUT == kInterleaved>(
+                unsure[n_head * blockDim.x], a.kc + id * a.page_stride + (((static_cast<int64_t>(h) << a.log2_page) + slot) * D),
+                k_row + static_cast<int64_t>(h) * D, p0 * 8, p1 * 8, half, a.turns, pos,
+                a.amplitude * scale_of(-k_exponents[n_head]));
         }
     }
 }
@@ -387,16 +537,22 @@ extern "C" blink_status blink_paged_append(const blink_bf16 *k, int64_t k_stride
     a.rot = rot;
     a.amplitude = amplitude;
     a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
-    // Pages that max_new tokens can touch, and the heads of a block: as many as leave the SMs four blocks each.
+    // Pages that max_new tokens can touch, and the heads of a block: as many as leave the SMs two blocks each, which is what they run at a time.
     const int pages = (max_new + page_tokens - 2) / page_tokens + 1;
     const int64_t busy = (static_cast<int64_t>(n) + page_tokens - 1) / page_tokens + S;
-    const int64_t groups = (4LL * current_sm_count() + busy - 1) / busy;
+    const int64_t groups = (2LL * current_sm_count() + busy - 1) / busy;
     a.heads_per_block = groups >= Hkv ? 1 : static_cast<int>((Hkv + groups - 1) / groups);
+    if (a.heads_per_block > kMaxBlockHeads) a.heads_per_block = kMaxBlockHeads;
     const dim3 grid(static_cast<unsigned>(pages), static_cast<unsigned>((Hkv + a.heads_per_block - 1) / a.heads_per_block),
                     static_cast<unsigned>(S));
     const unsigned threads = static_cast<unsigned>(page_tokens * (d / 16));
     const int layout = rot == 0 ? kNoRotation : interleaved ? kInterleaved : rot % 16 == 0 ? kHalves : kHalvesByElement;
-    auto launch = [&](auto kern) { kern<<<grid, threads, 0, stream>>>(a); };
+    const int smem = static_cast<int>(threads) * (64 * kStages + 2 * a.heads_per_block);
+    bool set = true;
+    auto launch = [&](auto kern) {
+        set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d * 8 * (64 * kStages + 2 * kMaxBlockHeads)) == cudaSuccess;
+        if (set) kern<<<grid, threads, smem, stream>>>(a);
+    };
     if (d == 128) {
         if (layout == kNoRotation) launch(append_kernel<128, kNoRotation>);
         if (layout == kHalves) launch(append_kernel<128, kHalves>);
@@ -408,6 +564,7 @@ extern "C" blink_status blink_paged_append(const blink_bf16 *k, int64_t k_stride
         if (layout == kInterleaved) launch(append_kernel<64, kInterleaved>);
         if (layout == kHalvesByElement) launch(append_kernel<64, kHalvesByElement>);
     }
+    if (!set) return BLINK_CUDA_ERROR;
     return cudaGetLastError() == cudaSuccess ? BLINK_OK : BLINK_CUDA_ERROR;
 }
 

@@ -58,5 +58,24 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi)
     return r;
 }
 
+// Four values, two pairs of 32-bit ones, as the codes of a word.
+__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(uint64_t a, uint64_t b)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 t, u;\n\t.reg .f32 a0, a1, b0, b1;\n\tmov.b64 {a0, a1}, %1;\n\tmov.b64 {b0, b1}, %2;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 t, a1, a0;\n\tcvt.rn.satfinite.e4m3x2.f32 u, b1, b0;\n\tmov.b32 %0, {t, u};\n\t}"
+        : "=r"(r)
+        : "l"(a), "l"(b));
+    return r;
+}
+
+// The larger of two bf16 values, pair by pair; a NaN counts as nothing.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 #endif
 }  // namespace blink

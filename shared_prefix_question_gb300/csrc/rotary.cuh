@@ -9,14 +9,100 @@
 
 namespace blink {
 
-// cos and sin of pos * turns, times `amplitude`.  The remainder's upper 32 bits are a signed part of a half turn:
-// 2^-32 turns is 1.5e-9 radians, below the 6e-8 that 32-bit values of cos and sin are rounded to.
+// cos and sin of pos * turns, times `amplitude`: the nearest quarter turn, which only swaps and negates, and the Taylor
+// series of what is left (at most pi / 4: the terms after the ninth and tenth power are below 2e-9).  The remainder's
+// upper 32 bits are enough, 2^-32 turns being 1.5e-9 radians.  x is off by two half steps of 32 bits (1.6 * 2^-24 at most),
+// which cos and sin take times the other's size, and adding the last term adds half a step of each: 2 * 2^-24 bounds what
+// they lack (1.63 * 2^-24 was the most of a million random angles).
 __device__ __forceinline__ void turn_cos_sin(uint64_t turns, int32_t pos, float amplitude, float &c, float &s)
 {
+    const uint32_t phase = static_cast<uint32_t>(static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns >> 32);
+    const uint32_t quarter = (phase + (1u << 29)) >> 30;
+    const float x = static_cast<float>(static_cast<int32_t>(phase - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float y = x * x;
+    float ss = fmaf(y, 1.f / 362880.f, -1.f / 5040.f), cc = fmaf(y, -1.f / 3628800.f, 1.f / 40320.f);
+    ss = fmaf(y, ss, 1.f / 120.f);
+    cc = fmaf(y, cc, -1.f / 720.f);
+    ss = fmaf(y, ss, -1.f / 6.f);
+    cc = fmaf(y, cc, 1.f / 24.f);
+    ss = fmaf(y * x, ss, x);
+    cc = fmaf(y, fmaf(y, cc, -0.5f), 1.f);
+    const float cs = quarter & 1u ? ss : cc, sc = quarter & 1u ? cc : ss;
+    c = ((quarter + 1u) & 2u ? -cs : cs) * amplitude;
+    s = (quarter & 2u ? -sc : sc) * amplitude;
+}
+
+// Sums of two 32-bit values, the second what the first lacks: some 44 bits.  (64-bit arithmetic takes about a microsecond
+// an operation here.)
+struct Two {
+    float h, l;
+};
+
+__device__ __forceinline__ Two two_sum(float a, float b)
+{
+    const float s = a + b, t = s - a;
+    return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Two add(Two a, Two b)
+{
+    const Two s = two_sum(a.h, b.h);
+    return two_sum(s.h, s.l + (a.l + b.l));
+}
+__device__ __forceinline__ Two mul(Two a, Two b)
+{
+    const float p = a.h * b.h;
+    return two_sum(p, fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h));
+}
+
+// cos(2 pi k / 64) for k = 0 .. 16.
+#define BLINK_TWO(x) {static_cast<float>(x), static_cast<float>((x) - static_cast<double>(static_cast<float>(x)))}
+__device__ __constant__ Two kCosine[17] = {
+    BLINK_TWO(1.0),
+    BLINK_TWO(0.9951847266721969),
+    BLINK_TWO(0.9807852804032304),
+    BLINK_TWO(0.9569403357322088),
+    BLINK_TWO(0.9238795325112867),
+    BLINK_TWO(0.881921264348355),
+    BLINK_TWO(0.8314696123025452),
+    BLINK_TWO(0.773010453362737),
+    BLINK_TWO(0.7071067811865476),
+    BLINK_TWO(0.6343932841636455),
+    BLINK_TWO(0.5555702330196023),
+    BLINK_TWO(0.4713967368259978),
+    BLINK_TWO(0.38268343236508984),
+    BLINK_TWO(0.29028467725446233),
+    BLINK_TWO(0.19509032201612833),
+    BLINK_TWO(0.09801714032956077),
+    BLINK_TWO(0.0),
+};
+#undef BLINK_TWO
+
+__device__ __forceinline__ Two cosine_64(uint32_t j)  // of 2 pi j / 64
+{
+    const uint32_t k = j & 15u, quadrant = j >> 4 & 3u;
+    const Two v = kCosine[quadrant & 1u ? 16u - k : k];
+    return quadrant == 1u || quadrant == 2u ? Two{-v.h, -v.l} : v;
+}
+
+// cos and sin of pos * turns to some 40 bits: the nearest 64th of a turn from the table and the Taylor series of what is
+// left (at most 0.05: its terms after the seventh and eighth power are below 2e-17).
+__device__ __forceinline__ void turn_cos_sin(uint64_t turns, int32_t pos, Two &c, Two &s)
+{
     const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns;
-    sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-    c *= amplitude;
-    s *= amplitude;
+    const uint64_t step = (phase + (1ull << 57)) >> 58;
+    const int64_t rest = static_cast<int64_t>(phase - (step << 58));
+    const float rh = static_cast<float>(rest), rl = static_cast<float>(rest - static_cast<int64_t>(rh));
+    constexpr float uh = static_cast<float>(3.4061215800309573e-19);  // 2 pi / 2^64
+    constexpr float ul = static_cast<float>(3.4061215800309573e-19 - static_cast<double>(uh));
+    const Two x = mul({rh, rl}, {uh, ul}), y = mul(x, x);
+    const float z = y.h;
+    // sin x = x + x^3 (-1/6 + x^2/120 - x^4/5040), its second term below 2^-15 of the first; cos x likewise
+    const Two sn = add(x, {x.h * z * fmaf(z, fmaf(z, -1.f / 5040.f, 1.f / 120.f), -1.f / 6.f), 0.f});
+    const Two cn = add(add({1.f, 0.f}, {-0.5f * y.h, -0.5f * y.l}), {z * z * fmaf(z, fmaf(z, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), 0.f});
+    const Two ct = cosine_64(static_cast<uint32_t>(step)), st = cosine_64(static_cast<uint32_t>(step) + 48u);
+    const Two a = mul(st, sn), b = mul(ct, sn);
+    c = add(mul(ct, cn), {-a.h, -a.l});
+    s = add(mul(st, cn), b);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
