@@ -716,15 +716,20 @@ def _cache_of(cache, Hkv, d):
     k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     n, page = (k.shape[0], k.shape[2]) if getattr(k, "ndim", 0) == 4 else (None, None)
     _need("cache k", k, torch.float8_e4m3fn, (n, Hkv, page, d), inner=3)
-    _need("cache v", v, torch.float8_e4m3fn, (n, Hkv, page, d), inner=3)
     _need("cache k_scale", ks, torch.float8_e8m0fnu, (n, Hkv))
-    _need("cache v_scale", vs, torch.float8_e8m0fnu, (n, Hkv))
-    if n < 1:
-        raise ValueError("a cache has at least one page")
-    if n > INT32_MAX:
-        _sizes(n)
-    stride, scale_stride = (k.stride(0), ks.stride(0)) if n > 1 else (Hkv * page * d, Hkv)
-    if n > 1 and (v.stride(0) != stride or vs.stride(0) != scale_stride):
+    strides, scale_strides = k.stride(), ks.stride()
+    if not (isinstance(v, torch.Tensor) and v.is_cuda and v.dtype is torch.float8_e4m3fn and v.shape == k.shape and
+            v.stride() == strides):
+        _refuse("cache v", v, torch.float8_e4m3fn, (n, Hkv, page, d), 3)
+    if not (isinstance(vs, torch.Tensor) and vs.is_cuda and vs.dtype is torch.float8_e8m0fnu and vs.shape == ks.shape and
+            vs.stride() == scale_strides):
+        _refuse("cache v_scale", vs, torch.float8_e8m0fnu, (n, Hkv), 1)
+    if not 1 <= n <= INT32_MAX:
+        raise ValueError(f"a cache has 1..{INT32_MAX} pages, not {n}")
+    stride, scale_stride = strides[0], scale_strides[0]
+    if n == 1:  # a single page has any stride
+        stride, scale_stride = Hkv * page * d, Hkv
+    elif v.stride(0) != stride or vs.stride(0) != scale_stride:
         raise ValueError("k and v of a cache, and their scales, must have the same page strides")
     return (k, v, ks, vs), (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), stride, scale_stride, n, page)
 
@@ -732,7 +737,8 @@ def _cache_of(cache, Hkv, d):
 def _table_of(table):
     rows, width = table.shape if getattr(table, "ndim", 0) == 2 else (None, None)
     _need("page_table", table, torch.int32, (rows, width))
-    _sizes(rows, width)
+    if width > INT32_MAX or rows > INT32_MAX:
+        _sizes(rows, width)
     return rows, (table.data_ptr(), table.stride(0) if rows > 1 else width, width)
 
 
@@ -789,6 +795,8 @@ def blink_paged_token_attention(q, cache: dict, page_table, length, max_len: int
     Hkv = cache["k"].shape[1] if getattr(cache["k"], "ndim", 0) == 4 else None
     tensors, args = _cache_of(cache, Hkv, d)
     rows, table = _table_of(page_table)
+    if Hq > INT32_MAX or T > INT32_MAX:
+        _sizes(T, Hq)
     if rows != S:
         raise ValueError(f"page_table must have a row for each of {S} sequences, not {rows}")
     _need("length", length, torch.int32, (S,))
@@ -797,11 +805,10 @@ def blink_paged_token_attention(q, cache: dict, page_table, length, max_len: int
     if lse is not None:
         _need("lse", lse, torch.float32, (Hq, S * T), inner=2)
     _bytes("ws", ws)
-    _sizes(S, T, Hq)
     max_len = _int32("max_len", max_len)
     with _Launch(stream, q, *tensors, page_table, length, out, lse, ws) as call:
         if out is None:
-            out = call.empty(torch.bfloat16, S, T, Hq, d)
+            out = torch.empty_like(q)
         if lse is None and want_lse:
             lse = call.empty(torch.float32, Hq, S * T)
         if ws is None:
@@ -843,10 +850,8 @@ def blink_paged_prefix_tail_attention(q, cache: dict, page_table, prefix_len, k_
     if len(prefix_len) != n_req or len(req_rows) != n_req + 1:
         raise ValueError(f"page_table has {n_req} requests: prefix_len needs as many values, req_rows one more")
     B, max_tail = _int32("B", B), _int32("max_tail", max_tail)
-    if seq_start is None:
-        _need("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
-    else:
-        _need("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+    _need("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+    if seq_start is not None:
         _need("seq_start", seq_start, torch.int32, (B,))
     if out is not None:
         _need("out", out, torch.bfloat16, (rows, Hq, d), inner=3)
@@ -857,7 +862,7 @@ def blink_paged_prefix_tail_attention(q, cache: dict, page_table, prefix_len, k_
     h_rows, h_len = _int32s("req_rows", req_rows), _int32s("prefix_len", prefix_len)
     with _Launch(stream, q, *tensors, page_table, k_tail, v_tail, cu_seqlens, seq_start, out, lse, ws) as call:
         if out is None:
-            out = call.empty(torch.bfloat16, rows, Hq, d)
+            out = torch.empty_like(q)
         if lse is None and want_lse:
             lse = call.empty(torch.float32, Hq, rows)
         if ws is None:

@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------------------------------ pages to rows
-constexpr int kMaxRequests = 64;
+constexpr int kMaxRequests = kMaxPagedRequests;
 constexpr int kTile = 128;  // a region's rows are a multiple of the attention's key tile: zeros past its last token
 
 struct GatherArgs {
@@ -575,6 +575,8 @@ extern "C" size_t blink_paged_prefix_tail_workspace(const int32_t *h_req_rows, c
     if (!h_req_rows || n_req < 1 || n_req > kMaxRequests || Hkv < 1 || d < 1 ||
         check_requests(h_req_rows, h_prefix_len, n_req, h_req_rows[n_req]) != BLINK_OK)
         return kHeaderBytes;
+    if (Hq >= Hkv && few_tail_rows(h_req_rows, h_prefix_len, n_req, Hq / Hkv))
+        return few_tail_workspace(h_req_rows, h_prefix_len, n_req, Hkv, Hq / Hkv, d);
     return tail_layout(h_prefix_len, n_req, h_req_rows[n_req], B, Hq, Hkv, d).total;
 }
 
@@ -604,6 +606,13 @@ extern "C" blink_status blink_paged_prefix_tail_attention(
     for (int r = 0; r < n_req; ++r) {
         if (h_prefix_len[r] > static_cast<int64_t>(table_width) * page_tokens) return BLINK_OUT_OF_RANGE;
         longest = h_prefix_len[r] > longest ? h_prefix_len[r] : longest;
+    }
+    if (few_tail_rows(h_req_rows, h_prefix_len, n_req, Hq / Hkv)) {
+        if (static_cast<int64_t>(rows) * Hq > 0x7FFFFFFF) return BLINK_OUT_OF_RANGE;
+        if (ws_bytes < few_tail_workspace(h_req_rows, h_prefix_len, n_req, Hkv, Hq / Hkv, d)) return BLINK_WORKSPACE_TOO_SMALL;
+        return few_tail_attention(a.c, page_tokens, q, d_page_table, table_stride, table_width, k_tail, v_tail, d_cu_seqlens,
+                                  d_seq_start, B, rows, n_req, h_req_rows, h_prefix_len, max_tail, Hq, Hkv, d, scale, out, lse,
+                                  d_ws, stream);
     }
     const TailLayout lay = tail_layout(h_prefix_len, n_req, rows, B, Hq, Hkv, d);
     if (lay.rows > 0x7FFFFFFF) return BLINK_OUT_OF_RANGE;

@@ -26,6 +26,18 @@ struct PagedCache {
 blink_status check_cache(PagedCache &c, const void *k, const void *v, const void *ks, const void *vs, int64_t page_stride,
                          int64_t scale_stride, int32_t n_pages, int32_t page_tokens, int32_t Hkv, int32_t d);
 
+constexpr int kMaxPagedRequests = 64;
+
+// Prefix-tail attention of few rows, read from the pages as they are (pagedattn.cu).  few_tail_rows: whether a call is of
+// that kind; arguments as blink_paged_prefix_tail_attention has checked them.
+bool few_tail_rows(const int32_t *h_req_rows, const int32_t *h_len, int n_req, int g);
+size_t few_tail_workspace(const int32_t *h_req_rows, const int32_t *h_len, int n_req, int Hkv, int g, int d);
+blink_status few_tail_attention(const PagedCache &c, int page_tokens, const uint16_t *q, const int32_t *d_page_table,
+                                int64_t table_stride, int table_width, const uint16_t *k_tail, const uint16_t *v_tail,
+                                const int32_t *d_cu, const int32_t *d_seq_start, int B, int rows, int n_req,
+                                const int32_t *h_req_rows, const int32_t *h_len, int max_tail, int Hq, int Hkv, int d, float scale,
+                                uint16_t *out, float *lse, void *d_ws, cudaStream_t stream);
+
 #ifdef __CUDACC__
 
 __device__ __forceinline__ float scale_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + kScaleBias) << 23); }

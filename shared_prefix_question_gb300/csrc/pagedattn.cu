@@ -1,4 +1,5 @@
-// pagedattn.cu -- attention of the last tokens of each sequence over its 8-bit pages.
+// pagedattn.cu -- attention of a few rows over 8-bit pages: the last tokens of each sequence, or few tail rows of
+// requests whose prefix the pages hold.
 //
 // One pass over the keys with a running maximum and sum.  A step is 16 keys of one kv head, always within a page.  Keys
 // are the rows of the first product (S^T = K Q^T) and channels those of the second (O^T = V^T P^T); the columns of both
@@ -27,9 +28,19 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;                        // keys
 constexpr int kRound = kStep * kWarps;           // keys of a block per step of its warps
 constexpr int kMaxChunk = 32 * kRound;           // a lane holds the page of one step of its warp
+constexpr int kFewRows = 64;                     // (row, query head) rows of a kv head up to which tail rows read the pages
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e37f;                 // below any score
 constexpr float kHead = 6.f, kSlack = 8.f;       // weights start at 2^kHead and may grow by 2^kSlack before the maximum moves
+
+// Tail rows: which rows of the call belong to each request, and the lengths of the prefixes.
+struct TailRows {
+    int row[kMaxPagedRequests + 1];
+    int len[kMaxPagedRequests];
+    int n_req, rows, B, max_tail;
+    const uint16_t *k, *v;             // [rows][Hkv][d]
+    const int32_t *cu, *seq_start;
+};
 
 struct TokenArgs {
     PagedCache c;
@@ -43,8 +54,9 @@ struct TokenArgs {
     float scale_log2;
     uint16_t *out;
     float *lse;
-    float *part_lse, *part_o;              // [S][Hkv][T g][chunks] and the same with [D] behind
+    float *part_lse, *part_o;              // [token][Hq][chunks] and the same with [D] behind
     int *err;
+    TailRows tail;                         // with S = its requests; T and len are not used then
 };
 
 // A sequence's cached length, inside what the call allows; `bad`: it was not.
@@ -102,7 +114,7 @@ __device__ __forceinline__ int piece_at(int row, int piece)
     return row * D + ((D == 128 ? piece ^ (row & 7) : piece ^ (row >> 1 & 3)) << 4);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool TAIL>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ TokenArgs a)
 {
@@ -114,15 +126,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, quad = lane & 3;  // products: rows r and r + 8, columns 2 quad and 2 quad + 1
     const int seq = blockIdx.z, h = blockIdx.y / a.tiles, tile = blockIdx.y - h * a.tiles;
-    const int Tg = a.T * a.g, rho0 = tile * Sh::kRows, rows = min(Sh::kRows, Tg - rho0);
+    const int T = TAIL ? a.tail.row[seq + 1] - a.tail.row[seq] : a.T;
+    const int64_t token0 = TAIL ? a.tail.row[seq] : static_cast<int64_t>(seq) * a.T;
+    const int Tg = T * a.g, rho0 = tile * Sh::kRows, rows = min(Sh::kRows, Tg - rho0);
 
     ptx::grid_launch_dependents();
+    if (TAIL && rows <= 0) return;  // fewer rows than another request
     // The pages of this warp's steps, one a lane, read before the length is known.
     const int k0 = blockIdx.x * a.chunk;
     const int64_t index = (static_cast<int64_t>(k0) + (warp + lane * kWarps) * kStep) >> a.c.log2_page;
     int page = index < a.table_width ? __ldg(a.table + seq * a.table_stride + index) : -1;
-    bool bad;
-    const int len = length_of(a, seq, bad), k1 = min(len, k0 + a.chunk);
+    bool bad = false;
+    const int len = TAIL ? a.tail.len[seq] : length_of(a, seq, bad), k1 = min(len, k0 + a.chunk);
     if (bad && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
     if (k0 >= k1 && a.chunks > 1) return;  // the join knows the length too
     const int steps = max(0, (k1 - k0 + kStep - 1) / kStep);
@@ -177,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
             w[2 * p] = w[2 * p + 1] = make_uint4(0, 0, 0, 0);
             if (rho < Tg) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(
-                    a.q + ((static_cast<int64_t>(seq) * a.T + t) * a.Hq + h * a.g + j) * D + quad * 16 * Sh::kPieces + p * 16);
+                    a.q + ((token0 + t) * a.Hq + h * a.g + j) * D + quad * 16 * Sh::kPieces + p * 16);
                 w[2 * p] = __ldg(src);
                 w[2 * p + 1] = __ldg(src + 1);
             }
@@ -199,11 +214,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             base[y][c] = __shfl_sync(0xFFFFFFFFu, back, (2 * quad + c) * 4);
-            see[y][c] = len - (a.T - 1 - min(rho0 + 8 * y + 2 * quad + c, Tg - 1) / a.g);
+            see[y][c] = TAIL ? len : len - (T - 1 - min(rho0 + 8 * y + 2 * quad + c, Tg - 1) / a.g);
         }
     }
-    const int t_first = rho0 / a.g, t_last = (rho0 + rows - 1) / a.g;
-    const int see_least = len - (a.T - 1 - t_first);  // the fewest keys that a row sees
+    const int t_first = TAIL ? 0 : rho0 / a.g, t_last = TAIL ? 0 : (rho0 + rows - 1) / a.g;
+    const int see_least = TAIL ? len : len - (T - 1 - t_first);  // the fewest keys that a row sees
 
     float o[NT][Sh::kCols / 2][4];  // channels kCols r + 2 j (first two) and + 1, rows 2 quad and 2 quad + 1
 #pragma unroll
@@ -348,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
             // Keys that a row does not see may hold anything, a NaN times its zero weight too: for each token of the tile
             // the products run on the keys that it sees, and its rows take them.
             for (int t = t_first; t <= t_last; ++t) {
-                const int limit = len - (a.T - 1 - t);
+                const int limit = TAIL ? len : len - (T - 1 - t);
                 uint32_t keep[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) keep[e] = id >= 0 && key + 2 * quad + (e & 1) + (e >> 1) * 8 < limit ? 0xFFFFFFFFu : 0u;
@@ -363,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
                         mma16816(d, va, pb[y][0], pb[y][1]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            o[y][j][e] += (rho0 + 8 * y + 2 * quad + (e & 1)) / a.g == t ? d[e] : 0.f;
+                            o[y][j][e] += TAIL || (rho0 + 8 * y + 2 * quad + (e & 1)) / a.g == t ? d[e] : 0.f;
                     }
                 }
             }
@@ -419,14 +434,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
         const bool none = total == 0.f;  // no key: zeros, and -inf
         const float inv = none ? 0.f : 1.f / total, l2 = none ? -INFINITY : top + log2f(total);
         v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-        const int rho = rho0 + row;
-        if (a.chunks > 1) {
-            const int64_t at = ((static_cast<int64_t>(seq) * a.Hkv + h) * Tg + rho) * a.chunks + blockIdx.x;
+        const int rho = rho0 + row, t = rho / a.g, head = h * a.g + rho - t * a.g;
+        const int64_t tok = token0 + t;
+        if (TAIL || a.chunks > 1) {
+            const int64_t at = (tok * a.Hq + head) * a.chunks + blockIdx.x;
             *reinterpret_cast<float4 *>(a.part_o + at * D + col) = v;
             if (col == 0) a.part_lse[at] = l2;
         } else {
-            const int t = rho / a.g, head = h * a.g + rho - t * a.g;
-            const int64_t tok = static_cast<int64_t>(seq) * a.T + t;
             *reinterpret_cast<uint2 *>(a.out + (tok * a.Hq + head) * D + col) =
                 make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
             if (col == 0 && a.lse) a.lse[head * static_cast<int64_t>(a.S) * a.T + tok] = l2 * kLn2;
@@ -437,47 +451,94 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
 constexpr int kJoinWarps = 16;
 constexpr int kJoinBatch = 8;  // chunks of a warp whose loads are in flight at once
 
-// The chunks of a row joined by their log-sum-exp, a block a row: its warps share the chunks out, a lane holds D / 32
-// channels.  Bound by latency: a warp loads eight chunks at once, knows nothing of the others' maxima before the end,
-// and there are warps for all chunks up to 128.
 template <int D>
+__device__ __forceinline__ void load_channels(float (&x)[D / 32], const float *p)
+{
+    if constexpr (D == 128) {
+        const float4 w = *reinterpret_cast<const float4 *>(p);
+        x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+    } else {
+        const float2 w = *reinterpret_cast<const float2 *>(p);
+        x[0] = w.x, x[1] = w.y;
+    }
+}
+template <int D>
+__device__ __forceinline__ void load_channels(float (&x)[D / 32], const uint16_t *p)
+{
+    if constexpr (D == 128) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+        x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(p));
+        x[0] = __uint_as_float(w << 16), x[1] = __uint_as_float(w & 0xFFFF0000u);
+    }
+}
+
+// The last question that starts at or before `row` (by a whole warp, 32 starts at a time), and where it starts; -1: none.
+__device__ __forceinline__ int question_of(const TailRows &t, int row, int &start)
+{
+    const int lane = threadIdx.x & 31, base = t.seq_start ? 0 : __ldg(t.cu);
+    const int32_t *starts = t.seq_start ? t.seq_start : t.cu;
+    int lo = -1, hi = t.B;  // the answer lies in lo .. hi - 1
+    while (hi - lo > 1) {
+        const int step = (hi - lo - 1 + 31) / 32, at = lo + (lane + 1) * step;
+        const bool before = at < hi && __ldg(starts + at) - base <= row;
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, before));  // starts grow: the first n probes
+        if (n < 32) hi = min(hi, lo + (n + 1) * step);
+        lo += n * step;
+    }
+    start = lo >= 0 ? __ldg(starts + lo) - base : 0;
+    return lo;
+}
+
+// The chunks of a row joined by their log-sum-exp, a block a (token, query head): its warps share the chunks out, a lane
+// holds D / 32 channels.  Bound by latency: a warp loads eight chunks at once, knows nothing of the others' maxima
+// before the end, and there are warps for all chunks up to 128.  With TAIL the row's own question's keys (bf16, up to
+// the row itself) are shared out to the warps as well.
+template <int D, bool TAIL>
 __global__ void __launch_bounds__(kJoinWarps * 32) token_join_kernel(const __grid_constant__ TokenArgs a)
 {
     constexpr int kVec = D / 32;
     __shared__ float so[kJoinWarps][D], sw[kJoinWarps], st[kJoinWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, Tg = a.T * a.g;
-    const int64_t row = blockIdx.x;
-    const int rho = static_cast<int>(row % Tg), h = static_cast<int>(row / Tg % a.Hkv), seq = static_cast<int>(row / Tg / a.Hkv);
-    bool bad;
-    const int len = length_of(a, seq, bad), n = (len + a.chunk - 1) / a.chunk;
-    ptx::grid_dep_wait();
-    const float *pl = a.part_lse + row * a.chunks, *po = a.part_o + row * a.chunks * D + lane * kVec;
-    float top = -INFINITY, total = 0.f, v[kVec] = {};
-    for (int c0 = warp; c0 < n; c0 += warps * kJoinBatch) {
-        float l[kJoinBatch], x[kJoinBatch][kVec];
-#pragma unroll
-        for (int i = 0; i < kJoinBatch; ++i) {
-            const int c = c0 + i * warps;
-            l[i] = -INFINITY;
-            if (c < n) {
-                l[i] = pl[c];
-                if constexpr (kVec == 4) {
-                    const float4 w = *reinterpret_cast<const float4 *>(po + static_cast<int64_t>(c) * D);
-                    x[i][0] = w.x, x[i][1] = w.y, x[i][2] = w.z, x[i][3] = w.w;
-                } else {
-                    const float2 w = *reinterpret_cast<const float2 *>(po + static_cast<int64_t>(c) * D);
-                    x[i][0] = w.x, x[i][1] = w.y;
-                }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t row = blockIdx.x, tok = row / a.Hq;
+    const int head = static_cast<int>(row - tok * a.Hq);
+    int len, first = 0, keys = 0;  // keys of the question, from row `first` on
+    bool owned = true;
+    if constexpr (TAIL) {
+        const TailRows &t = a.tail;
+        int req = 0;
+        while (req + 1 < t.n_req && t.row[req + 1] <= tok) ++req;
+        len = t.len[req];
+        const int b = question_of(t, static_cast<int>(tok), first);
+        const int n = b < 0 ? 0 : __ldg(t.cu + b + 1) - __ldg(t.cu + b);
+        const bool bad = b < 0 ? !t.seq_start : n < 1 || n > t.max_tail || static_cast<int64_t>(first) + n > t.rows || first < t.row[req];
+        if (bad && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+        owned = b >= 0 && !bad && tok < first + n;  // padding rows have no question
+        keys = owned ? static_cast<int>(tok) - first + 1 : 0;
+        if (row == 0)  // every question's length, also of those without a row
+            for (int i = threadIdx.x; i < t.B; i += blockDim.x) {
+                const int m = __ldg(t.cu + i + 1) - __ldg(t.cu + i);
+                if (m < 1 || m > t.max_tail) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
             }
-        }
+    } else {
+        bool bad;
+        len = length_of(a, static_cast<int>(tok / a.T), bad);
+    }
+    const int n = owned ? (len + a.chunk - 1) / a.chunk : 0;
+    float top = -INFINITY, total = 0.f, v[kVec] = {};
+    auto take = [&](const float (&l)[kJoinBatch], const float (&x)[kJoinBatch][kVec]) {
         float now = top;
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i) now = fmaxf(now, l[i]);
         const float f = top == -INFINITY ? 0.f : ptx::ex2(top - now);
-        top = now;
-        total *= f;
+        if (top != -INFINITY || total == 0.f) {  // what a NaN made stays
+            total *= f;
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] *= f;
+            for (int e = 0; e < kVec; ++e) v[e] *= f;
+        }
+        top = now;
 #pragma unroll
         for (int i = 0; i < kJoinBatch; ++i) {
             if (l[i] == -INFINITY) continue;  // no chunk, or one without keys; a NaN counts
@@ -486,6 +547,47 @@ __global__ void __launch_bounds__(kJoinWarps * 32) token_join_kernel(const __gri
 #pragma unroll
             for (int e = 0; e < kVec; ++e) v[e] += w * x[i][e];
         }
+    };
+    if constexpr (TAIL) {  // does not wait for the prefix part
+        float q[kVec];
+        load_channels<D>(q, a.q + row * D + lane * kVec);
+        const int64_t stride = static_cast<int64_t>(a.Hkv) * D, at = first * stride + (head / a.g) * D + lane * kVec;
+        for (int k0 = warp; k0 < keys; k0 += warps * kJoinBatch) {
+            float l[kJoinBatch], x[kJoinBatch][kVec];
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i) {
+                const int k = k0 + i * warps;
+                l[i] = 0.f;
+                if (k < keys) {
+                    load_channels<D>(x[i], a.tail.k + at + k * stride);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) l[i] = fmaf(q[e], x[i][e], l[i]);
+                    load_channels<D>(x[i], a.tail.v + at + k * stride);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], o);
+                l[i] = k0 + i * warps < keys ? l[i] * a.scale_log2 : -INFINITY;
+            }
+            take(l, x);
+        }
+    }
+    ptx::grid_dep_wait();
+    const float *pl = a.part_lse + row * a.chunks, *po = a.part_o + row * a.chunks * D + lane * kVec;
+    for (int c0 = warp; c0 < n; c0 += warps * kJoinBatch) {
+        float l[kJoinBatch], x[kJoinBatch][kVec];
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            const int c = c0 + i * warps;
+            l[i] = -INFINITY;
+            if (c < n) {
+                l[i] = pl[c];
+                load_channels<D>(x[i], po + static_cast<int64_t>(c) * D);
+            }
+        }
+        take(l, x);
     }
 #pragma unroll
     for (int e = 0; e < kVec; ++e) so[warp][lane * kVec + e] = v[e];
@@ -505,12 +607,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) token_join_kernel(const __gri
     }
     const bool none = total == 0.f;
     const float inv = none ? 0.f : 1.f / total;
-    const int t = rho / a.g, head = h * a.g + rho - t * a.g;
-    const int64_t tok = static_cast<int64_t>(seq) * a.T + t;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (tok * a.Hq + head) * D + lane * kVec);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + row * D + lane * kVec);
 #pragma unroll
     for (int e = 0; e < kVec; e += 2) dst[e / 2] = ptx::pack_bf16x2(v[e] * inv, v[e + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[head * static_cast<int64_t>(a.S) * a.T + tok] = none ? -INFINITY : (top + log2f(total)) * kLn2;
+    const int64_t tokens = TAIL ? a.tail.rows : static_cast<int64_t>(a.S) * a.T;
+    if (lane == 0 && a.lse) a.lse[head * tokens + tok] = none ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
 struct TokenPlan {
@@ -521,7 +622,8 @@ struct TokenPlan {
 
 // Keys of a block: the keys of all (sequence, head, tile) units are cut into about as many chunks as blocks run at a
 // time; a chunk is whole rounds of the block's warps, and at most what the lanes can hold pages for.
-TokenPlan token_plan(int64_t S, int64_t T, int64_t max_len, int64_t Hkv, int64_t g, int d)
+// T: the most rows of a sequence; `tokens` of them in all; `joined`: partial results also of a single chunk.
+TokenPlan token_plan(int64_t S, int64_t T, int64_t tokens, int64_t max_len, int64_t Hkv, int64_t g, int d, bool joined)
 {
     TokenPlan p{};
     p.wide = T * g > 8 ? 2 : 1;
@@ -537,12 +639,54 @@ TokenPlan token_plan(int64_t S, int64_t T, int64_t max_len, int64_t Hkv, int64_t
     p.chunks = static_cast<int>(max_len > 0 ? (max_len + chunk - 1) / chunk : 1);
     p.lse = kHeaderBytes;
     p.o = p.total = kHeaderBytes;
-    if (p.chunks > 1) {
-        const size_t parts = static_cast<size_t>(S) * Hkv * T * g * p.chunks;
+    if (p.chunks > 1 || joined) {
+        const size_t parts = static_cast<size_t>(tokens) * Hkv * g * p.chunks;
         p.o = p.lse + align_up(parts * sizeof(float), 256);
         p.total = p.o + parts * d * sizeof(float);
     }
     return p;
+}
+
+template <int D, bool TAIL>
+bool launch_pages(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const TokenArgs &a, const TokenPlan &plan, cudaStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.Hkv * a.tiles), static_cast<unsigned>(a.S));
+    auto launch = [&](auto kern, int smem) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+        kern<<<grid, kThreads, smem, stream>>>(tm_k, tm_v, a);
+        return cudaGetLastError() == cudaSuccess;
+    };
+    return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL>, Shape<D, 1>::kSmem)
+                          : launch(token_attention_kernel<D, 2, TAIL>, Shape<D, 2>::kSmem);
+}
+
+// The pages' part, then the join of `joined` rows as its programmatic dependent.
+template <bool TAIL>
+blink_status launch_token(const TokenArgs &a, const TokenPlan &plan, int page_tokens, int d, int64_t joined, cudaStream_t stream)
+{
+    // A page is rows of d bytes, head by head; a step's 16 keys are rows of one page.
+    CUtensorMap tm_k, tm_v;
+    const uint64_t page_rows = static_cast<uint64_t>(a.Hkv) * page_tokens;
+    if (!encode_tmap_3d_bytes(&tm_k, a.c.k, d, page_rows, a.c.n_pages, d, a.c.page_stride, d, kStep, 1, d) ||
+        !encode_tmap_3d_bytes(&tm_v, a.c.v, d, page_rows, a.c.n_pages, d, a.c.page_stride, d, kStep, 1, d))
+        return BLINK_CUDA_ERROR;
+    if (!(d == 128 ? launch_pages<128, TAIL>(tm_k, tm_v, a, plan, stream) : launch_pages<64, TAIL>(tm_k, tm_v, a, plan, stream)))
+        return BLINK_CUDA_ERROR;
+    if (!TAIL && a.chunks == 1) return BLINK_OK;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    int warps = (a.chunks + kJoinBatch - 1) / kJoinBatch;
+    if (TAIL && warps < (a.tail.max_tail + kJoinBatch - 1) / kJoinBatch) warps = (a.tail.max_tail + kJoinBatch - 1) / kJoinBatch;
+    cfg.gridDim = dim3(static_cast<unsigned>(joined));
+    cfg.blockDim = dim3(static_cast<unsigned>(warps < kJoinWarps ? warps : kJoinWarps) * 32);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = d == 128 ? cudaLaunchKernelEx(&cfg, token_join_kernel<128, TAIL>, a)
+                                   : cudaLaunchKernelEx(&cfg, token_join_kernel<64, TAIL>, a);
+    return e == cudaSuccess ? BLINK_OK : BLINK_CUDA_ERROR;
 }
 
 bool token_sizes(int32_t S, int32_t T, int32_t max_len, int32_t Hq, int32_t Hkv, int32_t d, blink_status &st)
@@ -557,7 +701,77 @@ bool token_sizes(int32_t S, int32_t T, int32_t max_len, int32_t Hq, int32_t Hkv,
     return true;
 }
 
+struct TailSizes {
+    int most, longest;  // rows of a request, tokens of a prefix
+};
+
+TailSizes tail_sizes(const int32_t *h_req_rows, const int32_t *h_len, int n_req)
+{
+    TailSizes z{0, 0};
+    for (int r = 0; r < n_req; ++r) {
+        if (h_req_rows[r + 1] - h_req_rows[r] > z.most) z.most = h_req_rows[r + 1] - h_req_rows[r];
+        if (h_len[r] > z.longest) z.longest = h_len[r];
+    }
+    return z;
+}
+
 }  // namespace
+
+bool few_tail_rows(const int32_t *h_req_rows, const int32_t *h_len, int n_req, int g)
+{
+    (void)h_len;
+    return static_cast<int64_t>(tail_sizes(h_req_rows, h_len, n_req).most) * g <= kFewRows;
+}
+
+size_t few_tail_workspace(const int32_t *h_req_rows, const int32_t *h_len, int n_req, int Hkv, int g, int d)
+{
+    const TailSizes z = tail_sizes(h_req_rows, h_len, n_req);
+    return token_plan(n_req, z.most, h_req_rows[n_req], z.longest, Hkv, g, d, true).total;
+}
+
+blink_status few_tail_attention(const PagedCache &c, int page_tokens, const uint16_t *q, const int32_t *d_page_table,
+                                int64_t table_stride, int table_width, const uint16_t *k_tail, const uint16_t *v_tail,
+                                const int32_t *d_cu, const int32_t *d_seq_start, int B, int rows, int n_req,
+                                const int32_t *h_req_rows, const int32_t *h_len, int max_tail, int Hq, int Hkv, int d, float scale,
+                                uint16_t *out, float *lse, void *d_ws, cudaStream_t stream)
+{
+    const TailSizes z = tail_sizes(h_req_rows, h_len, n_req);
+    const TokenPlan plan = token_plan(n_req, z.most, rows, z.longest, Hkv, Hq / Hkv, d, true);
+    TokenArgs a{};
+    auto *ws = static_cast<uint8_t *>(d_ws);
+    a.c = c;
+    a.q = q;
+    a.table = d_page_table;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.max_len = z.longest;
+    a.S = n_req;
+    a.T = 1;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.g = Hq / Hkv;
+    a.tiles = plan.tiles;
+    a.chunk = plan.chunk;
+    a.chunks = plan.chunks;
+    a.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(d))) * kLog2e;
+    a.out = out;
+    a.lse = lse;
+    a.part_lse = reinterpret_cast<float *>(ws + plan.lse);
+    a.part_o = reinterpret_cast<float *>(ws + plan.o);
+    a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
+    for (int r = 0; r < n_req; ++r) a.tail.row[r] = h_req_rows[r], a.tail.len[r] = h_len[r];
+    a.tail.row[n_req] = h_req_rows[n_req];
+    a.tail.n_req = n_req;
+    a.tail.rows = rows;
+    a.tail.B = B;
+    a.tail.max_tail = max_tail;
+    a.tail.k = k_tail;
+    a.tail.v = v_tail;
+    a.tail.cu = d_cu;
+    a.tail.seq_start = d_seq_start;
+    return launch_token<true>(a, plan, page_tokens, d, static_cast<int64_t>(rows) * Hq, stream);
+}
+
 }  // namespace blink
 
 extern "C" size_t blink_paged_token_attention_workspace(int32_t S, int32_t T, int32_t max_len, int32_t Hq, int32_t Hkv, int32_t d)
@@ -565,7 +779,7 @@ extern "C" size_t blink_paged_token_attention_workspace(int32_t S, int32_t T, in
     using namespace blink;
     blink_status st;
     if (!token_sizes(S, T, max_len, Hq, Hkv, d, st)) return kHeaderBytes;
-    return token_plan(S, T, max_len, Hkv, Hq / Hkv, d).total;
+    return token_plan(S, T, static_cast<int64_t>(S) * T, max_len, Hkv, Hq / Hkv, d, false).total;
 }
 
 extern "C" blink_status blink_paged_token_attention(
@@ -582,7 +796,7 @@ extern "C" blink_status blink_paged_token_attention(
     if (!q || !d_page_table || !d_len || !out || !d_ws) return BLINK_INVALID_ARG;
     if (table_width < 1 || (S > 1 && table_stride < table_width) || std::isnan(scale) || std::isinf(scale)) return BLINK_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(d_ws)) return BLINK_INVALID_ARG;
-    const TokenPlan plan = token_plan(S, T, max_len, Hkv, Hq / Hkv, d);
+    const TokenPlan plan = token_plan(S, T, static_cast<int64_t>(S) * T, max_len, Hkv, Hq / Hkv, d, false);
     const int64_t joined = static_cast<int64_t>(S) * T * Hq;  // rows of the second launch
     if (joined > 0x7FFFFFFF) return BLINK_OUT_OF_RANGE;
     if (ws_bytes < plan.total) return BLINK_WORKSPACE_TOO_SMALL;
@@ -607,34 +821,5 @@ extern "C" blink_status blink_paged_token_attention(
     a.part_lse = reinterpret_cast<float *>(ws + plan.lse);
     a.part_o = reinterpret_cast<float *>(ws + plan.o);
     a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
-    const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(Hkv * a.tiles), static_cast<unsigned>(S));
-    // A page is rows of d bytes, head by head; a step's 16 keys are rows of one page.
-    CUtensorMap tm_k, tm_v;
-    const uint64_t page_rows = static_cast<uint64_t>(Hkv) * page_tokens;
-    if (!encode_tmap_3d_bytes(&tm_k, k_codes, d, page_rows, n_pages, d, page_stride, d, kStep, 1, d) ||
-        !encode_tmap_3d_bytes(&tm_v, v_codes, d, page_rows, n_pages, d, page_stride, d, kStep, 1, d))
-        return BLINK_CUDA_ERROR;
-    auto launch = [&](auto kern, int smem) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
-        kern<<<grid, kThreads, smem, stream>>>(tm_k, tm_v, a);
-        return cudaGetLastError() == cudaSuccess;
-    };
-    const bool launched = d == 128 ? (plan.wide == 1 ? launch(token_attention_kernel<128, 1>, Shape<128, 1>::kSmem)
-                                                     : launch(token_attention_kernel<128, 2>, Shape<128, 2>::kSmem))
-                                   : (plan.wide == 1 ? launch(token_attention_kernel<64, 1>, Shape<64, 1>::kSmem)
-                                                     : launch(token_attention_kernel<64, 2>, Shape<64, 2>::kSmem));
-    if (!launched) return BLINK_CUDA_ERROR;
-    if (a.chunks == 1) return BLINK_OK;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(joined));
-    const int warps = (a.chunks + kJoinBatch - 1) / kJoinBatch;
-    cfg.blockDim = dim3(static_cast<unsigned>(warps < kJoinWarps ? warps : kJoinWarps) * 32);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = d == 128 ? cudaLaunchKernelEx(&cfg, token_join_kernel<128>, a) : cudaLaunchKernelEx(&cfg, token_join_kernel<64>, a);
-    return e == cudaSuccess ? BLINK_OK : BLINK_CUDA_ERROR;
+    return launch_token<false>(a, plan, page_tokens, d, joined, stream);
 }

@@ -165,8 +165,9 @@ def test_workspaces(lib):
     assert one >= 256
     assert blink.paged_token_attention_workspace_bytes(8, 1, 131072, 32, 8, 128) > one
     assert lib.blink_paged_token_attention_workspace(0, 1, 10, 4, 2, 64) == 256  # refused by the call itself
-    # the prefixes' rows in whole key tiles, K and V, 2 bytes a value
-    assert blink.paged_prefix_tail_workspace_bytes([0, 5, 10], [1, 129], 2, 4, 2, 64) >= (128 + 256) * 2 * 64 * 2 * 2
+    # many tail rows: the prefixes' rows in whole key tiles, K and V, 2 bytes a value; few rows: less
+    assert blink.paged_prefix_tail_workspace_bytes([0, 500, 1000], [1, 129], 2, 4, 2, 64) >= (128 + 256) * 2 * 64 * 2 * 2
+    assert blink.paged_prefix_tail_workspace_bytes([0, 1, 2], [1, 131072], 2, 4, 2, 64) < 131072 * 2 * 64 * 2 * 2
     with pytest.raises(ValueError):
         blink.paged_prefix_tail_workspace_bytes([0, 5], [1, 129], 2, 4, 2, 64)
 

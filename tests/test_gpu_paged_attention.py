@@ -218,6 +218,86 @@ def test_prefix_tail_in_pages(Hq, Hkv, d, page, prefix, tails):
     assert float((lse.double() - want_lse).abs().max()) <= 2e-3 * max(1.0, float(want_lse.abs().max()))
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,page", [(4, 2, 64, 16), (32, 8, 128, 64), (5, 1, 64, 128), (40, 2, 128, 32), (64, 1, 64, 64)])
+@pytest.mark.parametrize("prefix,tails", [([300], [[1]]), ([0], [[1]]), ([9000], [[1, 1, 2]]), ([129, 0, 4000, 33], [[1], [1], [2, 1], [1, 1]]),
+                                          ([131072], [[1]]), ([77], [[1] * 3])])
+def test_few_tail_rows(Hq, Hkv, d, page, prefix, tails):
+    """One token, or a few rows, of each request: closer than the tensor-core form, as no score is rounded and weights
+    enter the products in fp16 (the prefix) and 32 bits (the tail).  Slots that hold no token are NaN, in the padding
+    rows of k_tail too."""
+    g = ph.gen(sum(prefix) + Hq)
+    table, total = ph.table_for(g, prefix, page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, table, prefix)
+    flat = [t for r in tails for t in r]
+    cu = [sum(flat[:i]) for i in range(len(flat) + 1)]
+    req_rows = [sum(sum(r) for r in tails[:i]) for i in range(len(tails) + 1)]
+    rows = cu[-1]
+    q, k, v = (ph.randn(g, rows, H, d).to(torch.bfloat16) for H in (Hq, Hkv, Hkv))
+    out, lse, ws = blink.blink_paged_prefix_tail_attention(q, cache, table, prefix, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                                                           len(flat), max(flat), req_rows=req_rows, want_lse=True)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+    ref = [torch.empty(rows, 1, Hq, d, dtype=torch.float64, device="cuda"), torch.empty(Hq, rows, dtype=torch.float64, device="cuda"),
+           torch.empty(2, rows, 1, Hq, d, dtype=torch.float64, device="cuda"), torch.empty(Hq, rows, dtype=torch.float64, device="cuda")]
+    for b in range(len(flat)):
+        r = next(i for i in range(len(prefix)) if req_rows[i] <= cu[b] < req_rows[i + 1])
+        pre = [ph.values(cache, n, table[r], prefix[r]) for n in ("k", "v")]
+        for i in range(cu[b], cu[b + 1]):
+            kk, vv = (torch.cat([x, y[cu[b]:i + 1].double().transpose(0, 1)], dim=1) for x, y in zip(pre, (k, v)))
+            ref[0][i, 0], ref[1][:, i], ref[2][:, i, 0], ref[3][:, i] = ph.attend(q[i], kk, vv, 1 / math.sqrt(d))
+    if max(b - a for a, b in zip(req_rows, req_rows[1:])) * (Hq // Hkv) > 64:  # four rows of 20 heads: the tensor-core form,
+        # whose weights are rounded to bf16 (half a step 2^-8, against 2^-11)
+        assert float((out.double() - ref[0][:, 0]).abs().max()) <= 2e-2 * float(ref[0].abs().max())
+        return
+    ph.check_attention(out.view(rows, 1, Hq, d), lse, ref)
+
+
+def test_few_tail_rows_padded_and_bad_questions():
+    """Rows of no question get zeros and -inf; a question of a bad length is flagged and the others are right."""
+    g = ph.gen(23)
+    Hq, Hkv, d, page, P = 4, 2, 64, 16, 100
+    table, total = ph.table_for(g, [P], page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, table, [P])
+    rows = 12
+    q, k, v = (ph.randn(g, rows, H, d).to(torch.bfloat16) for H in (Hq, Hkv, Hkv))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out, lse, ws = blink.blink_paged_prefix_tail_attention(q, cache, table, [P], k, v, i32(5, 7, 12), 2, 5, seq_start=i32(1, 6), want_lse=True)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+    none = [0, 3, 4, 5, 11]
+    assert bool((out[none] == 0).all()) and bool((lse[:, none] == -math.inf).all())
+    want, want_lse = _tail_reference(q[1:3], cache, table, [P], [0, 2], k[1:3], v[1:3], [0, 2], 1 / 8)
+    assert float((out[1:3].double() - want).abs().max()) <= 2 * ph.BF16 * float(want.abs().max())
+    assert float((lse[:, 1:3].double() - want_lse).abs().max()) <= 1e-5
+    # lengths beyond max_tail, none, past the rows; a question that begins before its request's rows
+    for cu, B, max_tail, req in ((i32(0, 6, 12), 2, 5, None), (i32(0, 0, 12), 2, 12, None), (i32(0, 13), 1, 13, None),
+                                 (i32(0, 8, 12), 2, 8, [0, 4, 12])):
+        n = 1 if req is None else 2
+        t = table.expand(n, -1).contiguous()
+        _, _, ws = blink.blink_paged_prefix_tail_attention(q, cache, t, [P] * n, k, v, cu, B, max_tail, req_rows=req)
+        assert blink.blink_read_device_status(ws) == blink.BLINK_DEVICE_FLAG
+    bad = table.clone()
+    bad[0, 2] = total
+    _, _, ws = blink.blink_paged_prefix_tail_attention(q, cache, bad, [P], k, v, i32(0, 12), 1, 12)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_DEVICE_FLAG
+
+
+def test_prefix_tail_forms_agree():
+    """The rows of a question alone (the few-row form) and among many others (the tensor-core form)."""
+    g = ph.gen(24)
+    Hq, Hkv, d, page, P = 32, 8, 128, 64, 777
+    table, total = ph.table_for(g, [P], page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, table, [P])
+    rows = 3 + 120
+    q, k, v = (ph.randn(g, rows, H, d).to(torch.bfloat16) for H in (Hq, Hkv, Hkv))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    many, lse, _ = blink.blink_paged_prefix_tail_attention(q, cache, table, [P], k, v, i32(0, 3, rows), 2, 120, want_lse=True)
+    few, lse3, _ = blink.blink_paged_prefix_tail_attention(q[:3], cache, table, [P], k[:3], v[:3], i32(0, 3), 1, 3, want_lse=True)
+    assert float((few.double() - many[:3].double()).abs().max()) <= 2e-2 * float(many[:3].abs().max())
+    assert float((lse3 - lse[:, :3]).abs().max()) <= 2e-3
+
+
 def test_prefix_tail_equals_the_arena():
     """Bit for bit what the bf16 arena with the same values gives, for one request and for several that share pages."""
     g = ph.gen(21)
