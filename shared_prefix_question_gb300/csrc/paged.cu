@@ -186,14 +186,19 @@ __global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_con
     auto pair_of = [&](int e) { return LAYOUT == kHalves ? p0 * 8 + e : e < 4 ? p0 * 4 + e : p1 * 4 + e - 4; };
     if constexpr (LAYOUT == kHalves || LAYOUT == kInterleaved) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float cc[2] = {1.f, 1.f}, ss[2] = {0.f, 0.f};
+        for (int e = 0; e < 4; ++e) c[e] = ptx::f32x2(1.f, 1.f), minus_s[e] = 0;
+        if (fresh && turn) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-                if (fresh && turn && pair_of(2 * e + b) < half)
-                    turn_cos_sin(__ldg(a.turns + pair_of(2 * e + b)), pos, a.amplitude, cc[b], ss[b]);
-            c[e] = ptx::f32x2(cc[0], cc[1]);
-            minus_s[e] = ptx::f32x2(-ss[0], -ss[1]);
+            for (int e = 0; e < 4; ++e) {
+                float cc[2], ss[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {  // pairs past rot get any angle: they are not turned
+                    const int i = LAYOUT == kHalves ? pair_of(2 * e + b) : min(pair_of(2 * e + b), half - 1);
+                    turn_cos_sin(__ldg(a.turns + i), pos, a.amplitude, cc[b], ss[b]);
+                }
+                c[e] = ptx::f32x2(cc[0], cc[1]);
+                minus_s[e] = ptx::f32x2(-ss[0], -ss[1]);
+            }
         }
     }
 

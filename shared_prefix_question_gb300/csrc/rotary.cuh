@@ -16,9 +16,11 @@ namespace blink {
 // they lack (1.63 * 2^-24 was the most of a million random angles).
 __device__ __forceinline__ void turn_cos_sin(uint64_t turns, int32_t pos, float amplitude, float &c, float &s)
 {
-    const uint32_t phase = static_cast<uint32_t>(static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns >> 32);
-    const uint32_t quarter = (phase + (1u << 29)) >> 30;
-    const float x = static_cast<float>(static_cast<int32_t>(phase - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    // bits 32 .. 63 of the product
+    const uint32_t lo = static_cast<uint32_t>(turns), hi = static_cast<uint32_t>(turns >> 32), p = static_cast<uint32_t>(pos);
+    const uint32_t phase = __umulhi(p, lo) + p * hi - (pos < 0 ? lo : 0u);
+    const uint32_t quarter = phase + (1u << 29);  // its upper two bits
+    const float x = static_cast<float>(static_cast<int32_t>(phase - (quarter & 0xC0000000u))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
     const float y = x * x;
     float ss = fmaf(y, 1.f / 362880.f, -1.f / 5040.f), cc = fmaf(y, -1.f / 3628800.f, 1.f / 40320.f);
     ss = fmaf(y, ss, 1.f / 120.f);
@@ -27,9 +29,10 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t turns, int32_t pos, float 
     cc = fmaf(y, cc, 1.f / 24.f);
     ss = fmaf(y * x, ss, x);
     cc = fmaf(y, fmaf(y, cc, -0.5f), 1.f);
-    const float cs = quarter & 1u ? ss : cc, sc = quarter & 1u ? cc : ss;
-    c = ((quarter + 1u) & 2u ? -cs : cs) * amplitude;
-    s = (quarter & 2u ? -sc : sc) * amplitude;
+    const bool odd = quarter & 0x40000000u;
+    const uint32_t cs = __float_as_uint((odd ? ss : cc) * amplitude), sc = __float_as_uint((odd ? cc : ss) * amplitude);
+    c = __uint_as_float(cs ^ ((quarter + 0x40000000u) & 0x80000000u));
+    s = __uint_as_float(sc ^ (quarter & 0x80000000u));
 }
 
 // Sums of two 32-bit values, the second what the first lacks: some 44 bits.  (64-bit arithmetic takes about a microsecond
