@@ -498,8 +498,8 @@ blink_status blink_token_logprobs(const blink_bf16 *hidden, int64_t hidden_row_s
  * blink_rope turns the first `rot` values of every head of q and, if given, k, and copies the others:
  * (y0, y1) = amplitude (x0 cos - x1 sin, x0 sin + x1 cos), in 32 bits, rounded once.
  *   q [rows, Hq, d], k [rows, Hkv, d]  bf16, heads d apart, rows *_stride elements apart (slices of one
- *               projection's rows are fine); k NULL: q alone.  16-byte pieces are used where bases and
- *               strides are 16-byte aligned, d is a multiple of 8 and (halves) rot one of 16
+ *               projection's rows are fine); k NULL: q alone.  Any alignment of 2 bytes; fastest where
+ *               addresses, strides, d and (halves) rot/2 are multiples of 8 values
  *   d_positions [rows]   any int32 values (negative ones turn back)
  *   d           2..BLINK_MAX_ROPE_DIM;  rows 0..2^30 (0: nothing is done)
  *   interleaved 0: pair i is values (i, i + rot/2); 1: values (2 i, 2 i + 1)

@@ -30,7 +30,7 @@ struct RopeArgs {
     float amplitude;
     int rows, d, rot;
     int per_block;                        // rows of a block
-    int turned, passed;                   // items of a row: 16-byte pieces (pairs of them in the halves' layout) that turn, pieces that pass
+    int turned, passed;                   // items of a row: pieces (pairs of them in the halves' layout) that turn, pieces that pass
 };
 
 __device__ __forceinline__ void block_angles(const RopeArgs &a, int row0, int n, float2 *cs)
@@ -45,9 +45,39 @@ __device__ __forceinline__ void block_angles(const RopeArgs &a, int row0, int n,
     __syncthreads();
 }
 
-// 16-byte pieces.  Halves: an item is pieces i and i + rot / 16 of a head, eight pairs.  Interleaved: an item is one
-// piece, four pairs.  Threads lie over (row, item), what is left of the block over heads.
-template <int LAYOUT>
+template <int W>
+struct Piece {
+    uint32_t w[W / 2];
+};
+template <int W>
+__device__ __forceinline__ Piece<W> load_piece(const uint16_t *p)
+{
+    Piece<W> x;
+    if constexpr (W == 8) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        x.w[0] = v.x, x.w[1] = v.y, x.w[2] = v.z, x.w[3] = v.w;
+    } else if constexpr (W == 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        x.w[0] = v.x, x.w[1] = v.y;
+    } else {
+        x.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+    return x;
+}
+template <int W>
+__device__ __forceinline__ void store_piece(uint16_t *p, const Piece<W> &x)
+{
+    if constexpr (W == 8)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    else if constexpr (W == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(x.w[0], x.w[1]);
+    else
+        *reinterpret_cast<uint32_t *>(p) = x.w[0];
+}
+
+// Pieces of W values (16, 8 or 4 bytes).  Halves: an item is pieces i and i + rot / 2 / W of a head, W pairs.
+// Interleaved: an item is one piece, W / 2 pairs.  Threads lie over (row, item), what is left of the block over heads.
+template <int LAYOUT, int W>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a)
 {
     extern __shared__ float2 cs[];  // [rows of the block][rot / 2]
@@ -55,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int n = min(a.per_block, a.rows - row0);
     block_angles(a, row0, n, cs);
 
-    constexpr int kPairs = LAYOUT == kHalves ? 8 : 4;
+    constexpr int kPairs = LAYOUT == kHalves ? W : W / 2;
     constexpr int kPieces = LAYOUT == kHalves ? 2 : 1;
     const int items = a.turned + a.passed, lanes = a.per_block * items;
     const int group = threadIdx.x / lanes, groups = blockDim.x / lanes;
@@ -64,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     if (group >= groups || r >= n) return;
     const bool turn = item < a.turned;
     const int half = a.rot / 2;
-    const int first = turn ? item : (LAYOUT == kHalves ? a.rot / 8 : a.turned) + item - a.turned;  // piece
+    const int first = (turn || LAYOUT != kHalves ? item : a.rot / W + item - a.turned) * W;  // value
     float c[kPairs], s[kPairs];
     if (turn) {
 #pragma unroll
@@ -78,45 +108,39 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int64_t row = row0 + r;
     const int H = a.heads[0] + a.heads[1];
     for (int h0 = group; h0 < H; h0 += groups * kBatch) {
-        uint4 x[kBatch][kPieces];
+        Piece<W> x[kBatch][kPieces];
         bool on[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int hh = h0 + b * groups, t = hh >= a.heads[0];
             on[b] = hh < H && (turn || a.copy[t]);
             if (!on[b]) continue;
-            const uint4 *p = reinterpret_cast<const uint4 *>(a.in[t] + row * a.in_stride[t] + static_cast<int64_t>(hh - t * a.heads[0]) * a.d);
-            x[b][0] = p[first];
-            if (LAYOUT == kHalves && turn) x[b][kPieces - 1] = p[first + a.turned];
+            const uint16_t *p = a.in[t] + row * a.in_stride[t] + static_cast<int64_t>(hh - t * a.heads[0]) * a.d + first;
+            x[b][0] = load_piece<W>(p);
+            if (LAYOUT == kHalves && turn) x[b][kPieces - 1] = load_piece<W>(p + half);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             if (!on[b]) continue;
             const int hh = h0 + b * groups, t = hh >= a.heads[0];
-            uint4 *p = reinterpret_cast<uint4 *>(a.out[t] + row * a.out_stride[t] + static_cast<int64_t>(hh - t * a.heads[0]) * a.d);
-            if (!turn) {
-                p[first] = x[b][0];
-                continue;
-            }
-            uint32_t *u = reinterpret_cast<uint32_t *>(&x[b][0]);
-            if constexpr (LAYOUT == kHalves) {
-                uint32_t *v = reinterpret_cast<uint32_t *>(&x[b][kPieces - 1]);
+            uint16_t *p = a.out[t] + row * a.out_stride[t] + static_cast<int64_t>(hh - t * a.heads[0]) * a.d + first;
+            if (turn) {
+                uint32_t *u = x[b][0].w, *v = x[b][kPieces - 1].w;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float u0 = bf16_lo(u[e]), u1 = bf16_hi(u[e]), v0 = bf16_lo(v[e]), v1 = bf16_hi(v[e]);
-                    u[e] = ptx::pack_bf16x2(u0 * c[2 * e] - v0 * s[2 * e], u1 * c[2 * e + 1] - v1 * s[2 * e + 1]);
-                    v[e] = ptx::pack_bf16x2(u0 * s[2 * e] + v0 * c[2 * e], u1 * s[2 * e + 1] + v1 * c[2 * e + 1]);
-                }
-                p[first + a.turned] = x[b][kPieces - 1];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < W / 2; ++e) {
                     const float u0 = bf16_lo(u[e]), u1 = bf16_hi(u[e]);
-                    // the piece in which rot ends: pairs past it stay as they are, whatever they hold
-                    if (item * 4 + e < half) u[e] = ptx::pack_bf16x2(u0 * c[e] - u1 * s[e], u0 * s[e] + u1 * c[e]);
+                    if constexpr (LAYOUT == kHalves) {
+                        const float v0 = bf16_lo(v[e]), v1 = bf16_hi(v[e]);
+                        u[e] = ptx::pack_bf16x2(u0 * c[2 * e] - v0 * s[2 * e], u1 * c[2 * e + 1] - v1 * s[2 * e + 1]);
+                        v[e] = ptx::pack_bf16x2(u0 * s[2 * e] + v0 * c[2 * e], u1 * s[2 * e + 1] + v1 * c[2 * e + 1]);
+                    } else if (item * kPairs + e < half) {
+                        // the piece in which rot ends: pairs past it stay as they are, whatever they hold
+                        u[e] = ptx::pack_bf16x2(u0 * c[e] - u1 * s[e], u0 * s[e] + u1 * c[e]);
+                    }
                 }
+                if (LAYOUT == kHalves) store_piece<W>(p + half, x[b][kPieces - 1]);
             }
-            p[first] = x[b][0];
+            store_piece<W>(p, x[b][0]);
         }
     }
 }
@@ -203,7 +227,8 @@ extern "C" blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const 
     blink_bf16 *out[2] = {q_out, k_out};
     const int64_t is[2] = {q_stride, k_stride}, os[2] = {q_out_stride, k_out_stride};
     const int heads[2] = {Hq, Hkv};
-    bool pieces = d % 8 == 0 && (interleaved || rot % 16 == 0);  // rows of 16-byte pieces, pairs in whole pieces
+    // Values of a piece: as many as sizes, strides and addresses are multiples of, at most 16 bytes; 1: by element.
+    int64_t fit = d | (interleaved ? 0 : rot / 2);
     RopeArgs a{};
     for (int t = 0; t < (k ? 2 : 1); ++t) {
         const int64_t wide = static_cast<int64_t>(heads[t]) * d;
@@ -219,7 +244,8 @@ extern "C" blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const 
         a.out_stride[t] = os[t];
         a.heads[t] = heads[t];
         a.copy[t] = !in_place;
-        pieces = pieces && aligned16(in[t]) && aligned16(out[t]) && is[t] % 8 == 0 && os[t] % 8 == 0;
+        fit |= is[t] | os[t] | static_cast<int64_t>(reinterpret_cast<uintptr_t>(in[t]) / 2) |
+               static_cast<int64_t>(reinterpret_cast<uintptr_t>(out[t]) / 2);
     }
     if (k && strided_overlap(q_out, 2 * q_out_stride, rows, k_out, 2 * k_out_stride, rows, 2LL * Hq * d, 2LL * Hkv * d))
         return BLINK_INVALID_ARG;
@@ -230,12 +256,13 @@ extern "C" blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const 
     a.rows = rows;
     a.d = d;
     a.rot = rot;
-    if (!pieces) {
+    const int W = fit % 8 == 0 ? 8 : fit % 4 == 0 ? 4 : fit % 2 == 0 ? 2 : 1;
+    if (W == 1) {
         rope_element_kernel<<<static_cast<unsigned>(rows), kThreads, 0, stream>>>(a, interleaved != 0);
     } else {
         const bool copy = a.copy[0] || a.copy[1];
-        a.turned = interleaved ? (rot + 7) / 8 : rot / 16;
-        a.passed = !copy ? 0 : interleaved ? d / 8 - a.turned : (d - rot) / 8;
+        a.turned = interleaved ? (rot + W - 1) / W : rot / 2 / W;
+        a.passed = !copy ? 0 : interleaved ? d / W - a.turned : (d - rot) / W;
         // Rows of a block: two warps over (row, item) (one took 6 % longer on 18432 rows of 32/8 heads, four the same), more where
         // there are too few heads for the other threads, fewer where blocks would not fill the SMs twice.
         const int items = a.turned + a.passed;
@@ -245,10 +272,11 @@ extern "C" blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const 
             a.per_block *= 2;
         const unsigned grid = static_cast<unsigned>((rows + a.per_block - 1) / a.per_block);
         const int smem = a.per_block * (rot / 2) * static_cast<int>(sizeof(float2));  // at most 32 KB
+        auto launch = [&](auto kern) { kern<<<grid, kThreads, smem, stream>>>(a); };
         if (interleaved)
-            rope_kernel<kInterleaved><<<grid, kThreads, smem, stream>>>(a);
+            W == 8 ? launch(rope_kernel<kInterleaved, 8>) : W == 4 ? launch(rope_kernel<kInterleaved, 4>) : launch(rope_kernel<kInterleaved, 2>);
         else
-            rope_kernel<kHalves><<<grid, kThreads, smem, stream>>>(a);
+            W == 8 ? launch(rope_kernel<kHalves, 8>) : W == 4 ? launch(rope_kernel<kHalves, 4>) : launch(rope_kernel<kHalves, 2>);
     }
     return cudaGetLastError() == cudaSuccess ? BLINK_OK : BLINK_CUDA_ERROR;
 }
