@@ -1,0 +1,177 @@
+"""The paged calls where they could go wrong between calls: pages past 4 GB, two streams at once, captured calls whose
+inputs change, tables wider than the sequences, workspaces used again, one page, other devices' checks."""
+import math
+
+import pytest
+import torch
+
+from shared_prefix_question_gb300 import blink
+
+pytestmark = pytest.mark.gpu
+from tests import paged_helpers as ph  # noqa: E402
+
+
+def _i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def test_pages_past_four_gigabytes():
+    """70,000 pages of 64 KB: the pages in use are the last ones, beyond 2^32 bytes of K and of V."""
+    g = ph.gen(41)
+    Hq, Hkv, d, page, total = 16, 8, 128, 64, 70000
+    k = torch.empty(total, Hkv, page, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    v = torch.empty_like(k)
+    scale = [torch.full((total, Hkv), 120, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu) for _ in range(2)]
+    cache = {"k": k, "v": v, "k_scale": scale[0], "v_scale": scale[1]}
+    n = 200
+    table = _i32(69999, 66001, 69990, 65537).view(1, 4)
+    kk, vv = (ph.randn(g, n, Hkv, d).to(torch.bfloat16) for _ in range(2))
+    turns, _ = blink.blink_rope_table(d)
+    blink.blink_paged_append(kk, vv, cache, table, _i32(0, n), _i32(0), n, turns=turns)
+    small = ph.new_cache(g, 4, Hkv, page, d)
+    blink.blink_paged_append(kk, vv, small, _i32(0, 1, 2, 3).view(1, 4), _i32(0, n), _i32(0), n, turns=turns)
+    for x in cache:
+        assert torch.equal(cache[x][table[0, :3].long()].view(torch.uint8), small[x][:3].view(torch.uint8))
+        assert torch.equal(cache[x][65537].view(torch.uint8)[:, :8], small[x][3].view(torch.uint8)[:, :8]) if x in "kv" else True
+    q = ph.randn(g, 1, 1, Hq, d).to(torch.bfloat16)
+    out, lse, _ = blink.blink_paged_token_attention(q, cache, table, _i32(n), n, want_lse=True)
+    ph.check_attention(out, lse, ph.token_reference(q, cache, table, [n]))
+    rows = 50
+    qt, kt, vt = (ph.randn(g, rows, H, d).to(torch.bfloat16) for H in (Hq, Hkv, Hkv))
+    far, _, _ = blink.blink_paged_prefix_tail_attention(qt, cache, table, [n], kt, vt, _i32(0, rows), 1, rows)
+    near, _, _ = blink.blink_paged_prefix_tail_attention(qt, small, _i32(0, 1, 2, 3).view(1, 4), [n], kt, vt, _i32(0, rows), 1, rows)
+    assert torch.equal(far, near)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with a workspace each, over the same cache."""
+    g = ph.gen(42)
+    lens, Hq, Hkv, d, page = [9000, 300], 8, 2, 128, 64
+    table, total = ph.table_for(g, lens, page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, table, lens)
+    length = _i32(*lens)
+    qs = [ph.randn(g, 2, 1, Hq, d).to(torch.bfloat16) for _ in range(2)]
+    want = [blink.blink_paged_token_attention(q, cache, table, length, 9000, want_lse=True)[:2] for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    need = blink.paged_token_attention_workspace_bytes(2, 1, 9000, Hq, Hkv, d)
+    ws = [blink.new_workspace(need, "cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(blink.blink_paged_token_attention(qs[i], cache, table, length, 9000, want_lse=True, ws=ws[i], stream=streams[i])[:2])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i][0]) and torch.equal(l, want[i][1]) for o, l in got[i])
+
+
+@pytest.mark.parametrize("rows", [3, 90])
+def test_prefix_tail_captured_twice_over_one_workspace(rows):
+    """Two graphs that share a workspace, replayed in turn, follow their inputs."""
+    g = ph.gen(43)
+    Hq, Hkv, d, page, P = 8, 2, 64, 32, 500
+    table, total = ph.table_for(g, [P], page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, table, [P])
+    cu = _i32(0, 1, rows)
+    ins = [tuple(ph.randn(g, rows, H, d).to(torch.bfloat16) for H in (Hq, Hkv, Hkv)) for _ in range(2)]
+    ws = blink.new_workspace(blink.paged_prefix_tail_workspace_bytes([0, rows], [P], 2, Hq, Hkv, d), "cuda")
+    outs, graphs = [torch.empty_like(ins[0][0]) for _ in range(2)], []
+
+    def call(i, **kw):
+        return blink.blink_paged_prefix_tail_attention(ins[i][0], cache, table, [P], ins[i][1], ins[i][2], cu, 2, rows, **kw)[0]
+    for i in range(2):
+        call(i, ws=ws)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            call(i, ws=ws, out=outs[i])
+    for step in range(4):
+        for i in range(2):
+            ins[i][0].copy_(ph.randn(g, rows, Hq, d))
+            graphs[i].replay()
+        for i in range(2):
+            assert torch.equal(outs[i], call(i))
+
+
+def test_wider_tables_and_bounds_than_needed():
+    """A table wider than any sequence (strided rows of a larger one) and a larger max_len give the same, and a workspace
+    for more serves less."""
+    g = ph.gen(44)
+    lens, Hq, Hkv, d, page = [100, 37, 64], 4, 2, 64, 16
+    table, total = ph.table_for(g, lens, page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, table, lens)
+    q = ph.randn(g, 3, 2, Hq, d).to(torch.bfloat16)
+    want = ph.token_reference(q, cache, table, lens)
+    big = torch.full((3, 500), -1, dtype=torch.int32, device="cuda")
+    big[:, 100:100 + table.shape[1]] = table
+    wide = big[:, 100:400]
+    ws = blink.new_workspace(blink.paged_token_attention_workspace_bytes(3, 2, 131072, Hq, Hkv, d), "cuda")
+    for t, bound in ((table, 100), (wide, 100), (wide, 4800), (table, 131072)):
+        out, lse, _ = blink.blink_paged_token_attention(q, cache, t, _i32(*lens), bound, want_lse=True, ws=ws)
+        assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+        ph.check_attention(out, lse, want)
+
+
+def test_one_page_and_one_token():
+    g = ph.gen(45)
+    cache = blink.blink_paged_cache(1, 128, 1, 128)
+    table = _i32(0).view(1, 1)
+    k, v = (ph.randn(g, 1, 1, 128).to(torch.bfloat16) for _ in range(2))
+    blink.blink_paged_append(k, v, cache, table, _i32(0, 1), _i32(0), 1)
+    q = ph.randn(g, 1, 1, 7, 128).to(torch.bfloat16)
+    out, lse, _ = blink.blink_paged_token_attention(q, cache, table, _i32(1), 1, want_lse=True)
+    kd, vd = (ph.values(cache, n, table[0], 1)[0, 0] for n in ("k", "v"))
+    assert torch.equal(out[0, 0], vd.to(torch.bfloat16).expand(7, -1))
+    want = (q[0, 0].double() @ kd) / math.sqrt(128)
+    assert float((lse[:, 0].double() - want).abs().max()) <= 64 * ph.F32 * float((q[0, 0].double().abs() @ kd.abs()).max()) / math.sqrt(128) + 2.0 ** -20
+    # nothing to do: no tokens, no keys
+    none = torch.empty(0, 1, 128, dtype=torch.bfloat16, device="cuda")
+    before = cache["k"].view(torch.uint8).clone()
+    blink.blink_paged_append(none, none, cache, table, _i32(0, 0), _i32(1), 0)
+    assert torch.equal(cache["k"].view(torch.uint8), before)
+    out, lse, ws = blink.blink_paged_token_attention(q, cache, table, _i32(0), 0, want_lse=True)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all()) and blink.blink_read_device_status(ws) == blink.BLINK_OK
+
+
+def test_append_repeated_is_the_same_bits_and_order_of_sequences_does_not_matter():
+    g = ph.gen(46)
+    n, Hkv, d, page = [70, 1, 33], 2, 64, 32
+    table, total = ph.table_for(g, n, page)
+    x = [ph.randn(g, sum(n), Hkv, d).to(torch.bfloat16) for _ in range(2)]
+    turns, _ = blink.blink_rope_table(d)
+    a, b = ph.new_cache(g, total, Hkv, page, d), ph.new_cache(g, total, Hkv, page, d)
+    cu = [0, 70, 71, 104]
+    blink.blink_paged_append(*x, a, table, _i32(*cu), _i32(0, 0, 0), 70, turns=turns)
+    order = [2, 0, 1]
+    rows = torch.cat([torch.arange(cu[s], cu[s + 1]) for s in order]).cuda()
+    blink.blink_paged_append(x[0][rows], x[1][rows], b, table[order].contiguous(), _i32(0, 33, 103, 104), _i32(0, 0, 0), 70, turns=turns)
+    assert all(torch.equal(a[t].view(torch.uint8), b[t].view(torch.uint8)) for t in a)
+
+
+def test_codes_are_those_of_the_exact_rotation():
+    """A few hundred thousand keys with values of very different sizes: every code is the nearest to the rotation in 64 bits
+    (off by one only where 64 bits cannot tell: within 2^-34 of the sizes of the border)."""
+    g = ph.gen(47)
+    n, Hkv, d, page = 3000, 4, 128, 64
+    table, total = ph.table_for(g, [n], page)
+    k = (ph.randn(g, n, Hkv, d) * torch.exp(2.0 * ph.randn(g, 1, Hkv, d))).to(torch.bfloat16)
+    for interleaved, rot in ((False, 128), (True, 128), (False, 122)):
+        cache = ph.new_cache(g, total, Hkv, page, d)
+        turns, _ = blink.blink_rope_table(rot, 500000.0)
+        blink.blink_paged_append(k, k, cache, table, _i32(0, n), _i32(0), n, turns=turns, interleaved=interleaved,
+                                 positions=torch.arange(n, device="cuda", dtype=torch.int32) * 41)
+        # the table's own frequencies, so that only the rotation is compared
+        theta = (turns.double() * (2 * math.pi / 2.0 ** 64)).tolist()
+        y, size = ph.rotate(k, torch.arange(n, device="cuda") * 41, theta, 1.0, interleaved)
+        at = table[0, torch.arange(n, device="cuda") // page].long()
+        slot = torch.arange(n, device="cuda") % page
+        scale = torch.exp2(cache["k_scale"].view(torch.uint8)[at].double() - 127)[..., None]
+        got = cache["k"].view(torch.uint8)[at, :, slot].view(torch.float8_e4m3fn).double()
+        lo, hi = ph.e4m3((y - size * 2.0 ** -34) / scale), ph.e4m3((y + size * 2.0 ** -34) / scale)
+        assert bool(((got == lo) | (got == hi)).all())
+        # the window hides little: 2^-33 of a pair's sizes against steps of 2^-4 of a value.  (The first token and the values
+        # past rot are not turned: one in 16 of their 8-bit values lies on a border, and goes to the even code.)
+        assert float((lo != hi)[1:, :, :rot].double().mean()) < 1e-6
+        assert torch.equal(got[0], ph.e4m3(y[0] / scale[0])) and torch.equal(got[..., rot:], ph.e4m3(y / scale)[..., rot:])
