@@ -607,8 +607,11 @@ blink_status blink_paged_token_attention(const blink_bf16 *q, const uint8_t *k_c
  *
  * h_req_rows [n_req+1], h_prefix_len [n_req]  host arrays; lengths 0..131072, n_req 1..64
  * d_ws   blink_paged_prefix_tail_workspace(...) bytes (of the current device), 32-byte aligned, its first 256
- *        zero-filled before its first use; not shared by calls that may run at the same time.  It holds the
- *        prefixes as bf16 rows for the time of the call: one such workspace serves the caches of all layers
+ *        zero-filled before its first use; not shared by calls that may run at the same time; one serves the
+ *        caches of all layers
+ * Where no request has more than 64 rows times Hq/Hkv the pages are read as they are (weights enter the second
+ * product in fp16, a question's own keys in 32 bits); otherwise the workspace holds the prefixes as bf16 rows,
+ * exactly, and the result is that of the calls named.
  * Other arguments as there.  A page index outside [0, n_pages) latches BLINK_DEVICE_FLAG (its values count as 0).
  * Errors: BLINK_INVALID_ARG, BLINK_OUT_OF_RANGE, BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR; device-side:
  * BLINK_DEVICE_FLAG, BLINK_DEVICE_TIMEOUT.

@@ -28,7 +28,10 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;                        // keys
 constexpr int kRound = kStep * kWarps;           // keys of a block per step of its warps
 constexpr int kMaxChunk = 32 * kRound;           // a lane holds the page of one step of its warp
-constexpr int kFewRows = 64;                     // (row, query head) rows of a kv head up to which tail rows read the pages
+// (Row, query head) rows of a kv head, in any request, up to which tail rows read the pages: every 16 of them read and convert
+// all codes again, while bf16 rows are written once and shared by 128.  18432 keys, one request of 16 tokens and 32/8 heads
+// (64 rows): 30 us from the pages, 43 by way of bf16 rows; of 32 tokens 62 and 44; 2048 keys: 12 and 19, 18 and 19.
+constexpr int kFewRows = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e37f;                 // below any score
 constexpr float kHead = 6.f, kSlack = 8.f;       // weights start at 2^kHead and may grow by 2^kSlack before the maximum moves
@@ -617,7 +620,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) token_join_kernel(const __gri
 }
 
 struct TokenPlan {
-    int wide;              // column tiles of a block: two where the rows of a head need them
+    // Column tiles of a block.  Two where a head's rows need them: the codes are converted once for both (16 sequences
+    // of four tokens and 32/8 heads 65 us, with two blocks of one tile 75).  Two warps with a tile each over the same ring,
+    // which convert twice, took 89.
+    int wide;
     int tiles, chunk, chunks;
     size_t lse, o, total;  // offsets of the partial results in the workspace
 };
