@@ -7,6 +7,7 @@ device every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import operator
 import os
@@ -627,6 +628,19 @@ def blink_token_logprobs(hidden, unembed, targets=None, row_idx=None, temperatur
     return {"logprob": logprob, "entropy": entropy, "lse": lse, "top_ids": ids, "top_logprobs": lps, "ws": ws}
 
 
+_E4M3, _E8M0, _BF16, _I32, _F32 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.bfloat16, torch.int32, torch.float32
+
+
+def _usual_stream(stream, index):
+    """The stream's handle where the call is on the current device and its current stream, else None.  The calls below
+    check the usual arguments (contiguous, new outputs) in one expression each, which takes a fifth off a small call's
+    time; whatever that expression does not let through takes the checks that say what is wrong, or that allow for
+    strides, given outputs, other streams and devices."""
+    if stream is None and index >= 0 and _raw_stream is not None and index == torch.cuda.current_device():
+        return _raw_stream(index)
+    return None
+
+
 # ------------------------------------------------------------------------------------------------ rotary positions
 ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "by_dim": 3, "by_turns": 4}
 _ROPE_TURNS = {"by_dim": (1.0, 32.0), "by_turns": (1.0, 4.0)}  # low and high where the caller gives none
@@ -673,6 +687,27 @@ def blink_rope(q, k, positions, turns, interleaved: bool = False, amplitude: flo
     (i, i + rot/2), or (2 i, 2 i + 1) if `interleaved`, with blink_rope_table's `turns` and amplitude.  Rows may be
     strided (slices of one projection).  q_out / k_out: None for new tensors, q / k themselves for in place.
     Returns (q_out, k_out)."""
+    if k is not None and q_out is None and k_out is None:
+        try:
+            index = q.get_device()
+            handle = _usual_stream(stream, index)
+            (rows, Hq, d), Hkv, n = q.shape, k.shape[1], turns.shape[0]
+            q_strides, k_strides = q.stride(), k.stride()
+            if (handle is not None and q.dtype is _BF16 and k.dtype is _BF16 and positions.dtype is _I32 and turns.dtype is torch.int64 and
+                    k.shape == (rows, Hkv, d) and positions.shape == (rows,) and turns.dim() == 1 and 1 <= n <= d // 2 and
+                    k.get_device() == index and positions.get_device() == index and turns.get_device() == index and
+                    q_strides[1] == d and q_strides[2] == 1 and k_strides[1] == d and k_strides[2] == 1 and 1 < rows <= INT32_MAX and
+                    Hq <= INT32_MAX and Hkv <= INT32_MAX and positions.is_contiguous() and turns.is_contiguous()):
+                q_out = torch.empty((rows, Hq, d), dtype=_BF16, device=q.device)
+                k_out = torch.empty((rows, Hkv, d), dtype=_BF16, device=q.device)
+        except (AttributeError, TypeError, ValueError, IndexError):
+            pass
+        if q_out is not None:
+            st = lib().blink_rope(q.data_ptr(), q_strides[0], k.data_ptr(), k_strides[0], positions.data_ptr(), rows, Hq, Hkv, d, 2 * n,
+                                  turns.data_ptr(), amplitude, 1 if interleaved else 0, q_out.data_ptr(), Hq * d, k_out.data_ptr(),
+                                  Hkv * d, handle)
+            _check(st, "blink_rope")
+            return q_out, k_out
     rows, Hq, d = q.shape if getattr(q, "ndim", 0) == 3 else (None,) * 3
     q_stride = _need_rows("q", q, rows, Hq, d)
     Hkv = k_stride = k_out_stride = 0
@@ -709,6 +744,24 @@ def blink_paged_cache(n_pages: int, page_tokens: int, Hkv: int, d: int, device="
     return {"k": zeros(n_pages, Hkv, page_tokens, d).view(torch.float8_e4m3fn),
             "v": zeros(n_pages, Hkv, page_tokens, d).view(torch.float8_e4m3fn),
             "k_scale": zeros(n_pages, Hkv).view(torch.float8_e8m0fnu), "v_scale": zeros(n_pages, Hkv).view(torch.float8_e8m0fnu)}
+
+
+def _usual_cache(cache, table, index):
+    """(sizes n, Hkv, page, d, arguments of the C calls, those of the table) of a contiguous cache and table on device
+    `index`, else None."""
+    k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
+    if not (k.dtype is _E4M3 and v.dtype is _E4M3 and ks.dtype is _E8M0 and vs.dtype is _E8M0 and table.dtype is _I32 and
+            k.get_device() == index and v.get_device() == index and ks.get_device() == index and vs.get_device() == index and
+            table.get_device() == index and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and
+            vs.is_contiguous() and table.is_contiguous()):
+        return None
+    shape, (S, width) = k.shape, table.shape
+    n, Hkv, page, d = shape
+    if not (v.shape == shape and ks.shape == (n, Hkv) and vs.shape == (n, Hkv) and 0 < n <= INT32_MAX and
+            S <= INT32_MAX and width <= INT32_MAX):
+        return None
+    return (n, Hkv, page, d, (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), Hkv * page * d, Hkv, n, page), S,
+            (table.data_ptr(), width, width))
 
 
 def _cache_of(cache, Hkv, d):
@@ -758,6 +811,34 @@ def blink_paged_append(k, v, cache: dict, page_table, cu_new, start, max_new: in
     Keys are turned by `positions` (int32 [n]; None: start + 0, 1, ...) with blink_rope_table's `turns` and amplitude
     (turns None: they are rotated already).  max_new: upper bound of a sequence's new tokens.  Returns ws; device-side
     problems (a bad length or page) are read with blink_read_device_status(ws)."""
+    max_new = _int32("max_new", max_new)
+    try:
+        index = k.get_device()
+        handle = _usual_stream(stream, index)
+        usual = None if handle is None else _usual_cache(cache, page_table, index)
+        if usual is not None:
+            n, Hkv, d = k.shape
+            _, heads, _, width, args, S, table = usual
+            if not (v.shape == k.shape and heads == Hkv and width == d and k.dtype is _BF16 and v.dtype is _BF16 and
+                    v.get_device() == index and 1 < n <= INT32_MAX and k.stride()[1:] == (d, 1) and v.stride()[1:] == (d, 1) and
+                    cu_new.dtype is _I32 and start.dtype is _I32 and cu_new.shape == (S + 1,) and start.shape == (S,) and
+                    cu_new.get_device() == index and start.get_device() == index and cu_new.is_contiguous() and
+                    start.is_contiguous() and positions is None and
+                    (turns is None or (turns.dtype is torch.int64 and turns.get_device() == index and turns.dim() == 1 and
+                                       turns.is_contiguous() and 1 <= turns.shape[0] <= d // 2)) and
+                    (ws is None or (ws.dtype is torch.uint8 and ws.get_device() == index and ws.is_contiguous()))):
+                usual = None
+    except (AttributeError, TypeError, ValueError):
+        usual = None
+    if usual is not None:
+        if ws is None:
+            ws = _Launch(None, k).workspace(paged_append_workspace_bytes())
+        st = lib().blink_paged_append(k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), n, Hkv, d, *args, *table,
+                                      cu_new.data_ptr(), start.data_ptr(), S, max_new, None, _addr(turns),
+                                      0 if turns is None else 2 * turns.shape[0], amplitude, 1 if interleaved else 0,
+                                      ws.data_ptr(), ws.numel(), handle)
+        _check(st, "blink_paged_append")
+        return ws
     n, Hkv, d = k.shape if getattr(k, "ndim", 0) == 3 else (None,) * 3
     k_stride, v_stride = _need_rows("k", k, n, Hkv, d), _need_rows("v", v, n, Hkv, d)
     tensors, args = _cache_of(cache, Hkv, d)
@@ -769,7 +850,6 @@ def blink_paged_append(k, v, cache: dict, page_table, cu_new, start, max_new: in
     rot = 0 if turns is None else _turns_of(turns, d)
     _bytes("ws", ws)
     _sizes(n, S)
-    max_new = _int32("max_new", max_new)
     with _Launch(stream, k, v, *tensors, page_table, cu_new, start, positions, turns, ws) as call:
         if ws is None:
             ws = call.workspace(paged_append_workspace_bytes())
@@ -790,13 +870,36 @@ def blink_paged_token_attention(q, cache: dict, page_table, length, max_len: int
     """Attention of the last T tokens of S sequences, q [S, T, Hq, d] bf16, over the pages that hold them: sequence s
     has length[s] (int32, on the device) tokens in row s of page_table, and token t sees the first length - T + 1 + t.
     max_len: upper bound of `length`.  Returns (out [S, T, Hq, d], lse [Hq, S * T] or None, ws)."""
+    max_len = _int32("max_len", max_len)
+    try:
+        index = q.get_device()
+        handle = _usual_stream(stream, index)
+        usual = None if handle is None else _usual_cache(cache, page_table, index)
+        if usual is not None:
+            S, T, Hq, d = q.shape
+            _, Hkv, _, width, args, rows, table = usual
+            if not (width == d and rows == S and q.dtype is _BF16 and q.is_contiguous() and length.dtype is _I32 and
+                    length.shape == (S,) and length.get_device() == index and length.is_contiguous() and
+                    T <= INT32_MAX and Hq <= INT32_MAX and out is None and lse is None and
+                    (ws is None or (ws.dtype is torch.uint8 and ws.get_device() == index and ws.is_contiguous()))):
+                usual = None
+    except (AttributeError, TypeError, ValueError):
+        usual = None
+    if usual is not None:
+        out = torch.empty_like(q)
+        lse = torch.empty((Hq, S * T), dtype=_F32, device=q.device) if want_lse else None
+        if ws is None:
+            ws = _Launch(None, q).workspace(paged_token_attention_workspace_bytes(S, T, max_len, Hq, Hkv, d))
+        st = lib().blink_paged_token_attention(q.data_ptr(), *args, *table, length.data_ptr(), S, T, max_len, Hq, Hkv, d, scale,
+                                               out.data_ptr(), _addr(lse), ws.data_ptr(), ws.numel(), handle)
+        _check(st, "blink_paged_token_attention")
+        return out, lse, ws
     S, T, Hq, d = q.shape if getattr(q, "ndim", 0) == 4 else (None,) * 4
     _need("q", q, torch.bfloat16, (S, T, Hq, d), inner=4)
     Hkv = cache["k"].shape[1] if getattr(cache["k"], "ndim", 0) == 4 else None
     tensors, args = _cache_of(cache, Hkv, d)
     rows, table = _table_of(page_table)
-    if Hq > INT32_MAX or T > INT32_MAX:
-        _sizes(T, Hq)
+    _sizes(T, Hq)
     if rows != S:
         raise ValueError(f"page_table must have a row for each of {S} sequences, not {rows}")
     _need("length", length, torch.int32, (S,))
@@ -805,7 +908,6 @@ def blink_paged_token_attention(q, cache: dict, page_table, length, max_len: int
     if lse is not None:
         _need("lse", lse, torch.float32, (Hq, S * T), inner=2)
     _bytes("ws", ws)
-    max_len = _int32("max_len", max_len)
     with _Launch(stream, q, *tensors, page_table, length, out, lse, ws) as call:
         if out is None:
             out = torch.empty_like(q)
@@ -820,15 +922,20 @@ def blink_paged_token_attention(q, cache: dict, page_table, length, max_len: int
 
 
 def _int32s(name, values):
-    """A host list as a C array of int32."""
-    return (ctypes.c_int32 * len(values))(*[_int32(name, x) for x in values])
+    """A host list as an array of int32 (and its address)."""
+    try:
+        a = array.array("i", values)
+    except OverflowError:
+        raise ValueError(f"{name} must fit 32 bits: {list(values)}") from None
+    return a, a.buffer_info()[0]
 
 
 def paged_prefix_tail_workspace_bytes(req_rows, prefix_len, B, Hq, Hkv, d) -> int:
     if len(req_rows) != len(prefix_len) + 1:
         raise ValueError("req_rows must have one value more than prefix_len")
-    return int(lib().blink_paged_prefix_tail_workspace(_int32s("req_rows", req_rows), _int32s("prefix_len", prefix_len),
-                                                       len(prefix_len), int(B), int(Hq), int(Hkv), int(d)))
+    rows, at_rows = _int32s("req_rows", req_rows)
+    lens, at_lens = _int32s("prefix_len", prefix_len)
+    return int(lib().blink_paged_prefix_tail_workspace(at_rows, at_lens, len(lens), int(B), int(Hq), int(Hkv), int(d)))
 
 
 def blink_paged_prefix_tail_attention(q, cache: dict, page_table, prefix_len, k_tail, v_tail, cu_seqlens, B: int, max_tail: int,
@@ -838,28 +945,55 @@ def blink_paged_prefix_tail_attention(q, cache: dict, page_table, prefix_len, k_
     [rows, Hq, d] and k_tail / v_tail [rows, Hkv, d] bf16 (req_rows None: one request has them all) and attends to the
     first prefix_len[r] tokens of row r of page_table.  prefix_len and req_rows are host lists; the rest as
     blink_prefix_tail_attention.  Returns (out, lse, ws)."""
-    rows, Hq, d = q.shape if getattr(q, "ndim", 0) == 3 else (None,) * 3
-    _need("q", q, torch.bfloat16, (rows, Hq, d), inner=3)
-    Hkv = k_tail.shape[1] if getattr(k_tail, "ndim", 0) == 3 else None
-    _need("k_tail", k_tail, torch.bfloat16, (rows, Hkv, d), inner=3)
-    _need("v_tail", v_tail, torch.bfloat16, (rows, Hkv, d), inner=3)
-    tensors, args = _cache_of(cache, Hkv, d)
-    n_req, table = _table_of(page_table)
+    B, max_tail = _int32("B", B), _int32("max_tail", max_tail)
+    try:
+        index = q.get_device()
+        handle = _usual_stream(stream, index)
+        usual = None if handle is None else _usual_cache(cache, page_table, index)
+        if usual is not None:
+            rows, Hq, d = q.shape
+            _, Hkv, _, width, args, n_req, table = usual
+            if not (width == d and q.dtype is _BF16 and k_tail.dtype is _BF16 and v_tail.dtype is _BF16 and
+                    cu_seqlens.dtype is _I32 and k_tail.shape == (rows, Hkv, d) and v_tail.shape == (rows, Hkv, d) and
+                    cu_seqlens.shape == (B + 1,) and k_tail.get_device() == index and v_tail.get_device() == index and
+                    cu_seqlens.get_device() == index and q.is_contiguous() and k_tail.is_contiguous() and v_tail.is_contiguous() and
+                    cu_seqlens.is_contiguous() and seq_start is None and out is None and lse is None and rows <= INT32_MAX and
+                    Hq <= INT32_MAX and (ws is None or (ws.dtype is torch.uint8 and ws.get_device() == index and ws.is_contiguous()))):
+                usual = None
+    except (AttributeError, TypeError, ValueError):
+        usual = None
+    if usual is None:
+        rows, Hq, d = q.shape if getattr(q, "ndim", 0) == 3 else (None,) * 3
+        _need("q", q, torch.bfloat16, (rows, Hq, d), inner=3)
+        Hkv = k_tail.shape[1] if getattr(k_tail, "ndim", 0) == 3 else None
+        _need("k_tail", k_tail, torch.bfloat16, (rows, Hkv, d), inner=3)
+        _need("v_tail", v_tail, torch.bfloat16, (rows, Hkv, d), inner=3)
+        tensors, args = _cache_of(cache, Hkv, d)
+        n_req, table = _table_of(page_table)
+        _need("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+        if seq_start is not None:
+            _need("seq_start", seq_start, torch.int32, (B,))
+        if out is not None:
+            _need("out", out, torch.bfloat16, (rows, Hq, d), inner=3)
+        if lse is not None:
+            _need("lse", lse, torch.float32, (Hq, rows), inner=2)
+        _bytes("ws", ws)
+        _sizes(rows, Hq, n_req)
     if req_rows is None:
         req_rows = [0, rows]
     if len(prefix_len) != n_req or len(req_rows) != n_req + 1:
         raise ValueError(f"page_table has {n_req} requests: prefix_len needs as many values, req_rows one more")
-    B, max_tail = _int32("B", B), _int32("max_tail", max_tail)
-    _need("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
-    if seq_start is not None:
-        _need("seq_start", seq_start, torch.int32, (B,))
-    if out is not None:
-        _need("out", out, torch.bfloat16, (rows, Hq, d), inner=3)
-    if lse is not None:
-        _need("lse", lse, torch.float32, (Hq, rows), inner=2)
-    _bytes("ws", ws)
-    _sizes(rows, Hq, n_req)
-    h_rows, h_len = _int32s("req_rows", req_rows), _int32s("prefix_len", prefix_len)
+    (host_rows, h_rows), (host_len, h_len) = _int32s("req_rows", req_rows), _int32s("prefix_len", prefix_len)  # read by the call
+    if usual is not None:
+        out = torch.empty_like(q)
+        lse = torch.empty((Hq, rows), dtype=_F32, device=q.device) if want_lse else None
+        if ws is None:
+            ws = _Launch(None, q).workspace(paged_prefix_tail_workspace_bytes(req_rows, prefix_len, B, Hq, Hkv, d))
+        st = lib().blink_paged_prefix_tail_attention(
+            q.data_ptr(), *args, *table, k_tail.data_ptr(), v_tail.data_ptr(), cu_seqlens.data_ptr(), None, B, rows, n_req, h_rows,
+            h_len, max_tail, Hq, Hkv, d, scale, out.data_ptr(), _addr(lse), ws.data_ptr(), ws.numel(), handle)
+        _check(st, "blink_paged_prefix_tail_attention")
+        return out, lse, ws
     with _Launch(stream, q, *tensors, page_table, k_tail, v_tail, cu_seqlens, seq_start, out, lse, ws) as call:
         if out is None:
             out = torch.empty_like(q)

@@ -175,3 +175,50 @@ def test_codes_are_those_of_the_exact_rotation():
         # past rot are not turned: one in 16 of their 8-bit values lies on a border, and goes to the even code.)
         assert float((lo != hi)[1:, :, :rot].double().mean()) < 1e-6
         assert torch.equal(got[0], ph.e4m3(y[0] / scale[0])) and torch.equal(got[..., rot:], ph.e4m3(y / scale)[..., rot:])
+
+
+def test_usual_and_other_calls_are_one():
+    """The binding's short way (contiguous tensors, new outputs, the current stream) and its long one (strides, given
+    outputs, another stream) give the same, and wrong arguments are refused on either."""
+    g = ph.gen(48)
+    lens, Hq, Hkv, d, page = [70, 20], 4, 2, 64, 16
+    table, total = ph.table_for(g, lens, page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, table, lens)
+    length, q = _i32(*lens), ph.randn(g, 2, 1, Hq, d).to(torch.bfloat16)
+    usual = blink.blink_paged_token_attention(q, cache, table, length, 70, want_lse=True)
+    wide = torch.full((2, 9), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    other = blink.blink_paged_token_attention(q, cache, wide[:, :table.shape[1]], length, 70, out=torch.empty_like(q), want_lse=True)
+    assert torch.equal(usual[0], other[0]) and torch.equal(usual[1], other[1])
+    for bad in (dict(q=q.float()), dict(q=q[0]), dict(length=length.long()), dict(length=length[:1]), dict(table=table.long()),
+                dict(table=table[:1]), dict(q=q[..., :32]), dict(ws=torch.zeros(64, device="cuda")), dict(cache={**cache, "v": cache["v"][:1]}),
+                dict(cache={**cache, "k_scale": cache["k_scale"].view(torch.uint8)}), dict(q=q.cpu()), dict(q=None), dict(max_len=2**40)):
+        a = dict(q=q, cache=cache, table=table, length=length, max_len=70, ws=None)
+        a.update(bad)
+        with pytest.raises((ValueError, TypeError)):
+            blink.blink_paged_token_attention(a["q"], a["cache"], a["table"], a["length"], a["max_len"], ws=a["ws"])
+    with pytest.raises(blink.BlinkError):
+        blink.blink_paged_token_attention(q, cache, table, length, 131073)
+    k = ph.randn(g, 3, Hkv, d).to(torch.bfloat16)
+    turns, _ = blink.blink_rope_table(d)
+    for bad in (dict(k=k.half()), dict(v=k[:2]), dict(cu=_i32(0, 2)), dict(start=_i32(0)), dict(turns=turns.float()),
+                dict(turns=torch.zeros(33, dtype=torch.int64, device="cuda")), dict(ws=torch.zeros(64, device="cuda")), dict(k=k[..., ::2]),
+                dict(start=_i32(0, 0).cpu()), dict(positions=_i32(1, 2))):
+        a = dict(k=k, v=k, cu=_i32(0, 2, 3), start=_i32(0, 0), turns=turns, ws=None, positions=None)
+        a.update(bad)
+        with pytest.raises((ValueError, TypeError)):
+            blink.blink_paged_append(a["k"], a["v"], cache, table, a["cu"], a["start"], 2, positions=a["positions"], turns=a["turns"], ws=a["ws"])
+    rows = ph.randn(g, 5, Hq, d).to(torch.bfloat16)
+    kv = ph.randn(g, 5, Hkv, d).to(torch.bfloat16)
+    for bad in (dict(q=rows[0]), dict(k=kv[:4]), dict(v=kv.float()), dict(cu=_i32(0, 5, 5)), dict(prefix=[70]), dict(req=[0, 5]),
+                dict(cu=_i32(0, 5).cpu()), dict(prefix=[70, 2**33])):
+        a = dict(q=rows, k=kv, v=kv, cu=_i32(0, 5), prefix=[70, 20], req=[0, 5, 5])
+        a.update(bad)
+        with pytest.raises((ValueError, TypeError)):
+            blink.blink_paged_prefix_tail_attention(a["q"], cache, table, a["prefix"], a["k"], a["v"], a["cu"], 1, 5, req_rows=a["req"])
+    for bad in (dict(q=rows.half()), dict(k=kv[:4]), dict(pos=_i32(1, 2)), dict(turns=turns.int()), dict(turns=turns[:0]), dict(pos=None)):
+        a = dict(q=rows, k=kv, pos=_i32(0, 1, 2, 3, 4), turns=turns)
+        a.update(bad)
+        with pytest.raises((ValueError, TypeError)):
+            blink.blink_rope(a["q"], a["k"], a["pos"], a["turns"])
