@@ -696,16 +696,17 @@ def blink_rope(q, k, positions, turns, interleaved: bool = False, amplitude: flo
             if (handle is not None and q.dtype is _BF16 and k.dtype is _BF16 and positions.dtype is _I32 and turns.dtype is torch.int64 and
                     k.shape == (rows, Hkv, d) and positions.shape == (rows,) and turns.dim() == 1 and 1 <= n <= d // 2 and
                     k.get_device() == index and positions.get_device() == index and turns.get_device() == index and
-                    q_strides[1] == d and q_strides[2] == 1 and k_strides[1] == d and k_strides[2] == 1 and 1 < rows <= INT32_MAX and
+                    q_strides[1] == d and q_strides[2] == 1 and k_strides[1] == d and k_strides[2] == 1 and 0 < rows <= INT32_MAX and
                     Hq <= INT32_MAX and Hkv <= INT32_MAX and positions.is_contiguous() and turns.is_contiguous()):
                 q_out = torch.empty((rows, Hq, d), dtype=_BF16, device=q.device)
                 k_out = torch.empty((rows, Hkv, d), dtype=_BF16, device=q.device)
         except (AttributeError, TypeError, ValueError, IndexError):
             pass
         if q_out is not None:
-            st = lib().blink_rope(q.data_ptr(), q_strides[0], k.data_ptr(), k_strides[0], positions.data_ptr(), rows, Hq, Hkv, d, 2 * n,
-                                  turns.data_ptr(), amplitude, 1 if interleaved else 0, q_out.data_ptr(), Hq * d, k_out.data_ptr(),
-                                  Hkv * d, handle)
+            one = rows == 1  # a single row has any stride
+            st = lib().blink_rope(q.data_ptr(), Hq * d if one else q_strides[0], k.data_ptr(), Hkv * d if one else k_strides[0],
+                                  positions.data_ptr(), rows, Hq, Hkv, d, 2 * n, turns.data_ptr(), amplitude, 1 if interleaved else 0,
+                                  q_out.data_ptr(), Hq * d, k_out.data_ptr(), Hkv * d, handle)
             _check(st, "blink_rope")
             return q_out, k_out
     rows, Hq, d = q.shape if getattr(q, "ndim", 0) == 3 else (None,) * 3
@@ -820,7 +821,7 @@ def blink_paged_append(k, v, cache: dict, page_table, cu_new, start, max_new: in
             n, Hkv, d = k.shape
             _, heads, _, width, args, S, table = usual
             if not (v.shape == k.shape and heads == Hkv and width == d and k.dtype is _BF16 and v.dtype is _BF16 and
-                    v.get_device() == index and 1 < n <= INT32_MAX and k.stride()[1:] == (d, 1) and v.stride()[1:] == (d, 1) and
+                    v.get_device() == index and 0 < n <= INT32_MAX and k.stride()[1:] == (d, 1) and v.stride()[1:] == (d, 1) and
                     cu_new.dtype is _I32 and start.dtype is _I32 and cu_new.shape == (S + 1,) and start.shape == (S,) and
                     cu_new.get_device() == index and start.get_device() == index and cu_new.is_contiguous() and
                     start.is_contiguous() and positions is None and
@@ -833,7 +834,9 @@ def blink_paged_append(k, v, cache: dict, page_table, cu_new, start, max_new: in
     if usual is not None:
         if ws is None:
             ws = _Launch(None, k).workspace(paged_append_workspace_bytes())
-        st = lib().blink_paged_append(k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), n, Hkv, d, *args, *table,
+        row = Hkv * d  # a single row has any stride
+        st = lib().blink_paged_append(k.data_ptr(), k.stride(0) if n > 1 else row, v.data_ptr(), v.stride(0) if n > 1 else row,
+                                      n, Hkv, d, *args, *table,
                                       cu_new.data_ptr(), start.data_ptr(), S, max_new, None, _addr(turns),
                                       0 if turns is None else 2 * turns.shape[0], amplitude, 1 if interleaved else 0,
                                       ws.data_ptr(), ws.numel(), handle)

@@ -222,3 +222,22 @@ def test_usual_and_other_calls_are_one():
         a.update(bad)
         with pytest.raises((ValueError, TypeError)):
             blink.blink_rope(a["q"], a["k"], a["pos"], a["turns"])
+
+
+def test_a_single_row_of_a_projection():
+    """One token: slices of one projection's row, whose first stride means nothing."""
+    g = ph.gen(49)
+    Hq, Hkv, d = 4, 2, 64
+    row = ph.randn(g, 1, (Hq + 2 * Hkv) * d).to(torch.bfloat16)
+    q, k, v = row[:, :Hq * d].view(1, Hq, d), row[:, Hq * d:(Hq + Hkv) * d].view(1, Hkv, d), row[:, (Hq + Hkv) * d:].view(1, Hkv, d)
+    odd = torch.as_strided(k, (1, Hkv, d), (1, d, 1))  # as a single row's stride may be
+    turns, _ = blink.blink_rope_table(d)
+    qr, kr = blink.blink_rope(q, odd, _i32(77), turns)
+    theta, _ = ph.frequencies(d, 10000.0)
+    for got, x in ((qr, q), (kr, k)):
+        want, size = ph.rotate(x, _i32(77), theta, 1.0, False)
+        assert bool(((got.double() - want).abs() <= ph.BF16 * want.abs() + 8 * ph.F32 * size + 2.0 ** -133).all())
+    a, b = (blink.blink_paged_cache(2, 16, Hkv, d) for _ in range(2))
+    blink.blink_paged_append(odd, v, a, _i32(1).view(1, 1), _i32(0, 1), _i32(5), 1, turns=turns)
+    blink.blink_paged_append(k.contiguous(), v.contiguous(), b, _i32(1).view(1, 1), _i32(0, 1), _i32(5), 1, turns=turns)
+    assert all(torch.equal(a[n].view(torch.uint8), b[n].view(torch.uint8)) for n in a)
