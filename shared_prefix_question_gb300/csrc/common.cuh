@@ -37,6 +37,24 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 bool strided_overlap(const void *a, int64_t sa, int64_t na, const void *b, int64_t sb, int64_t nb, int64_t width_a,
                      int64_t width_b);
 
+// Launches `kern` with programmatic stream serialization: it may be scheduled while the kernel before it in the stream drains
+// (where that one allows it) and has to wait (griddepcontrol.wait) before it touches memory.
+template <class Kernel, class... Args>
+cudaError_t launch_programmatic(Kernel kern, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 int current_sm_count();  // of the current device; 0 if it cannot be asked
 
 }  // namespace blink

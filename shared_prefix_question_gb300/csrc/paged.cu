@@ -132,6 +132,8 @@ __global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_con
     extern __shared__ uint4 ring[];
     __shared__ uint32_t part[2][2][32];
     __shared__ int16_t k_exponents[kMaxBlockHeads];
+    ptx::grid_dep_wait();
+    ptx::grid_launch_dependents();
     const int seq = blockIdx.z;
     const int c0 = __ldg(a.cu + seq) - __ldg(a.cu), n = __ldg(a.cu + seq + 1) - __ldg(a.cu + seq), start = __ldg(a.start + seq);
     if (n == 0) return;
@@ -417,6 +419,7 @@ template <int D>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ GatherArgs a)
 {
     constexpr int kPieces = D / 16;
+    ptx::grid_dep_wait();
     const int r = blockIdx.y;
     const int len = a.len[r], padded = (len + kTile - 1) / kTile * kTile;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x;
@@ -557,7 +560,7 @@ extern "C" blink_status blink_paged_append(const blink_bf16 *k, int64_t k_stride
     bool set = true;
     auto launch = [&](auto kern) {
         set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d * 8 * (64 * kStages + 2 * kMaxBlockHeads)) == cudaSuccess;
-        if (set) kern<<<grid, threads, smem, stream>>>(a);
+        set = set && launch_programmatic(kern, grid, threads, smem, stream, a) == cudaSuccess;
     };
     if (d == 128) {
         if (layout == kNoRotation) launch(append_kernel<128, kNoRotation>);
@@ -570,8 +573,7 @@ extern "C" blink_status blink_paged_append(const blink_bf16 *k, int64_t k_stride
         if (layout == kInterleaved) launch(append_kernel<64, kInterleaved>);
         if (layout == kHalvesByElement) launch(append_kernel<64, kHalvesByElement>);
     }
-    if (!set) return BLINK_CUDA_ERROR;
-    return cudaGetLastError() == cudaSuccess ? BLINK_OK : BLINK_CUDA_ERROR;
+    return set ? BLINK_OK : BLINK_CUDA_ERROR;
 }
 
 extern "C" size_t blink_paged_prefix_tail_workspace(const int32_t *h_req_rows, const int32_t *h_prefix_len, int32_t n_req,
@@ -643,11 +645,9 @@ extern "C" blink_status blink_paged_prefix_tail_attention(
         a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
         const int64_t items = static_cast<int64_t>((longest + kTile - 1) / kTile * kTile) * Hkv * (d / 16);
         const dim3 grid(static_cast<unsigned>((items + kGatherThreads - 1) / kGatherThreads), static_cast<unsigned>(n_req));
-        if (d == 128)
-            gather_kernel<128><<<grid, kGatherThreads, 0, stream>>>(a);
-        else
-            gather_kernel<64><<<grid, kGatherThreads, 0, stream>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return BLINK_CUDA_ERROR;
+        const cudaError_t e = d == 128 ? launch_programmatic(gather_kernel<128>, grid, kGatherThreads, 0, stream, a)
+                                       : launch_programmatic(gather_kernel<64>, grid, kGatherThreads, 0, stream, a);
+        if (e != cudaSuccess) return BLINK_CUDA_ERROR;
     }
     const int64_t row = static_cast<int64_t>(Hkv) * d;
     if (n_req == 1)

@@ -135,6 +135,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
     const int64_t token0 = TAIL ? a.tail.row[seq] : static_cast<int64_t>(seq) * a.T;
     const int Tg = T * a.g, rho0 = tile * Sh::kRows, rows = min(Sh::kRows, Tg - rho0);
 
+    // What is launched behind this grid starts when all its blocks are past this wait, so the join, which reads lengths,
+    // queries and tails before it waits for this grid, finds what was written before this grid.
+    ptx::grid_dep_wait();
     ptx::grid_launch_dependents();
     if (TAIL && rows <= 0) return;  // fewer rows than another request
     // The pages of this warp's steps, one a lane, read before the length is known.
@@ -580,6 +583,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) token_join_kernel(const __gri
         }
     }
     ptx::grid_dep_wait();
+    ptx::grid_launch_dependents();
     const float *pl = a.part_lse + row * a.chunks, *po = a.part_o + row * a.chunks * D + lane * kVec;
     for (int c0 = warp; c0 < n; c0 += warps * kJoinBatch) {
         float l[kJoinBatch], x[kJoinBatch][kVec];
@@ -663,8 +667,7 @@ bool launch_pages(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const TokenA
     const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.Hkv * a.tiles), static_cast<unsigned>(a.S));
     auto launch = [&](auto kern, int smem) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
-        kern<<<grid, kThreads, smem, stream>>>(tm_k, tm_v, a);
-        return cudaGetLastError() == cudaSuccess;
+        return launch_programmatic(kern, grid, kThreads, smem, stream, tm_k, tm_v, a) == cudaSuccess;
     };
     return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL>, Shape<D, 1>::kSmem)
                           : launch(token_attention_kernel<D, 2, TAIL>, Shape<D, 2>::kSmem);
@@ -683,19 +686,12 @@ blink_status launch_token(const TokenArgs &a, const TokenPlan &plan, int page_to
     if (!(d == 128 ? launch_pages<128, TAIL>(tm_k, tm_v, a, plan, stream) : launch_pages<64, TAIL>(tm_k, tm_v, a, plan, stream)))
         return BLINK_CUDA_ERROR;
     if (!TAIL && a.chunks == 1) return BLINK_OK;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
     int warps = (a.chunks + kJoinBatch - 1) / kJoinBatch;
     if (TAIL && warps < (a.tail.max_tail + kJoinBatch - 1) / kJoinBatch) warps = (a.tail.max_tail + kJoinBatch - 1) / kJoinBatch;
-    cfg.gridDim = dim3(static_cast<unsigned>(joined));
-    cfg.blockDim = dim3(static_cast<unsigned>(warps < kJoinWarps ? warps : kJoinWarps) * 32);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = d == 128 ? cudaLaunchKernelEx(&cfg, token_join_kernel<128, TAIL>, a)
-                                   : cudaLaunchKernelEx(&cfg, token_join_kernel<64, TAIL>, a);
+    const unsigned threads = static_cast<unsigned>(warps < kJoinWarps ? warps : kJoinWarps) * 32;
+    const dim3 rows(static_cast<unsigned>(joined));
+    const cudaError_t e = d == 128 ? launch_programmatic(token_join_kernel<128, TAIL>, rows, threads, 0, stream, a)
+                                   : launch_programmatic(token_join_kernel<64, TAIL>, rows, threads, 0, stream, a);
     return e == cudaSuccess ? BLINK_OK : BLINK_CUDA_ERROR;
 }
 

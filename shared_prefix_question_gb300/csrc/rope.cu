@@ -81,6 +81,8 @@ template <int LAYOUT, int W>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a)
 {
     extern __shared__ float2 cs[];  // [rows of the block][rot / 2]
+    ptx::grid_dep_wait();
+    ptx::grid_launch_dependents();
     const int row0 = blockIdx.x * a.per_block;
     const int n = min(a.per_block, a.rows - row0);
     block_angles(a, row0, n, cs);
@@ -152,6 +154,8 @@ __device__ __forceinline__ uint16_t bf16_bits(float x) { return static_cast<uint
 __global__ void __launch_bounds__(kThreads) rope_element_kernel(const __grid_constant__ RopeArgs a, bool interleaved)
 {
     __shared__ float2 cs[kMaxDim / 2];
+    ptx::grid_dep_wait();
+    ptx::grid_launch_dependents();
     const int64_t row = blockIdx.x;
     block_angles(a, blockIdx.x, 1, cs);
     const int half = a.rot / 2, items = half + a.d - a.rot;
@@ -257,8 +261,9 @@ extern "C" blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const 
     a.d = d;
     a.rot = rot;
     const int W = fit % 8 == 0 ? 8 : fit % 4 == 0 ? 4 : fit % 2 == 0 ? 2 : 1;
+    cudaError_t launched = cudaSuccess;
     if (W == 1) {
-        rope_element_kernel<<<static_cast<unsigned>(rows), kThreads, 0, stream>>>(a, interleaved != 0);
+        launched = launch_programmatic(rope_element_kernel, dim3(static_cast<unsigned>(rows)), kThreads, 0, stream, a, interleaved != 0);
     } else {
         const bool copy = a.copy[0] || a.copy[1];
         a.turned = interleaved ? (rot + W - 1) / W : rot / 2 / W;
@@ -272,11 +277,11 @@ extern "C" blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const 
             a.per_block *= 2;
         const unsigned grid = static_cast<unsigned>((rows + a.per_block - 1) / a.per_block);
         const int smem = a.per_block * (rot / 2) * static_cast<int>(sizeof(float2));  // at most 32 KB
-        auto launch = [&](auto kern) { kern<<<grid, kThreads, smem, stream>>>(a); };
+        auto launch = [&](auto kern) { launched = launch_programmatic(kern, dim3(grid), kThreads, smem, stream, a); };
         if (interleaved)
             W == 8 ? launch(rope_kernel<kInterleaved, 8>) : W == 4 ? launch(rope_kernel<kInterleaved, 4>) : launch(rope_kernel<kInterleaved, 2>);
         else
             W == 8 ? launch(rope_kernel<kHalves, 8>) : W == 4 ? launch(rope_kernel<kHalves, 4>) : launch(rope_kernel<kHalves, 2>);
     }
-    return cudaGetLastError() == cudaSuccess ? BLINK_OK : BLINK_CUDA_ERROR;
+    return launched == cudaSuccess ? BLINK_OK : BLINK_CUDA_ERROR;
 }

@@ -241,3 +241,40 @@ def test_a_single_row_of_a_projection():
     blink.blink_paged_append(odd, v, a, _i32(1).view(1, 1), _i32(0, 1), _i32(5), 1, turns=turns)
     blink.blink_paged_append(k.contiguous(), v.contiguous(), b, _i32(1).view(1, 1), _i32(0, 1), _i32(5), 1, turns=turns)
     assert all(torch.equal(a[n].view(torch.uint8), b[n].view(torch.uint8)) for n in a)
+
+
+def test_calls_behind_one_another_see_what_was_written():
+    """Rotation, append, token attention and few-row prefix-tail attention issued without a pause, each reading what the
+    one before wrote, against the same calls with the device waited for in between."""
+    g = ph.gen(50)
+    S, Hq, Hkv, d, page, P = 2, 8, 2, 64, 16, 700
+    table, total = ph.table_for(g, [P + 64] * S, page)
+    filled = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, filled, table, [P] * S)
+    turns, _ = blink.blink_rope_table(d)
+    n = 30
+    x = [tuple(ph.randn(g, S, H, d).to(torch.bfloat16) for H in (Hq, Hkv, Hkv)) for _ in range(n)]
+    one = _i32(0, 1, 2)
+    starts = [_i32(P + i, P + i) for i in range(n + 1)]
+    ws = [blink.new_workspace(1 << 22, "cuda") for _ in range(3)]
+
+    def steps(wait):
+        cache = {k: v.clone() for k, v in filled.items()}
+        q_buf, k_buf = torch.empty_like(x[0][0]), torch.empty_like(x[0][1])
+        torch.cuda.synchronize()
+        got = []
+        for i, (q, k, v) in enumerate(x):
+            blink.blink_rope(q, k, starts[i], turns, q_out=q_buf, k_out=k_buf)
+            wait()
+            out, lse, _ = blink.blink_paged_prefix_tail_attention(q_buf, cache, table, [P, P + i], k_buf, v, one, 2, 1, req_rows=[0, 1, 2],
+                                                                  want_lse=True, ws=ws[0])
+            wait()
+            blink.blink_paged_append(k, v, cache, table, one, starts[i], 1, turns=turns, ws=ws[1])
+            wait()
+            tok, lse2, _ = blink.blink_paged_token_attention(q_buf.view(S, 1, Hq, d), cache, table, starts[i + 1], P + n, want_lse=True, ws=ws[2])
+            wait()
+            got += [out, lse, tok, lse2]
+        torch.cuda.synchronize()
+        return got
+    slow, fast = steps(torch.cuda.synchronize), steps(lambda: None)
+    assert all(torch.equal(a, b) for a, b in zip(slow, fast))
