@@ -115,18 +115,20 @@ __device__ __noinline__ void write_nearer_codes(uint32_t mask, uint8_t *codes, c
 }
 
 constexpr int kStages = 2;        // heads whose keys and values are in shared memory, one of them in use
+constexpr int kSlots = 2;         // token slots of a thread
 constexpr int kMaxBlockHeads = 8;
 
-// A block owns one page of a sequence and goes over some of its heads; a thread owns 16 values of one of the page's
-// token slots, as two 16-byte pieces (a pair of halves that turn together), of K and of V.  The largest magnitude needs
+// A block owns one page of a sequence and goes over some of its heads; a thread owns 16 values of K and of V in each of two
+// of the page's token slots, as two 16-byte pieces each (a pair of halves that turn together).  The largest magnitude needs
 // all of a page's new tokens before the first code is written: one barrier a head, for K and V together.  Bound by
 // HBM: 2 bytes read and 1 written a value; each thread copies its own pieces of the next heads into its own places
 // in shared memory meanwhile (no registers, no barrier).  The angles belong to the slot, so a thread computes its own
 // once for all heads.
 // Codes are those of the exact rotation: where the 32-bit one is too near the border of two codes to tell (one value of
-// some 10,000), a bit remembers it, and when the block's heads are done those values are computed to 40 bits.
+// some 10,000), a bit remembers it, and when the block's heads are done those values are computed to 40 bits.  (In a page
+// whose keys hold an infinity the 32-bit rotation decides.)
 template <int D, int LAYOUT>
-__global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_constant__ AppendArgs a)
+__global__ void __launch_bounds__(D * 4) append_kernel(const __grid_constant__ AppendArgs a)
 {
     constexpr int kLanes = D / 16;  // threads of a token slot
     extern __shared__ uint4 ring[];
@@ -145,11 +147,19 @@ __global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_con
     if (base >= static_cast<int64_t>(start) + n) return;
     const int id = index < a.table_width ? __ldg(a.table + seq * a.table_stride + index) : -1;
     const int filled = static_cast<int>(max(start - base, static_cast<int64_t>(0)));  // tokens the page holds already
-    const int slot = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-    const int64_t token = base + slot - start;  // among the sequence's new ones
-    const bool fresh = token >= 0 && token < n, kept = slot < filled;
+    const int lane = threadIdx.x % kLanes;
+    int slot[kSlots];
+    int64_t row[kSlots];  // of k and v
+    bool fresh[kSlots];
+#pragma unroll
+    for (int t = 0; t < kSlots; ++t) {
+        slot[t] = threadIdx.x / kLanes + (t << (a.log2_page - 1));
+        const int64_t token = base + slot[t] - start;  // among the sequence's new ones
+        fresh[t] = token >= 0 && token < n;
+        row[t] = c0 + token;
+    }
 
-    // The thread's two pieces of eight values.
+    // The thread's two pieces of eight values of a slot.
     int p0 = lane, p1 = lane + kLanes;
     const int half = a.rot / 2;
     bool turn = LAYOUT != kNoRotation;
@@ -159,19 +169,22 @@ __global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_con
         p1 = p0 + (turn ? a.rot / 16 : (D - a.rot) / 16);
     }
     const int h_begin = blockIdx.y * a.heads_per_block, h_end = min(a.Hkv, h_begin + a.heads_per_block);
-    const uint16_t *k_row = a.k + (c0 + token) * a.k_stride, *v_row = a.v + (c0 + token) * a.v_stride;
     const uint32_t mine = ptx::smem_u32(ring) + threadIdx.x * 16;
-    const uint32_t plane = blockDim.x * 16;  // bytes of one piece of all threads; a stage is four
-    uint16_t *unsure = reinterpret_cast<uint16_t *>(ring + kStages * 4 * blockDim.x) + threadIdx.x;  // a mask per head
-    uint32_t any_unsure = 0;
+    const uint32_t plane = blockDim.x * 16;  // bytes of one piece of all threads; a stage is four for each slot
+    uint16_t *unsure = reinterpret_cast<uint16_t *>(ring + kStages * kSlots * 4 * blockDim.x) + threadIdx.x;  // masks
+    uint32_t any_unsure = 0;                                                          // a bit for each head and slot
     auto copy = [&](int h, int stage) {
-        if (fresh && h < h_end) {
-            const uint16_t *k = k_row + static_cast<int64_t>(h) * D, *v = v_row + static_cast<int64_t>(h) * D;
-            const uint32_t to = mine + stage * 4 * plane;
-            ptx::cp_async16(to, k + p0 * 8);
-            ptx::cp_async16(to + plane, k + p1 * 8);
-            ptx::cp_async16(to + 2 * plane, v + p0 * 8);
-            ptx::cp_async16(to + 3 * plane, v + p1 * 8);
+        if (h < h_end) {
+#pragma unroll
+            for (int t = 0; t < kSlots; ++t) {
+                if (!fresh[t]) continue;
+                const uint16_t *k = a.k + row[t] * a.k_stride + h * D, *v = a.v + row[t] * a.v_stride + h * D;
+                const uint32_t to = mine + (stage * kSlots + t) * 4 * plane;
+                ptx::cp_async16(to, k + p0 * 8);
+                ptx::cp_async16(to + plane, k + p1 * 8);
+                ptx::cp_async16(to + 2 * plane, v + p0 * 8);
+                ptx::cp_async16(to + 3 * plane, v + p1 * 8);
+            }
         }
         ptx::cp_async_commit();
     };
@@ -183,23 +196,27 @@ __global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_con
         return;
     }
 
-    const int32_t pos = !fresh ? 0 : a.pos ? __ldg(a.pos + c0 + token) : static_cast<int32_t>(start + token);
-    uint64_t c[4], minus_s[4];  // of eight pairs
+    int32_t pos[kSlots];
+    uint64_t c[kSlots][4], minus_s[kSlots][4];  // of eight pairs
     auto pair_of = [&](int e) { return LAYOUT == kHalves ? p0 * 8 + e : e < 4 ? p0 * 4 + e : p1 * 4 + e - 4; };
-    if constexpr (LAYOUT == kHalves || LAYOUT == kInterleaved) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = ptx::f32x2(1.f, 1.f), minus_s[e] = 0;
-        if (fresh && turn) {
+    for (int t = 0; t < kSlots; ++t) {
+        pos[t] = !fresh[t] ? 0 : a.pos ? __ldg(a.pos + row[t]) : static_cast<int32_t>(base + slot[t]);
+        if constexpr (LAYOUT == kHalves || LAYOUT == kInterleaved) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float cc[2], ss[2];
+            for (int e = 0; e < 4; ++e) c[t][e] = ptx::f32x2(1.f, 1.f), minus_s[t][e] = 0;
+            if (fresh[t] && turn) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {  // pairs past rot get any angle: they are not turned
-                    const int i = LAYOUT == kHalves ? pair_of(2 * e + b) : min(pair_of(2 * e + b), half - 1);
-                    turn_cos_sin(__ldg(a.turns + i), pos, a.amplitude, cc[b], ss[b]);
+                for (int e = 0; e < 4; ++e) {
+                    float cc[2], ss[2];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {  // pairs past rot get any angle: they are not turned
+                        const int i = LAYOUT == kHalves ? pair_of(2 * e + b) : min(pair_of(2 * e + b), half - 1);
+                        turn_cos_sin(__ldg(a.turns + i), pos[t], a.amplitude, cc[b], ss[b]);
+                    }
+                    c[t][e] = ptx::f32x2(cc[0], cc[1]);
+                    minus_s[t][e] = ptx::f32x2(-ss[0], -ss[1]);
                 }
-                c[e] = ptx::f32x2(cc[0], cc[1]);
-                minus_s[e] = ptx::f32x2(-ss[0], -ss[1]);
             }
         }
     }
@@ -214,78 +231,81 @@ __global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_con
             ev_old = min(static_cast<int>(*reinterpret_cast<volatile uint8_t *>(v_scale)) - kScaleBias, kScaleMax);
         }
         ptx::cp_async_wait<kStages - 1>();
-        const uint4 *own = ring + stage * 4 * blockDim.x + threadIdx.x;
+        const uint4 *own = ring + stage * kSlots * 4 * blockDim.x + threadIdx.x;
         if (++stage == kStages) stage = 0;
+        auto piece = [&](int t, int i) { return own[(t * 4 + i) * blockDim.x]; };
 
-        // The rotated keys as pairs of 32-bit values: x[e] holds values 2 e and 2 e + 1 of the thread's 16.
-        uint64_t x[8];
-        uint32_t mk = 0, mv = 0;
-        const uint16_t *k = k_row + static_cast<int64_t>(h) * D;
-        if (fresh) {
+        // The rotated keys as pairs of 32-bit values: x[t][e] holds values 2 e and 2 e + 1 of the thread's 16 in a slot.
+        uint64_t x[kSlots][8];
+        float m = 0.f;
+        uint32_t w = 0;
+#pragma unroll
+        for (int t = 0; t < kSlots; ++t) {
+            if (!fresh[t]) continue;
             {
-                const uint4 u0 = own[0], u1 = own[blockDim.x];
+                const uint4 u0 = piece(t, 0), u1 = piece(t, 1);
                 const uint32_t u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = ptx::f32x2(bf16_lo(u[e]), bf16_hi(u[e]));
+                for (int e = 0; e < 8; ++e) x[t][e] = ptx::f32x2(bf16_lo(u[e]), bf16_hi(u[e]));
             }
             if constexpr (LAYOUT == kHalves) {
                 if (turn) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint64_t y = x[e], z = x[4 + e];
-                        x[e] = ptx::fma_f32x2(z, minus_s[e], ptx::mul_f32x2(y, c[e]));
-                        x[4 + e] = ptx::fma_f32x2(z, c[e], ptx::mul_f32x2(y, minus_s[e] ^ 0x8000000080000000ull));
+                        const uint64_t y = x[t][e], z = x[t][4 + e];
+                        x[t][e] = ptx::fma_f32x2(z, minus_s[t][e], ptx::mul_f32x2(y, c[t][e]));
+                        x[t][4 + e] = ptx::fma_f32x2(z, c[t][e], ptx::mul_f32x2(y, minus_s[t][e] ^ 0x8000000080000000ull));
                     }
                 }
             } else if constexpr (LAYOUT == kInterleaved) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     float y, z, cc0, cc1, ss0, ss1;
-                    ptx::f32x2_split(x[e], y, z);
-                    ptx::f32x2_split(c[e / 2], cc0, cc1);
-                    ptx::f32x2_split(minus_s[e / 2], ss0, ss1);
+                    ptx::f32x2_split(x[t][e], y, z);
+                    ptx::f32x2_split(c[t][e / 2], cc0, cc1);
+                    ptx::f32x2_split(minus_s[t][e / 2], ss0, ss1);
                     const float cc = e & 1 ? cc1 : cc0, ss = e & 1 ? ss1 : ss0;
-                    if (pair_of(e) < half) x[e] = ptx::f32x2(y * cc + z * ss, z * cc - y * ss);  // others stay, whatever they hold
+                    if (pair_of(e) < half) x[t][e] = ptx::f32x2(y * cc + z * ss, z * cc - y * ss);  // others stay, whatever they hold
                 }
             } else if constexpr (LAYOUT == kHalvesByElement) {
+                const uint16_t *k = a.k + row[t] * a.k_stride + h * D;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int j = (e < 8 ? p0 : p1) * 8 + (e & 7), i = j < half ? j : j - half;
                     if (j < a.rot) {
                         float cc, ss, lo, hi;
-                        turn_cos_sin(__ldg(a.turns + i), pos, a.amplitude, cc, ss);
+                        turn_cos_sin(__ldg(a.turns + i), pos[t], a.amplitude, cc, ss);
                         const float y = bf16_lo(k[i]), z = bf16_lo(k[i + half]), r = j < half ? y * cc - z * ss : y * ss + z * cc;
-                        ptx::f32x2_split(x[e / 2], lo, hi);
-                        x[e / 2] = e & 1 ? ptx::f32x2(lo, r) : ptx::f32x2(r, hi);
+                        ptx::f32x2_split(x[t][e / 2], lo, hi);
+                        x[t][e / 2] = e & 1 ? ptx::f32x2(lo, r) : ptx::f32x2(r, hi);
                     }
                 }
             }
-            float m = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float lo, hi;
-                ptx::f32x2_split(x[e], lo, hi);
+                ptx::f32x2_split(x[t][e], lo, hi);
                 m = ptx::max3(m, fabsf(lo), fabsf(hi));  // a NaN counts as nothing
             }
-            mk = __float_as_uint(m);
-            const uint4 w0 = own[2 * blockDim.x], w1 = own[3 * blockDim.x];
+            const uint4 w0 = piece(t, 2), w1 = piece(t, 3);
             const uint32_t v[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-            uint32_t w = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) w = max_bf16x2(w, v[e] & 0x7FFF7FFFu);
-            mv = max(w << 16, w & 0xFFFF0000u);
         }
+        uint32_t mk = __float_as_uint(m), mv = max(w << 16, w & 0xFFFF0000u);
         block_max(mk, mv, part[flip]);
         flip ^= 1;
-        const bool infinite = mk == 0x7F800000u || mv == 0x7F800000u;
-        if (infinite) {  // the scale is that of the finite values; infinities take the largest code
+        const bool infinite_key = mk == 0x7F800000u;
+        if (infinite_key || mv == 0x7F800000u) {  // the scale is that of the finite values; infinities take the largest code
             mk = mv = 0;
-            if (fresh) {
+#pragma unroll
+            for (int t = 0; t < kSlots; ++t) {
+                if (!fresh[t]) continue;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const uint32_t b = static_cast<uint32_t>(x[e / 2] >> 32 * (e & 1)) & 0x7FFFFFFFu;
-                    const uint32_t y = (reinterpret_cast<const uint32_t *>(own + (2 + e / 8) * blockDim.x)[e / 2 & 3] << (e & 1 ? 0 : 16)) &
-                                       0x7FFF0000u;
+                    const uint32_t b = static_cast<uint32_t>(x[t][e / 2] >> 32 * (e & 1)) & 0x7FFFFFFFu;
+                    const uint4 q = piece(t, 2 + e / 8);
+                    const uint32_t y = (reinterpret_cast<const uint32_t *>(&q)[e / 2 & 3] << (e & 1 ? 0 : 16)) & 0x7FFF0000u;
                     mk = b < 0x7F800000u ? max(mk, b) : mk;
                     mv = y < 0x7F800000u ? max(mv, y) : mv;
                 }
@@ -295,86 +315,86 @@ __global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_con
         }
         int ek = scale_exponent(__uint_as_float(mk)), ev = scale_exponent(__uint_as_float(mv));
         if (filled > 0) ek = max(ek, ek_old), ev = max(ev, ev_old);
-        const int64_t at = id * a.page_stride + (((static_cast<int64_t>(h) << a.log2_page) + slot) * D);
-        uint2 *kc = reinterpret_cast<uint2 *>(a.kc + at), *vc = reinterpret_cast<uint2 *>(a.vc + at);
-        if (fresh) {
-            {
-                const uint64_t f = ptx::f32x2(scale_of(-ev), scale_of(-ev));
-                const uint4 w0 = own[2 * blockDim.x], w1 = own[3 * blockDim.x];
-                const uint32_t v[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-                uint32_t w[4];
+        const int64_t head = id * a.page_stride + ((static_cast<int64_t>(h) << a.log2_page) * D);
+        const float fk = scale_of(-ek), fv = scale_of(-ev);
+        const uint64_t fk2 = ptx::f32x2(fk, fk), fv2 = ptx::f32x2(fv, fv);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = f32x4_to_e4m3x4(ptx::mul_f32x2(ptx::f32x2(bf16_lo(v[2 * i]), bf16_hi(v[2 * i])), f),
-                                           ptx::mul_f32x2(ptx::f32x2(bf16_lo(v[2 * i + 1]), bf16_hi(v[2 * i + 1])), f));
-                vc[p0] = make_uint2(w[0], w[1]);
-                vc[p1] = make_uint2(w[2], w[3]);
-            }
-            const float fk = scale_of(-ek);
-            const uint64_t f = ptx::f32x2(fk, fk);
+        for (int t = 0; t < kSlots; ++t) {
+            uint2 *kc = reinterpret_cast<uint2 *>(a.kc + head + slot[t] * D), *vc = reinterpret_cast<uint2 *>(a.vc + head + slot[t] * D);
+            if (fresh[t]) {
+                uint32_t q[4];
+                {
+                    const uint4 w0 = piece(t, 2), w1 = piece(t, 3);
+                    const uint32_t v[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = ptx::mul_f32x2(x[e], f);
-            uint32_t w[4];
-            if (LAYOUT == kNoRotation || infinite) {
+                    for (int i = 0; i < 4; ++i)
+                        q[i] = f32x4_to_e4m3x4(ptx::mul_f32x2(ptx::f32x2(bf16_lo(v[2 * i]), bf16_hi(v[2 * i])), fv2),
+                                               ptx::mul_f32x2(ptx::f32x2(bf16_lo(v[2 * i + 1]), bf16_hi(v[2 * i + 1])), fv2));
+                    vc[p0] = make_uint2(q[0], q[1]);
+                    vc[p1] = make_uint2(q[2], q[3]);
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = f32x4_to_e4m3x4(x[2 * i], x[2 * i + 1]);
-                kc[p0] = make_uint2(w[0], w[1]);
-                kc[p1] = make_uint2(w[2], w[3]);
-            } else {
-                // Codes of the least and the most that each exact value can be.
-                const float error = turn ? kTurnError : 0.f;
-                const uint64_t more = ptx::f32x2(error, error), less = ptx::f32x2(-error, -error);
-                uint32_t differ[4];
+                for (int e = 0; e < 8; ++e) x[t][e] = ptx::mul_f32x2(x[t][e], fk2);
+                if (LAYOUT == kNoRotation || infinite_key) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint64_t l[2], u[2];
+                    for (int i = 0; i < 4; ++i) q[i] = f32x4_to_e4m3x4(x[t][2 * i], x[t][2 * i + 1]);
+                    kc[p0] = make_uint2(q[0], q[1]);
+                    kc[p1] = make_uint2(q[2], q[3]);
+                } else {
+                    // Codes of the least and the most that each exact value can be.
+                    const float error = turn ? kTurnError : 0.f;
+                    const uint64_t more = ptx::f32x2(error, error), less = ptx::f32x2(-error, -error);
+                    uint64_t size[8];  // what the error is relative to, for values 2 e and 2 e + 1
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int e = 2 * i + q;
-                        uint64_t size;  // what the error is relative to, for values 2 e and 2 e + 1
+                    for (int e = 0; e < 8; ++e) {
                         float y0, y1, z0, z1;
-                        ptx::f32x2_split(x[e], y0, y1);
+                        ptx::f32x2_split(x[t][e], y0, y1);
                         if constexpr (LAYOUT == kHalves) {
-                            ptx::f32x2_split(x[e ^ 4], z0, z1);
-                            size = ptx::f32x2(fabsf(y0) + fabsf(z0), fabsf(y1) + fabsf(z1));
+                            ptx::f32x2_split(x[t][e ^ 4], z0, z1);
+                            size[e] = e < 4 ? ptx::f32x2(fabsf(y0) + fabsf(z0), fabsf(y1) + fabsf(z1)) : size[e & 3];
                         } else if constexpr (LAYOUT == kInterleaved) {
-                            const float t = pair_of(e) < half ? fabsf(y0) + fabsf(y1) : 0.f;
-                            size = ptx::f32x2(t, t);
+                            const float b = pair_of(e) < half ? fabsf(y0) + fabsf(y1) : 0.f;
+                            size[e] = ptx::f32x2(b, b);
                         } else {
-                            float t[2];
+                            const uint16_t *k = a.k + row[t] * a.k_stride + h * D;
+                            float r[2];
 #pragma unroll
                             for (int b = 0; b < 2; ++b) {
-                                const int j = (i < 2 ? p0 : p1) * 8 + (2 * e & 7) + b, n = j < half ? j : j - half;
-                                t[b] = j < a.rot ? fabsf(a.amplitude) * (fabsf(bf16_lo(k[n])) + fabsf(bf16_lo(k[n + half]))) * fk : 0.f;
+                                const int j = (e < 4 ? p0 : p1) * 8 + (2 * e & 7) + b, i = j < half ? j : j - half;
+                                r[b] = j < a.rot ? fabsf(a.amplitude) * (fabsf(bf16_lo(k[i])) + fabsf(bf16_lo(k[i + half]))) * fk : 0.f;
                             }
-                            size = ptx::f32x2(t[0], t[1]);
+                            size[e] = ptx::f32x2(r[0], r[1]);
                         }
-                        l[q] = ptx::fma_f32x2(size, less, x[e]);
-                        u[q] = ptx::fma_f32x2(size, more, x[e]);
                     }
-                    w[i] = f32x4_to_e4m3x4(l[0], l[1]);
-                    differ[i] = w[i] ^ f32x4_to_e4m3x4(u[0], u[1]);
-                }
-                kc[p0] = make_uint2(w[0], w[1]);
-                kc[p1] = make_uint2(w[2], w[3]);
-                if (differ[0] | differ[1] | differ[2] | differ[3]) {
-                    uint32_t mask = 0;
+                    uint32_t differ[4];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) mask |= (differ[e / 4] >> 8 * (e & 3) & 0xFFu) ? 1u << e : 0u;
-                    any_unsure |= 1u << (h - h_begin);
-                    unsure[(h - h_begin) * blockDim.x] = static_cast<uint16_t>(mask);
+                    for (int i = 0; i < 4; ++i) {
+                        q[i] = f32x4_to_e4m3x4(ptx::fma_f32x2(size[2 * i], less, x[t][2 * i]), ptx::fma_f32x2(size[2 * i + 1], less, x[t][2 * i + 1]));
+                        differ[i] = q[i] ^ f32x4_to_e4m3x4(ptx::fma_f32x2(size[2 * i], more, x[t][2 * i]),
+                                                           ptx::fma_f32x2(size[2 * i + 1], more, x[t][2 * i + 1]));
+                    }
+                    kc[p0] = make_uint2(q[0], q[1]);
+                    kc[p1] = make_uint2(q[2], q[3]);
+                    if (differ[0] | differ[1] | differ[2] | differ[3]) {
+                        uint32_t mask = 0;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) mask |= (differ[e / 4] >> 8 * (e & 3) & 0xFFu) ? 1u << e : 0u;
+                        const int which = (h - h_begin) * kSlots + t;
+                        any_unsure |= 1u << which;
+                        unsure[which * blockDim.x] = static_cast<uint16_t>(mask);
+                    }
                 }
-            }
-        } else if (kept) {
-            if (ek > ek_old) {
-                const float f = scale_of(ek_old - ek);
-                kc[p0] = requantised(kc[p0], f);
-                kc[p1] = requantised(kc[p1], f);
-            }
-            if (ev > ev_old) {
-                const float f = scale_of(ev_old - ev);
-                vc[p0] = requantised(vc[p0], f);
-                vc[p1] = requantised(vc[p1], f);
+            } else if (slot[t] < filled) {
+                if (ek > ek_old) {
+                    const float f = scale_of(ek_old - ek);
+                    kc[p0] = requantised(kc[p0], f);
+                    kc[p1] = requantised(kc[p1], f);
+                }
+                if (ev > ev_old) {
+                    const float f = scale_of(ev_old - ev);
+                    vc[p0] = requantised(vc[p0], f);
+                    vc[p1] = requantised(vc[p1], f);
+                }
             }
         }
         if (threadIdx.x == 0) {
@@ -386,11 +406,13 @@ __global__ void __launch_bounds__(D * 8, 128 / D) append_kernel(const __grid_con
     if constexpr (LAYOUT != kNoRotation) {
         if (!__syncthreads_or(static_cast<int>(any_unsure))) return;
         for (; any_unsure; any_unsure &= any_unsure - 1) {
-            const int n_head = __ffs(any_unsure) - 1, h = h_begin + n_head;
+            const int which = __ffs(any_unsure) - 1, n_head = which / kSlots, h = h_begin + n_head;
+            const bool second = which % kSlots;
             write_nearer_codes<LAYOUT == kInterleaved>(
-                unsure[n_head * blockDim.x], a.kc + id * a.page_stride + (((static_cast<int64_t>(h) << a.log2_page) + slot) * D),
-                k_row + static_cast<int64_t>(h) * D, p0 * 8, p1 * 8, half, a.turns, pos,
-                a.amplitude * scale_of(-k_exponents[n_head]));
+                unsure[which * blockDim.x],
+                a.kc + id * a.page_stride + (((static_cast<int64_t>(h) << a.log2_page) + (second ? slot[1] : slot[0])) * D),
+                a.k + (second ? row[1] : row[0]) * a.k_stride + static_cast<int64_t>(h) * D, p0 * 8, p1 * 8, half, a.turns,
+                second ? pos[1] : pos[0], a.amplitude * scale_of(-k_exponents[n_head]));
         }
     }
 }
@@ -554,9 +576,9 @@ extern "C" blink_status blink_paged_append(const blink_bf16 *k, int64_t k_stride
     if (a.heads_per_block > kMaxBlockHeads) a.heads_per_block = kMaxBlockHeads;
     const dim3 grid(static_cast<unsigned>(pages), static_cast<unsigned>((Hkv + a.heads_per_block - 1) / a.heads_per_block),
                     static_cast<unsigned>(S));
-    const unsigned threads = static_cast<unsigned>(page_tokens * (d / 16));
+    const unsigned threads = static_cast<unsigned>(page_tokens * (d / 16) / kSlots);
     const int layout = rot == 0 ? kNoRotation : interleaved ? kInterleaved : rot % 16 == 0 ? kHalves : kHalvesByElement;
-    const int smem = static_cast<int>(threads) * (64 * kStages + 2 * a.heads_per_block);
+    const int smem = static_cast<int>(threads) * kSlots * (64 * kStages + 2 * a.heads_per_block);
     bool set = true;
     auto launch = [&](auto kern) {
         set = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d * 8 * (64 * kStages + 2 * kMaxBlockHeads)) == cudaSuccess;
