@@ -632,9 +632,9 @@ struct TokenPlan {
     size_t lse, o, total;  // offsets of the partial results in the workspace
 };
 
-// Keys of a block: the keys of all (sequence, head, tile) units are cut into about as many chunks as blocks run at a
-// time, or twice, three times as many where that would be more than the lanes can hold pages for; a chunk is whole
-// rounds of the block's warps.
+// Keys of a block: every (sequence, head, tile) unit is cut into as many chunks as let whole waves of blocks hold all of
+// them, one wave if a chunk is then no longer than the lanes can hold pages for; a chunk is whole rounds of the block's
+// warps.  (320 blocks where 304 run at a time: 39 us instead of 30 for 16 tail rows against 18432 keys.)
 // T: the most rows of a sequence; `tokens` of them in all; `joined`: partial results also of a single chunk.
 TokenPlan token_plan(int64_t S, int64_t T, int64_t tokens, int64_t max_len, int64_t Hkv, int64_t g, int d, bool joined)
 {
@@ -644,8 +644,10 @@ TokenPlan token_plan(int64_t S, int64_t T, int64_t tokens, int64_t max_len, int6
     const int64_t units = S * Hkv * p.tiles;
     const int64_t at_once = static_cast<int64_t>(current_sm_count() > 0 ? current_sm_count() : 1) *
                             (p.wide == 1 ? Shape<128, 1>::kResident : Shape<128, 2>::kResident);
-    const int64_t waves = max_len * units / (at_once * kMaxChunk) + 1;
-    int64_t chunk = (max_len * units + at_once * waves - 1) / (at_once * waves);
+    const int64_t least = (max_len + kMaxChunk - 1) / kMaxChunk;  // chunks of a unit
+    const int64_t waves = (least * units + at_once - 1) / at_once;
+    const int64_t fit = waves * at_once / units;
+    int64_t chunk = fit > 0 ? (max_len + fit - 1) / fit : 0;
     chunk = (chunk + kRound - 1) / kRound * kRound;
     if (chunk > kMaxChunk) chunk = kMaxChunk;
     if (chunk < kRound) chunk = kRound;
