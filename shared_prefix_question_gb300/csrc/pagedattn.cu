@@ -644,7 +644,11 @@ TokenPlan token_plan(int64_t S, int64_t T, int64_t tokens, int64_t max_len, int6
     const int64_t units = S * Hkv * p.tiles;
     const int64_t at_once = static_cast<int64_t>(current_sm_count() > 0 ? current_sm_count() : 1) *
                             (p.wide == 1 ? Shape<128, 1>::kResident : Shape<128, 2>::kResident);
-    const int64_t least = (max_len + kMaxChunk - 1) / kMaxChunk;  // chunks of a unit
+    int64_t least = (max_len + kMaxChunk - 1) / kMaxChunk;  // chunks of a unit
+    // Several sequences differ in length, and blocks without keys leave the last wave uneven: shorter chunks where there are few
+    // waves (8 sequences of up to 18432 tokens: 34 us, 39 otherwise; 16: 52, 57; 64, with ten waves: the same).  Blocks of two
+    // tiles cost more each, and lose (16 sequences of four tokens: 76 us, 65 with the longer chunks).
+    if (S > 1 && p.wide == 1 && least * units < 4 * at_once) least *= 2;
     const int64_t waves = (least * units + at_once - 1) / at_once;
     const int64_t fit = waves * at_once / units;
     int64_t chunk = fit > 0 ? (max_len + fit - 1) / fit : 0;
