@@ -30,7 +30,7 @@ constexpr int kRound = kStep * kWarps;           // keys of a block per step of 
 constexpr int kMaxChunk = 32 * kRound;           // a lane holds the page of one step of its warp
 // (Row, query head) rows of a kv head, in any request, up to which tail rows read the pages: every 16 of them read and convert
 // all codes again, while bf16 rows are written once and shared by 128.  18432 keys, one request of 16 tokens and 32/8 heads
-// (64 rows): 30 us from the pages, 43 by way of bf16 rows; of 32 tokens 62 and 44; 2048 keys: 12 and 19, 18 and 19.
+// (64 rows): 29 us from the pages, 43 by way of bf16 rows; of 32 tokens 62 and 44; 2048 keys: 12 and 19, 18 and 19.
 constexpr int kFewRows = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e37f;                 // below any score
@@ -97,9 +97,11 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v)  // of an 8 x 8 matri
 template <int D, int NT>
 struct Shape {
     // Blocks of an SM, and steps of a warp in shared memory (one of them in use): fewer warps with more bytes in flight
-    // each (4 blocks and 3 steps: 195 us instead of 186 on 64 sequences of up to 18432 tokens), without spills.
-    static constexpr int kResident = NT == 1 ? 3 : 2;
-    static constexpr int kDepth = NT == 1 ? 4 : 6;
+    // each.  (One tile: four blocks with three steps spill, and take 195 us instead of 186 on 64 sequences of up to 18432
+    // tokens.  Two tiles: two blocks with six steps take 235 us instead of 212 on 8 sequences of up to 131072 with four
+    // tokens each; three cost six registers spilled.)
+    static constexpr int kResident = 3;
+    static constexpr int kDepth = 4;
     static constexpr int kRows = 8 * NT;
     static constexpr int kPieces = D / 64;                 // 16-byte pieces of a key for one lane
     static constexpr int kCols = D / 8;                    // consecutive channels of a lane in the second product
@@ -624,9 +626,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) token_join_kernel(const __gri
 }
 
 struct TokenPlan {
-    // Column tiles of a block.  Two where a head's rows need them: the codes are converted once for both (16 sequences
-    // of four tokens and 32/8 heads 65 us, with two blocks of one tile 75).  Two warps with a tile each over the same ring,
-    // which convert twice, took 89.
+    // Column tiles of a block.  Two where a head's rows need them: the codes are converted once for both (8 sequences of up
+    // to 131072 with four tokens each, 32/8 heads: 212 us, with two blocks of one tile 264).  Two warps with a tile each over
+    // the same ring, which convert twice, took 271.
     int wide;
     int tiles, chunk, chunks;
     size_t lse, o, total;  // offsets of the partial results in the workspace
@@ -634,7 +636,7 @@ struct TokenPlan {
 
 // Keys of a block: every (sequence, head, tile) unit is cut into as many chunks as let whole waves of blocks hold all of
 // them, one wave if a chunk is then no longer than the lanes can hold pages for; a chunk is whole rounds of the block's
-// warps.  (320 blocks where 304 run at a time: 39 us instead of 30 for 16 tail rows against 18432 keys.)
+// warps.  (320 blocks where 304 ran at a time: 39 us instead of 30 for 16 tail rows against 18432 keys.)
 // T: the most rows of a sequence; `tokens` of them in all; `joined`: partial results also of a single chunk.
 TokenPlan token_plan(int64_t S, int64_t T, int64_t tokens, int64_t max_len, int64_t Hkv, int64_t g, int d, bool joined)
 {
@@ -642,13 +644,12 @@ TokenPlan token_plan(int64_t S, int64_t T, int64_t tokens, int64_t max_len, int6
     p.wide = T * g > 8 ? 2 : 1;
     p.tiles = static_cast<int>((T * g + 8 * p.wide - 1) / (8 * p.wide));
     const int64_t units = S * Hkv * p.tiles;
-    const int64_t at_once = static_cast<int64_t>(current_sm_count() > 0 ? current_sm_count() : 1) *
-                            (p.wide == 1 ? Shape<128, 1>::kResident : Shape<128, 2>::kResident);
+    const int64_t at_once = static_cast<int64_t>(current_sm_count() > 0 ? current_sm_count() : 1) * Shape<128, 1>::kResident;
     int64_t least = (max_len + kMaxChunk - 1) / kMaxChunk;  // chunks of a unit
     // Several sequences differ in length, and blocks without keys leave the last wave uneven: shorter chunks where there are few
-    // waves (8 sequences of up to 18432 tokens: 34 us, 39 otherwise; 16: 52, 57; 64, with ten waves: the same).  Blocks of two
-    // tiles cost more each, and lose (16 sequences of four tokens: 76 us, 65 with the longer chunks).
-    if (S > 1 && p.wide == 1 && least * units < 4 * at_once) least *= 2;
+    // waves (8 sequences of up to 18432 tokens: 34 us, 39 otherwise; 16: 52, 57; 16 of four tokens each: 66, 69; 64, with
+    // ten waves: the same).
+    if (S > 1 && least * units < 4 * at_once) least *= 2;
     const int64_t waves = (least * units + at_once - 1) / at_once;
     const int64_t fit = waves * at_once / units;
     int64_t chunk = fit > 0 ? (max_len + fit - 1) / fit : 0;
