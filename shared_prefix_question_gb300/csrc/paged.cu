@@ -605,7 +605,7 @@ extern "C" size_t blink_paged_prefix_tail_workspace(const int32_t *h_req_rows, c
     if (!h_req_rows || n_req < 1 || n_req > kMaxRequests || Hkv < 1 || d < 1 ||
         check_requests(h_req_rows, h_prefix_len, n_req, h_req_rows[n_req]) != BLINK_OK)
         return kHeaderBytes;
-    if (Hq >= Hkv && few_tail_rows(h_req_rows, h_prefix_len, n_req, Hq / Hkv))
+    if (Hq >= Hkv && few_tail_rows(h_req_rows, n_req, Hq / Hkv))
         return few_tail_workspace(h_req_rows, h_prefix_len, n_req, Hkv, Hq / Hkv, d);
     return tail_layout(h_prefix_len, n_req, h_req_rows[n_req], B, Hq, Hkv, d).total;
 }
@@ -637,7 +637,7 @@ extern "C" blink_status blink_paged_prefix_tail_attention(
         if (h_prefix_len[r] > static_cast<int64_t>(table_width) * page_tokens) return BLINK_OUT_OF_RANGE;
         longest = h_prefix_len[r] > longest ? h_prefix_len[r] : longest;
     }
-    if (few_tail_rows(h_req_rows, h_prefix_len, n_req, Hq / Hkv)) {
+    if (few_tail_rows(h_req_rows, n_req, Hq / Hkv)) {
         if (static_cast<int64_t>(rows) * Hq > 0x7FFFFFFF) return BLINK_OUT_OF_RANGE;
         if (ws_bytes < few_tail_workspace(h_req_rows, h_prefix_len, n_req, Hkv, Hq / Hkv, d)) return BLINK_WORKSPACE_TOO_SMALL;
         return few_tail_attention(a.c, page_tokens, q, d_page_table, table_stride, table_width, k_tail, v_tail, d_cu_seqlens,

@@ -30,7 +30,7 @@ constexpr int kMaxPagedRequests = 64;
 
 // Prefix-tail attention of few rows, read from the pages as they are (pagedattn.cu).  few_tail_rows: whether a call is of
 // that kind; arguments as blink_paged_prefix_tail_attention has checked them.
-bool few_tail_rows(const int32_t *h_req_rows, const int32_t *h_len, int n_req, int g);
+bool few_tail_rows(const int32_t *h_req_rows, int n_req, int g);
 size_t few_tail_workspace(const int32_t *h_req_rows, const int32_t *h_len, int n_req, int Hkv, int g, int d);
 blink_status few_tail_attention(const PagedCache &c, int page_tokens, const uint16_t *q, const int32_t *d_page_table,
                                 int64_t table_stride, int table_width, const uint16_t *k_tail, const uint16_t *v_tail,

@@ -730,10 +730,11 @@ TailSizes tail_sizes(const int32_t *h_req_rows, const int32_t *h_len, int n_req)
 
 }  // namespace
 
-bool few_tail_rows(const int32_t *h_req_rows, const int32_t *h_len, int n_req, int g)
+bool few_tail_rows(const int32_t *h_req_rows, int n_req, int g)
 {
-    (void)h_len;
-    return static_cast<int64_t>(tail_sizes(h_req_rows, h_len, n_req).most) * g <= kFewRows;
+    int64_t most = 0;
+    for (int r = 0; r < n_req; ++r) most = h_req_rows[r + 1] - h_req_rows[r] > most ? h_req_rows[r + 1] - h_req_rows[r] : most;
+    return most * g <= kFewRows;
 }
 
 size_t few_tail_workspace(const int32_t *h_req_rows, const int32_t *h_len, int n_req, int Hkv, int g, int d)
