@@ -278,3 +278,51 @@ def test_calls_behind_one_another_see_what_was_written():
         return got
     slow, fast = steps(torch.cuda.synchronize), steps(lambda: None)
     assert all(torch.equal(a, b) for a, b in zip(slow, fast))
+
+
+def test_captured_behind_copies_and_other_streams():
+    """Calls captured right behind a copy, a fill, and work of another stream that is waited for: they see its results."""
+    g = ph.gen(51)
+    S, Hq, Hkv, d, page, P = 2, 8, 2, 64, 16, 3000
+    table, total = ph.table_for(g, [P + 8] * S, page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, table, [P] * S)
+    turns, _ = blink.blink_rope_table(d)
+    new = [ph.randn(g, S, H, d).to(torch.bfloat16) for H in (Hq, Hkv, Hkv)]
+    q, k, v = (torch.zeros_like(x) for x in new)
+    qr, kr = torch.empty_like(q), torch.empty_like(k)
+    pos, length = _i32(0, 0), _i32(0, 0)
+    one = _i32(0, 1, 2)
+    ws = [blink.new_workspace(1 << 22, "cuda") for _ in range(3)]
+    out, tok = torch.empty_like(q), torch.empty(S, 1, Hq, d, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+
+    def work():
+        main = torch.cuda.current_stream()
+        pos.fill_(P)
+        for a, b in zip((q, k, v), new):
+            a.copy_(b)                                   # copies
+        blink.blink_rope(q, k, pos, turns, q_out=qr, k_out=kr)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            length.copy_(pos)
+            length.add_(1)
+        blink.blink_paged_append(k, v, cache, table, one, pos, 1, turns=turns, ws=ws[0])
+        main.wait_stream(side)                           # two grids, of two streams, before the next call
+        blink.blink_paged_token_attention(qr.view(S, 1, Hq, d), cache, table, length, P + 8, out=tok, ws=ws[1])
+        out.zero_()
+        blink.blink_paged_prefix_tail_attention(qr, cache, table, [P, P], kr, v, one, 2, 1, req_rows=[0, 1, 2], out=out, ws=ws[2])
+    work()
+    torch.cuda.synchronize()
+    want = (out.clone(), tok.clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for _ in range(20):
+        for x in (q, k, v, qr, kr, pos, length, out, tok):
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(tok, want[1])
+    ph.check_attention(tok, blink.blink_paged_token_attention(qr.view(S, 1, Hq, d), cache, table, length, P + 8, want_lse=True)[1],
+                       ph.token_reference(qr.view(S, 1, Hq, d), cache, table, [P + 1] * S))
