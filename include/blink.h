@@ -530,7 +530,8 @@ blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const blink_bf16 
  *                   each, page_stride bytes apart (>= Hkv * page_tokens * d, a multiple of 16; 16-byte
  *                   aligned), d in {64, 128}, Hkv 1..BLINK_MAX_PAGED_HEADS
  * k_scale, v_scale  [Hkv] e8m0 scales each (a byte b stands for 2^(b - 127)), scale_stride bytes apart:
- *                   a value is its code times the scale of its page and head
+ *                   a value is its code times the scale of its page and head.  e is read as the nearest in
+ *                   BLINK_PAGED_SCALE_MIN..MAX, which the calls write (a page of zeros is zeros)
  * d_page_table      int32, sequence s's pages at d_page_table + s * table_stride, table_width of them:
  *                   token p lies in slot p % page_tokens of page p / page_tokens
  *

@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(D * 4) append_kernel(const __grid_constant__ A
         uint8_t *k_scale = a.ks + id * a.scale_stride + h, *v_scale = a.vs + id * a.scale_stride + h;
         int ek_old = kScaleMin, ev_old = kScaleMin;
         if (filled > 0) {
-            ek_old = min(static_cast<int>(*reinterpret_cast<volatile uint8_t *>(k_scale)) - kScaleBias, kScaleMax);
-            ev_old = min(static_cast<int>(*reinterpret_cast<volatile uint8_t *>(v_scale)) - kScaleBias, kScaleMax);
+            ek_old = exponent_of(*reinterpret_cast<volatile uint8_t *>(k_scale));
+            ev_old = exponent_of(*reinterpret_cast<volatile uint8_t *>(v_scale));
         }
         ptx::cp_async_wait<kStages - 1>();
         const uint4 *own = ring + stage * kSlots * 4 * blockDim.x + threadIdx.x;
@@ -461,8 +461,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
                                ((static_cast<int64_t>(h) << a.c.log2_page) + (token & ((1 << a.c.log2_page) - 1))) * D + piece * 16;
             k = __ldg(reinterpret_cast<const uint4 *>(a.c.k + at));
             v = __ldg(reinterpret_cast<const uint4 *>(a.c.v + at));
-            fk = scale_of(static_cast<int>(__ldg(a.c.k_scale + id * a.c.scale_stride + h)) - kScaleBias);
-            fv = scale_of(static_cast<int>(__ldg(a.c.v_scale + id * a.c.scale_stride + h)) - kScaleBias);
+            fk = scale_of(exponent_of(__ldg(a.c.k_scale + id * a.c.scale_stride + h)));
+            fv = scale_of(exponent_of(__ldg(a.c.v_scale + id * a.c.scale_stride + h)));
         }
     }
     auto put = [&](const uint4 &codes, float f, uint16_t *dst) {

@@ -41,6 +41,12 @@ blink_status few_tail_attention(const PagedCache &c, int page_tokens, const uint
 #ifdef __CUDACC__
 
 __device__ __forceinline__ float scale_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + kScaleBias) << 23); }
+// A scale's exponent as it is read: one outside the range (a page that was never written has 0) is the nearest in it, so
+// that no difference of two exponents leaves those of a float.
+__device__ __forceinline__ int exponent_of(uint8_t scale)
+{
+    return min(max(static_cast<int>(scale) - kScaleBias, kScaleMin), kScaleMax);
+}
 
 // Two e4m3 codes (the lower byte first) as two fp16 values, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)

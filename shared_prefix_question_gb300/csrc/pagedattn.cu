@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
         if (lane < mine) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
         page = -1;  // past the end, or not a page: its keys are masked
     } else {
-        scales = static_cast<int>(__ldg(a.c.k_scale + page * a.c.scale_stride + h)) |
-                 static_cast<int>(__ldg(a.c.v_scale + page * a.c.scale_stride + h)) << 8;
+        scales = (exponent_of(__ldg(a.c.k_scale + page * a.c.scale_stride + h)) + kScaleBias) |
+                 (exponent_of(__ldg(a.c.v_scale + page * a.c.scale_stride + h)) + kScaleBias) << 8;
     }
     uint8_t *ring = smem + warp * kDepth * Sh::kStage;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Sh::kBars) + warp * kDepth;

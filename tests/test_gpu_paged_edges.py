@@ -326,3 +326,84 @@ def test_captured_behind_copies_and_other_streams():
         assert torch.equal(out, want[0]) and torch.equal(tok, want[1])
     ph.check_attention(tok, blink.blink_paged_token_attention(qr.view(S, 1, Hq, d), cache, table, length, P + 8, want_lse=True)[1],
                        ph.token_reference(qr.view(S, 1, Hq, d), cache, table, [P + 1] * S))
+
+
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 16)])
+def test_pages_never_written_are_zeros(d, page):
+    """Lengths that take in pages that nothing was written to: a cache's zeros, with scales of byte 0, between pages whose
+    values are large.  Such keys score 0 and add zeros."""
+    g = ph.gen(52)
+    lens, Hq, Hkv = [900, 77, 2500], 8, 2
+    table, total = ph.table_for(g, lens, page)
+    cache = blink.blink_paged_cache(total, page, Hkv, d)
+    written = [list(range(0, -(-n // page), 2 + s)) for s, n in enumerate(lens)]  # every second, third, fourth page
+    for s, n in enumerate(lens):
+        for i in written[s]:
+            k, v = (0.3 * ph.randn(g, page, Hkv, d).to(torch.bfloat16) for _ in range(2))
+            v = v * 2.0 ** (3 * (i % 5) - 2)
+            blink.blink_paged_append(k, v, cache, table[s:s + 1, i:i + 1], _i32(0, page), _i32(0), page)
+    q = ph.randn(g, 3, 4, Hq, d).to(torch.bfloat16)
+    out, lse, ws = blink.blink_paged_token_attention(q, cache, table, _i32(*lens), max(lens), want_lse=True)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+    ph.check_attention(out, lse, ph.token_reference(q, cache, table, lens))
+    pre = [[ph.values(cache, n, table[s], lens[s]) for n in ("k", "v")] for s in range(3)]
+    for r in (1, 90):  # rows of a request: from the pages, and by way of bf16 rows
+        rows = 3 * r
+        qt, kt, vt = (ph.randn(g, rows, H, d).to(torch.bfloat16) for H in (Hq, Hkv, Hkv))
+        got, got_lse, ws = blink.blink_paged_prefix_tail_attention(qt, cache, table, lens, kt, vt, _i32(0, r, 2 * r, rows), 3, r,
+                                                                   req_rows=[0, r, 2 * r, rows], want_lse=True)
+        assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+        ref = []
+        for i in range(rows):
+            s = i // r
+            k, v = (torch.cat([x, y[s * r:i + 1].double().transpose(0, 1)], dim=1) for x, y in zip(pre[s], (kt, vt)))
+            ref.append(ph.attend(qt[i], k, v, 1 / math.sqrt(d)))
+        o, l, mag, size = zip(*ref)
+        o, l = torch.stack(o)[:, None], torch.stack(l, dim=1)
+        if r == 1:
+            ph.check_attention(got[:, None], got_lse, (o, l, torch.stack(mag, dim=1)[:, :, None], torch.stack(size, dim=1)))
+        else:  # the attention's own tolerances
+            assert float((got.double() - o[:, 0]).abs().max()) <= 2e-2 * float(o.abs().max())
+            assert float((got_lse.double() - l).abs().max()) <= 2e-3 * max(1.0, float(l.abs().max()))
+
+
+def test_scales_outside_the_range_are_read_as_the_nearest():
+    g = ph.gen(53)
+    P, Hq, Hkv, d, page = 500, 4, 2, 64, 32
+    table, total = ph.table_for(g, [P], page)
+    one = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, one, table, [P], k_exp=(-10, -8))
+    two = {n: x.clone() for n, x in one.items()}
+    for n, bytes_ in (("k_scale", (0, 1, 60, 78)), ("v_scale", (0, 40, 200, 255, 160, 78))):
+        for i, b in enumerate(bytes_):
+            one[n].view(torch.uint8)[table[0, 2 * i].long()] = b
+            two[n].view(torch.uint8)[table[0, 2 * i].long()] = min(max(b, 127 - 48), 127 + 32)
+    q = ph.randn(g, 1, 1, Hq, d).to(torch.bfloat16)
+    want, lse, _ = blink.blink_paged_token_attention(q, two, table, _i32(P), P, want_lse=True)
+    got, got_lse, _ = blink.blink_paged_token_attention(q, one, table, _i32(P), P, want_lse=True)
+    assert torch.equal(got, want) and torch.equal(got_lse, lse)
+    ph.check_attention(want, lse, ph.token_reference(q, two, table, [P]))
+    for rows in (2, 100):
+        qt, kt, vt = (ph.randn(g, rows, H, d).to(torch.bfloat16) for H in (Hq, Hkv, Hkv))
+        a, b = (blink.blink_paged_prefix_tail_attention(qt, c, table, [P], kt, vt, _i32(0, rows), 1, rows)[0] for c in (one, two))
+        assert torch.equal(a, b) and bool(a.isfinite().all())
+
+
+@pytest.mark.parametrize("byte", [0, 50, 255])
+def test_append_behind_slots_of_a_page_never_written(byte):
+    """A page whose first slots hold zeros with a scale outside the range: the zeros stay, the new tokens get the scale that
+    they need (or the largest one, where the page has it)."""
+    g = ph.gen(54)
+    Hkv, d, page, filled, n = 2, 128, 32, 5, 9
+    cache = blink.blink_paged_cache(1, page, Hkv, d)
+    for s in ("k_scale", "v_scale"):
+        cache[s].view(torch.uint8).fill_(byte)
+    k, v = (2000 * ph.randn(g, n, Hkv, d).to(torch.bfloat16) for _ in range(2))
+    blink.blink_paged_append(k, v, cache, _i32(0).view(1, 1), _i32(0, n), _i32(filled), n)
+    for name, x in (("k", k), ("v", v)):
+        codes = cache[name].view(torch.uint8)[0]
+        assert bool((codes[:, :filled] == 0).all()) and bool((codes[:, filled + n:] == 0).all())
+        for h in range(Hkv):
+            e = 32 if byte == 255 else ph.scale_exponent(float(x[:, h].abs().max()))
+            assert int(cache[name + "_scale"].view(torch.uint8)[0, h]) == 127 + e
+            assert torch.equal(codes[h, filled:filled + n].view(torch.float8_e4m3fn).double(), ph.e4m3(x[:, h].double() * 2.0 ** -e))
