@@ -552,6 +552,7 @@ blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const blink_bf16 
  * d_ws              blink_paged_append_workspace() bytes: the error word
  * A page that two sequences share must not be written (sharers append to pages of their own).  A bad length,
  * a page index outside [0, n_pages) or past table_width latches BLINK_DEVICE_FLAG; those pages are not written.
+ * Where d_cu_new falls, which of the other sequences are written is open.
  * Errors: BLINK_INVALID_ARG, BLINK_OUT_OF_RANGE, BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR.
  * ------------------------------------------------------------------------------------------ */
 #define BLINK_MAX_PAGED_HEADS 1024

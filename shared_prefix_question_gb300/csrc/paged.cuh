@@ -48,6 +48,21 @@ __device__ __forceinline__ int exponent_of(uint8_t scale)
     return min(max(static_cast<int>(scale) - kScaleBias, kScaleMin), kScaleMax);
 }
 
+// By a whole warp: the last of lo + 1 .. hi - 1 for which `before` holds (it holds up to some place and not behind it), 32
+// places at a time; lo if it holds for none.  Any other answers of `before` give some place of lo .. hi - 1.
+template <class F>
+__device__ __forceinline__ int last_before(int lo, int hi, F before)
+{
+    const int lane = threadIdx.x & 31;
+    while (hi - lo > 1) {
+        const int step = (hi - lo - 1 + 31) / 32, at = lo + (lane + 1) * step;
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, at < hi && before(at)));
+        if (n < 32) hi = min(hi, lo + (n + 1) * step);
+        lo += n * step;
+    }
+    return lo;
+}
+
 // Two e4m3 codes (the lower byte first) as two fp16 values, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
 {

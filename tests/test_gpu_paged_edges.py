@@ -407,3 +407,68 @@ def test_append_behind_slots_of_a_page_never_written(byte):
             e = 32 if byte == 255 else ph.scale_exponent(float(x[:, h].abs().max()))
             assert int(cache[name + "_scale"].view(torch.uint8)[0, h]) == 127 + e
             assert torch.equal(codes[h, filled:filled + n].view(torch.float8_e4m3fn).double(), ph.e4m3(x[:, h].double() * 2.0 ** -e))
+
+
+@pytest.mark.parametrize("S,page,long_at", [(40, 16, (7,)), (3, 64, (2,)), (200, 32, (0, 150)), (3000, 16, (2999,))])
+def test_append_one_long_sequence_among_short_ones(S, page, long_at):
+    """max_new far above what most sequences get: the same bits as one call for each kind, rows of a slice (cu does not start
+    at 0), empty sequences, and a bad sequence flagged that leaves the others as they should be."""
+    g = ph.gen(S)
+    Hkv, d = 2, 64
+    new = torch.randint(0, 4, (S,), generator=torch.Generator().manual_seed(S)).tolist()
+    for i in long_at:
+        new[i] = 1000 + i
+    start = torch.randint(0, 3 * page, (S,), generator=torch.Generator().manual_seed(S + 1)).tolist()
+    ends = [a + b for a, b in zip(start, new)]
+    table, total = ph.table_for(g, ends, page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, table, start if S < 300 else [0] * S)
+    other = {n: x.clone() for n, x in cache.items()}
+    third = {n: x.clone() for n, x in cache.items()}
+    n = sum(new)
+    k, v = (ph.randn(g, n, Hkv, d).to(torch.bfloat16) for _ in range(2))
+    cu = [sum(new[:i]) for i in range(S + 1)]
+    turns, _ = blink.blink_rope_table(d)
+    most = max(new)
+    assert n // page + 2 * S < ((most + page - 2) // page + 1) * S
+    ws = blink.blink_paged_append(k, v, cache, table, _i32(*cu) + 5, _i32(*start), most, turns=turns)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+    short = [0 if i in long_at else x for i, x in enumerate(new)]
+    rows = [r for i in range(S) if i not in long_at for r in range(cu[i], cu[i + 1])]
+    cus = [sum(short[:i]) for i in range(S + 1)]
+    blink.blink_paged_append(k[rows], v[rows], other, table, _i32(*cus), _i32(*start), 4, turns=turns)
+    for i in long_at:
+        blink.blink_paged_append(k[cu[i]:cu[i + 1]], v[cu[i]:cu[i + 1]], other, table[i:i + 1], _i32(0, new[i]), _i32(start[i]), new[i], turns=turns)
+    for x in cache:
+        assert torch.equal(cache[x].view(torch.uint8), other[x].view(torch.uint8))
+    # a bad start: flagged, its pages left, the rest written
+    bad = next(i for i in range(S) if new[i] and i not in long_at)
+    worse = list(start)
+    worse[bad] = -1
+    ws = blink.blink_paged_append(k, v, third, table, _i32(*cu), _i32(*worse), most, turns=turns)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_DEVICE_FLAG
+    kept = torch.ones(total, dtype=torch.bool, device="cuda")
+    kept[table[bad][table[bad] >= 0].long()] = False
+    for x in cache:
+        assert torch.equal(cache[x].view(torch.uint8)[kept], third[x].view(torch.uint8)[kept])
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 8, 8), (1, 4, 1), (3, 16, 2)])
+@pytest.mark.parametrize("bound", [10000, 131072])
+def test_sequences_shorter_than_the_bound(T, Hq, Hkv, bound):
+    """Lengths about the borders of how a sequence is cut, one sequence at a time and several."""
+    g = ph.gen(T + Hkv + bound)
+    d, page = 64, 64
+    lens = [1, 63, 64, 65, 1000, 2048, 2049, 3647, 3648, 3649, 7295, 7296, 7297, 9999, 10000]
+    table, total = ph.table_for(g, [10000], page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, table, [10000])
+    ws = blink.new_workspace(blink.paged_token_attention_workspace_bytes(len(lens), T, bound, Hq, Hkv, d), "cuda")
+    q = ph.randn(g, len(lens), T, Hq, d).to(torch.bfloat16)
+    for n, x in zip(lens, q):
+        out, lse, _ = blink.blink_paged_token_attention(x[None], cache, table, _i32(n), bound, want_lse=True, ws=ws)
+        ph.check_attention(out, lse, ph.token_reference(x[None], cache, table, [n]))
+    rows = table.expand(len(lens), -1).contiguous()
+    out, lse, _ = blink.blink_paged_token_attention(q, cache, rows, _i32(*lens), bound, want_lse=True, ws=ws)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+    ph.check_attention(out, lse, ph.token_reference(q, cache, rows, lens))
