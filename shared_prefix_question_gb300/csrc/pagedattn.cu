@@ -53,7 +53,9 @@ struct TokenArgs {
     int table_width;
     const int32_t *len;
     int max_len, S, T, Hq, Hkv, g, tiles;  // tiles: M tiles of a sequence and kv head
-    int chunk, chunks;                     // keys of a block, blocks of a sequence, head and tile
+    int chunk, chunks;                     // most keys of a block, blocks of a sequence, head and tile
+    int share;                             // blocks that a short sequence is cut into, if they get kRound keys each
+    uint32_t one_share;                    // 2^32 / share, rounded up, of a share above 1
     float scale_log2;
     uint16_t *out;
     float *lse;
@@ -70,6 +72,15 @@ __device__ __forceinline__ int length_of(const TokenArgs &a, int seq, bool &bad)
     const int most = room < a.max_len ? static_cast<int>(room) : a.max_len;
     bad = n < 0 || n > most;
     return n < 0 ? 0 : n > most ? most : n;
+}
+
+// Keys of a block of a sequence of `len`: whole rounds of its warps, in at most a.chunks blocks.
+__device__ __forceinline__ int chunk_of(const TokenArgs &a, int len)
+{
+    if (a.chunks == 1) return a.chunk;
+    // ceil(len / share): the product is off by less than 2^-13 of a whole, a share at least 2^-11
+    const int even = a.share == 1 ? len : static_cast<int>(__umulhi(static_cast<uint32_t>(len + a.share - 1), a.one_share));
+    return min(max((even + kRound - 1) / kRound, 1) * kRound, a.chunk);
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -142,14 +153,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
     ptx::grid_dep_wait();
     ptx::grid_launch_dependents();
     if (TAIL && rows <= 0) return;  // fewer rows than another request
-    // The pages of this warp's steps, one a lane, read before the length is known.
-    const int k0 = blockIdx.x * a.chunk;
-    const int64_t index = (static_cast<int64_t>(k0) + (warp + lane * kWarps) * kStep) >> a.c.log2_page;
-    int page = index < a.table_width ? __ldg(a.table + seq * a.table_stride + index) : -1;
+    // The pages of this warp's steps, one a lane, read before the length is known, and again if it takes shorter chunks.
+    auto page_from = [&](int k0) {
+        const int64_t index = (static_cast<int64_t>(k0) + (warp + lane * kWarps) * kStep) >> a.c.log2_page;
+        return index < a.table_width ? __ldg(a.table + seq * a.table_stride + index) : -1;
+    };
+    int page = page_from(blockIdx.x * a.chunk);
     bool bad = false;
-    const int len = TAIL ? a.tail.len[seq] : length_of(a, seq, bad), k1 = min(len, k0 + a.chunk);
+    const int len = TAIL ? a.tail.len[seq] : length_of(a, seq, bad), chunk = chunk_of(a, len);
+    const int k0 = blockIdx.x * chunk, k1 = min(len, k0 + chunk);
     if (bad && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
     if (k0 >= k1 && a.chunks > 1) return;  // the join knows the length too
+    if (chunk != a.chunk) page = page_from(k0);
     const int steps = max(0, (k1 - k0 + kStep - 1) / kStep);
     const int mine = steps > warp ? (steps - warp + kWarps - 1) / kWarps : 0;
     int scales = kScaleBias | kScaleBias << 8;
@@ -485,21 +500,14 @@ __device__ __forceinline__ void load_channels(float (&x)[D / 32], const uint16_t
     }
 }
 
-// The last question that starts at or before `row` (by a whole warp, 32 starts at a time), and where it starts; -1: none.
+// The last question that starts at or before `row` (by a whole warp), and where it starts; -1: none.
 __device__ __forceinline__ int question_of(const TailRows &t, int row, int &start)
 {
-    const int lane = threadIdx.x & 31, base = t.seq_start ? 0 : __ldg(t.cu);
+    const int base = t.seq_start ? 0 : __ldg(t.cu);
     const int32_t *starts = t.seq_start ? t.seq_start : t.cu;
-    int lo = -1, hi = t.B;  // the answer lies in lo .. hi - 1
-    while (hi - lo > 1) {
-        const int step = (hi - lo - 1 + 31) / 32, at = lo + (lane + 1) * step;
-        const bool before = at < hi && __ldg(starts + at) - base <= row;
-        const int n = __popc(__ballot_sync(0xFFFFFFFFu, before));  // starts grow: the first n probes
-        if (n < 32) hi = min(hi, lo + (n + 1) * step);
-        lo += n * step;
-    }
-    start = lo >= 0 ? __ldg(starts + lo) - base : 0;
-    return lo;
+    const int b = last_before(-1, t.B, [&](int i) { return __ldg(starts + i) - base <= row; });
+    start = b >= 0 ? __ldg(starts + b) - base : 0;
+    return b;
 }
 
 // The chunks of a row joined by their log-sum-exp, a block a (token, query head): its warps share the chunks out, a lane
@@ -536,7 +544,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) token_join_kernel(const __gri
         bool bad;
         len = length_of(a, static_cast<int>(tok / a.T), bad);
     }
-    const int n = owned ? (len + a.chunk - 1) / a.chunk : 0;
+    const int chunk = chunk_of(a, len), n = owned ? (len + chunk - 1) / chunk : 0;
     float top = -INFINITY, total = 0.f, v[kVec] = {};
     auto take = [&](const float (&l)[kJoinBatch], const float (&x)[kJoinBatch][kVec]) {
         float now = top;
@@ -630,7 +638,7 @@ struct TokenPlan {
     // to 131072 with four tokens each, 32/8 heads: 212 us, with two blocks of one tile 264).  Two warps with a tile each over
     // the same ring, which convert twice, took 271.
     int wide;
-    int tiles, chunk, chunks;
+    int tiles, chunk, chunks, share;
     size_t lse, o, total;  // offsets of the partial results in the workspace
 };
 
@@ -645,19 +653,23 @@ TokenPlan token_plan(int64_t S, int64_t T, int64_t tokens, int64_t max_len, int6
     p.tiles = static_cast<int>((T * g + 8 * p.wide - 1) / (8 * p.wide));
     const int64_t units = S * Hkv * p.tiles;
     const int64_t at_once = static_cast<int64_t>(current_sm_count() > 0 ? current_sm_count() : 1) * Shape<128, 1>::kResident;
-    int64_t least = (max_len + kMaxChunk - 1) / kMaxChunk;  // chunks of a unit
     // Several sequences differ in length, and blocks without keys leave the last wave uneven: shorter chunks where there are few
     // waves (8 sequences of up to 18432 tokens: 34 us, 39 otherwise; 16: 52, 57; 16 of four tokens each: 66, 69; 64, with
     // ten waves: the same).
-    if (S > 1 && least * units < 4 * at_once) least *= 2;
-    const int64_t waves = (least * units + at_once - 1) / at_once;
-    const int64_t fit = waves * at_once / units;
+    auto fit_of = [&](int64_t least) {  // chunks of a unit, at least `least`
+        if (S > 1 && least * units < 4 * at_once) least *= 2;
+        return (least * units + at_once - 1) / at_once * at_once / units;
+    };
+    const int64_t fit = fit_of((max_len + kMaxChunk - 1) / kMaxChunk);
     int64_t chunk = fit > 0 ? (max_len + fit - 1) / fit : 0;
     chunk = (chunk + kRound - 1) / kRound * kRound;
     if (chunk > kMaxChunk) chunk = kMaxChunk;
     if (chunk < kRound) chunk = kRound;
     p.chunk = static_cast<int>(chunk);
     p.chunks = static_cast<int>(max_len > 0 ? (max_len + chunk - 1) / chunk : 1);
+    // A sequence much shorter than max_len is cut as if it were the longest (one of 1000 tokens, max_len 131072: 7.1 us, 13.4
+    // in chunks for the longest; eight: 14.0, 18.7).
+    p.share = static_cast<int>(fit_of(1) < p.chunks ? fit_of(1) : p.chunks);
     p.lse = kHeaderBytes;
     p.o = p.total = kHeaderBytes;
     if (p.chunks > 1 || joined) {
@@ -767,6 +779,8 @@ blink_status few_tail_attention(const PagedCache &c, int page_tokens, const uint
     a.tiles = plan.tiles;
     a.chunk = plan.chunk;
     a.chunks = plan.chunks;
+    a.share = plan.share;
+    a.one_share = static_cast<uint32_t>(((1ull << 32) + plan.share - 1) / plan.share);
     a.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(d))) * kLog2e;
     a.out = out;
     a.lse = lse;
@@ -829,6 +843,8 @@ extern "C" blink_status blink_paged_token_attention(
     a.tiles = plan.tiles;
     a.chunk = plan.chunk;
     a.chunks = plan.chunks;
+    a.share = plan.share;
+    a.one_share = static_cast<uint32_t>(((1ull << 32) + plan.share - 1) / plan.share);
     a.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(d))) * kLog2e;
     a.out = out;
     a.lse = lse;
