@@ -32,6 +32,11 @@ constexpr int kMaxChunk = 32 * kRound;           // a lane holds the page of one
 // all codes again, while bf16 rows are written once and shared by 128.  18432 keys, one request of 16 tokens and 32/8 heads
 // (64 rows): 29 us from the pages, 43 by way of bf16 rows; of 32 tokens 62 and 44; 2048 keys: 12 and 19, 18 and 19.
 constexpr int kFewRows = 64;
+// Waves of blocks from which, and sequences up to which, a grid of as many blocks as run at once takes the chunks that there are,
+// one after the other, in place of a grid for all chunks that max_len allows.  A block without keys takes some 1.3 ns, but next
+// chunks taken by a counter cost up to 2 % (max_len 131072, sequences of 1000 tokens, 64 of them: 72 and 39 us; 256: 257 and 112;
+// 256 of 8000: 633 and 616; with max_len 18432, 11 waves, 64 of up to 18432: 187 and 191).
+constexpr int kPackedWaves = 16, kMaxPacked = 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e37f;                 // below any score
 constexpr float kHead = 6.f, kSlack = 8.f;       // weights start at 2^kHead and may grow by 2^kSlack before the maximum moves
@@ -61,6 +66,7 @@ struct TokenArgs {
     float *lse;
     float *part_lse, *part_o;              // [token][Hq][chunks] and the same with [D] behind
     int *err;
+    int *taken;                            // items that blocks have taken past their first ones; 0 between calls
     TailRows tail;                         // with S = its requests; T and len are not used then
 };
 
@@ -132,7 +138,43 @@ __device__ __forceinline__ int piece_at(int row, int piece)
     return row * D + ((D == 128 ? piece ^ (row & 7) : piece ^ (row >> 1 & 3)) << 4);
 }
 
-template <int D, int NT, bool TAIL>
+// The chunks that the sequences before each have together, `first`, and all of them (returned), by a whole block.
+__device__ __forceinline__ int count_chunks(const TokenArgs &a, int *first)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, each = (a.S + kThreads - 1) / kThreads;
+    const int begin = min(threadIdx.x * each, a.S), end = min(begin + each, a.S);
+    int mine = 0;
+    for (int s = begin; s < end; ++s) {
+        bool bad;
+        const int len = length_of(a, s, bad), chunk = chunk_of(a, len);
+        if (bad && blockIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+        first[s] = mine;
+        mine += (len + chunk - 1) / chunk;
+    }
+    int before = mine;  // with the lanes before
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int n = __shfl_up_sync(0xFFFFFFFFu, before, d);
+        before += lane >= d ? n : 0;
+    }
+    if (lane == 31) first[a.S + warp] = before;
+    __syncthreads();
+    int total = 0;
+    before -= mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const int n = first[a.S + w];
+        before += w < warp ? n : 0;
+        total += n;
+    }
+    for (int s = begin; s < end; ++s) first[s] += before;
+    __syncthreads();
+    return total;
+}
+
+// PACKED: a grid of as many blocks as run at once goes over the chunks that the sequences have, in place of a grid of those that
+// the longest allowed one could have.
+template <int D, int NT, bool TAIL, bool PACKED>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ TokenArgs a)
 {
@@ -141,335 +183,363 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (-ptx::smem_u32(smem_raw) & 1023u);
     int *abort_flag = reinterpret_cast<int *>(smem + Sh::kBars + kWarps * kDepth * 8);
+    int *first = abort_flag + 4;                  // [S], and the warps' sums behind them
+    int *next = first + (PACKED ? a.S : 0) + kWarps;  // this block's next item, in two places by turns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, quad = lane & 3;  // products: rows r and r + 8, columns 2 quad and 2 quad + 1
-    const int seq = blockIdx.z, h = blockIdx.y / a.tiles, tile = blockIdx.y - h * a.tiles;
-    const int T = TAIL ? a.tail.row[seq + 1] - a.tail.row[seq] : a.T;
-    const int64_t token0 = TAIL ? a.tail.row[seq] : static_cast<int64_t>(seq) * a.T;
-    const int Tg = T * a.g, rho0 = tile * Sh::kRows, rows = min(Sh::kRows, Tg - rho0);
+    uint8_t *ring = smem + warp * kDepth * Sh::kStage;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Sh::kBars) + warp * kDepth;
+    auto init_bars = [&] {
+        if (lane == 0) {
+            *abort_flag = 0;
+            for (int i = 0; i < kDepth; ++i) ptx::mbar_init(&bars[i], 1);
+            ptx::fence_mbar_init();
+        }
+        __syncwarp();
+    };
+    int stage = 0;
+    uint32_t parity = 0;
 
     // What is launched behind this grid starts when all its blocks are past this wait, so the join, which reads lengths,
     // queries and tails before it waits for this grid, finds what was written before this grid.
     ptx::grid_dep_wait();
     ptx::grid_launch_dependents();
-    if (TAIL && rows <= 0) return;  // fewer rows than another request
-    // The pages of this warp's steps, one a lane, read before the length is known, and again if it takes shorter chunks.
-    auto page_from = [&](int k0) {
-        const int64_t index = (static_cast<int64_t>(k0) + (warp + lane * kWarps) * kStep) >> a.c.log2_page;
-        return index < a.table_width ? __ldg(a.table + seq * a.table_stride + index) : -1;
-    };
-    int page = page_from(blockIdx.x * a.chunk);
-    bool bad = false;
-    const int len = TAIL ? a.tail.len[seq] : length_of(a, seq, bad), chunk = chunk_of(a, len);
-    const int k0 = blockIdx.x * chunk, k1 = min(len, k0 + chunk);
-    if (bad && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
-    if (k0 >= k1 && a.chunks > 1) return;  // the join knows the length too
-    if (chunk != a.chunk) page = page_from(k0);
-    const int steps = max(0, (k1 - k0 + kStep - 1) / kStep);
-    const int mine = steps > warp ? (steps - warp + kWarps - 1) / kWarps : 0;
-    int scales = kScaleBias | kScaleBias << 8;
-    if (page < 0 || page >= a.c.n_pages || lane >= mine) {
-        if (lane < mine) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
-        page = -1;  // past the end, or not a page: its keys are masked
-    } else {
-        scales = (exponent_of(__ldg(a.c.k_scale + page * a.c.scale_stride + h)) + kScaleBias) |
-                 (exponent_of(__ldg(a.c.v_scale + page * a.c.scale_stride + h)) + kScaleBias) << 8;
+    int items = 1;
+    if constexpr (PACKED) {
+        init_bars();
+        items = count_chunks(a, first) * a.Hkv * a.tiles;
     }
-    uint8_t *ring = smem + warp * kDepth * Sh::kStage;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Sh::kBars) + warp * kDepth;
-    if (lane == 0) {
-        *abort_flag = 0;
-        for (int i = 0; i < kDepth; ++i) ptx::mbar_init(&bars[i], 1);
-        ptx::fence_mbar_init();
-    }
-    __syncwarp();
+    for (int item = PACKED ? blockIdx.x : 0, turn = 0; item < items; turn ^= 1) {
+        int ticket = 0;
+        if (PACKED && threadIdx.x == 0) ticket = atomicAdd(a.taken, 1) + gridDim.x;
+        int seq = blockIdx.z, ht = blockIdx.y, part = blockIdx.x;  // ht: kv head and tile
+        if constexpr (PACKED) {
+            const int units = a.Hkv * a.tiles, c = item / units;
+            ht = item - c * units;
+            seq = last_before(0, a.S, [&](int s) { return first[s] <= c; });  // the last of those that start there has keys
+            part = c - first[seq];
+        }
+        const int h = ht / a.tiles, tile = ht - h * a.tiles;
+        const int T = TAIL ? a.tail.row[seq + 1] - a.tail.row[seq] : a.T;
+        const int64_t token0 = TAIL ? a.tail.row[seq] : static_cast<int64_t>(seq) * a.T;
+        const int Tg = T * a.g, rho0 = tile * Sh::kRows, rows = min(Sh::kRows, Tg - rho0);
 
-    // Copies of step i into its slot, which all lanes have read before.
-    auto issue = [&](int i, int stage) {
-        const int id = __shfl_sync(0xFFFFFFFFu, page, i & 31);
-        if (i < mine && lane == 0) {
-            const int key = k0 + (warp + i * kWarps) * kStep;
-            uint8_t *slot = ring + stage * Sh::kStage;
-            if (id >= 0) {
-                const int row = (h << a.c.log2_page) + (key & ((1 << a.c.log2_page) - 1));
-                ptx::mbar_arrive_expect_tx(&bars[stage], Sh::kStage);
-                ptx::tma_load_3d(slot, &tm_k, 0, row, id, &bars[stage]);
-                ptx::tma_load_3d(slot + Sh::kTile, &tm_v, 0, row, id, &bars[stage]);
-            } else {
-                ptx::mbar_arrive(&bars[stage]);  // no page: the slot holds anything, and nothing reads it as a key
+        if (TAIL && rows <= 0) return;  // fewer rows than another request
+        // The pages of this warp's steps, one a lane, read before the length is known, and again if it takes shorter chunks.
+        auto page_from = [&](int k0) {
+            const int64_t index = (static_cast<int64_t>(k0) + (warp + lane * kWarps) * kStep) >> a.c.log2_page;
+            return index < a.table_width ? __ldg(a.table + seq * a.table_stride + index) : -1;
+        };
+        int page = page_from(part * a.chunk);
+        bool bad = false;
+        const int len = TAIL ? a.tail.len[seq] : length_of(a, seq, bad), chunk = chunk_of(a, len);
+        const int k0 = part * chunk, k1 = min(len, k0 + chunk);
+        if (!PACKED && bad && threadIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+        if (!PACKED && k0 >= k1 && a.chunks > 1) return;  // the join knows the length too
+        if (chunk != a.chunk) page = page_from(k0);
+        const int steps = max(0, (k1 - k0 + kStep - 1) / kStep);
+        const int mine = steps > warp ? (steps - warp + kWarps - 1) / kWarps : 0;
+        int scales = kScaleBias | kScaleBias << 8;
+        if (page < 0 || page >= a.c.n_pages || lane >= mine) {
+            if (lane < mine) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
+            page = -1;  // past the end, or not a page: its keys are masked
+        } else {
+            scales = (exponent_of(__ldg(a.c.k_scale + page * a.c.scale_stride + h)) + kScaleBias) |
+                     (exponent_of(__ldg(a.c.v_scale + page * a.c.scale_stride + h)) + kScaleBias) << 8;
+        }
+        if constexpr (!PACKED) init_bars();
+
+        // Copies of step i into its slot, which all lanes have read before.
+        auto issue = [&](int i, int stage) {
+            const int id = __shfl_sync(0xFFFFFFFFu, page, i & 31);
+            if (i < mine && lane == 0) {
+                const int key = k0 + (warp + i * kWarps) * kStep;
+                uint8_t *slot = ring + stage * Sh::kStage;
+                if (id >= 0) {
+                    const int row = (h << a.c.log2_page) + (key & ((1 << a.c.log2_page) - 1));
+                    ptx::mbar_arrive_expect_tx(&bars[stage], Sh::kStage);
+                    ptx::tma_load_3d(slot, &tm_k, 0, row, id, &bars[stage]);
+                    ptx::tma_load_3d(slot + Sh::kTile, &tm_v, 0, row, id, &bars[stage]);
+                } else {
+                    ptx::mbar_arrive(&bars[stage]);  // no page: the slot holds anything, and nothing reads it as a key
+                }
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kDepth - 1; ++i) issue(i, !PACKED ? i : stage + i < kDepth ? stage + i : stage + i - kDepth);
+
+        // Queries as the second operand, in the order of the key bytes: product step 4 p + w takes channels
+        // 16 kPieces quad + 16 p + 4 w .. + 3 of this lane; the lane holds row r of each tile.
+        uint32_t qb[NT][4 * Sh::kPieces][2];
+        float base[NT][2];  // of rows 2 quad and 2 quad + 1: the factor of their scores
+        int see[NT][2];     // keys that they see
+#pragma unroll
+        for (int y = 0; y < NT; ++y) {
+            const int rho = rho0 + 8 * y + r, t = rho / a.g, j = rho - t * a.g;
+            uint4 w[2 * Sh::kPieces];
+#pragma unroll
+            for (int p = 0; p < Sh::kPieces; ++p) {
+                w[2 * p] = w[2 * p + 1] = make_uint4(0, 0, 0, 0);
+                if (rho < Tg) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        a.q + ((token0 + t) * a.Hq + h * a.g + j) * D + quad * 16 * Sh::kPieces + p * 16);
+                    w[2 * p] = __ldg(src);
+                    w[2 * p + 1] = __ldg(src + 1);
+                }
+            }
+            const uint32_t *x = reinterpret_cast<const uint32_t *>(w);
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8 * Sh::kPieces; ++e)
+                m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            // the row's largest value between 2^9 and 2^10: values 2^-33 of it and smaller lose bits, none overflows
+            int move = 9 - (static_cast<int>(__float_as_uint(m) >> 23) - 127);
+            move = !(m > 0.f) || m == INFINITY ? 0 : min(move, 126);
+            const float f = scale_of(move), back = a.scale_log2 * scale_of(-move);
+#pragma unroll
+            for (int e = 0; e < 8 * Sh::kPieces; ++e)  // word e: channels 2 e, 2 e + 1 of the lane's 16 of a piece
+                qb[y][e / 2][e & 1] = pack_f16x2(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xFFFF0000u) * f);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                base[y][c] = __shfl_sync(0xFFFFFFFFu, back, (2 * quad + c) * 4);
+                see[y][c] = TAIL ? len : len - (T - 1 - min(rho0 + 8 * y + 2 * quad + c, Tg - 1) / a.g);
             }
         }
-    };
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) issue(i, i);
+        const int t_first = TAIL ? 0 : rho0 / a.g, t_last = TAIL ? 0 : (rho0 + rows - 1) / a.g;
+        const int see_least = TAIL ? len : len - (T - 1 - t_first);  // the fewest keys that a row sees
 
-    // Queries as the second operand, in the order of the key bytes: product step 4 p + w takes channels
-    // 16 kPieces quad + 16 p + 4 w .. + 3 of this lane; the lane holds row r of each tile.
-    uint32_t qb[NT][4 * Sh::kPieces][2];
-    float base[NT][2];  // of rows 2 quad and 2 quad + 1: the factor of their scores
-    int see[NT][2];     // keys that they see
-#pragma unroll
-    for (int y = 0; y < NT; ++y) {
-        const int rho = rho0 + 8 * y + r, t = rho / a.g, j = rho - t * a.g;
-        uint4 w[2 * Sh::kPieces];
-#pragma unroll
-        for (int p = 0; p < Sh::kPieces; ++p) {
-            w[2 * p] = w[2 * p + 1] = make_uint4(0, 0, 0, 0);
-            if (rho < Tg) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    a.q + ((token0 + t) * a.Hq + h * a.g + j) * D + quad * 16 * Sh::kPieces + p * 16);
-                w[2 * p] = __ldg(src);
-                w[2 * p + 1] = __ldg(src + 1);
-            }
-        }
-        const uint32_t *x = reinterpret_cast<const uint32_t *>(w);
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8 * Sh::kPieces; ++e)
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        // the row's largest value between 2^9 and 2^10: values 2^-33 of it and smaller lose bits, none overflows
-        int move = 9 - (static_cast<int>(__float_as_uint(m) >> 23) - 127);
-        move = !(m > 0.f) || m == INFINITY ? 0 : min(move, 126);
-        const float f = scale_of(move), back = a.scale_log2 * scale_of(-move);
-#pragma unroll
-        for (int e = 0; e < 8 * Sh::kPieces; ++e)  // word e: channels 2 e, 2 e + 1 of the lane's 16 of a piece
-            qb[y][e / 2][e & 1] = pack_f16x2(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xFFFF0000u) * f);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            base[y][c] = __shfl_sync(0xFFFFFFFFu, back, (2 * quad + c) * 4);
-            see[y][c] = TAIL ? len : len - (T - 1 - min(rho0 + 8 * y + 2 * quad + c, Tg - 1) / a.g);
-        }
-    }
-    const int t_first = TAIL ? 0 : rho0 / a.g, t_last = TAIL ? 0 : (rho0 + rows - 1) / a.g;
-    const int see_least = TAIL ? len : len - (T - 1 - t_first);  // the fewest keys that a row sees
-
-    float o[NT][Sh::kCols / 2][4];  // channels kCols r + 2 j (first two) and + 1, rows 2 quad and 2 quad + 1
-#pragma unroll
-    for (int y = 0; y < NT; ++y)
-#pragma unroll
-        for (int j = 0; j < Sh::kCols / 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[y][j][e] = 0.f;
-    float most[NT][2], sum[NT][2];
-#pragma unroll
-    for (int y = 0; y < NT; ++y) most[y][0] = most[y][1] = kNoMax, sum[y][0] = sum[y][1] = 0.f;
-    int unit = kScaleMin - 1;  // o is in units of 2^unit
-
-    int stage = 0;
-    uint32_t parity = 0;
-    bool fine = true;
-    for (int i = 0; i < mine; ++i) {
-        __syncwarp();
-        issue(i + kDepth - 1, stage == 0 ? kDepth - 1 : stage - 1);
-        fine = ptx::mbar_wait_warp(&bars[stage], parity, abort_flag, a.err, BLINK_DEVICE_TIMEOUT);
-        if (!fine) {  // the copies in flight still land in this block's memory: wait for them, again with a limit
-            int other = 0;
-            for (int n = i; n < min(mine, i + kDepth); ++n) {
-                ptx::mbar_wait(&bars[stage], parity, &other, a.err, BLINK_DEVICE_TIMEOUT);
-                other = 0;
-                if (++stage == kDepth) stage = 0, parity ^= 1;
-            }
-            break;
-        }
-        const int key = k0 + (warp + i * kWarps) * kStep;
-        const int id = __shfl_sync(0xFFFFFFFFu, page, i), both = __shfl_sync(0xFFFFFFFFu, scales, i);
-        const int ek = (both & 0xFF) - kScaleBias, ev = (both >> 8) - kScaleBias;
-        const uint8_t *slot = ring + stage * Sh::kStage;
-        if (++stage == kDepth) stage = 0, parity ^= 1;
-
-        float s[NT][2][4];
+        float o[NT][Sh::kCols / 2][4];  // channels kCols r + 2 j (first two) and + 1, rows 2 quad and 2 quad + 1
 #pragma unroll
         for (int y = 0; y < NT; ++y)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int j = 0; j < Sh::kCols / 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[y][b][e] = 0.f;
+                for (int e = 0; e < 4; ++e) o[y][j][e] = 0.f;
+        float most[NT][2], sum[NT][2];
 #pragma unroll
-        for (int p = 0; p < Sh::kPieces; ++p) {
-            const uint4 klo = *reinterpret_cast<const uint4 *>(slot + piece_at<D>(r, quad * Sh::kPieces + p));      // key r
-            const uint4 khi = *reinterpret_cast<const uint4 *>(slot + piece_at<D>(r + 8, quad * Sh::kPieces + p));  // key r + 8
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(&klo), *x = reinterpret_cast<const uint32_t *>(&khi);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t ka[4] = {e4m3x2_to_f16x2(w[e]), e4m3x2_to_f16x2(x[e]), e4m3x2_hi_to_f16x2(w[e]),
-                                        e4m3x2_hi_to_f16x2(x[e])};
-#pragma unroll
-                for (int y = 0; y < NT; ++y) mma16816(s[y][e & 1], ka, qb[y][4 * p + e][0], qb[y][4 * p + e][1]);
+        for (int y = 0; y < NT; ++y) most[y][0] = most[y][1] = kNoMax, sum[y][0] = sum[y][1] = 0.f;
+        int unit = kScaleMin - 1;  // o is in units of 2^unit
+
+        bool fine = true;
+        for (int i = 0; i < mine; ++i) {
+            __syncwarp();
+            issue(i + kDepth - 1, stage == 0 ? kDepth - 1 : stage - 1);
+            fine = ptx::mbar_wait_warp(&bars[stage], parity, abort_flag, a.err, BLINK_DEVICE_TIMEOUT);
+            if (!fine) {  // the copies in flight still land in this block's memory: wait for them, again with a limit
+                int other = 0;
+                for (int n = i; n < min(mine, i + kDepth); ++n) {
+                    ptx::mbar_wait(&bars[stage], parity, &other, a.err, BLINK_DEVICE_TIMEOUT);
+                    other = 0;
+                    if (++stage == kDepth) stage = 0, parity ^= 1;
+                }
+                break;
             }
-        }
-        const bool edge = key + kStep > see_least || id < 0;  // warp-uniform
-        const float fk = scale_of(ek);
-        float x[NT][4];  // keys r (first two) and r + 8, rows 2 quad and 2 quad + 1
-        bool grow = false;
-#pragma unroll
-        for (int y = 0; y < NT; ++y) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[y][e] = (s[y][0][e] + s[y][1][e]) * (base[y][e & 1] * fk);
-            if (edge) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (key + r + 8 * (e >> 1) >= see[y][e & 1] || id < 0) x[y][e] = -INFINITY;
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) grow = grow || fmaxf(x[y][c], x[y][c + 2]) > most[y][c] + (kSlack + kHead);
-        }
-        // The maximum moves only when a weight would pass 2^(kHead + kSlack), the unit when a page's V scale is above
-        // it (a weight might overflow fp16) or far below (weights would lose bits).
-        const bool shift = ev > unit || ev < unit - 6;
-        if (__any_sync(0xFFFFFFFFu, grow) || shift) {
-            const float fu = unit < kScaleMin || !shift ? 1.f : scale_of(unit - ev);
-            if (shift) unit = ev;
+            const int key = k0 + (warp + i * kWarps) * kStep;
+            const int id = __shfl_sync(0xFFFFFFFFu, page, i), both = __shfl_sync(0xFFFFFFFFu, scales, i);
+            const int ek = (both & 0xFF) - kScaleBias, ev = (both >> 8) - kScaleBias;
+            const uint8_t *slot = ring + stage * Sh::kStage;
+            if (++stage == kDepth) stage = 0, parity ^= 1;
+
+            float s[NT][2][4];
 #pragma unroll
             for (int y = 0; y < NT; ++y)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float m = fmaxf(x[y][c], x[y][c + 2]);
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-                    float f = 1.f;
-                    if (m > most[y][c] + (kSlack + kHead)) {
-                        const float now = m - kHead;
-                        f = ptx::ex2(most[y][c] - now);
-                        most[y][c] = now;
-                        sum[y][c] *= f;
-                    }
-                    f *= fu;
+                    for (int e = 0; e < 4; ++e) s[y][b][e] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < Sh::kCols / 2; ++j) {
-                        o[y][j][c] *= f;
-                        o[y][j][c + 2] *= f;
-                    }
+            for (int p = 0; p < Sh::kPieces; ++p) {
+                const uint4 klo = *reinterpret_cast<const uint4 *>(slot + piece_at<D>(r, quad * Sh::kPieces + p));      // key r
+                const uint4 khi = *reinterpret_cast<const uint4 *>(slot + piece_at<D>(r + 8, quad * Sh::kPieces + p));  // key r + 8
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(&klo), *x = reinterpret_cast<const uint32_t *>(&khi);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t ka[4] = {e4m3x2_to_f16x2(w[e]), e4m3x2_to_f16x2(x[e]), e4m3x2_hi_to_f16x2(w[e]),
+                                            e4m3x2_hi_to_f16x2(x[e])};
+#pragma unroll
+                    for (int y = 0; y < NT; ++y) mma16816(s[y][e & 1], ka, qb[y][4 * p + e][0], qb[y][4 * p + e][1]);
                 }
-        }
-        const float fv = scale_of(ev - unit);
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int y = 0; y < NT; ++y) {
-            float p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(x[y][e] - most[y][e & 1]);
-            sum[y][0] += p[0] + p[2];
-            sum[y][1] += p[1] + p[3];
-            pb[y][0] = transposed(pack_f16x2(p[0] * fv, p[1] * fv));
-            pb[y][1] = transposed(pack_f16x2(p[2] * fv, p[3] * fv));
-        }
-        uint32_t v[4][Sh::kCols / 4];
-        const uint8_t *vs = slot + Sh::kTile;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // keys 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9
-            const int row = 2 * quad + (e & 1) + (e >> 1) * 8;
-            if constexpr (Sh::kCols == 16) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(vs + piece_at<D>(row, r));
-                v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
-            } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(vs + piece_at<D>(row, r >> 1) + (r & 1) * 8);
-                v[e][0] = w.x, v[e][1] = w.y;
             }
-        }
-        auto operand = [](uint32_t (&va)[4], uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3, uint32_t pick) {
-            const uint32_t lo = __byte_perm(v0, v1, pick), hi = __byte_perm(v2, v3, pick);  // two channels of two keys each
-            va[0] = e4m3x2_to_f16x2(lo);
-            va[1] = e4m3x2_hi_to_f16x2(lo);
-            va[2] = e4m3x2_to_f16x2(hi);
-            va[3] = e4m3x2_hi_to_f16x2(hi);
-        };
-        if (!edge) {
+            const bool edge = key + kStep > see_least || id < 0;  // warp-uniform
+            const float fk = scale_of(ek);
+            float x[NT][4];  // keys r (first two) and r + 8, rows 2 quad and 2 quad + 1
+            bool grow = false;
 #pragma unroll
-            for (int j = 0; j < Sh::kCols / 2; ++j) {
-                const int w = j / 2;
-                uint32_t va[4];
-                operand(va, v[0][w], v[1][w], v[2][w], v[3][w], j & 1 ? 0x7362u : 0x5140u);
+            for (int y = 0; y < NT; ++y) {
 #pragma unroll
-                for (int y = 0; y < NT; ++y) mma16816(o[y][j], va, pb[y][0], pb[y][1]);
+                for (int e = 0; e < 4; ++e) x[y][e] = (s[y][0][e] + s[y][1][e]) * (base[y][e & 1] * fk);
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (key + r + 8 * (e >> 1) >= see[y][e & 1] || id < 0) x[y][e] = -INFINITY;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) grow = grow || fmaxf(x[y][c], x[y][c + 2]) > most[y][c] + (kSlack + kHead);
             }
-        } else {
-            // Keys that a row does not see may hold anything, a NaN times its zero weight too: for each token of the tile
-            // the products run on the keys that it sees, and its rows take them.
-            for (int t = t_first; t <= t_last; ++t) {
-                const int limit = TAIL ? len : len - (T - 1 - t);
-                uint32_t keep[4];
+            // The maximum moves only when a weight would pass 2^(kHead + kSlack), the unit when a page's V scale is above
+            // it (a weight might overflow fp16) or far below (weights would lose bits).
+            const bool shift = ev > unit || ev < unit - 6;
+            if (__any_sync(0xFFFFFFFFu, grow) || shift) {
+                const float fu = unit < kScaleMin || !shift ? 1.f : scale_of(unit - ev);
+                if (shift) unit = ev;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) keep[e] = id >= 0 && key + 2 * quad + (e & 1) + (e >> 1) * 8 < limit ? 0xFFFFFFFFu : 0u;
+                for (int y = 0; y < NT; ++y)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float m = fmaxf(x[y][c], x[y][c + 2]);
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+                        float f = 1.f;
+                        if (m > most[y][c] + (kSlack + kHead)) {
+                            const float now = m - kHead;
+                            f = ptx::ex2(most[y][c] - now);
+                            most[y][c] = now;
+                            sum[y][c] *= f;
+                        }
+                        f *= fu;
+#pragma unroll
+                        for (int j = 0; j < Sh::kCols / 2; ++j) {
+                            o[y][j][c] *= f;
+                            o[y][j][c + 2] *= f;
+                        }
+                    }
+            }
+            const float fv = scale_of(ev - unit);
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int y = 0; y < NT; ++y) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(x[y][e] - most[y][e & 1]);
+                sum[y][0] += p[0] + p[2];
+                sum[y][1] += p[1] + p[3];
+                pb[y][0] = transposed(pack_f16x2(p[0] * fv, p[1] * fv));
+                pb[y][1] = transposed(pack_f16x2(p[2] * fv, p[3] * fv));
+            }
+            uint32_t v[4][Sh::kCols / 4];
+            const uint8_t *vs = slot + Sh::kTile;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // keys 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9
+                const int row = 2 * quad + (e & 1) + (e >> 1) * 8;
+                if constexpr (Sh::kCols == 16) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(vs + piece_at<D>(row, r));
+                    v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(vs + piece_at<D>(row, r >> 1) + (r & 1) * 8);
+                    v[e][0] = w.x, v[e][1] = w.y;
+                }
+            }
+            auto operand = [](uint32_t (&va)[4], uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3, uint32_t pick) {
+                const uint32_t lo = __byte_perm(v0, v1, pick), hi = __byte_perm(v2, v3, pick);  // two channels of two keys each
+                va[0] = e4m3x2_to_f16x2(lo);
+                va[1] = e4m3x2_hi_to_f16x2(lo);
+                va[2] = e4m3x2_to_f16x2(hi);
+                va[3] = e4m3x2_hi_to_f16x2(hi);
+            };
+            if (!edge) {
 #pragma unroll
                 for (int j = 0; j < Sh::kCols / 2; ++j) {
                     const int w = j / 2;
                     uint32_t va[4];
-                    operand(va, v[0][w] & keep[0], v[1][w] & keep[1], v[2][w] & keep[2], v[3][w] & keep[3], j & 1 ? 0x7362u : 0x5140u);
+                    operand(va, v[0][w], v[1][w], v[2][w], v[3][w], j & 1 ? 0x7362u : 0x5140u);
 #pragma unroll
-                    for (int y = 0; y < NT; ++y) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma16816(d, va, pb[y][0], pb[y][1]);
+                    for (int y = 0; y < NT; ++y) mma16816(o[y][j], va, pb[y][0], pb[y][1]);
+                }
+            } else {
+                // Keys that a row does not see may hold anything, a NaN times its zero weight too: for each token of the tile
+                // the products run on the keys that it sees, and its rows take them.
+                for (int t = t_first; t <= t_last; ++t) {
+                    const int limit = TAIL ? len : len - (T - 1 - t);
+                    uint32_t keep[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[y][j][e] += TAIL || (rho0 + 8 * y + 2 * quad + (e & 1)) / a.g == t ? d[e] : 0.f;
+                    for (int e = 0; e < 4; ++e) keep[e] = id >= 0 && key + 2 * quad + (e & 1) + (e >> 1) * 8 < limit ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+                    for (int j = 0; j < Sh::kCols / 2; ++j) {
+                        const int w = j / 2;
+                        uint32_t va[4];
+                        operand(va, v[0][w] & keep[0], v[1][w] & keep[1], v[2][w] & keep[2], v[3][w] & keep[3], j & 1 ? 0x7362u : 0x5140u);
+#pragma unroll
+                        for (int y = 0; y < NT; ++y) {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma16816(d, va, pb[y][0], pb[y][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                o[y][j][e] += TAIL || (rho0 + 8 * y + 2 * quad + (e & 1)) / a.g == t ? d[e] : 0.f;
+                        }
                     }
                 }
             }
         }
-    }
 
-    // The warps' sums joined through shared memory, over the ring: every copy of this block has landed by the barrier.
-    if (__syncthreads_or(!fine)) return;
-    float *so = reinterpret_cast<float *>(smem);
-    float *sm = so + kWarps * Sh::kRows * Sh::kPad, *sl = sm + kWarps * Sh::kRows;
+        // The warps' sums joined through shared memory, over the ring: every copy of this block has landed by the barrier.
+        if (PACKED && threadIdx.x == 0) next[turn] = ticket;
+        if (__syncthreads_or(!fine)) return;
+        float *so = reinterpret_cast<float *>(smem);
+        float *sm = so + kWarps * Sh::kRows * Sh::kPad, *sl = sm + kWarps * Sh::kRows;
 #pragma unroll
-    for (int y = 0; y < NT; ++y)
+        for (int y = 0; y < NT; ++y)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 2; ++c) {
 #pragma unroll
-            for (int d = 4; d < 32; d *= 2) sum[y][c] += __shfl_xor_sync(0xFFFFFFFFu, sum[y][c], d);
-            if (r == 0) {
-                sm[warp * Sh::kRows + 8 * y + 2 * quad + c] = most[y][c];
-                sl[warp * Sh::kRows + 8 * y + 2 * quad + c] = sum[y][c];
+                for (int d = 4; d < 32; d *= 2) sum[y][c] += __shfl_xor_sync(0xFFFFFFFFu, sum[y][c], d);
+                if (r == 0) {
+                    sm[warp * Sh::kRows + 8 * y + 2 * quad + c] = most[y][c];
+                    sl[warp * Sh::kRows + 8 * y + 2 * quad + c] = sum[y][c];
+                }
             }
-        }
-    __syncthreads();
+        __syncthreads();
 #pragma unroll
-    for (int y = 0; y < NT; ++y)
+        for (int y = 0; y < NT; ++y)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int row = 8 * y + 2 * quad + c;
-            if (row >= rows) continue;
-            float top = kNoMax;
+            for (int c = 0; c < 2; ++c) {
+                const int row = 8 * y + 2 * quad + c;
+                if (row >= rows) continue;
+                float top = kNoMax;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * Sh::kRows + row]);
+                const float f = ptx::ex2(most[y][c] - top + static_cast<float>(unit));
+                float *dst = so + (warp * Sh::kRows + row) * Sh::kPad + r * Sh::kCols;
+#pragma unroll
+                for (int j = 0; j < Sh::kCols / 2; j += 2)
+                    *reinterpret_cast<float4 *>(dst + 2 * j) =
+                        make_float4(o[y][j][c] * f, o[y][j][c + 2] * f, o[y][j + 1][c] * f, o[y][j + 1][c + 2] * f);
+            }
+        __syncthreads();
+        constexpr int kVec = D / 4;
+        for (int e = threadIdx.x; e < rows * kVec; e += kThreads) {
+            const int row = e / kVec, col = (e - row * kVec) * 4;
+            float top = kNoMax, total = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * Sh::kRows + row]);
-            const float f = ptx::ex2(most[y][c] - top + static_cast<float>(unit));
-            float *dst = so + (warp * Sh::kRows + row) * Sh::kPad + r * Sh::kCols;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < Sh::kCols / 2; j += 2)
-                *reinterpret_cast<float4 *>(dst + 2 * j) =
-                    make_float4(o[y][j][c] * f, o[y][j][c + 2] * f, o[y][j + 1][c] * f, o[y][j + 1][c + 2] * f);
+            for (int w = 0; w < kWarps; ++w) {
+                total += sl[w * Sh::kRows + row] * ptx::ex2(sm[w * Sh::kRows + row] - top);
+                const float4 p = *reinterpret_cast<const float4 *>(so + (w * Sh::kRows + row) * Sh::kPad + col);
+                v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+            }
+            const bool none = total == 0.f;  // no key: zeros, and -inf
+            const float inv = none ? 0.f : 1.f / total, l2 = none ? -INFINITY : top + log2f(total);
+            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+            const int rho = rho0 + row, t = rho / a.g, head = h * a.g + rho - t * a.g;
+            const int64_t tok = token0 + t;
+            if (TAIL || a.chunks > 1) {
+                const int64_t at = (tok * a.Hq + head) * a.chunks + part;
+                *reinterpret_cast<float4 *>(a.part_o + at * D + col) = v;
+                if (col == 0) a.part_lse[at] = l2;
+            } else {
+                *reinterpret_cast<uint2 *>(a.out + (tok * a.Hq + head) * D + col) =
+                    make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
+                if (col == 0 && a.lse) a.lse[head * static_cast<int64_t>(a.S) * a.T + tok] = l2 * kLn2;
+            }
         }
-    __syncthreads();
-    constexpr int kVec = D / 4;
-    for (int e = threadIdx.x; e < rows * kVec; e += kThreads) {
-        const int row = e / kVec, col = (e - row * kVec) * 4;
-        float top = kNoMax, total = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * Sh::kRows + row]);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            total += sl[w * Sh::kRows + row] * ptx::ex2(sm[w * Sh::kRows + row] - top);
-            const float4 p = *reinterpret_cast<const float4 *>(so + (w * Sh::kRows + row) * Sh::kPad + col);
-            v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+        if constexpr (PACKED) {  // the next copies land where the sums were
+            ptx::fence_proxy_async_smem();
+            __syncthreads();
         }
-        const bool none = total == 0.f;  // no key: zeros, and -inf
-        const float inv = none ? 0.f : 1.f / total, l2 = none ? -INFINITY : top + log2f(total);
-        v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-        const int rho = rho0 + row, t = rho / a.g, head = h * a.g + rho - t * a.g;
-        const int64_t tok = token0 + t;
-        if (TAIL || a.chunks > 1) {
-            const int64_t at = (tok * a.Hq + head) * a.chunks + blockIdx.x;
-            *reinterpret_cast<float4 *>(a.part_o + at * D + col) = v;
-            if (col == 0) a.part_lse[at] = l2;
-        } else {
-            *reinterpret_cast<uint2 *>(a.out + (tok * a.Hq + head) * D + col) =
-                make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
-            if (col == 0 && a.lse) a.lse[head * static_cast<int64_t>(a.S) * a.T + tok] = l2 * kLn2;
-        }
+        item = PACKED ? next[turn] : 1;
     }
 }
 
@@ -594,6 +664,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) token_join_kernel(const __gri
     }
     ptx::grid_dep_wait();
     ptx::grid_launch_dependents();
+    if (!TAIL && row == 0 && threadIdx.x == 0) *a.taken = 0;
     const float *pl = a.part_lse + row * a.chunks, *po = a.part_o + row * a.chunks * D + lane * kVec;
     for (int c0 = warp; c0 < n; c0 += warps * kJoinBatch) {
         float l[kJoinBatch], x[kJoinBatch][kVec];
@@ -683,13 +754,23 @@ TokenPlan token_plan(int64_t S, int64_t T, int64_t tokens, int64_t max_len, int6
 template <int D, bool TAIL>
 bool launch_pages(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const TokenArgs &a, const TokenPlan &plan, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.Hkv * a.tiles), static_cast<unsigned>(a.S));
+    dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.Hkv * a.tiles), static_cast<unsigned>(a.S));
     auto launch = [&](auto kern, int smem) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
         return launch_programmatic(kern, grid, kThreads, smem, stream, tm_k, tm_v, a) == cudaSuccess;
     };
-    return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL>, Shape<D, 1>::kSmem)
-                          : launch(token_attention_kernel<D, 2, TAIL>, Shape<D, 2>::kSmem);
+    if constexpr (!TAIL) {
+        const int64_t blocks = static_cast<int64_t>(a.chunks) * a.Hkv * a.tiles * a.S;
+        const int64_t at_once = static_cast<int64_t>(current_sm_count()) * Shape<D, 1>::kResident;
+        if (a.chunks > 1 && a.S > 1 && a.S <= kMaxPacked && blocks > kPackedWaves * at_once && blocks <= 1 << 30) {
+            grid = dim3(static_cast<unsigned>(at_once));
+            const int more = (a.S + kWarps + 2) * static_cast<int>(sizeof(int));
+            return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL, true>, Shape<D, 1>::kSmem + more)
+                                  : launch(token_attention_kernel<D, 2, TAIL, true>, Shape<D, 2>::kSmem + more);
+        }
+    }
+    return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL, false>, Shape<D, 1>::kSmem)
+                          : launch(token_attention_kernel<D, 2, TAIL, false>, Shape<D, 2>::kSmem);
 }
 
 // The pages' part, then the join of `joined` rows as its programmatic dependent.
@@ -711,7 +792,9 @@ blink_status launch_token(const TokenArgs &a, const TokenPlan &plan, int page_to
     const dim3 rows(static_cast<unsigned>(joined));
     const cudaError_t e = d == 128 ? launch_programmatic(token_join_kernel<128, TAIL>, rows, threads, 0, stream, a)
                                    : launch_programmatic(token_join_kernel<64, TAIL>, rows, threads, 0, stream, a);
-    return e == cudaSuccess ? BLINK_OK : BLINK_CUDA_ERROR;
+    if (e == cudaSuccess) return BLINK_OK;
+    if (!TAIL) cudaMemsetAsync(a.taken, 0, sizeof(int), stream);  // as the join would have
+    return BLINK_CUDA_ERROR;
 }
 
 bool token_sizes(int32_t S, int32_t T, int32_t max_len, int32_t Hq, int32_t Hkv, int32_t d, blink_status &st)
@@ -851,5 +934,6 @@ extern "C" blink_status blink_paged_token_attention(
     a.part_lse = reinterpret_cast<float *>(ws + plan.lse);
     a.part_o = reinterpret_cast<float *>(ws + plan.o);
     a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
+    a.taken = &static_cast<WorkspaceHeader *>(d_ws)->reserved[0];
     return launch_token<false>(a, plan, page_tokens, d, joined, stream);
 }

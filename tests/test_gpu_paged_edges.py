@@ -472,3 +472,67 @@ def test_sequences_shorter_than_the_bound(T, Hq, Hkv, bound):
     out, lse, _ = blink.blink_paged_token_attention(q, cache, rows, _i32(*lens), bound, want_lse=True, ws=ws)
     assert blink.blink_read_device_status(ws) == blink.BLINK_OK
     ph.check_attention(out, lse, ph.token_reference(q, cache, rows, lens))
+
+
+@pytest.mark.parametrize("S,T,Hq,Hkv,d,page", [(70, 1, 16, 4, 128, 64), (90, 3, 24, 4, 64, 16), (300, 1, 8, 8, 64, 32), (1030, 2, 2, 1, 64, 16),
+                                               (40, 4, 16, 4, 128, 64), (1024, 1, 2, 1, 64, 16)])
+def test_many_sequences_far_below_the_bound(S, T, Hq, Hkv, d, page):
+    """max_len 131072 (a call captured for any length) over many short sequences, some empty, and one long one, over one
+    table: the plain form's results, the same bits each time, and bad lengths cut and flagged."""
+    g = ph.gen(S + T)
+    some = torch.randint(0, 700, (S,), generator=torch.Generator().manual_seed(S)).tolist()
+    lens = [0 if i % 11 == 0 else n for i, n in enumerate(some)]
+    lens[S - 3], lens[S // 2], lens[1] = 9000, 2049, 1
+    row, total = ph.table_for(g, [9000], page)  # the sequences share their pages
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, row, [9000])
+    table = row.expand(S, -1).contiguous()
+    q = ph.randn(g, S, T, Hq, d).to(torch.bfloat16)
+    length = _i32(*lens)
+    out, lse, ws = blink.blink_paged_token_attention(q, cache, table, length, 131072, want_lse=True)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+    ph.check_attention(out, lse, ph.token_reference(q, cache, table, lens))
+    for _ in range(5):
+        again, lse2, _ = blink.blink_paged_token_attention(q, cache, table, length, 131072, want_lse=True, ws=ws)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+    worse = list(lens)
+    worse[0], worse[S - 1] = -7, 131073
+    cut = list(lens)
+    cut[0], cut[S - 1] = 0, row.shape[1] * page
+    if cut[S - 1] > 9000:  # the table's last slots hold no token
+        table = table[:, :9000 // page].contiguous()
+        cut = [min(n, 9000 // page * page) for n in cut]
+        worse = [min(n, 9000 // page * page) if n <= 9000 else n for n in worse]
+    out, lse, ws = blink.blink_paged_token_attention(q, cache, table, _i32(*worse), 131072, want_lse=True, ws=ws)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_DEVICE_FLAG
+    ph.check_attention(out, lse, ph.token_reference(q, cache, table, cut))
+
+
+def test_two_captured_calls_far_below_the_bound():
+    """Two graphs over one workspace, each for many sequences whose lengths change between replays."""
+    g = ph.gen(55)
+    S, Hq, Hkv, d, page, most = 80, 8, 4, 128, 64, 4000
+    row, total = ph.table_for(g, [most], page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    ph.fill(g, cache, row, [most])
+    table = row.expand(S, -1).contiguous()
+    qs = [ph.randn(g, S, 1, Hq, d).to(torch.bfloat16) for _ in range(2)]
+    length, outs, graphs = torch.full((S,), 100, dtype=torch.int32, device="cuda"), [torch.empty_like(qs[0]) for _ in range(2)], []
+    ws = blink.new_workspace(blink.paged_token_attention_workspace_bytes(S, 1, 131072, Hq, Hkv, d), "cuda")
+    for i in range(2):
+        blink.blink_paged_token_attention(qs[i], cache, table, length, 131072, out=outs[i], ws=ws)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            blink.blink_paged_token_attention(qs[i], cache, table, length, 131072, out=outs[i], ws=ws)
+    for step in range(6):
+        lens = torch.randint(0, most if step % 2 else 90, (S,), device="cuda", generator=g).to(torch.int32)
+        length.copy_(lens)
+        for i in (0, 1, 0):
+            graphs[i].replay()
+        for i in range(2):
+            want, _, _ = blink.blink_paged_token_attention(qs[i], cache, table, lens, most)
+            a, b = outs[i].double(), want.double()  # cut otherwise: each within half a step and the weights' roundings
+            assert float((a - b).abs().max()) <= 2e-2 * float(b.abs().max())
+            assert bool((outs[i][lens == 0] == 0).all())
+    torch.cuda.synchronize()
+    assert blink.blink_read_device_status(ws) == blink.BLINK_OK
