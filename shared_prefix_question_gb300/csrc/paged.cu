@@ -452,7 +452,8 @@ struct GatherArgs {
     PagedCache c;
     const int32_t *table;
     int64_t table_stride;
-    int Hkv;
+    int Hkv, n_req;
+    int64_t rows;                 // of all regions
     int64_t first[kMaxRequests];  // row of each request's region
     int len[kMaxRequests];
     uint16_t *k, *v;              // [rows][Hkv][D]
@@ -463,20 +464,26 @@ constexpr int kGatherThreads = 256;
 
 // The prefix pages of each request as bf16 rows of a contiguous region (codes times scales are exact in bf16), so
 // that the tensor-core attention reads them by its tensor maps: 2 bytes read and 4 written a key and channel, once
-// per call, against hundreds of products a byte in the attention.  A thread turns 16 codes of K and of V.
+// per call, against hundreds of products a byte in the attention.  A thread turns 16 codes of K and of V.  The grid goes over
+// the rows of all regions (a request of 131072 tokens among 63 of 1000: 1866 us a call; as many blocks for each as the longest
+// takes: 2844).
 template <int D>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ GatherArgs a)
 {
     constexpr int kPieces = D / 16;
     ptx::grid_dep_wait();
-    const int r = blockIdx.y;
-    const int len = a.len[r], padded = (len + kTile - 1) / kTile * kTile;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x;
     const int piece = static_cast<int>(item % kPieces);
     const int64_t th = item / kPieces;
     const int h = static_cast<int>(th % a.Hkv);
-    const int64_t token = th / a.Hkv;
-    if (token >= padded) return;
+    const int64_t row = th / a.Hkv;  // of all regions, which lie one behind the other
+    if (row >= a.rows) return;
+    int r = 0;                       // the last request whose region starts at or before it
+    if (a.n_req > 1)
+#pragma unroll
+        for (int step = kMaxRequests / 2; step; step /= 2) r += r + step < a.n_req && a.first[r + step] <= row ? step : 0;
+    const int64_t token = row - a.first[r];
+    const int len = a.len[r];
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
     float fk = 0.f, fv = 0.f;
     if (token < len) {
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
         }
         ptx::st_global_v8(dst, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);
     };
-    const int64_t to = ((a.first[r] + token) * a.Hkv + h) * D + piece * 16;
+    const int64_t to = (row * a.Hkv + h) * D + piece * 16;
     put(k, fk, a.k + to);
     put(v, fv, a.v + to);
 }
@@ -665,11 +672,8 @@ extern "C" blink_status blink_paged_prefix_tail_attention(
     if (reinterpret_cast<uintptr_t>(d_ws) % 32 != 0) return BLINK_INVALID_ARG;  // rows are written 32 bytes at a time
     if (std::isnan(scale) || std::isinf(scale)) return BLINK_INVALID_ARG;
     if (B < 1 || B > BLINK_MAX_PLAN_SEQUENCES || max_tail > BLINK_MAX_INPUT_TOKENS) return BLINK_OUT_OF_RANGE;
-    int longest = 0;
-    for (int r = 0; r < n_req; ++r) {
+    for (int r = 0; r < n_req; ++r)
         if (h_prefix_len[r] > static_cast<int64_t>(table_width) * page_tokens) return BLINK_OUT_OF_RANGE;
-        longest = h_prefix_len[r] > longest ? h_prefix_len[r] : longest;
-    }
     if (few_tail_rows(h_req_rows, n_req, Hq / Hkv)) {
         if (static_cast<int64_t>(rows) * Hq > 0x7FFFFFFF) return BLINK_OUT_OF_RANGE;
         if (ws_bytes < few_tail_workspace(h_req_rows, h_prefix_len, n_req, Hkv, Hq / Hkv, d)) return BLINK_WORKSPACE_TOO_SMALL;
@@ -691,15 +695,18 @@ extern "C" blink_status blink_paged_prefix_tail_attention(
         a.len[r] = h_prefix_len[r];
         at += (h_prefix_len[r] + kTile - 1) / kTile * kTile;
     }
-    if (longest > 0) {
+    if (lay.rows > 0) {
         a.table = d_page_table;
         a.table_stride = table_stride;
         a.Hkv = Hkv;
         a.k = ka;
         a.v = va;
         a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
-        const int64_t items = static_cast<int64_t>((longest + kTile - 1) / kTile * kTile) * Hkv * (d / 16);
-        const dim3 grid(static_cast<unsigned>((items + kGatherThreads - 1) / kGatherThreads), static_cast<unsigned>(n_req));
+        a.n_req = n_req;
+        a.rows = lay.rows;
+        const int64_t blocks = (lay.rows * Hkv * (d / 16) + kGatherThreads - 1) / kGatherThreads;
+        if (blocks > 0x7FFFFFFF) return BLINK_OUT_OF_RANGE;
+        const dim3 grid(static_cast<unsigned>(blocks));
         const cudaError_t e = d == 128 ? launch_programmatic(gather_kernel<128>, grid, kGatherThreads, 0, stream, a)
                                        : launch_programmatic(gather_kernel<64>, grid, kGatherThreads, 0, stream, a);
         if (e != cudaSuccess) return BLINK_CUDA_ERROR;
