@@ -139,14 +139,15 @@ __device__ __forceinline__ int piece_at(int row, int piece)
 }
 
 // The chunks that the sequences before each have together, `first`, and all of them (returned), by a whole block.
+template <bool TAIL>
 __device__ __forceinline__ int count_chunks(const TokenArgs &a, int *first)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, each = (a.S + kThreads - 1) / kThreads;
     const int begin = min(threadIdx.x * each, a.S), end = min(begin + each, a.S);
     int mine = 0;
     for (int s = begin; s < end; ++s) {
-        bool bad;
-        const int len = length_of(a, s, bad), chunk = chunk_of(a, len);
+        bool bad = false;
+        const int len = TAIL ? a.tail.len[s] : length_of(a, s, bad), chunk = chunk_of(a, len);
         if (bad && blockIdx.x == 0) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
         first[s] = mine;
         mine += (len + chunk - 1) / chunk;
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
     int items = 1;
     if constexpr (PACKED) {
         init_bars();
-        items = count_chunks(a, first) * a.Hkv * a.tiles;
+        items = count_chunks<TAIL>(a, first) * a.Hkv * a.tiles;
     }
     for (int item = PACKED ? blockIdx.x : 0, turn = 0; item < items; turn ^= 1) {
         int ticket = 0;
@@ -224,7 +225,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
         const int64_t token0 = TAIL ? a.tail.row[seq] : static_cast<int64_t>(seq) * a.T;
         const int Tg = T * a.g, rho0 = tile * Sh::kRows, rows = min(Sh::kRows, Tg - rho0);
 
-        if (TAIL && rows <= 0) return;  // fewer rows than another request
+        if (TAIL && rows <= 0) {  // fewer rows than another request
+            if constexpr (!PACKED) return;
+            if (threadIdx.x == 0) next[turn] = ticket;
+            __syncthreads();
+            item = next[turn];
+            continue;
+        }
         // The pages of this warp's steps, one a lane, read before the length is known, and again if it takes shorter chunks.
         auto page_from = [&](int k0) {
             const int64_t index = (static_cast<int64_t>(k0) + (warp + lane * kWarps) * kStep) >> a.c.log2_page;
@@ -664,7 +671,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) token_join_kernel(const __gri
     }
     ptx::grid_dep_wait();
     ptx::grid_launch_dependents();
-    if (!TAIL && row == 0 && threadIdx.x == 0) *a.taken = 0;
+    if (row == 0 && threadIdx.x == 0) *a.taken = 0;
     const float *pl = a.part_lse + row * a.chunks, *po = a.part_o + row * a.chunks * D + lane * kVec;
     for (int c0 = warp; c0 < n; c0 += warps * kJoinBatch) {
         float l[kJoinBatch], x[kJoinBatch][kVec];
@@ -759,15 +766,13 @@ bool launch_pages(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const TokenA
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
         return launch_programmatic(kern, grid, kThreads, smem, stream, tm_k, tm_v, a) == cudaSuccess;
     };
-    if constexpr (!TAIL) {
-        const int64_t blocks = static_cast<int64_t>(a.chunks) * a.Hkv * a.tiles * a.S;
-        const int64_t at_once = static_cast<int64_t>(current_sm_count()) * Shape<D, 1>::kResident;
-        if (a.chunks > 1 && a.S > 1 && a.S <= kMaxPacked && blocks > kPackedWaves * at_once && blocks <= 1 << 30) {
-            grid = dim3(static_cast<unsigned>(at_once));
-            const int more = (a.S + kWarps + 2) * static_cast<int>(sizeof(int));
-            return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL, true>, Shape<D, 1>::kSmem + more)
-                                  : launch(token_attention_kernel<D, 2, TAIL, true>, Shape<D, 2>::kSmem + more);
-        }
+    const int64_t blocks = static_cast<int64_t>(a.chunks) * a.Hkv * a.tiles * a.S;
+    const int64_t at_once = static_cast<int64_t>(current_sm_count()) * Shape<D, 1>::kResident;
+    if (a.chunks > 1 && a.S > 1 && a.S <= kMaxPacked && blocks > kPackedWaves * at_once && blocks <= 1 << 30) {
+        grid = dim3(static_cast<unsigned>(at_once));
+        const int more = (a.S + kWarps + 2) * static_cast<int>(sizeof(int));
+        return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL, true>, Shape<D, 1>::kSmem + more)
+                              : launch(token_attention_kernel<D, 2, TAIL, true>, Shape<D, 2>::kSmem + more);
     }
     return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL, false>, Shape<D, 1>::kSmem)
                           : launch(token_attention_kernel<D, 2, TAIL, false>, Shape<D, 2>::kSmem);
@@ -793,7 +798,7 @@ blink_status launch_token(const TokenArgs &a, const TokenPlan &plan, int page_to
     const cudaError_t e = d == 128 ? launch_programmatic(token_join_kernel<128, TAIL>, rows, threads, 0, stream, a)
                                    : launch_programmatic(token_join_kernel<64, TAIL>, rows, threads, 0, stream, a);
     if (e == cudaSuccess) return BLINK_OK;
-    if (!TAIL) cudaMemsetAsync(a.taken, 0, sizeof(int), stream);  // as the join would have
+    cudaMemsetAsync(a.taken, 0, sizeof(int), stream);  // as the join would have
     return BLINK_CUDA_ERROR;
 }
 
@@ -870,6 +875,7 @@ blink_status few_tail_attention(const PagedCache &c, int page_tokens, const uint
     a.part_lse = reinterpret_cast<float *>(ws + plan.lse);
     a.part_o = reinterpret_cast<float *>(ws + plan.o);
     a.err = &static_cast<WorkspaceHeader *>(d_ws)->error;
+    a.taken = &static_cast<WorkspaceHeader *>(d_ws)->reserved[0];
     for (int r = 0; r < n_req; ++r) a.tail.row[r] = h_req_rows[r], a.tail.len[r] = h_len[r];
     a.tail.row[n_req] = h_req_rows[n_req];
     a.tail.n_req = n_req;

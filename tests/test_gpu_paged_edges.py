@@ -536,3 +536,39 @@ def test_two_captured_calls_far_below_the_bound():
             assert bool((outs[i][lens == 0] == 0).all())
     torch.cuda.synchronize()
     assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,page,most", [(4, 2, 64, 16, 12), (4, 4, 128, 64, 3)])
+def test_few_tail_rows_against_prefixes_of_unequal_lengths(Hq, Hkv, d, page, most):
+    """64 requests of a few rows, or none, against prefixes of 0 to 131072 tokens: one question each."""
+    g = ph.gen(most)
+    prefix = torch.randint(0, 500, (64,), generator=torch.Generator().manual_seed(most)).tolist()
+    prefix[5], prefix[40], prefix[63] = 131072, 0, 5000
+    news = torch.randint(0, most + 1, (64,), generator=torch.Generator().manual_seed(most + 1)).tolist()
+    news[5], news[40], news[63] = 2, 1, most
+    row, total = ph.table_for(g, [131072], page)
+    cache = ph.new_cache(g, total, Hkv, page, d)
+    scale = [torch.randint(119, 123, (total, Hkv), device="cuda", generator=g).to(torch.uint8) for _ in range(2)]
+    for n, e in zip("kv", scale):
+        cache[n].view(torch.uint8).copy_((110 * ph.randn(g, *cache[n].shape)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+        cache[n + "_scale"].view(torch.uint8).copy_(e)
+    table = row.expand(64, -1).contiguous()  # requests share their pages
+    at = [sum(news[:i]) for i in range(65)]
+    cu = sorted(set(at))
+    rows = at[-1]
+    q, k, v = (ph.randn(g, rows, H, d).to(torch.bfloat16) for H in (Hq, Hkv, Hkv))
+    args = (q, cache, table, prefix, k, v, _i32(*cu), len(cu) - 1, most)
+    out, lse, ws = blink.blink_paged_prefix_tail_attention(*args, req_rows=at, want_lse=True)
+    assert blink.blink_read_device_status(ws) == blink.BLINK_OK
+    ref = []
+    for r in range(64):
+        pre = [ph.values(cache, n, table[r], prefix[r]) for n in "kv"]
+        for i in range(at[r], at[r + 1]):
+            kk, vv = (torch.cat([x, y[at[r]:i + 1].double().transpose(0, 1)], dim=1) for x, y in zip(pre, (k, v)))
+            ref.append(ph.attend(q[i], kk, vv, 1 / math.sqrt(d)))
+    o, l, mag, size = zip(*ref)
+    ph.check_attention(out[:, None], lse, (torch.stack(o)[:, None], torch.stack(l, dim=1), torch.stack(mag, dim=1)[:, :, None],
+                                           torch.stack(size, dim=1)))
+    for _ in range(3):
+        again, lse2, _ = blink.blink_paged_prefix_tail_attention(*args, req_rows=at, want_lse=True, ws=ws)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
