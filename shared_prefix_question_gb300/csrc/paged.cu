@@ -91,8 +91,8 @@ __device__ __forceinline__ void block_max(uint32_t &k, uint32_t &v, uint32_t (*p
 constexpr float kTurnError = 7.f * 5.9604645e-8f;
 
 // Rotated values that the 32-bit rotation leaves between two codes (bit e of `mask`: value e of the thread's 16, eight
-// from place j0 and eight from j1 of a head): computed to some 40 bits, and the nearer code written.  `factor`: the
-// amplitude over the scale.
+// from place j0 and eight from j1 of a head, all of them below rot): computed to some 40 bits, and the nearer code written.
+// `factor`: the amplitude over the scale.
 template <bool INTERLEAVED>
 __device__ __noinline__ void write_nearer_codes(uint32_t mask, uint8_t *codes, const uint16_t *k, int j0, int j1, int half,
                                                 const uint64_t *turns, int32_t pos, float factor)
@@ -403,12 +403,18 @@ __global__ void __launch_bounds__(D * 4) append_kernel(const __grid_constant__ A
                     kc[p0] = make_uint2(q[0], q[1]);
                     kc[p1] = make_uint2(q[2], q[3]);
                     if (differ[0] | differ[1] | differ[2] | differ[3]) {
+                        // Of values that turn: one that passes is exact, and a zero's two codes differ in their signs.
+                        auto turns = [&](int e) {
+                            return LAYOUT == kHalves ? turn : LAYOUT == kInterleaved ? pair_of(e / 2) < half : (e < 8 ? p0 : p1) * 8 + (e & 7) < a.rot;
+                        };
                         uint32_t mask = 0;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) mask |= (differ[e / 4] >> 8 * (e & 3) & 0xFFu) ? 1u << e : 0u;
-                        const int which = (h - h_begin) * kSlots + t;
-                        any_unsure |= 1u << which;
-                        unsure[which * blockDim.x] = static_cast<uint16_t>(mask);
+                        for (int e = 0; e < 16; ++e) mask |= turns(e) && (differ[e / 4] >> 8 * (e & 3) & 0xFFu) ? 1u << e : 0u;
+                        if (mask) {
+                            const int which = (h - h_begin) * kSlots + t;
+                            any_unsure |= 1u << which;
+                            unsure[which * blockDim.x] = static_cast<uint16_t>(mask);
+                        }
                     }
                 }
             } else if (slot[t] < filled) {
