@@ -362,15 +362,14 @@ __global__ void __launch_bounds__(D * 4) append_kernel(const __grid_constant__ A
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[t][e] = ptx::mul_f32x2(x[t][e], fk2);
-                if (LAYOUT == kNoRotation || infinite_key) {
+                if (LAYOUT == kNoRotation || infinite_key || (LAYOUT == kHalves && !turn)) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) q[i] = f32x4_to_e4m3x4(x[t][2 * i], x[t][2 * i + 1]);
                     kc[p0] = make_uint2(q[0], q[1]);
                     kc[p1] = make_uint2(q[2], q[3]);
                 } else {
                     // Codes of the least and the most that each exact value can be.
-                    const float error = turn ? kTurnError : 0.f;
-                    const uint64_t more = ptx::f32x2(error, error), less = ptx::f32x2(-error, -error);
+                    const uint64_t more = ptx::f32x2(kTurnError, kTurnError), less = ptx::f32x2(-kTurnError, -kTurnError);
                     uint64_t size[8];  // what the error is relative to, for values 2 e and 2 e + 1
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -405,7 +404,7 @@ __global__ void __launch_bounds__(D * 4) append_kernel(const __grid_constant__ A
                     if (differ[0] | differ[1] | differ[2] | differ[3]) {
                         // Of values that turn: one that passes is exact, and a zero's two codes differ in their signs.
                         auto turns = [&](int e) {
-                            return LAYOUT == kHalves ? turn : LAYOUT == kInterleaved ? pair_of(e / 2) < half : (e < 8 ? p0 : p1) * 8 + (e & 7) < a.rot;
+                            return LAYOUT == kHalves || (LAYOUT == kInterleaved ? pair_of(e / 2) < half : (e < 8 ? p0 : p1) * 8 + (e & 7) < a.rot);
                         };
                         uint32_t mask = 0;
 #pragma unroll

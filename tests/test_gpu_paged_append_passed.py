@@ -53,3 +53,32 @@ def test_zeros_of_either_sign_pass(d, rot, interleaved):
     x[3, 1, rot:] = -0.0
     got, want = _append(x, d, rot, interleaved)
     assert torch.equal(got, want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("d,rot,interleaved", PARTS)
+def test_nan_passes_alone(d, rot, interleaved):
+    """A NaN among the passed values is one NaN code: the other values of its key, its pair's place among them, get their own."""
+    g = ph.gen(d + rot + 1)
+    n, Hkv = 70, 2
+    x = ph.randn(g, n, Hkv, d).to(torch.bfloat16)
+    alone = torch.rand(n, Hkv, d - rot, device="cuda", generator=g) < 0.1
+    x[..., rot:][alone] = math.nan
+    got, want = _append(x, d, rot, interleaved)
+    assert torch.equal(got.view(torch.float8_e4m3fn).double().isnan(), alone)
+    assert torch.equal(got[~alone], want.view(torch.uint8)[~alone])
+
+
+@pytest.mark.parametrize("d,rot,interleaved", PARTS)
+def test_infinities_pass_alone(d, rot, interleaved):
+    """Infinities, a NaN and zeros of either sign among the passed values: infinities take the largest code, the scale is that
+    of the finite values, and the others get the codes that they have without them."""
+    g = ph.gen(d + rot + 2)
+    n, Hkv = 70, 2
+    x = ph.randn(g, n, Hkv, d).to(torch.bfloat16)
+    pick = torch.randint(0, 40, (n, Hkv, d - rot), device="cuda", generator=g)
+    for i, value in enumerate((math.inf, -math.inf, math.nan, -0.0, 0.0)):
+        x[..., rot:][pick == i] = value
+    got, want = _append(x, d, rot, interleaved)
+    assert bool((got[pick == 0] == 0x7E).all()) and bool((got[pick == 1] == 0xFE).all())
+    assert torch.equal(got[pick != 2], want.view(torch.uint8)[pick != 2])
+    assert bool(got[pick == 2].view(torch.float8_e4m3fn).double().isnan().all())
