@@ -762,20 +762,25 @@ template <int D, bool TAIL>
 bool launch_pages(const CUtensorMap &tm_k, const CUtensorMap &tm_v, const TokenArgs &a, const TokenPlan &plan, cudaStream_t stream)
 {
     dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.Hkv * a.tiles), static_cast<unsigned>(a.S));
-    auto launch = [&](auto kern, int smem) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+    // The kernel's limit is the most that any call takes: it belongs to the function, and another thread's call may set it between
+    // this one's setting and its launch.
+    auto launch = [&](auto kern, int smem, int limit) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, limit) != cudaSuccess) return false;
         return launch_programmatic(kern, grid, kThreads, smem, stream, tm_k, tm_v, a) == cudaSuccess;
     };
     const int64_t blocks = static_cast<int64_t>(a.chunks) * a.Hkv * a.tiles * a.S;
     const int64_t at_once = static_cast<int64_t>(current_sm_count()) * Shape<D, 1>::kResident;
     if (a.chunks > 1 && a.S > 1 && a.S <= kMaxPacked && blocks > kPackedWaves * at_once && blocks <= 1 << 30) {
         grid = dim3(static_cast<unsigned>(at_once));
-        const int more = (a.S + kWarps + 2) * static_cast<int>(sizeof(int));
-        return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL, true>, Shape<D, 1>::kSmem + more)
-                              : launch(token_attention_kernel<D, 2, TAIL, true>, Shape<D, 2>::kSmem + more);
+        constexpr int kInt = sizeof(int);
+        const int more = (a.S + kWarps + 2) * kInt;
+        constexpr int kMost = (kMaxPacked + kWarps + 2) * kInt;
+        return plan.wide == 1
+                   ? launch(token_attention_kernel<D, 1, TAIL, true>, Shape<D, 1>::kSmem + more, Shape<D, 1>::kSmem + kMost)
+                   : launch(token_attention_kernel<D, 2, TAIL, true>, Shape<D, 2>::kSmem + more, Shape<D, 2>::kSmem + kMost);
     }
-    return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL, false>, Shape<D, 1>::kSmem)
-                          : launch(token_attention_kernel<D, 2, TAIL, false>, Shape<D, 2>::kSmem);
+    return plan.wide == 1 ? launch(token_attention_kernel<D, 1, TAIL, false>, Shape<D, 1>::kSmem, Shape<D, 1>::kSmem)
+                          : launch(token_attention_kernel<D, 2, TAIL, false>, Shape<D, 2>::kSmem, Shape<D, 2>::kSmem);
 }
 
 // The pages' part, then the join of `joined` rows as its programmatic dependent.
