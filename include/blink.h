@@ -614,7 +614,8 @@ blink_status blink_paged_token_attention(const blink_bf16 *q, const uint8_t *k_c
  * Where no request has more than 64 rows times Hq/Hkv the pages are read as they are (weights enter the second
  * product in fp16, a question's own keys in 32 bits); otherwise the workspace holds the prefixes as bf16 rows,
  * exactly, and the result is that of the calls named.
- * Other arguments as there.  A page index outside [0, n_pages) latches BLINK_DEVICE_FLAG (its values count as 0).
+ * Other arguments as there.  A page index outside [0, n_pages) latches BLINK_DEVICE_FLAG; its keys and values are zeros
+ * either way (they score 0 and have that weight).
  * Errors: BLINK_INVALID_ARG, BLINK_OUT_OF_RANGE, BLINK_WORKSPACE_TOO_SMALL, BLINK_CUDA_ERROR; device-side:
  * BLINK_DEVICE_FLAG, BLINK_DEVICE_TIMEOUT.
  * ------------------------------------------------------------------------------------------ */

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
         int scales = kScaleBias | kScaleBias << 8;
         if (page < 0 || page >= a.c.n_pages || lane >= mine) {
             if (lane < mine) atomicCAS(a.err, 0, BLINK_DEVICE_FLAG);
-            page = -1;  // past the end, or not a page: its keys are masked
+            page = -1;  // past the end, or not a page: its keys are masked (TAIL: zeros, as in the rows that pages are turned to)
         } else {
             scales = (exponent_of(__ldg(a.c.k_scale + page * a.c.scale_stride + h)) + kScaleBias) |
                      (exponent_of(__ldg(a.c.v_scale + page * a.c.scale_stride + h)) + kScaleBias) << 8;
@@ -380,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
                 if (edge) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (key + r + 8 * (e >> 1) >= see[y][e & 1] || id < 0) x[y][e] = -INFINITY;
+                        if (key + r + 8 * (e >> 1) >= see[y][e & 1] || (!TAIL && id < 0)) x[y][e] = -INFINITY;
+                        else if (TAIL && id < 0) x[y][e] = 0.f;
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) grow = grow || fmaxf(x[y][c], x[y][c + 2]) > most[y][c] + (kSlack + kHead);
