@@ -542,7 +542,8 @@ blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const blink_bf16 
  * not a multiple of page_tokens) keeps its scale if that is larger; if the scale grows, its tokens' codes
  * are rounded again, which changes only those that become subnormal.  Slots that get no token keep
  * their codes.
- * k [n, Hkv, d], v  bf16, rows *_stride elements apart (multiples of 8, 16-byte aligned); keys not yet rotated
+ * k [n, Hkv, d], v  bf16, rows *_stride elements apart (multiples of 8, 16-byte aligned); keys not yet rotated; n 0:
+ *                   nothing is done or checked on the device
  * d_cu_new [S+1]    sequence s's tokens are rows cu[s] - cu[0] .. of k and v (none is fine)
  * d_start [S]       tokens that the sequence holds; its new ones follow them
  * S, max_new        1..BLINK_MAX_PLAN_SEQUENCES; upper bound of the new tokens of a sequence, checked on the

@@ -588,7 +588,7 @@ extern "C" blink_status blink_paged_append(const blink_bf16 *k, int64_t k_stride
     if (interleaved != 0 && interleaved != 1) return BLINK_INVALID_ARG;
     if (rot < 0 || rot > d || rot % 2 != 0 || (rot > 0 && (!d_turns || !std::isfinite(amplitude)))) return BLINK_INVALID_ARG;
     if (ws_bytes < kHeaderBytes) return BLINK_WORKSPACE_TOO_SMALL;
-    if (n == 0 || max_new == 0) return BLINK_OK;
+    if (n == 0) return BLINK_OK;
 
     AppendArgs a{};
     a.k = k;
