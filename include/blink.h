@@ -22,6 +22,7 @@
  *   - bf16 tensors are passed as `blink_bf16` (16-bit storage of bfloat16 values), row-major.
  *   - Calls are asynchronous on `stream` unless a host output is requested, in which case the
  *     call synchronises the stream before returning.
+ *   - Any host thread may call, several at once with a workspace each (but see the readout that allocates nothing).
  *   - Arguments are checked on the host first (BLINK_INVALID_ARG / BLINK_OUT_OF_RANGE, nothing
  *     launched).  Problems only visible on the device (a bad length or label id inside a
  *     device array, a bounded wait that ran out) are latched in a device error word, read back
@@ -537,8 +538,9 @@ blink_status blink_rope(const blink_bf16 *q, int64_t q_stride, const blink_bf16 
  *
  * blink_paged_append writes the next tokens of S sequences and turns their keys on the way.  With m the
  * largest finite magnitude of the tokens that a page gets for a head, the scale is the smallest 2^e with
- * m <= 448 * 2^e, e in BLINK_PAGED_SCALE_MIN..MAX; a code is value / scale rounded to the nearest (ties to
- * even) and at most 448, a NaN stays one.  A page that holds tokens of the sequence already (start is
+ * m <= 448 * 2^e, e in BLINK_PAGED_SCALE_MIN..MAX (m of the keys turned in 32 bits); a code is value / scale rounded to the
+ * nearest (ties to even) and at most 448, an infinity too, a NaN stays one.  Turned keys' codes are those of the exact rotation,
+ * but those of a page and head among whose new keys is an infinity, which are of the 32-bit one.  A page that holds tokens of the sequence already (start is
  * not a multiple of page_tokens) keeps its scale if that is larger; if the scale grows, its tokens' codes
  * are rounded again, which changes only those that become subnormal.  Slots that get no token keep
  * their codes.

@@ -153,8 +153,8 @@ constexpr int kMaxBlockHeads = 8;
 // in shared memory meanwhile (no registers, no barrier).  The angles belong to the slot, so a thread computes its own
 // once for all heads.
 // Codes are those of the exact rotation: where the 32-bit one is too near the border of two codes to tell (one value of
-// some 10,000), a bit remembers it, and when the block's heads are done those values are computed to 40 bits.  (In a page
-// whose keys hold an infinity the 32-bit rotation decides.)
+// some 10,000), a bit remembers it, and when the block's heads are done those values are computed to some 40 bits.  (In a page
+// whose keys hold an infinity the 32-bit rotation decides.)  Values that pass and pairs of zeros are exact and never among them.
 template <int D, int LAYOUT>
 __global__ void __launch_bounds__(D * 4) append_kernel(const __grid_constant__ AppendArgs a)
 {
@@ -626,7 +626,8 @@ extern "C" blink_status blink_paged_append(const blink_bf16 *k, int64_t k_stride
     if (a.heads_per_block > kMaxBlockHeads) a.heads_per_block = kMaxBlockHeads;
     // As many pages for each sequence as max_new tokens can touch, or (with a search in each block) places for those that n
     // tokens of S sequences can, whichever are fewer (18432 tokens and 63 single ones: 52 us with empty pages for each, 32
-    // packed; 64 single ones with max_new 18432: 90, 8.8; 16 pieces of up to 511: 8.8, 8.0; 16 of 100 to 3850: 42.3, 43.4).
+    // packed; 64 single ones with max_new 18432: 90, 10.5; 16 pieces of up to 511: 8.8, 8.0).  Where half of the pages are empty the
+    // search can cost more than they do (16 of 100 to 3850: 42.3, 43.3).
     const int64_t places = n / page_tokens + 2LL * S;
     a.packed = places < static_cast<int64_t>(pages) * S;
     const dim3 grid(static_cast<unsigned>(a.packed ? places : pages),

@@ -30,12 +30,14 @@ constexpr int kRound = kStep * kWarps;           // keys of a block per step of 
 constexpr int kMaxChunk = 32 * kRound;           // a lane holds the page of one step of its warp
 // (Row, query head) rows of a kv head, in any request, up to which tail rows read the pages: every 16 of them read and convert
 // all codes again, while bf16 rows are written once and shared by 128.  18432 keys, one request of 16 tokens and 32/8 heads
-// (64 rows): 29 us from the pages, 43 by way of bf16 rows; of 32 tokens 62 and 44; 2048 keys: 12 and 19, 18 and 19.
+// (64 rows): 29 us from the pages, 43 by way of bf16 rows; of 32 tokens 62 and 44; 2048 keys: 12 and 19, 18 and 19.  The limit
+// does not look at the prefix: up to some 2048 keys it is too low for 128 rows, by a microsecond.
 constexpr int kFewRows = 64;
 // Waves of blocks from which, and sequences up to which, a grid of as many blocks as run at once takes the chunks that there are,
 // one after the other, in place of a grid for all chunks that max_len allows.  A block without keys takes some 1.3 ns, but next
 // chunks taken by a counter cost up to 2 % (max_len 131072, sequences of 1000 tokens, 64 of them: 72 and 39 us; 256: 257 and 112;
-// 256 of 8000: 633 and 616; with max_len 18432, 11 waves, 64 of up to 18432: 187 and 191).
+// 256 of 8000: 633 and 616; with max_len 18432, 11 waves, 64 of up to 18432: 187 and 191).  The lengths are on the device, so below
+// the limit a call far below its max_len keeps the direct grid (eight of 1000, max_len 131072: 13.7 us, by the counter 9.8).
 constexpr int kPackedWaves = 16, kMaxPacked = 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e37f;                 // below any score
@@ -301,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kResident) token_atten
                 m = fmaxf(m, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            // the row's largest value between 2^9 and 2^10: values 2^-33 of it and smaller lose bits, none overflows
+            // the row's largest value between 2^9 and 2^10: none overflows, and values below 2^-26 of it lose bits (fp16's last
+            // step is 2^-24, a value's eight bits end 2^-7 below its first)
             int move = 9 - (static_cast<int>(__float_as_uint(m) >> 23) - 127);
             move = !(m > 0.f) || m == INFINITY ? 0 : min(move, 126);
             const float f = scale_of(move), back = a.scale_log2 * scale_of(-move);

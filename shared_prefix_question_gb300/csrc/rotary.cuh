@@ -35,8 +35,8 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t turns, int32_t pos, float 
     s = __uint_as_float(sc ^ (quarter & 0x80000000u));
 }
 
-// Sums of two 32-bit values, the second what the first lacks: some 44 bits.  (64-bit arithmetic takes about a microsecond
-// an operation here.)
+// Sums of two 32-bit values, the second what the first lacks: some 44 bits.  (In 64-bit arithmetic, whose rate is a small part of
+// the 32-bit one, the append's undecided codes took 53 us for 18432 tokens of 8 heads in place of 27.)
 struct Two {
     float h, l;
 };
